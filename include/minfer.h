@@ -45,10 +45,11 @@ extern "C" {
 #define MINFER_ERR_SHAPE (-5)          /* unknown tensor name, wrong ne0/ne1/type, or hparams
                                           the kernels are not built for */
 #define MINFER_ERR_CUDA (-6)           /* a CUDA runtime/driver call failed */
-#define MINFER_ERR_OOM (-7)            /* device allocation failed */
+#define MINFER_ERR_OOM (-7)            /* device allocation failed; page pool exhausted */
 #define MINFER_ERR_DEVICE (-8)         /* a kernel gave up a bounded wait (status word set) */
 #define MINFER_ERR_STATE (-9)          /* call order violated (e.g. prefill before finalize) */
-#define MINFER_ERR_TOO_LARGE (-10)     /* the problem does not fit a fixed-size scratch area */
+#define MINFER_ERR_TOO_LARGE (-10)     /* the problem does not fit a fixed-size scratch area
+                                          (or, for the batch operators, its buffers) */
 
 /* Device status codes (minfer_device_status): which bounded wait of which
  * kernel gave up first when a call returned MINFER_ERR_DEVICE. */
@@ -62,6 +63,8 @@ extern "C" {
 
 /* ---------------------------------------------------------------- tensors */
 #define MINFER_F32 0  /* float32 values */
+#define MINFER_F16 1   /* IEEE half values (batch operators) */
+#define MINFER_BF16 30 /* bfloat16 values (batch operators) */
 #define MINFER_Q8_0 8 /* blocks of 34 bytes: uint16 fp16 scale bits (little endian),
                          then 32 int8 codes; a row of ne0 values holds ceil(ne0/32)
                          blocks, the missing tail elements of a partial block are 0 */
@@ -357,6 +360,176 @@ int minfer_op_qknorm_rope_store(const float* d_qkv, const float* d_bias, const f
 int minfer_op_gemm_noalloc(const int8_t* d_xq, const uint16_t* d_xd, int64_t M,
                            const int8_t* d_wq, const uint16_t* d_wd, int64_t N, int64_t K,
                            float* d_y);
+
+/* ---------------------------------------------------------------- batch operators
+ * The operators of one step of a batch of requests whose K/V rows live in a
+ * pool of pages shared by all of them: the pages (block) table and the slot of
+ * every new token, RoPE with the K/V store into the pages, the attention of one
+ * new token per request, and the log probabilities of logits rows.
+ *
+ * Conventions of this section
+ *  - All pointers are device memory of the current device unless a comment
+ *    says host; the work is enqueued on `stream` (a cudaStream_t, NULL: the
+ *    legacy default stream) without any host synchronization or allocation, so
+ *    every call can be captured into a CUDA graph.  The calls hold no state:
+ *    two of them may run at once as long as they share no buffer that one of
+ *    them writes, a workspace included.
+ *  - Host arguments are checked before anything is enqueued
+ *    (MINFER_ERR_ARG / _SHAPE / _TOO_LARGE).  What only the device can see
+ *    (lengths, page ids, positions, slots, token ids) is checked by the kernels
+ *    before it is used as an index: the first error found is recorded as a
+ *    MINFER_ERR_* code in *d_status (int, never cleared by the library; may be
+ *    NULL) and what the error belongs to (a request, a token's row) is not
+ *    written.
+ *  - Types: MINFER_F32, MINFER_F16, MINFER_BF16.  Strides count elements. */
+
+/* A pool of n_pages pages of page_size K/V rows each; row s of page p, head h
+ * starts at p*page_stride + s*row_stride + h*head_stride in both k and v, its
+ * head_dim values are contiguous.  Slot p*page_size + s names row s of page p.
+ * k and v are 16-byte aligned and so is every stride; head_dim is 64 or 128. */
+typedef struct minfer_paged_cache {
+  void* k;
+  void* v;
+  int type;
+  int n_pages, page_size, n_head_kv, head_dim;
+  int64_t page_stride, row_stride, head_stride;
+} minfer_paged_cache;
+
+#define MINFER_ROPE_HALF 0        /* pairs (i, i + rot_dim/2) */
+#define MINFER_ROPE_INTERLEAVED 1 /* pairs (2i, 2i + 1) */
+#define MINFER_ROPE_NONE 0   /* angle = pos * f_i, f_i = theta^(-2i/rot_dim) */
+#define MINFER_ROPE_LINEAR 1 /* f_i / factor */
+#define MINFER_ROPE_NTK 2    /* theta * factor^(rot_dim/(rot_dim-2)) in place of theta */
+#define MINFER_ROPE_YARN 3   /* f_i (1-g_i) + f_i/factor g_i; g_i rises from 0 to 1 between the pairs that
+                                turn beta_fast and beta_slow times over n_ctx_orig positions; cos and sin
+                                times 0.1 ln(factor) + 1 */
+
+/* Rotary positions of one head layout (host).  rot_dim leading dims of a head
+ * are rotated (even, 2..head_dim), the others pass through.  beta_fast and
+ * beta_slow of 0 mean 32 and 1; attn_factor of 0 means the scaling's own factor
+ * on cos and sin (1 except for YaRN), another value replaces it. */
+typedef struct minfer_rope_spec {
+  int head_dim, rot_dim, style, scaling;
+  double theta, factor;
+  int n_ctx_orig;
+  double beta_fast, beta_slow, attn_factor;
+} minfer_rope_spec;
+/* What minfer_op_rope_paged_store takes: the turn of every pair per position
+ * as a 64-bit binary fraction of a full turn (so pos * turn mod 2^64 is the
+ * exact phase at any position).  Plain host memory, copied into the launch. */
+typedef struct minfer_rope_table {
+  uint64_t turn[64];
+  float mscale;
+  int head_dim, rot_dim, style;
+} minfer_rope_table;
+
+/* Fill *out from *spec (host only, no CUDA call): "05 · Graph build", section
+ * 2.5: RoPE by position with the hparams' frequency base; the scalings and the
+ * interleaved pairs have no counterpart on the pages.  MINFER_ERR_SHAPE for a
+ * head_dim other than 64 or 128 or an odd or too large rot_dim, MINFER_ERR_ARG
+ * for an unknown style or scaling, theta <= 1, factor <= 0, or YaRN without
+ * n_ctx_orig. */
+int minfer_rope_prepare(const minfer_rope_spec* spec, minfer_rope_table* out);
+
+/* Block tables and slot maps of a step, from the requests' lengths.  The pages'
+ * engine gives every conversation its own contiguous regions ("09 · Prefill",
+ * section 2.5); shared pages have no counterpart there.
+ *   Request r holds d_len[r] rows in the pages d_table[r*max_pages + i],
+ *   i < ceil(d_len[r]/page_size), and is to hold d_target[r]: more (its new
+ *   tokens of this step), fewer (a rollback) or none (it is over).
+ *   d_free[n_pages] is a stack of unused page ids, *d_n_free entries deep.
+ * Pages that a request no longer needs are pushed in request and table order;
+ * then every new page, in request and table order, is popped from the top and
+ * entered in the table (other entries stay as they are).  The stack's new depth
+ * goes to *d_n_free_out (which may be d_n_free).  d_start[n_req + 1]: exclusive
+ * prefix sum of the new tokens max(0, target - len).  d_pos, d_slot
+ * [max_tokens]: position and slot of every new token, request by request; -1
+ * in the rows behind the last token, which the operators below skip.
+ * All or nothing: with an error (MINFER_ERR_POS_OOB: a length or target outside
+ * 0..max_pages*page_size; MINFER_ERR_TOO_LARGE: more than max_tokens new
+ * tokens; MINFER_ERR_OOM: too few free pages; MINFER_ERR_ARG: a page id in use
+ * or a depth out of range) table, stack and *d_n_free_out stay as they were,
+ * and the step has no token: d_start is 0 and d_pos, d_slot are -1.
+ * n_req <= 16384; n_req*max_pages, max_pages*page_size and n_pages*page_size
+ * fit 31 bits (MINFER_ERR_TOO_LARGE otherwise). */
+int minfer_op_page_tables(const int32_t* d_len, const int32_t* d_target, int n_req, int page_size,
+                          int n_pages, int32_t* d_table, int max_pages, int32_t* d_free,
+                          const int32_t* d_n_free, int32_t* d_n_free_out, int32_t* d_start,
+                          int32_t* d_pos, int32_t* d_slot, int max_tokens, int* d_status,
+                          void* stream);
+
+/* RoPE and paged K/V store of n_tokens rows Q|K|V ("09 · Prefill", section 2.2;
+ * "05 · Graph build", section 2.5, and section 3.2 for the QK-norm): row t of
+ * d_qkv (type `type`, row_stride elements apart, (n_head + 2 n_head_kv) *
+ * head_dim values) plus d_bias (f32, may be NULL); with d_qnorm and d_knorm
+ * (f32 [head_dim], both or neither) every head of Q and K is RMS-normalized;
+ * Q and K are rotated by d_pos[t]; Q goes to d_q_out (the cache's type, rows of
+ * n_head*head_dim values q_stride apart), K and V to slot d_slot[t].  A row
+ * with a negative slot is padding: it is neither read nor written.  Slots of
+ * one call are distinct.  `type` is MINFER_F32 or the cache's type; all
+ * arithmetic is f32, rounded once.  Device errors: MINFER_ERR_POS_OOB for a
+ * slot past the pool or a negative position of a stored row (that row is not
+ * written). */
+int minfer_op_rope_paged_store(const void* d_qkv, int type, int64_t row_stride,
+                               const float* d_bias, const float* d_qnorm, const float* d_knorm,
+                               float eps, const minfer_rope_table* rope, const int32_t* d_pos,
+                               const int32_t* d_slot, int n_tokens, int n_head,
+                               const minfer_paged_cache* cache, void* d_q_out, int64_t q_stride,
+                               int* d_status, void* stream);
+
+/* Bytes of workspace of minfer_op_paged_attention for n_req requests of n_head
+ * query heads on the current device (no counterpart on the pages).  The
+ * workspace needs no initialization and carries nothing from call to call. */
+int minfer_op_paged_attention_workspace(int n_req, int n_head, const minfer_paged_cache* cache,
+                                        int64_t* bytes);
+
+/* Attention of one new token per request over its pages ("05 · Graph build",
+ * section 2.5; the decode shape of "09 · Prefill", section 2.1): query row r
+ * (the cache's type, q_stride apart, n_head heads; head h reads KV head
+ * h / (n_head / n_head_kv)) sees the d_len[r] rows that
+ * d_table[r*table_stride + i], i < max_pages, holds; the new token's own row is
+ * one of them (minfer_op_rope_paged_store first).  d_o: the cache's type, rows
+ * o_stride apart.  d_lse (f32 [n_req][n_head], may be NULL): natural log of the
+ * sum of exp(scale * q.k), for joining with attention over other keys.
+ * scale 0 means 1/sqrt(head_dim).  A request of length 0 gets zeros and -inf.
+ * What lies in the pages behind a request's last row is never used, whatever
+ * its bits.  Scores, softmax statistics and sums are f32; with a 16-bit cache
+ * the softmax weights are rounded to its type for their product with V.  The
+ * result of a call depends on its inputs alone, bit for bit on one device
+ * type.  Device errors: MINFER_ERR_POS_OOB for a length outside
+ * 0..max_pages*page_size or a page id outside the pool (that request's row of
+ * d_o and d_lse is not written). */
+int minfer_op_paged_attention(const void* d_q, int64_t q_stride, const minfer_paged_cache* cache,
+                              const int32_t* d_table, int64_t table_stride, int max_pages,
+                              const int32_t* d_len, int n_req, int n_head, float scale, void* d_o,
+                              int64_t o_stride, float* d_lse, void* d_workspace,
+                              int64_t workspace_bytes, int* d_status, void* stream);
+
+/* Bytes of workspace of minfer_op_token_logprobs (no counterpart on the pages);
+ * the same rules as above. */
+int minfer_op_token_logprobs_workspace(int64_t rows, int64_t vocab, int k, int64_t* bytes);
+
+/* Log probabilities under the softmax of logits rows ("09 · Prefill", section
+ * 2.4: the n_out rows that minfer_prefill_device_n returns; what is made of
+ * them has no counterpart on the pages).  Row r of d_logits (`type`, row_stride
+ * apart, vocab values, any alignment of the type):
+ *   d_logprob[r] = x[d_ids[r]] - ln sum exp x; d_ids may be NULL (then
+ *     d_logprob is not written), a negative id marks a padding row, of which
+ *     no output is written;
+ *   d_entropy[r] = -sum p ln p (may be NULL);
+ *   d_top_ids, d_top_logprobs [rows][k]: the k largest logits in descending
+ *     order, equal ones by ascending id, and their log probabilities; 0 <= k
+ *     <= min(32, vocab).
+ * -inf logits are masked tokens: probability 0, log probability -inf.  A row
+ * with nothing but -inf has log probability -inf everywhere and entropy 0.
+ * NaN and +inf make the row's numbers NaN; in the order NaN stands above +inf.
+ * Device errors: MINFER_ERR_TOKEN_OOB for an id >= vocab (no output of that row
+ * is written). */
+int minfer_op_token_logprobs(const void* d_logits, int type, int64_t rows, int64_t vocab,
+                             int64_t row_stride, const int32_t* d_ids, int k, float* d_logprob,
+                             float* d_entropy, int32_t* d_top_ids, float* d_top_logprobs,
+                             void* d_workspace, int64_t workspace_bytes, int* d_status,
+                             void* stream);
 
 /* ---------------------------------------------------------------- misc */
 /* A static, NUL-terminated name of an error code (never NULL; "unknown error"

@@ -1,0 +1,639 @@
+// k_paged_attn.cu -- attention of one new token per request over a paged K/V
+// cache, split over the requests' lengths and joined.
+//
+//   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j - max),  j < len
+//
+// Work is counted in units of 64 keys of one (request, KV head); the units of
+// the whole batch, request by request, are cut into equal shares, one per CTA
+// of a grid that fills the GPU once, so ragged batches and single long
+// requests load every SM alike, without the host knowing a length.  A CTA
+// walks its share as a stream: a (request, KV head) that lies inside it is
+// finished there; one that crosses a share's border leaves a partial (max,
+// sum, unnormalized output) in the workspace, and paged_join_kernel adds the
+// partials up.
+//
+// Inside a CTA each of four warps takes 16 of a unit's 64 keys, copies their
+// K and V rows into its own ring in shared memory (cp.async of 16 bytes, page
+// by page; rows behind the request's last are filled with zeros) and runs an
+// online softmax of its own: no barrier before the end of the (request, KV
+// head).  The products are m16n8 MMAs with the query heads of the KV head as
+// the 16 rows.  One query token leaves the rows of a tcgen05 tile (128)
+// mostly empty and the bound is the bytes of K and V, so the accumulators stay
+// in registers, where the softmax needs them.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace minfer {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kKeys = 16;               // keys of a unit that one warp takes
+constexpr int kUnit = kWarps * kKeys;   // keys of a unit
+constexpr int kRows = 16;               // query heads of one MMA tile
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+template <typename T, int HD>
+struct Cfg {
+  static constexpr int kRowBytes = HD * (int)sizeof(T);
+  static constexpr int kChunks = kRowBytes / 16;  // 16-byte chunks of a row
+  static constexpr int kStageBytes = 2 * kKeys * kRowBytes;  // K and V rows of one warp
+  // CTAs per SM and ring depth: about 100 KB (two CTAs) of K/V in flight or at work
+  static constexpr int kStages = kRowBytes == 128 ? 5 : kRowBytes == 256 ? 2 : 2;
+  static constexpr int kCtas = kRowBytes == 512 ? 1 : 2;
+  static constexpr int kQBytes = sizeof(T) == 4 ? 2 * kRows * kRowBytes : 0;  // tf32 hi and lo of Q
+  static constexpr int kMergeBytes = kWarps * kRows * HD * 4 + kWarps * kRows * 8;
+  static constexpr int kSmem = kWarps * kStages * kStageBytes + kQBytes + kMergeBytes;
+};
+
+// The workspace: [0] total units (int64), then per request the first unit
+// (int64), then per CTA two partials: kRows (max, sum) pairs and kRows x HD.
+__host__ __device__ inline int64_t ws_part_offset(int n_req) { return ((int64_t)(n_req + 1) * 8 + 255) / 256 * 256; }
+__host__ __device__ inline int64_t ws_part_floats(int hd) { return (int64_t)kRows * (hd + 2); }
+
+// Units of a request; a length out of range counts as none.
+__device__ __forceinline__ int units_of(int len, int cap) {
+  return (len < 0 || len > cap) ? 0 : (len + kUnit - 1) / kUnit;
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __nv_bfloat16) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float) {
+  asm(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x = hi + lo, two tf32 values (11 significant bits each; the rest is below 2^-22 |x|)
+__device__ __forceinline__ void split_tf32(uint32_t x, uint32_t* hi, uint32_t* lo) {
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(*hi) : "f"(__uint_as_float(x)));
+  const float rest = __uint_as_float(x) - __uint_as_float(*hi);
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(*lo) : "f"(rest));
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void store_as(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store_as(__half* p, float x) { *p = __float2half_rn(x); }
+__device__ __forceinline__ void store_as(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// Walks the units of the batch: request r, head block v (KV head and group of
+// kRows query heads), unit u of it.  The next request's length is read one
+// request ahead.
+struct Walk {
+  int r, v, u, units, len, next_len;
+};
+__device__ __forceinline__ int len_at(const PagedAttnArgs& a, int r) { return r < a.n_req ? a.len[r] : 0; }
+__device__ __forceinline__ void walk_next(Walk& w, const PagedAttnArgs& a, int nv, int cap) {
+  if (++w.u < w.units) return;
+  w.u = 0;
+  if (++w.v < nv) return;
+  w.v = 0;
+  do {
+    ++w.r;
+    w.len = w.next_len;
+    w.next_len = len_at(a, w.r + 1);
+    w.units = units_of(w.len, cap);
+  } while (w.units == 0 && w.r < a.n_req);
+}
+
+// First unit of CTA c's share.
+__host__ __device__ inline int64_t share_begin(int64_t total, int c, int n) { return total * c / n; }
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD>::kCtas)
+    paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, int n_groups, float scale_log2) {
+  using C = Cfg<T, HD>;
+  constexpr bool kF32 = sizeof(T) == 4;
+  constexpr int kSteps = C::kChunks / 2;  // MMA steps over the head's dims (two chunks each)
+  constexpr int kTiles = HD / 8;          // n8 tiles of the output
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int64_t s_scan[kWarps];
+  __shared__ Walk s_walk;
+  __shared__ uint8_t s_bad[kWarps][C::kStages];
+  __shared__ int s_segbad[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int P = a.c.page_size, cap = a.max_pages * P;
+  const int G = a.nh / a.c.nkv, nv = a.c.nkv * n_groups;
+  int64_t* ws_units = static_cast<int64_t*>(a.ws);
+  float* ws_part = reinterpret_cast<float*>(static_cast<unsigned char*>(a.ws) + ws_part_offset(a.n_req));
+
+  pdl_trigger();
+  pdl_wait();
+
+  // ---- this CTA's share: total units, then the request its first unit lies in
+  if (tid < 2) s_segbad[tid] = 0;
+  int64_t mine = 0;
+  for (int r = tid; r < a.n_req; r += kWarps * 32) mine += units_of(a.len[r], cap);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) s_scan[warp] = mine;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) total += s_scan[i];
+  total *= nv;
+  const int64_t begin = share_begin(total, blockIdx.x, gridDim.x);
+  const int count = (int)(share_begin(total, blockIdx.x + 1, gridDim.x) - begin);
+  if (blockIdx.x == 0 && tid == 0) ws_units[0] = total;
+  if (count == 0) return;
+  {
+    // warp 0 scans the requests 32 at a time until the first unit is reached
+    if (warp == 0) {
+      int64_t base = 0;
+      for (int r0 = 0; r0 < a.n_req; r0 += 32) {
+        const int len = len_at(a, r0 + lane);
+        const int64_t own = r0 + lane < a.n_req ? (int64_t)units_of(len, cap) * nv : 0;
+        int64_t incl = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        const int64_t lo = base + incl - own;
+        const bool here = begin >= lo && begin < lo + own;
+        if (here) {
+          const int units = units_of(len, cap);
+          const int off = (int)(begin - lo);
+          s_walk.r = r0 + lane;
+          s_walk.v = off / units;
+          s_walk.u = off - s_walk.v * units;
+          s_walk.units = units;
+          s_walk.len = len;
+          s_walk.next_len = len_at(a, r0 + lane + 1);
+        }
+        if (__any_sync(0xffffffffu, here)) break;
+        base += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    __syncthreads();
+  }
+  Walk cw = s_walk;  // the unit being computed
+  Walk lw = cw;      // the unit being loaded
+
+  // ---- loads: lane l < 16 looks up the page of key l, all lanes copy
+  const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStageBytes;
+  const bool pow2 = (P & (P - 1)) == 0;
+  const int shift = __ffs(P) - 1;
+  int page_next = 0;  // page id of this lane's key of unit lw
+  auto lookup = [&](const Walk& w) {
+    const int key = w.u * kUnit + warp * kKeys + (lane & 15);
+    if (key >= w.len) return 0;
+    const int i = pow2 ? key >> shift : key / P;
+    return a.table[(int64_t)w.r * a.table_stride + i];
+  };
+  page_next = lookup(lw);
+  auto load_unit = [&](int stage) {
+    const int key0 = lw.u * kUnit + warp * kKeys;
+    const int key = key0 + (lane & 15);
+    const int in_page = pow2 ? key & (P - 1) : key % P;
+    const bool ok = (unsigned)page_next < (unsigned)a.c.n_pages;
+    const bool bad = key < lw.len && !ok;
+    int64_t off = 0;
+    if (key < lw.len && ok)
+      off = (int64_t)page_next * a.c.page_stride + (int64_t)in_page * a.c.row_stride +
+            (int64_t)(lw.v / n_groups) * a.c.head_stride;
+    const unsigned live = __ballot_sync(0xffffffffu, key < lw.len && ok);
+    const bool any_bad = __any_sync(0xffffffffu, bad);
+    if (lane == 0) s_bad[warp][stage] = any_bad;
+    // per instruction: 32 chunks = 32 / kChunks rows
+    constexpr int kRowsPer = 32 / C::kChunks > 0 ? 32 / C::kChunks : 1;
+    const int c = lane % C::kChunks;
+    const uint32_t kdst = ring + stage * C::kStageBytes, vdst = kdst + kKeys * C::kRowBytes;
+#pragma unroll
+    for (int j = 0; j < kKeys / kRowsPer; ++j) {
+      const int row = j * kRowsPer + lane / C::kChunks;
+      const int64_t o = __shfl_sync(0xffffffffu, off, row) * (int64_t)sizeof(T) + c * 16;
+      const int bytes = (live >> row) & 1 ? 16 : 0;
+      const uint32_t d = (uint32_t)(row * C::kRowBytes + ((c ^ (row & 7)) << 4));
+      cp16(kdst + d, static_cast<const unsigned char*>(a.c.k) + o, bytes);
+      cp16(vdst + d, static_cast<const unsigned char*>(a.c.v) + o, bytes);
+    }
+    walk_next(lw, a, nv, cap);
+  };
+
+  int issued = 0;
+#pragma unroll 1
+  for (; issued < C::kStages - 1; ++issued) {
+    if (issued < count) {
+      load_unit(issued);
+      if (issued + 1 < count) page_next = lookup(lw);
+    }
+    cp_commit();
+  }
+
+  // ---- one (request, head block) after another
+  unsigned char* qs = smem + kWarps * C::kStages * C::kStageBytes;
+  float* m_out = reinterpret_cast<float*>(qs + C::kQBytes);  // [warp][kRows][HD]
+  float2* m_ml = reinterpret_cast<float2*>(m_out + kWarps * kRows * HD);  // [warp][kRows]
+  const int g4 = lane >> 2, t4 = lane & 3;
+  int stage = 0, seg = 0;
+  for (int done = 0; done < count;) {
+    const int r = cw.r, kvh = cw.v / n_groups, grp = cw.v % n_groups;
+    const int rows = min(kRows, G - grp * kRows);
+    const int head0 = kvh * G + grp * kRows;
+    const bool from_start = cw.u == 0;
+    const int seg_units = min(cw.units - cw.u, count - done);
+    const bool to_end = cw.u + seg_units == cw.units;
+    const int seg_len = cw.len;
+    const T* qrow = static_cast<const T*>(a.q) + (int64_t)r * a.q_stride + (int64_t)head0 * HD;
+
+    // Q as the A operand: 16-bit types in registers, f32 as tf32 hi/lo in shared memory
+    uint32_t qa[kF32 ? 1 : kSteps][4];
+    if constexpr (!kF32) {
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int d = s * 16 + t4 * 2;
+        const uint32_t* lo = reinterpret_cast<const uint32_t*>(qrow + (int64_t)g4 * HD + d);
+        const uint32_t* hi = reinterpret_cast<const uint32_t*>(qrow + (int64_t)(g4 + 8) * HD + d);
+        qa[s][0] = g4 < rows ? lo[0] : 0u;
+        qa[s][2] = g4 < rows ? lo[4] : 0u;
+        qa[s][1] = g4 + 8 < rows ? hi[0] : 0u;
+        qa[s][3] = g4 + 8 < rows ? hi[4] : 0u;
+      }
+    } else {
+      // the barrier at the end of the previous segment freed qs
+      for (int i = tid; i < kRows * HD; i += kWarps * 32) {
+        const int row = i / HD, d = i % HD;
+        uint32_t hi = 0, lo = 0;
+        if (row < rows) split_tf32(__float_as_uint(reinterpret_cast<const float*>(qrow)[i]), &hi, &lo);
+        const uint32_t at = (uint32_t)(row * C::kRowBytes + (((d >> 2) ^ (row & 7)) << 4) + (d & 3) * 4);
+        *reinterpret_cast<uint32_t*>(qs + at) = hi;
+        *reinterpret_cast<uint32_t*>(qs + kRows * C::kRowBytes + at) = lo;
+      }
+      __syncthreads();
+    }
+
+    float o[kTiles][4];
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // rows g4, g4 + 8
+    bool bad = false;
+
+#pragma unroll 1
+    for (int i = 0; i < seg_units; ++i, ++done) {
+      // refill the stage that the previous unit freed, then wait for this one
+      __syncwarp();
+      if (issued < count) {
+        int st = stage + C::kStages - 1;
+        if (st >= C::kStages) st -= C::kStages;
+        load_unit(st);
+        ++issued;
+        if (issued < count) page_next = lookup(lw);
+      }
+      cp_commit();
+      cp_wait<C::kStages - 1>();
+      __syncwarp();
+      bad |= s_bad[warp][stage] != 0;
+      const uint32_t ks = ring + stage * C::kStageBytes, vs = ks + kKeys * C::kRowBytes;
+
+      // S = Q K^T: two n8 tiles of keys
+      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+      {
+        const int key = ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
+        const uint32_t kaddr = ks + key * C::kRowBytes;
+        if constexpr (!kF32) {
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s) {
+            uint32_t b[4];
+            ldsm4(b, kaddr + (((s * 2 + half) ^ (key & 7)) << 4));
+            mma(s0, qa[s], b[0], b[1], T());
+            mma(s1, qa[s], b[2], b[3], T());
+          }
+        } else {
+          // three tf32 products of the hi/lo halves; the small ones in sums of
+          // their own, so the large sum takes kSteps tensor-core adds
+          float e0[4] = {0.f, 0.f, 0.f, 0.f}, e1[4] = {0.f, 0.f, 0.f, 0.f};
+          const int qr = lane & 15, qh = lane >> 4;
+          const uint32_t qaddr = smem_u32(qs) + qr * C::kRowBytes;
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s) {
+            uint32_t b[4], bh[4], bl[4], ah[4], al[4];
+            ldsm4(b, kaddr + (((s * 2 + half) ^ (key & 7)) << 4));
+            const uint32_t qo = qaddr + (((s * 2 + qh) ^ (qr & 7)) << 4);
+            ldsm4(ah, qo);
+            ldsm4(al, qo + kRows * C::kRowBytes);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) split_tf32(b[j], &bh[j], &bl[j]);
+            mma(s0, ah, bh[0], bh[1], T());
+            mma(s1, ah, bh[2], bh[3], T());
+            mma(e0, ah, bl[0], bl[1], T());
+            mma(e1, ah, bl[2], bl[3], T());
+            mma(e0, al, bh[0], bh[1], T());
+            mma(e1, al, bh[2], bh[3], T());
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            s0[j] += e0[j];
+            s1[j] += e1[j];
+          }
+        }
+      }
+
+      // online softmax in log2 units
+      const int live = seg_len - ((cw.u + i) * kUnit + warp * kKeys);  // keys of this warp's 16
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = t4 * 2 + (j & 1);
+        s0[j] = k < live ? s0[j] * scale_log2 : -INFINITY;
+        s1[j] = k + 8 < live ? s1[j] * scale_log2 : -INFINITY;
+      }
+      float n0 = fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s1[0], s1[1]));
+      float n1 = fmaxf(fmaxf(s0[2], s0[3]), fmaxf(s1[2], s1[3]));
+      n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, 1));
+      n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, 1));
+      n0 = fmaxf(m0, fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, 2)));
+      n1 = fmaxf(m1, fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, 2)));
+      // nothing seen so far: any finite reference gives p = 0
+      const float z0 = n0 == -INFINITY ? 0.f : n0, z1 = n1 == -INFINITY ? 0.f : n1;
+      const float c0 = ex2(m0 - z0), c1 = ex2(m1 - z1);
+      m0 = n0;
+      m1 = n1;
+      s0[0] = ex2(s0[0] - z0);
+      s0[1] = ex2(s0[1] - z0);
+      s1[0] = ex2(s1[0] - z0);
+      s1[1] = ex2(s1[1] - z0);
+      s0[2] = ex2(s0[2] - z1);
+      s0[3] = ex2(s0[3] - z1);
+      s1[2] = ex2(s1[2] - z1);
+      s1[3] = ex2(s1[3] - z1);
+      // the row sums stay per thread until the end of the segment
+      l0 = fmaf(l0, c0, (s0[0] + s0[1]) + (s1[0] + s1[1]));
+      l1 = fmaf(l1, c1, (s0[2] + s0[3]) + (s1[2] + s1[3]));
+
+      // O = O * c + P V: every unit's product in a fresh accumulator, added in f32
+      if constexpr (!kF32) {
+        const uint32_t p[4] = {pack2(s0[0], s0[1], T()), pack2(s0[2], s0[3], T()), pack2(s1[0], s1[1], T()),
+                               pack2(s1[2], s1[3], T())};
+        const int key = (((lane >> 3) & 1) << 3) + (lane & 7), half = lane >> 4;
+        const uint32_t vaddr = vs + key * C::kRowBytes;
+#pragma unroll
+        for (int d = 0; d < HD / 16; ++d) {
+          uint32_t b[4];
+          ldsm4t(b, vaddr + (((d * 2 + half) ^ (key & 7)) << 4));
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float f[4] = {0.f, 0.f, 0.f, 0.f};
+            mma(f, p, b[2 * j], b[2 * j + 1], T());
+            float* q = o[2 * d + j];
+            q[0] = fmaf(q[0], c0, f[0]);
+            q[1] = fmaf(q[1], c0, f[1]);
+            q[2] = fmaf(q[2], c1, f[2]);
+            q[3] = fmaf(q[3], c1, f[3]);
+          }
+        }
+      } else {
+        // the MMA's k index t stands for key 2t, t + 4 for key 2t + 1 of a tile
+        // of 8: S's accumulator layout is then P's operand layout
+        uint32_t ph[2][4], pl[2][4];
+        const float* st[2] = {s0, s1};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          split_tf32(__float_as_uint(st[k][0]), &ph[k][0], &pl[k][0]);
+          split_tf32(__float_as_uint(st[k][2]), &ph[k][1], &pl[k][1]);
+          split_tf32(__float_as_uint(st[k][1]), &ph[k][2], &pl[k][2]);
+          split_tf32(__float_as_uint(st[k][3]), &ph[k][3], &pl[k][3]);
+        }
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) {
+          float f[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t bh[2], bl[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int key = k * 8 + t4 * 2 + j;
+              const uint32_t v = lds32(vs + key * C::kRowBytes + (((n * 2 + (g4 >> 2)) ^ (key & 7)) << 4) + (g4 & 3) * 4);
+              split_tf32(v, &bh[j], &bl[j]);
+            }
+            mma(f, ph[k], bh[0], bh[1], T());
+            mma(e, ph[k], bl[0], bl[1], T());
+            mma(e, pl[k], bh[0], bh[1], T());
+          }
+          o[n][0] = fmaf(o[n][0], c0, f[0] + e[0]);
+          o[n][1] = fmaf(o[n][1], c0, f[1] + e[1]);
+          o[n][2] = fmaf(o[n][2], c1, f[2] + e[2]);
+          o[n][3] = fmaf(o[n][3], c1, f[3] + e[3]);
+        }
+      }
+      if (++stage == C::kStages) stage = 0;
+    }
+
+    // ---- join the four warps; write the result or this share's partial
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    if (t4 == 0) {
+      m_ml[warp * kRows + g4] = make_float2(m0, l0);
+      m_ml[warp * kRows + g4 + 8] = make_float2(m1, l1);
+    }
+    float* mo = m_out + warp * kRows * HD;
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n) {
+      const int d = n * 8 + t4 * 2;
+      if (g4 < rows) *reinterpret_cast<float2*>(mo + g4 * HD + d) = make_float2(o[n][0], o[n][1]);
+      if (g4 + 8 < rows) *reinterpret_cast<float2*>(mo + (g4 + 8) * HD + d) = make_float2(o[n][2], o[n][3]);
+    }
+    if (bad && lane == 0) s_segbad[seg & 1] = 1;
+    __syncthreads();
+    const bool seg_bad = s_segbad[seg & 1] != 0;
+    const bool whole = from_start && to_end;
+    if (seg_bad && tid == 0) set_error(a.status, MINFER_ERR_POS_OOB);
+    float* part = ws_part + (int64_t)(blockIdx.x * 2 + (from_start ? 1 : 0)) * ws_part_floats(HD);
+    if (from_start && cw.v == 0 && tid == 0)
+      ws_units[1 + r] = begin + (done - seg_units);  // the request's first unit
+    for (int i = tid; i < rows * HD; i += kWarps * 32) {
+      const int row = i / HD, d = i % HD;
+      float m = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, m_ml[w * kRows + row].x);
+      const float z = m == -INFINITY ? 0.f : m;
+      float l = 0.f, acc = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 ml = m_ml[w * kRows + row];
+        const float c = ex2(ml.x - z);
+        l = fmaf(ml.y, c, l);
+        acc = fmaf(m_out[w * kRows * HD + i], c, acc);
+      }
+      if (whole) {
+        if (!seg_bad) {
+          store_as(static_cast<T*>(a.o) + (int64_t)r * a.o_stride + (int64_t)head0 * HD + i, l == 0.f ? 0.f : acc / l);
+          if (d == 0 && a.lse) a.lse[(int64_t)r * a.nh + head0 + row] = fmaf(m, kLn2, logf(l));
+        }
+      } else {
+        if (d == 0) reinterpret_cast<float2*>(part)[row] = make_float2(m, seg_bad ? -1.f : l);
+        part[2 * kRows + i] = acc;
+      }
+    }
+    // flag of the segment after the next, free since the barrier above
+    if (tid == 0) s_segbad[(seg + 1) & 1] = 0;
+    __syncthreads();
+    ++seg;
+    // on to the next (request, head block)
+    cw.u = cw.units - 1;
+    walk_next(cw, a, nv, cap);
+  }
+}
+
+// Adds up the partials of (request, query head)s whose units lie in more than
+// one share, and writes the rows of empty requests.  One CTA per (request,
+// query head): thread (g, d) takes partials g, g + kJoin, ... of dim d.
+constexpr int kJoin = 4;
+template <typename T, int HD>
+__global__ void __launch_bounds__(kJoin* HD) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, int n_groups, int n_shares) {
+  __shared__ float s_m[kJoin], s_l[kJoin], s_o[kJoin][HD];
+  __shared__ int s_bad;
+  const int r = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, d = tid % HD, g = tid / HD;
+  const int G = a.nh / a.c.nkv, kvh = h / G, in = h - kvh * G, grp = in / kRows, row = in % kRows;
+  if (tid == 0) s_bad = 0;
+  pdl_trigger();
+  pdl_wait();
+  const int cap = a.max_pages * a.c.page_size;
+  const int len = a.len[r];
+  T* out = static_cast<T*>(a.o) + (int64_t)r * a.o_stride + (int64_t)h * HD;
+  if (len <= 0 || len > cap) {
+    if (len == 0) {
+      if (g == 0) store_as(out + d, 0.f);
+      if (tid == 0 && a.lse) a.lse[(int64_t)r * a.nh + h] = -INFINITY;
+    } else if (tid == 0) {
+      set_error(a.status, MINFER_ERR_POS_OOB);
+    }
+    return;
+  }
+  const int64_t* ws_units = static_cast<const int64_t*>(a.ws);
+  const float* ws_part = reinterpret_cast<const float*>(static_cast<const unsigned char*>(a.ws) + ws_part_offset(a.n_req));
+  const int64_t total = ws_units[0];
+  const int units = units_of(len, cap);
+  const int64_t first = ws_units[1 + r] + (int64_t)(kvh * n_groups + grp) * units, last = first + units - 1;
+  // the share that holds unit x: the largest c with share_begin(c) <= x
+  auto share_of = [&](int64_t x) {
+    int c = (int)min((x * n_shares) / total, (int64_t)n_shares - 1);
+    while (c + 1 < n_shares && share_begin(total, c + 1, n_shares) <= x) ++c;
+    while (share_begin(total, c, n_shares) > x) --c;
+    return c;
+  };
+  const int c0 = share_of(first), c1 = share_of(last);
+  if (c0 == c1) return;  // finished by the share that holds it
+  float m = -INFINITY, l = 0.f, o = 0.f;
+  bool bad = false;
+  __syncthreads();  // s_bad is set
+  for (int c = c0 + g; c <= c1; c += kJoin) {
+    // a share that begins inside this head's units has it as its first piece
+    const int which = share_begin(total, c, n_shares) > first ? 0 : 1;
+    const float* part = ws_part + (int64_t)(c * 2 + which) * ws_part_floats(HD);
+    const float2 ml = reinterpret_cast<const float2*>(part)[row];
+    const float x = part[2 * kRows + row * HD + d];
+    bad |= ml.y < 0.f;
+    const float mn = fmaxf(m, ml.x), z = mn == -INFINITY ? 0.f : mn;
+    const float ca = ex2(m - z), cb = ex2(ml.x - z);
+    l = fmaf(l, ca, ml.y * cb);
+    o = fmaf(o, ca, x * cb);
+    m = mn;
+  }
+  if (bad) s_bad = 1;
+  if (d == 0) {
+    s_m[g] = m;
+    s_l[g] = l;
+  }
+  s_o[g][d] = o;
+  __syncthreads();
+  if (g != 0 || s_bad) return;
+  m = s_m[0];
+#pragma unroll
+  for (int i = 1; i < kJoin; ++i) m = fmaxf(m, s_m[i]);
+  const float z = m == -INFINITY ? 0.f : m;
+  l = o = 0.f;
+#pragma unroll
+  for (int i = 0; i < kJoin; ++i) {
+    const float c = ex2(s_m[i] - z);
+    l = fmaf(s_l[i], c, l);
+    o = fmaf(s_o[i][d], c, o);
+  }
+  store_as(out + d, l == 0.f ? 0.f : o / l);
+  if (d == 0 && a.lse) a.lse[(int64_t)r * a.nh + h] = fmaf(m, kLn2, logf(l));
+}
+
+int row_bytes(int hd, int type) { return hd * (type == MINFER_F32 ? 4 : 2); }
+int shares(int hd, int type, int num_sms) { return num_sms * (row_bytes(hd, type) == 512 ? 1 : 2); }
+
+template <typename T, int HD>
+cudaError_t launch(const PagedAttnArgs& a, int type, int num_sms, cudaStream_t st) {
+  using C = Cfg<T, HD>;
+  const int G = a.nh / a.c.nkv, n_groups = (G + kRows - 1) / kRows;
+  const int n = shares(HD, type, num_sms);
+  auto kernel = paged_attn_kernel<T, HD>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kernel, dim3((unsigned)n), dim3(kWarps * 32), C::kSmem, st, a, n_groups, a.scale * kLog2e);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(paged_join_kernel<T, HD>, dim3((unsigned)a.n_req, (unsigned)a.nh), dim3(kJoin * HD), 0, st, a, n_groups, n);
+}
+
+}  // namespace
+
+int64_t paged_attn_workspace(int n_req, int nh, int nkv, int hd, int type, int num_sms) {
+  (void)nh;
+  (void)nkv;
+  return ws_part_offset(n_req) + (int64_t)shares(hd, type, num_sms) * 2 * ws_part_floats(hd) * 4;
+}
+
+cudaError_t paged_attn_launch(const PagedAttnArgs& a, int type, int num_sms, cudaStream_t st) {
+  if (type == MINFER_F32)
+    return a.c.hd == 64 ? launch<float, 64>(a, type, num_sms, st) : launch<float, 128>(a, type, num_sms, st);
+  if (type == MINFER_F16)
+    return a.c.hd == 64 ? launch<__half, 64>(a, type, num_sms, st) : launch<__half, 128>(a, type, num_sms, st);
+  return a.c.hd == 64 ? launch<__nv_bfloat16, 64>(a, type, num_sms, st)
+                      : launch<__nv_bfloat16, 128>(a, type, num_sms, st);
+}
+
+}  // namespace minfer

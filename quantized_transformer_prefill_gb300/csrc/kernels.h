@@ -9,6 +9,8 @@
 
 #include <utility>
 
+#include "../../include/minfer.h"
+
 namespace minfer {
 
 // Launch with programmatic stream serialization (see pdl_trigger/pdl_wait).
@@ -308,5 +310,90 @@ cudaError_t gemm_plane_to_q8_launch(const __half* codes, const float* scales, in
 // Split-partials sum: out[m][n] = sum_s partials[s][m][n].
 cudaError_t sum_splits_launch(const float* partials, int nsplit, int64_t split_stride,
                               int64_t count, float* out, cudaStream_t stream);
+
+// ---------------------------------------------------------------- batch operators
+// Their launchers take checked arguments (batch.cu checks them).
+
+// k_paged.cu: block tables and slot maps from request lengths.
+struct PageTablesArgs {
+  const int32_t* len;
+  const int32_t* target;
+  int n_req, page_size, n_pages, max_pages, max_tokens;
+  int32_t* table;  // [n_req][max_pages]
+  int32_t* free_pages;
+  const int32_t* n_free;
+  int32_t* n_free_out;
+  int32_t* start;
+  int32_t* pos;
+  int32_t* slot;
+  int* status;
+};
+constexpr int kPageTablesMaxReq = 16384;  // three prefix arrays of n_req + 1 ints in shared memory
+cudaError_t page_tables_launch(const PageTablesArgs& a, cudaStream_t stream);
+
+// One page pool, the kernels' view of minfer_paged_cache (strides in elements).
+struct PagedCache {
+  void* k;
+  void* v;
+  int n_pages, page_size, nkv, hd;
+  int64_t page_stride, row_stride, head_stride;
+};
+
+// k_paged.cu: bias + QK-norm + RoPE + paged store of fused Q|K|V rows.
+struct RopePagedArgs {
+  const void* qkv;
+  int64_t row_stride;
+  const float* bias;
+  const float* q_norm;
+  const float* k_norm;
+  float eps;
+  const int32_t* pos;
+  const int32_t* slot;
+  int n_tokens, nh;
+  PagedCache c;
+  void* q_out;
+  int64_t q_stride;
+  int* status;
+  minfer_rope_table rope;
+};
+cudaError_t rope_paged_launch(const RopePagedArgs& a, int src_type, int cache_type,
+                              cudaStream_t stream);
+
+// k_paged_attn.cu: one query row per request over its pages.
+struct PagedAttnArgs {
+  const void* q;
+  int64_t q_stride;
+  PagedCache c;
+  const int32_t* table;
+  int64_t table_stride;
+  int max_pages;
+  const int32_t* len;
+  int n_req, nh;
+  float scale;
+  void* o;
+  int64_t o_stride;
+  float* lse;
+  void* ws;
+  int* status;
+};
+int64_t paged_attn_workspace(int n_req, int nh, int nkv, int hd, int type, int num_sms);
+cudaError_t paged_attn_launch(const PagedAttnArgs& a, int type, int num_sms, cudaStream_t stream);
+
+// k_logprobs.cu: log probabilities, entropy and top k of logits rows.
+struct LogprobsArgs {
+  const void* x;
+  int64_t rows, vocab, row_stride;
+  const int32_t* ids;
+  int k;
+  float* logprob;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logprobs;
+  void* ws;
+  int* status;
+};
+constexpr int kLogprobsMaxTop = 32;
+int64_t logprobs_workspace(int64_t rows, int64_t vocab, int k, int num_sms);
+cudaError_t logprobs_launch(const LogprobsArgs& a, int type, int num_sms, cudaStream_t stream);
 
 }  // namespace minfer
