@@ -191,12 +191,13 @@ struct Loader<__nv_bfloat16> {
   __device__ static float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 };
 
-// A part's result in the workspace: Stat, then (k > 0) k keys, descending.
+// A part's result in the workspace: Stat, then (k > 0) k keys, descending;
+// padded so that the next one is 16-byte aligned again.
 struct Plan {
   int parts;      // per row
   int64_t vecs;   // 16-byte vectors of a part
 };
-__host__ __device__ inline int64_t part_bytes(int k) { return 16 + 8 * (int64_t)k; }
+__host__ __device__ inline int64_t part_bytes(int k) { return 16 + 16 * (int64_t)((k + 1) / 2); }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constant__ LogprobsArgs a, Plan plan) {

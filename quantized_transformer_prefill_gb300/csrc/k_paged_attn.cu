@@ -145,8 +145,10 @@ __device__ __forceinline__ void walk_next(Walk& w, const PagedAttnArgs& a, int n
   } while (w.units == 0 && w.r < a.n_req);
 }
 
-// First unit of CTA c's share.
-__host__ __device__ inline int64_t share_begin(int64_t total, int c, int n) { return total * c / n; }
+// The units are cut into as many shares as there are CTAs, but no empty ones;
+// share c begins at share_begin(c).
+__device__ __forceinline__ int share_count(int64_t total, int n_ctas) { return (int)min(total, (int64_t)n_ctas); }
+__device__ __forceinline__ int64_t share_begin(int64_t total, int c, int n) { return total * c / n; }
 
 template <typename T, int HD>
 __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD>::kCtas)
@@ -181,10 +183,11 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD>::kCtas)
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) total += s_scan[i];
   total *= nv;
-  const int64_t begin = share_begin(total, blockIdx.x, gridDim.x);
-  const int count = (int)(share_begin(total, blockIdx.x + 1, gridDim.x) - begin);
   if (blockIdx.x == 0 && tid == 0) ws_units[0] = total;
-  if (count == 0) return;
+  const int n_shares = share_count(total, gridDim.x);
+  if ((int)blockIdx.x >= n_shares) return;
+  const int64_t begin = share_begin(total, blockIdx.x, n_shares);
+  const int count = (int)(share_begin(total, blockIdx.x + 1, n_shares) - begin);
   {
     // warp 0 scans the requests 32 at a time until the first unit is reached
     if (warp == 0) {
@@ -530,7 +533,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD>::kCtas)
 // query head): thread (g, d) takes partials g, g + kJoin, ... of dim d.
 constexpr int kJoin = 4;
 template <typename T, int HD>
-__global__ void __launch_bounds__(kJoin* HD) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, int n_groups, int n_shares) {
+__global__ void __launch_bounds__(kJoin* HD) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, int n_groups, int n_ctas) {
   __shared__ float s_m[kJoin], s_l[kJoin], s_o[kJoin][HD];
   __shared__ int s_bad;
   const int r = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, d = tid % HD, g = tid / HD;
@@ -553,6 +556,7 @@ __global__ void __launch_bounds__(kJoin* HD) paged_join_kernel(const __grid_cons
   const int64_t* ws_units = static_cast<const int64_t*>(a.ws);
   const float* ws_part = reinterpret_cast<const float*>(static_cast<const unsigned char*>(a.ws) + ws_part_offset(a.n_req));
   const int64_t total = ws_units[0];
+  const int n_shares = share_count(total, n_ctas);
   const int units = units_of(len, cap);
   const int64_t first = ws_units[1 + r] + (int64_t)(kvh * n_groups + grp) * units, last = first + units - 1;
   // the share that holds unit x: the largest c with share_begin(c) <= x
