@@ -1,15 +1,14 @@
 // k_logprobs.cu -- log probabilities of given tokens, entropy and the k
 // largest of logits rows, in one pass over the logits.
 //
-//   y = x log2 e,  z near max y,  s = sum 2^(y-z),  t = sum 2^(y-z) (y-z)
-//   log p_i = ln 2 ((y_i - z) - log2 s),   H = ln 2 (log2 s - t / s)
+//   m = max x,  s = sum e^(x-m),  t = sum e^(x-m) (x-m) log2 e
+//   log p_i = (x_i - m) - ln s,   H = ln 2 (log2 s - t / s)
 //
-// z is an f32 number that stands for itself (the rounded product of the
-// largest logit and log2 e), so nothing is lost where y - z is taken as one
-// fused multiply-add; the f32 log2 e is 1.3e-8 off in relative terms, which
-// stretches differences of logits by as much and no more.
+// x - m is taken before the factor log2 e: one multiply-add with a rounded
+// m log2 e would be off by 2^-24 |m|, which for logits of 1e30, or for rows
+// masked with the type's lowest value, is any power of two.
 //
-// A row is cut into parts, one CTA each; a part keeps a running (z, s, t) per
+// A row is cut into parts, one CTA each; a part keeps a running (m, s, t) per
 // thread and the k largest (value, id) pairs.  The pairs are compared as one
 // 64-bit key, the value's order-preserving bits above the complemented id, so
 // keys are distinct and equal values rank by ascending id whatever the order
@@ -64,18 +63,18 @@ __device__ __forceinline__ uint64_t make_key(float x, uint32_t id) {
 }
 __device__ __forceinline__ uint32_t key_id(uint64_t k) { return ~(uint32_t)k; }
 
-// (z, s, t) of a set of logits; z = -inf: empty or all masked.
+// (m, s, t) of a set of logits; m = -inf: empty or all masked.
 struct Stat {
-  float z, s, t;
+  float m, s, t;
 };
 __device__ __forceinline__ Stat join(const Stat& a, const Stat& b) {
   Stat r;
-  r.z = max_nan(a.z, b.z);
+  r.m = max_nan(a.m, b.m);
   // an empty side contributes nothing; its shift would be -inf
-  const float da = a.z == -INFINITY ? 0.f : a.z - r.z, db = b.z == -INFINITY ? 0.f : b.z - r.z;
+  const float da = a.m == -INFINITY ? 0.f : (a.m - r.m) * kLog2e, db = b.m == -INFINITY ? 0.f : (b.m - r.m) * kLog2e;
   const float ca = ex2(da), cb = ex2(db);
   r.s = a.s * ca + b.s * cb;
-  // sum 2^(y-z) (y-z) = c (t + (z_a - z) s); far below, c = 0 and the shift may overflow: no term
+  // the terms' shift d moves t by d s; far below, c = 0 and d may overflow: no term
   r.t = (ca == 0.f ? 0.f : ca * (a.t + da * a.s)) + (cb == 0.f ? 0.f : cb * (b.t + db * b.s));
   return r;
 }
@@ -83,7 +82,7 @@ __device__ __forceinline__ Stat warp_join(Stat v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     Stat w;
-    w.z = __shfl_xor_sync(0xffffffffu, v.z, o);
+    w.m = __shfl_xor_sync(0xffffffffu, v.m, o);
     w.s = __shfl_xor_sync(0xffffffffu, v.s, o);
     w.t = __shfl_xor_sync(0xffffffffu, v.t, o);
     // both lanes of a pair join in the same order: the sum does not depend on the lane
@@ -227,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
   const int64_t v0 = part * plan.vecs, v1 = min(nvec, v0 + plan.vecs);
   const T* base = x - head;
 
-  float m = -INFINITY, zl = 0.f, s = 0.f, t = 0.f;  // m: the largest logit so far, zl: its z
+  float m = -INFINITY, s = 0.f, t = 0.f;
   float thr = -INFINITY;                  // values up to thr cannot be among the k largest
   bool have = false;                      // thr is set
   for (int64_t w0 = v0; w0 < v1; w0 += kThreads * U) {
@@ -249,20 +248,19 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
 #pragma unroll
     for (int i = 1; i < kPer; ++i) top = max_nan(top, f[i]);
 
-    // running sums; one rescale per tile.  With nothing but -inf so far z is 0:
-    // any number does, all terms are 0.
-    const float mn = max_nan(m, top);
+    // running sums; one rescale per tile.  With nothing but -inf so far any
+    // reference does, all terms are 0.
+    const float mn = max_nan(m, top), z = mn == -INFINITY ? 0.f : mn;
     if (mn != m) {
-      const float zn = mn * kLog2e, shift = m == -INFINITY ? 0.f : zl - zn, c = ex2(shift);
+      const float shift = m == -INFINITY ? 0.f : (m - mn) * kLog2e, c = ex2(shift);
       t = c == 0.f ? 0.f : c * fmaf(shift, s, t);
       s *= c;
       m = mn;
-      zl = zn;
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       // 2^-200 is 0 in f32: the clamp changes no sum and keeps 0 * -inf out of t
-      const float d = max_nan(fmaf(f[i], kLog2e, -zl), -200.f);
+      const float d = max_nan((f[i] - z) * kLog2e, -200.f);
       const float e = ex2(d);
       s += e;
       t = fmaf(e, d, t);
@@ -314,13 +312,13 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
     cut_to_k(s_buf, n, k, s_best, s_red);
     if (tid < k) reinterpret_cast<uint64_t*>(out + 16)[tid] = tid < n ? s_buf[tid] : 0;
   }
-  Stat v = warp_join(Stat{m == -INFINITY ? -INFINITY : zl, s, t});
+  Stat v = warp_join(Stat{m, s, t});
   if (lane == 0) s_stat[warp] = v;
   __syncthreads();
   if (tid == 0) {
 #pragma unroll
     for (int i = 1; i < kThreads / 32; ++i) v = join(v, s_stat[i]);
-    *reinterpret_cast<float4*>(out) = make_float4(v.z, v.s, v.t, 0.f);
+    *reinterpret_cast<float4*>(out) = make_float4(v.m, v.s, v.t, 0.f);
   }
 }
 
@@ -356,9 +354,9 @@ __global__ void __launch_bounds__(kThreads) logprobs_join_kernel(const __grid_co
   v = s_stat[0];
 #pragma unroll
   for (int i = 1; i < kThreads / 32; ++i) v = join(v, s_stat[i]);
-  const bool none = v.z == -INFINITY;
+  const bool none = v.m == -INFINITY;
   const float log2s = log2f(v.s);
-  auto logp = [&](float x) { return none ? -INFINITY : kLn2 * (fmaf(x, kLog2e, -v.z) - log2s); };
+  auto logp = [&](float x) { return none ? -INFINITY : (x - v.m) - kLn2 * log2s; };
   if (tid == 0) {
     if (a.ids) a.logprob[row] = logp(Loader<T>::one(static_cast<const T*>(a.x) + row * a.row_stride + id));
     if (a.entropy) a.entropy[row] = none ? 0.f : kLn2 * (log2s - v.t / v.s);

@@ -206,7 +206,7 @@ def rope_by_formula(qkv, nh, nkv, hd, pos, f, scale, style, bias=None, norms=Non
     if bias is not None:
         x = x + bias.double()
         size = size + bias.double().abs()
-    x, size = x.view(n, -1, hd), size.view(n, -1, hd)
+    x, size = x.view(n, nh + 2 * nkv, hd), size.view(n, nh + 2 * nkv, hd)
     if norms is not None:
         y = x[:, :nh + nkv]
         w = torch.cat([norms[0].double().expand(nh, hd), norms[1].double().expand(nkv, hd)])
