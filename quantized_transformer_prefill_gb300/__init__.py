@@ -412,260 +412,16 @@ def op_rope_store(qkv, bias, pos, nh: int, nkv: int, hd: int, theta: float, K, V
 
 
 # ------------------------------------------------------------------ batch operators
-# One step of a batch of requests over a paged K/V cache: torch tensors (CUDA)
-# in and out.  The calls enqueue on the current stream of the tensors' device,
-# wait for nothing, and can be captured into a CUDA graph.  `out`, `workspace`
-# and the like may be given, so that a loop allocates nothing; `status` is an
-# int32 tensor of one element in which the kernels leave the first error code
-# they find (check_status reads it).
+# (batch.py; loaded with torch on first use)
 
-def _torch_types():
-    import torch
-    return {torch.float32: MINFER_F32, torch.float16: MINFER_F16, torch.bfloat16: MINFER_BF16}
+_BATCH = ("PagedCache", "RopeTable", "Workspace", "check_status", "op_page_tables",
+          "op_rope_paged_store", "op_paged_attention_workspace", "op_paged_attention",
+          "op_token_logprobs_workspace", "op_token_logprobs")
 
 
-def _type_of(t, what: str) -> int:
-    code = _torch_types().get(t.dtype)
-    if code is None:
-        raise MinferError(-5, f"{what}: {t.dtype} (float32, float16 or bfloat16 wanted)")
-    return code
-
-
-def _need(ok: bool, what: str, code: int = -1):
-    if not ok:
-        raise MinferError(code, what)
-
-
-def _vector(t, dtype, n: int, device, what: str):
-    """A contiguous tensor of one dimension, n elements (None: any number)."""
-    _need(t.dtype == dtype and t.dim() == 1 and t.device == device and t.is_contiguous()
-          and (n is None or t.shape[0] == n), f"{what}: {list(t.shape)} {t.dtype} on {t.device}")
-
-
-class _on:
-    """The tensors' device current during a call; .stream its current stream."""
-
-    def __init__(self, device):
-        import torch
-        _need(device.type == "cuda", f"tensors on {device} (a CUDA device wanted)")
-        self.guard = None
-        if device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
-        self.device = device
-
-    def __enter__(self):
-        import torch
-        if self.guard is not None:
-            self.guard.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-class PagedCache:
-    """A pool of K/V pages: k and v [n_pages, page_size, n_head_kv, head_dim], of
-    one type and with the same strides (a permuted view whose last dimension is
-    contiguous will do, e.g. of [n_pages, n_head_kv, page_size, head_dim])."""
-
-    def __init__(self, k, v):
-        _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.device == v.device
-              and k.stride() == v.stride() and k.stride(3) == 1,
-              "PagedCache: k and v differ, or are not [pages][rows][heads][dims] with contiguous dims")
-        self.k, self.v = k, v
-        self.device = k.device
-        n, rows, heads, dims = k.shape
-        self.n_pages, self.page_size, self.n_head_kv, self.head_dim = n, rows, heads, dims
-        self.dtype = k.dtype
-        self.desc = PagedCacheDesc(k.data_ptr(), v.data_ptr(), _type_of(k, "PagedCache"), n, rows,
-                                   heads, dims, k.stride(0), k.stride(1), k.stride(2))
-        self.ptr = ctypes.addressof(self.desc)
-
-
-class RopeTable:
-    """Rotary positions of one head layout (host memory): rot_dim leading dims
-    of a head (None: all), style "half" or "interleaved", scaling "none",
-    "linear", "ntk" or "yarn"."""
-
-    def __init__(self, head_dim: int, rot_dim: int | None = None, theta: float = 1.0e6,
-                 style: str = "half", scaling: str = "none", factor: float = 1.0,
-                 n_ctx_orig: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
-                 attn_factor: float = 0.0):
-        _need(style in ROPE_STYLES and scaling in ROPE_SCALINGS,
-              f"RopeTable: style {style!r}, scaling {scaling!r}")
-        spec = RopeSpec(head_dim, head_dim if rot_dim is None else rot_dim, ROPE_STYLES[style],
-                        ROPE_SCALINGS[scaling], theta, factor, n_ctx_orig, beta_fast, beta_slow,
-                        attn_factor)
-        self.desc = RopeTableDesc()
-        check(lib().minfer_rope_prepare(ctypes.byref(spec), ctypes.byref(self.desc)), "RopeTable")
-        self.head_dim = head_dim
-        self.ptr = ctypes.addressof(self.desc)
-
-
-def check_status(status):
-    """Raise the error that a batch operator left in `status`, if any (waits for
-    the device)."""
-    check(int(status.item()), "batch operator")
-
-
-def op_page_tables(length, target, page_size: int, table, free, n_free, n_pages: int,
-                   max_tokens: int, out=None, status=None):
-    """Block tables and slot maps of a step (minfer_op_page_tables): requests
-    holding `length` rows are to hold `target`.  int32 tensors; `table`
-    [n_req][max_pages] and the stack `free` [n_pages] are updated in place.
-    Returns (start [n_req + 1], pos [max_tokens], slot [max_tokens], n_free
-    [1]), or fills `out`, four such tensors; the last may be n_free itself."""
-    import torch
-    i32, dev = torch.int32, length.device
-    n = length.shape[0]
-    _vector(length, i32, n, dev, "length")
-    _vector(target, i32, n, dev, "target")
-    _vector(free, i32, n_pages, dev, "free")
-    _vector(n_free, i32, 1, dev, "n_free")
-    _need(table.dtype == i32 and table.dim() == 2 and table.shape[0] == n and table.is_contiguous()
-          and table.device == dev, "table: int32 [n_req][max_pages] wanted")
-    with _on(dev) as stream:
-        if out is None:
-            out = (torch.empty(n + 1, dtype=i32, device=dev), torch.empty(max_tokens, dtype=i32, device=dev),
-                   torch.empty(max_tokens, dtype=i32, device=dev), torch.empty(1, dtype=i32, device=dev))
-        else:
-            for t, m, what in zip(out, (n + 1, max_tokens, max_tokens, 1), ("start", "pos", "slot", "n_free")):
-                _vector(t, i32, m, dev, what)
-        if status is not None:
-            _vector(status, i32, 1, dev, "status")
-        start, pos, slot, left = out
-        check(lib().minfer_op_page_tables(_ptr(length), _ptr(target), n, page_size, n_pages, _ptr(table),
-                                          table.shape[1], _ptr(free), _ptr(n_free), _ptr(left), _ptr(start),
-                                          _ptr(pos), _ptr(slot), max_tokens, _ptr(status), stream),
-              "op_page_tables")
-    return out
-
-
-def op_rope_paged_store(qkv, rope: RopeTable, pos, slot, cache: PagedCache, n_head: int, bias=None,
-                        q_norm=None, k_norm=None, eps: float = 1e-6, out=None, status=None):
-    """Bias, QK-norm and RoPE of fused Q|K|V rows [n][(n_head + 2 n_head_kv) *
-    head_dim] (float32 or the cache's type), K and V stored at `slot`
-    (minfer_op_rope_paged_store).  Returns the rotated Q [n][n_head*head_dim]
-    in the cache's type; rows with a negative slot are skipped (without `out`
-    they are zero)."""
-    import torch
-    dev, f32 = qkv.device, torch.float32
-    n, hd = qkv.shape[0], cache.head_dim
-    width = (n_head + 2 * cache.n_head_kv) * hd
-    _need(qkv.dim() == 2 and qkv.shape[1] == width and qkv.stride(1) == 1 and cache.device == dev,
-          f"qkv: {list(qkv.shape)} on {dev} (rows of {width} on {cache.device} wanted)")
-    _vector(pos, torch.int32, n, dev, "pos")
-    _vector(slot, torch.int32, n, dev, "slot")
-    for t, m, what in ((bias, width, "bias"), (q_norm, hd, "q_norm"), (k_norm, hd, "k_norm")):
-        if t is not None:
-            _vector(t, f32, m, dev, what)
-    if status is not None:
-        _vector(status, torch.int32, 1, dev, "status")
-    with _on(dev) as stream:
-        if out is None:
-            out = torch.zeros((n, n_head * hd), dtype=cache.dtype, device=dev)
-        else:
-            _need(out.dim() == 2 and out.shape[0] == n and out.shape[1] == n_head * hd and out.stride(1) == 1
-                  and out.dtype == cache.dtype and out.device == dev, "out: the cache's type, [n][n_head*head_dim]")
-        check(lib().minfer_op_rope_paged_store(_ptr(qkv), _type_of(qkv, "qkv"), qkv.stride(0), _ptr(bias),
-                                               _ptr(q_norm), _ptr(k_norm), eps, rope.ptr, _ptr(pos), _ptr(slot),
-                                               n, n_head, cache.ptr, _ptr(out), out.stride(0), _ptr(status),
-                                               stream), "op_rope_paged_store")
-    return out
-
-
-def op_paged_attention_workspace(cache: PagedCache, n_req: int, n_head: int):
-    """A workspace for op_paged_attention calls of up to n_req requests, one call
-    at a time."""
-    import torch
-    n = ctypes.c_int64()
-    with _on(cache.device):
-        check(lib().minfer_op_paged_attention_workspace(n_req, n_head, cache.ptr, ctypes.byref(n)),
-              "op_paged_attention_workspace")
-        return torch.empty(n.value, dtype=torch.uint8, device=cache.device)
-
-
-def op_paged_attention(q, cache: PagedCache, table, length, n_head: int, scale: float | None = None,
-                       out=None, lse=None, workspace=None, status=None):
-    """Attention of one new token per request over its pages
-    (minfer_op_paged_attention): q [n_req][n_head*head_dim] in the cache's type,
-    table int32 [n_req][max_pages], length int32 [n_req] rows to attend to, the
-    new one included.  Returns o like q; `lse` (float32 [n_req][n_head]), when
-    given, gets ln sum exp(scale q.k)."""
-    import torch
-    dev, n, width = q.device, q.shape[0], n_head * cache.head_dim
-    _need(q.dim() == 2 and q.shape[1] == width and q.stride(1) == 1 and q.dtype == cache.dtype
-          and cache.device == dev, f"q: {list(q.shape)} {q.dtype} on {dev} (rows of {width} {cache.dtype} on {cache.device} wanted)")
-    _need(table.dtype == torch.int32 and table.dim() == 2 and table.shape[0] == n and table.stride(1) == 1
-          and table.device == dev, "table: int32 [n_req][max_pages] wanted")
-    _vector(length, torch.int32, n, dev, "length")
-    if lse is not None:
-        _need(lse.dtype == torch.float32 and lse.dim() == 2 and lse.shape[0] == n and lse.shape[1] == n_head
-              and lse.is_contiguous() and lse.device == dev, "lse: float32 [n_req][n_head] wanted")
-    if status is not None:
-        _vector(status, torch.int32, 1, dev, "status")
-    with _on(dev) as stream:
-        if out is None:
-            out = torch.empty((n, width), dtype=q.dtype, device=dev)
-        else:
-            _need(out.dim() == 2 and out.shape == q.shape and out.stride(1) == 1 and out.dtype == q.dtype
-                  and out.device == dev, "out: like q")
-        if workspace is None:
-            workspace = op_paged_attention_workspace(cache, n, n_head)
-        else:
-            _vector(workspace, torch.uint8, None, dev, "workspace")
-        check(lib().minfer_op_paged_attention(_ptr(q), q.stride(0), cache.ptr, _ptr(table), table.stride(0),
-                                              table.shape[1], _ptr(length), n, n_head, scale or 0.0, _ptr(out),
-                                              out.stride(0), _ptr(lse), _ptr(workspace), workspace.shape[0],
-                                              _ptr(status), stream), "op_paged_attention")
-    return out
-
-
-def op_token_logprobs_workspace(logits, k: int):
-    """A workspace for op_token_logprobs calls on logits of this shape, one call
-    at a time."""
-    import torch
-    n = ctypes.c_int64()
-    with _on(logits.device):
-        check(lib().minfer_op_token_logprobs_workspace(logits.shape[0], logits.shape[1], k, ctypes.byref(n)),
-              "op_token_logprobs_workspace")
-        return torch.empty(n.value, dtype=torch.uint8, device=logits.device)
-
-
-def op_token_logprobs(logits, ids=None, k: int = 0, out=None, workspace=None, status=None):
-    """Log probabilities of the tokens `ids` (int32 [rows], negative: skip the
-    row; or None) under logits [rows][vocab] (float32, float16 or bfloat16, any
-    row stride), the rows' entropy and k largest with their log probabilities
-    (minfer_op_token_logprobs).  Returns (logprob, entropy, top_ids,
-    top_logprobs), or fills `out`, four such tensors; logprob is None without
-    ids."""
-    import torch
-    dev, f32 = logits.device, torch.float32
-    _need(logits.dim() == 2 and (logits.stride(1) == 1 or logits.shape[1] == 1), "logits: [rows][vocab] wanted")
-    rows, vocab = logits.shape
-    if ids is not None:
-        _vector(ids, torch.int32, rows, dev, "ids")
-    if status is not None:
-        _vector(status, torch.int32, 1, dev, "status")
-    with _on(dev) as stream:
-        if out is None:
-            out = (None if ids is None else torch.empty(rows, dtype=f32, device=dev),
-                   torch.empty(rows, dtype=f32, device=dev),
-                   torch.empty((rows, k), dtype=torch.int32, device=dev), torch.empty((rows, k), dtype=f32, device=dev))
-        else:
-            for t, dtype, what in ((out[0], f32, "logprob"), (out[1], f32, "entropy")):
-                if t is not None:
-                    _vector(t, dtype, rows, dev, what)
-            for t, dtype, what in ((out[2], torch.int32, "top_ids"), (out[3], f32, "top_logprobs")):
-                _need(k == 0 or (t.dtype == dtype and t.dim() == 2 and t.shape[0] == rows and t.shape[1] == k
-                                 and t.is_contiguous() and t.device == dev), f"{what}: [rows][k] wanted")
-        if workspace is None:
-            workspace = op_token_logprobs_workspace(logits, k)
-        else:
-            _vector(workspace, torch.uint8, None, dev, "workspace")
-        check(lib().minfer_op_token_logprobs(_ptr(logits), _type_of(logits, "logits"), rows, vocab,
-                                             logits.stride(0), _ptr(ids), k, _ptr(out[0]), _ptr(out[1]),
-                                             _ptr(out[2]), _ptr(out[3]), _ptr(workspace), workspace.shape[0],
-                                             _ptr(status), stream), "op_token_logprobs")
-    return out
+def __getattr__(name: str):
+    if name in _BATCH:
+        from . import batch
+        globals().update({n: getattr(batch, n) for n in _BATCH})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

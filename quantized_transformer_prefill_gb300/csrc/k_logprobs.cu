@@ -8,17 +8,20 @@
 // m log2 e would be off by 2^-24 |m|, which for logits of 1e30, or for rows
 // masked with the type's lowest value, is any power of two.
 //
-// A row is cut into parts, one CTA each; a part keeps a running (m, s, t) per
-// thread and the k largest (value, id) pairs.  The pairs are compared as one
-// 64-bit key, the value's order-preserving bits above the complemented id, so
-// keys are distinct and equal values rank by ascending id whatever the order
-// in which threads meet them.  logprobs_join_kernel adds up a row's parts.
+// A row is cut into parts, one CTA each.  Every thread keeps a running
+// (reference, s, t); a warp reads chunks of 512 neighbouring logits and leaves
+// each chunk's largest one in the workspace.  The CTA that finishes a row last
+// (a counter per row) joins the parts' sums and finds the k largest logits:
+// they lie in the k chunks with the largest maxima (each of those holds a logit
+// at least as large as the k-th of these maxima; among equal maxima the chunks
+// with lower ids count first, as the order of the result wants it).  Those k
+// chunks are read again, 512 k of the row's logits, out of L2.  The streaming
+// part so carries one warp-wide maximum per 512 logits and nothing else for
+// the top k, whatever the values are.
 //
-// The k largest of a part: the k-th largest of the 32 lane maxima of a warp is
-// a lower bound of the part's k-th largest value, so after the first tile only
-// values from the best such bound on are collected; later tiles add what
-// exceeds the bound, and the collected pairs are cut back to k whenever they
-// pass a limit, which raises the bound.  Almost every value fails one compare.
+// Pairs (value, id) are compared as one 64-bit key, the value's
+// order-preserving bits above the complemented id: keys are distinct, and equal
+// values rank by ascending id whatever the order in which they are met.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -30,10 +33,10 @@ namespace minfer {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTile = 4096;            // values of a tile, kThreads x 16
-constexpr int kPer = kTile / kThreads;  // values of a thread
-constexpr int kCut = 512;               // collected pairs that trigger a cut back to k
-constexpr int kCap = kCut + kTile;
+constexpr int kWarps = kThreads / 32;
+constexpr int kChunk = 512;         // logits of a chunk
+constexpr int kPer = kChunk / 32;   // logits of a lane
+constexpr int kCtasPerSm = 24;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -91,62 +94,53 @@ __device__ __forceinline__ Stat warp_join(Stat v) {
   return v;
 }
 
-// The lane-th largest of the warp's 32 keys (bitonic sort, descending).
-__device__ __forceinline__ uint32_t warp_sort_desc(uint32_t v) {
+// The warp's 32 keys in descending order of lanes (bitonic sort).
+__device__ __forceinline__ uint64_t warp_sort(uint64_t v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int k = 2; k <= 32; k <<= 1)
 #pragma unroll
     for (int j = k >> 1; j > 0; j >>= 1) {
-      const uint32_t w = __shfl_xor_sync(0xffffffffu, v, j);
+      const uint64_t w = __shfl_xor_sync(0xffffffffu, v, j);
       const bool desc = (lane & k) == 0, low = (lane & j) == 0;
-      v = (desc == low) ? max(v, w) : min(v, w);
+      v = (desc == low) == (w > v) ? w : v;
     }
   return v;
 }
-
-// The largest key of the CTA; every thread gets it.  s: one slot per warp.
-__device__ __forceinline__ uint64_t block_max(uint64_t v, uint64_t* s) {
+// The 32 largest of two descending lists, descending: the larger one of each
+// key and its mirror image is a bitonic sequence of them.
+__device__ __forceinline__ uint64_t warp_merge(uint64_t a, uint64_t b) {
+  const int lane = threadIdx.x & 31;
+  const uint64_t r = __shfl_sync(0xffffffffu, b, 31 - lane);
+  uint64_t v = r > a ? r : a;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const uint64_t w = __shfl_xor_sync(0xffffffffu, v, o);
-    v = w > v ? w : v;
+  for (int j = 16; j > 0; j >>= 1) {
+    const uint64_t w = __shfl_xor_sync(0xffffffffu, v, j);
+    v = ((lane & j) == 0) == (w > v) ? w : v;
   }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = s[0];
-#pragma unroll
-  for (int i = 1; i < kThreads / 32; ++i) v = s[i] > v ? s[i] : v;
   return v;
 }
-
-// The min(k, n) largest of the n distinct keys buf[0..n) to the front, in
-// descending order.  All threads; ends with a barrier.
-__device__ void cut_to_k(uint64_t* buf, int n, int k, uint64_t* s_best, uint64_t* s_red) {
-  const int tid = threadIdx.x;
-  if (n <= kThreads) {
-    // a key's place is the number of keys above it
-    const uint64_t own = tid < n ? buf[tid] : 0;
-    int place = 0;
-    for (int i = 0; i < n; ++i) place += buf[i] > own;
-    __syncthreads();
-    if (tid < n && place < k) buf[place] = own;
-  } else {
-    uint64_t last = ~0ull;  // the key taken in the round before
-    for (int j = 0; j < k; ++j) {
-      uint64_t best = 0;
-      for (int i = tid; i < n; i += kThreads) {
-        const uint64_t v = buf[i];
-        best = (v < last && v > best) ? v : best;
-      }
-      last = block_max(best, s_red);
-      if (tid == 0) s_best[j] = last;
+// Takes one new key per lane into the warp's list of the 32 largest.
+__device__ __forceinline__ void warp_take(uint64_t& list, uint64_t key, int k) {
+  const uint64_t kth = __shfl_sync(0xffffffffu, list, k - 1);
+  if (__any_sync(0xffffffffu, key > kth)) list = warp_merge(list, warp_sort(key));
+}
+// The 32 largest of all warps' lists, in every warp.  s: [kWarps][32].
+__device__ __forceinline__ uint64_t block_merge(uint64_t list, uint64_t* s) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  s[warp * 32 + lane] = list;
+  __syncthreads();
+#pragma unroll
+  for (int n = kWarps / 2; n > 0; n >>= 1) {
+    if (warp < n) {
+      list = warp_merge(list, s[(warp + n) * 32 + lane]);
+      s[warp * 32 + lane] = list;
     }
     __syncthreads();
-    if (tid < k) buf[tid] = s_best[tid];
   }
+  list = s[lane];
   __syncthreads();
+  return list;
 }
 
 template <typename T>
@@ -190,226 +184,221 @@ struct Loader<__nv_bfloat16> {
   __device__ static float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 };
 
-// A part's result in the workspace: Stat, then (k > 0) k keys, descending;
-// padded so that the next one is 16-byte aligned again.
+// How rows are cut, and where the workspace holds what: a counter per row (zero
+// between calls; only rows of several parts have one, and there are fewer than
+// num_sms * kCtasPerSm of those, so their place is the same in every call), a
+// Stat per part, the largest key32 of every chunk.
 struct Plan {
-  int parts;      // per row
-  int64_t vecs;   // 16-byte vectors of a part
+  int chunks;  // of a row, at the worst alignment
+  int parts;   // of a row
+  int per;     // chunks of a part
+  int64_t stats, keys, bytes;  // offsets and size
 };
-__host__ __device__ inline int64_t part_bytes(int k) { return 16 + 16 * (int64_t)((k + 1) / 2); }
+
+// One lane's 16 logits of chunk c of a row: vectors of 16 bytes, lane after
+// lane.  Vector v holds the values [v*V - head, (v+1)*V - head): the row's first
+// address rounded down to 16 bytes is vector 0.  -inf outside of the row.
+template <typename T>
+__device__ __forceinline__ void load_chunk(const T* x, int head, int64_t vocab, int64_t c, float* f) {
+  using L = Loader<T>;
+  constexpr int V = L::kVec, U = kPer / V;
+  const int lane = threadIdx.x & 31;
+  const int64_t e0 = c * kChunk - head;
+  if (e0 >= 0 && e0 + kChunk <= vocab) {
+    const uint4* p = reinterpret_cast<const uint4*>(x + e0) + lane;
+    uint4 u[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) u[i] = __ldcg(p + i * 32);
+#pragma unroll
+    for (int i = 0; i < U; ++i) L::get(u[i], f + i * V);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int64_t e = e0 + ((i / V) * 32 + lane) * V + i % V;
+      f[i] = e >= 0 && e < vocab ? L::one(x + e) : -INFINITY;
+    }
+  }
+}
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constant__ LogprobsArgs a, Plan plan) {
+__global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constant__ LogprobsArgs a, const Plan plan) {
   using L = Loader<T>;
-  constexpr int V = L::kVec, U = kPer / V;  // vectors of a thread per tile
-  __shared__ uint64_t s_buf[kCap];
-  __shared__ uint64_t s_best[kLogprobsMaxTop], s_red[kThreads / 32];
-  __shared__ uint32_t s_thr[kThreads / 32];
-  __shared__ Stat s_stat[kThreads / 32];
-  __shared__ int s_n;
+  constexpr int V = L::kVec;
+  __shared__ uint64_t s_list[kWarps * 32];
+  __shared__ Stat s_stat[kWarps];
+  __shared__ int s_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = blockIdx.x / plan.parts;
   const int part = (int)(blockIdx.x - row * plan.parts);
   const int k = a.k;
-  if (tid == 0) s_n = 0;
-  pdl_trigger();
-  pdl_wait();
-  if (a.ids) {
-    const int id = a.ids[row];
-    if (id < 0 || id >= a.vocab) return;  // padding, or refused (the join reports it)
-  }
-  // Vector v of the row covers the values [v*V - head, (v+1)*V - head): the
-  // row's first address rounded down to 16 bytes is vector 0.
-  const T* x = static_cast<const T*>(a.x) + row * a.row_stride;
-  const int head = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-  const int64_t nvec = (a.vocab + head + V - 1) / V;
-  const int64_t v0 = part * plan.vecs, v1 = min(nvec, v0 + plan.vecs);
-  const T* base = x - head;
-
-  float m = -INFINITY, s = 0.f, t = 0.f;
-  float thr = -INFINITY;                  // values up to thr cannot be among the k largest
-  bool have = false;                      // thr is set
-  for (int64_t w0 = v0; w0 < v1; w0 += kThreads * U) {
-    float f[kPer];
-    // values outside the row: -inf for the sums, and never collected
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t v = w0 + u * kThreads + tid;
-      const int64_t e0 = v * V - head;
-      if (v < v1 && e0 >= 0 && e0 + V <= a.vocab) {
-        L::get(__ldcs(reinterpret_cast<const uint4*>(base + v * V)), f + u * V);
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          f[u * V + j] = (v < v1 && e0 + j >= 0 && e0 + j < a.vocab) ? L::one(x + e0 + j) : -INFINITY;
-      }
-    }
-    float top = f[0];
-#pragma unroll
-    for (int i = 1; i < kPer; ++i) top = max_nan(top, f[i]);
-
-    // running sums; one rescale per tile.  With nothing but -inf so far any
-    // reference does, all terms are 0.
-    const float mn = max_nan(m, top), z = mn == -INFINITY ? 0.f : mn;
-    if (mn != m) {
-      const float shift = m == -INFINITY ? 0.f : (m - mn) * kLog2e, c = ex2(shift);
-      t = c == 0.f ? 0.f : c * fmaf(shift, s, t);
-      s *= c;
-      m = mn;
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      // 2^-200 is 0 in f32: the clamp changes no sum and keeps 0 * -inf out of t
-      const float d = max_nan((f[i] - z) * kLog2e, -200.f);
-      const float e = ex2(d);
-      s += e;
-      t = fmaf(e, d, t);
-    }
-
-    if (k > 0) {
-      bool over = false;  // more than kCut pairs lie in the buffer
-      auto collect = [&](bool strict) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          if (strict ? !(f[i] <= thr) : !(f[i] < thr)) {
-            const int64_t id = (w0 + (i / V) * kThreads + tid) * V - head + i % V;
-            if (id >= 0 && id < a.vocab && w0 + (i / V) * kThreads + tid < v1) {
-              const int at = atomicAdd(&s_n, 1);
-              s_buf[at] = make_key(f[i], (uint32_t)id);
-              over |= at >= kCut;
-            }
-          }
-        }
-      };
-      if (!have) {
-        // the best k-th lane maximum of a warp (NaN ranks highest)
-        const uint32_t sorted = warp_sort_desc(key32(top));
-        const uint32_t kth = __shfl_sync(0xffffffffu, sorted, k - 1);
-        if (lane == 0) s_thr[warp] = kth;
-        __syncthreads();
-        uint32_t best = s_thr[0];
-#pragma unroll
-        for (int i = 1; i < kThreads / 32; ++i) best = max(best, s_thr[i]);
-        thr = key_value(best);
-        have = true;
-        if (!(top < thr)) collect(false);
-      } else if (!(top <= thr)) {
-        collect(true);
-      }
-      if (__syncthreads_or(over)) {
-        cut_to_k(s_buf, s_n, k, s_best, s_red);
-        thr = key_value((uint32_t)(s_buf[k - 1] >> 32));
-        if (tid == 0) s_n = k;
-        __syncthreads();
-      }
-    }
-  }
-
-  unsigned char* out = static_cast<unsigned char*>(a.ws) + (row * plan.parts + part) * part_bytes(k);
-  if (k > 0) {
-    __syncthreads();
-    const int n = s_n;
-    cut_to_k(s_buf, n, k, s_best, s_red);
-    if (tid < k) reinterpret_cast<uint64_t*>(out + 16)[tid] = tid < n ? s_buf[tid] : 0;
-  }
-  Stat v = warp_join(Stat{m, s, t});
-  if (lane == 0) s_stat[warp] = v;
-  __syncthreads();
-  if (tid == 0) {
-#pragma unroll
-    for (int i = 1; i < kThreads / 32; ++i) v = join(v, s_stat[i]);
-    *reinterpret_cast<float4*>(out) = make_float4(v.m, v.s, v.t, 0.f);
-  }
-}
-
-// One CTA per row: the parts' sums, the k largest of the parts' lists, and the
-// given token's log probability.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) logprobs_join_kernel(const __grid_constant__ LogprobsArgs a, Plan plan) {
-  __shared__ uint64_t s_red[kThreads / 32];
-  __shared__ Stat s_stat[kThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t row = blockIdx.x;
-  const int k = a.k;
+  unsigned char* ws = static_cast<unsigned char*>(a.ws);
+  float4* stats = reinterpret_cast<float4*>(ws + plan.stats) + row * plan.parts;
+  uint32_t* keys = reinterpret_cast<uint32_t*>(ws + plan.keys) + row * plan.chunks;
   pdl_trigger();
   pdl_wait();
   int id = -1;
   if (a.ids) {
     id = a.ids[row];
+    if (id < 0) return;  // padding
     if (id >= a.vocab) {
-      if (tid == 0) set_error(a.status, MINFER_ERR_TOKEN_OOB);
+      if (part == 0 && tid == 0) set_error(a.status, MINFER_ERR_TOKEN_OOB);
       return;
     }
-    if (id < 0) return;
   }
-  const unsigned char* in = static_cast<const unsigned char*>(a.ws) + row * plan.parts * part_bytes(k);
-  Stat v{-INFINITY, 0.f, 0.f};
-  for (int p = tid; p < plan.parts; p += kThreads) {
-    const float4 q = *reinterpret_cast<const float4*>(in + p * part_bytes(k));
-    v = join(v, Stat{q.x, q.y, q.z});
-  }
-  v = warp_join(v);
-  if (lane == 0) s_stat[warp] = v;
-  __syncthreads();
-  v = s_stat[0];
+  const T* x = static_cast<const T*>(a.x) + row * a.row_stride;
+  const int head = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+  const int chunks = (int)((a.vocab + head + kChunk - 1) / kChunk);
+  const int c1 = min(chunks, (part + 1) * plan.per);
+
+  // r: the reference, a logit near the largest so far (-inf: none yet).  Up to
+  // |r| = 2^20 the terms are 2^(x L - z), one multiply-add each, with z = r L
+  // rounded: z stands for itself and the sums are corrected by 2^(z - r L) at
+  // the end.  Beyond, where that factor is no longer near 1, x - r comes first.
+  float r = -INFINITY, z = 0.f, s = 0.f, t = 0.f;
+  auto exact = [&] {  // s, t from reference z to reference r
+    const float d = fmaf(r, kLog2e, -z), c = ex2(-d);
+    t = c * fmaf(-d, s, t);
+    s *= c;
+  };
+  for (int c = part * plan.per + warp; c < c1; c += kWarps) {
+    float f[kPer];
+    load_chunk<T>(x, head, a.vocab, c, f);
+    float top = f[0];
 #pragma unroll
-  for (int i = 1; i < kThreads / 32; ++i) v = join(v, s_stat[i]);
-  const bool none = v.m == -INFINITY;
-  const float log2s = log2f(v.s);
-  auto logp = [&](float x) { return none ? -INFINITY : (x - v.m) - kLn2 * log2s; };
-  if (tid == 0) {
-    if (a.ids) a.logprob[row] = logp(Loader<T>::one(static_cast<const T*>(a.x) + row * a.row_stride + id));
-    if (a.entropy) a.entropy[row] = none ? 0.f : kLn2 * (log2s - v.t / v.s);
-  }
-  uint64_t last = ~0ull;
-  for (int j = 0; j < k; ++j) {
-    uint64_t best = 0;
-    for (int p = tid; p < plan.parts; p += kThreads) {
-      // the part's list is descending: its first key below the last one taken
-      const uint64_t* list = reinterpret_cast<const uint64_t*>(in + p * part_bytes(k) + 16);
-      for (int i = 0; i < k; ++i) {
-        const uint64_t q = list[i];
-        if (q < last) {
-          best = q > best ? q : best;
-          break;
-        }
+    for (int i = 1; i < kPer; ++i) top = max_nan(top, f[i]);
+    if (k > 0) {
+      const uint32_t best = __reduce_max_sync(0xffffffffu, key32(top));
+      if (lane == 0) keys[c] = best;
+    }
+    // a new reference only when the terms get large: 2^(4 L) at most
+    if (!(top <= r + 4.f)) {
+      if (r != -INFINITY) {
+        if (fabsf(r) <= 0x1p20f) exact();
+        const float d = (r - top) * kLog2e, w = ex2(d);
+        t = w == 0.f ? 0.f : w * fmaf(d, s, t);
+        s *= w;
+      }
+      r = top;
+      z = r * kLog2e;
+      if (fabsf(r) <= 0x1p20f) {
+        const float d = fmaf(r, kLog2e, -z), w = ex2(d);
+        t = w * fmaf(d, s, t);
+        s *= w;
       }
     }
-    last = block_max(best, s_red);
-    if (tid == 0) {
-      a.top_ids[row * k + j] = (int32_t)key_id(last);
-      a.top_logprobs[row * k + j] = logp(key_value((uint32_t)(last >> 32)));
+    // 2^-200 is 0 in f32: the clamp changes no sum and keeps 0 * -inf out of t
+    if (r == -INFINITY || fabsf(r) <= 0x1p20f) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const float d = max_nan(fmaf(f[i], kLog2e, -z), -200.f), e = ex2(d);
+        s += e;
+        t = fmaf(e, d, t);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const float d = max_nan((f[i] - r) * kLog2e, -200.f), e = ex2(d);
+        s += e;
+        t = fmaf(e, d, t);
+      }
     }
+  }
+  if (fabsf(r) <= 0x1p20f) exact();
+
+  auto block_join = [&](Stat v) {
+    v = warp_join(v);
+    if (lane == 0) s_stat[warp] = v;
+    __syncthreads();
+    v = s_stat[0];
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) v = join(v, s_stat[i]);
+    return v;
+  };
+  Stat v = block_join(Stat{r, s, t});
+  if (plan.parts > 1) {
+    if (tid == 0) {
+      stats[part] = make_float4(v.m, v.s, v.t, 0.f);
+      __threadfence();  // also the other threads' keys: they came before block_join's barrier
+      unsigned* counter = reinterpret_cast<unsigned*>(ws) + row;
+      s_last = atomicAdd(counter, 1u) == (unsigned)plan.parts - 1;
+      if (s_last) *counter = 0;
+      __threadfence();
+    }
+    __syncthreads();
+    if (!s_last) return;
+    v = Stat{-INFINITY, 0.f, 0.f};
+    for (int p = tid; p < plan.parts; p += kThreads) {
+      const float4 q = __ldcg(stats + p);
+      v = join(v, Stat{q.x, q.y, q.z});
+    }
+    v = block_join(v);
+  }
+
+  const bool none = v.m == -INFINITY;
+  const float log2s = log2f(v.s);
+  auto logp = [&](float y) { return none ? -INFINITY : (y - v.m) - kLn2 * log2s; };
+  if (tid == 0) {
+    if (a.ids) a.logprob[row] = logp(L::one(x + id));
+    if (a.entropy) a.entropy[row] = none ? 0.f : kLn2 * (log2s - v.t / v.s);
+  }
+  if (k == 0) return;
+
+  // the k chunks with the largest maxima (an id is a chunk here)
+  uint64_t list = 0;
+  for (int c0 = warp * 32; c0 < chunks; c0 += kThreads) {
+    const int c = c0 + lane;
+    warp_take(list, c < chunks ? ((uint64_t)__ldcg(keys + c) << 32) | (uint32_t)~c : 0, k);
+  }
+  const uint64_t picked = block_merge(list, s_list);
+  // with fewer than k chunks the k-th key is 0 and everything counts
+  const uint32_t floor = (uint32_t)(__shfl_sync(0xffffffffu, picked, k - 1) >> 32);
+  list = 0;
+  for (int j = warp; j < k; j += kWarps) {
+    const uint64_t pick = __shfl_sync(0xffffffffu, picked, j);
+    if (pick == 0) break;
+    const int c = (int)key_id(pick);
+    float f[kPer];
+    load_chunk<T>(x, head, a.vocab, c, f);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int64_t e = (int64_t)c * kChunk - head + ((i / V) * 32 + lane) * V + i % V;
+      const uint64_t key = e >= 0 && e < a.vocab ? make_key(f[i], (uint32_t)e) : 0;
+      warp_take(list, (uint32_t)(key >> 32) >= floor ? key : 0, k);
+    }
+  }
+  list = block_merge(list, s_list);
+  if (tid < k) {
+    a.top_ids[row * k + tid] = (int32_t)key_id(list);
+    a.top_logprobs[row * k + tid] = logp(key_value((uint32_t)(list >> 32)));
   }
 }
 
-// Parts of a row: enough CTAs to fill the GPU several times over (the last
-// wave's idle share shrinks with their number), none below one vector per
-// thread.  vecs is the same for every row; a row's vectors vary by one with
-// its alignment.
-Plan plan_of(int64_t rows, int64_t vocab, int64_t vec, int num_sms) {
-  const int64_t nvec = (vocab + vec - 1) / vec + 1;
-  const int64_t want = std::max<int64_t>(1, ((int64_t)num_sms * 32 + rows - 1) / rows);
+// Parts of a row: about kCtasPerSm CTAs per SM (four rounds of what is resident,
+// so the last round's idle share is small), none with less than a chunk per warp.
+Plan plan_of(int64_t rows, int64_t vocab, int vec, int k, int num_sms) {
   Plan p;
-  int64_t parts = std::min<int64_t>(want, (nvec + kThreads - 1) / kThreads);
-  p.vecs = (nvec + parts - 1) / parts;
-  p.parts = (int)((nvec + p.vecs - 1) / p.vecs);
+  p.chunks = (int)((vocab + vec - 1 + kChunk - 1) / kChunk);
+  const int64_t want = std::max<int64_t>(1, ((int64_t)num_sms * kCtasPerSm + rows - 1) / rows);
+  const int64_t parts = std::min<int64_t>(want, (p.chunks + kWarps - 1) / kWarps);
+  p.per = (int)((p.chunks + parts - 1) / parts);
+  p.parts = (p.chunks + p.per - 1) / p.per;
+  p.stats = ((int64_t)num_sms * kCtasPerSm * 4 + 15) / 16 * 16;
+  p.keys = p.stats + rows * p.parts * 16;
+  p.bytes = p.keys + (k > 0 ? rows * p.chunks * 4 : 0);
   return p;
 }
 
 template <typename T>
 cudaError_t launch(const LogprobsArgs& a, int num_sms, cudaStream_t st) {
-  const Plan plan = plan_of(a.rows, a.vocab, Loader<T>::kVec, num_sms);
-  cudaError_t e = launch_pdl(logprobs_kernel<T>, dim3((unsigned)(a.rows * plan.parts)), dim3(kThreads), 0, st, a, plan);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(logprobs_join_kernel<T>, dim3((unsigned)a.rows), dim3(kThreads), 0, st, a, plan);
+  const Plan plan = plan_of(a.rows, a.vocab, Loader<T>::kVec, a.k, num_sms);
+  return launch_pdl(logprobs_kernel<T>, dim3((unsigned)(a.rows * plan.parts)), dim3(kThreads), 0, st, a, plan);
 }
 
 }  // namespace
 
 int64_t logprobs_workspace(int64_t rows, int64_t vocab, int k, int num_sms) {
   // the size does not depend on the logits' type: enough for vectors of 4 and of 8 values
-  return rows * std::max(plan_of(rows, vocab, 4, num_sms).parts, plan_of(rows, vocab, 8, num_sms).parts) * part_bytes(k);
+  return std::max(plan_of(rows, vocab, 4, k, num_sms).bytes, plan_of(rows, vocab, 8, k, num_sms).bytes);
 }
 
 cudaError_t logprobs_launch(const LogprobsArgs& a, int type, int num_sms, cudaStream_t stream) {

@@ -395,7 +395,7 @@ cudaError_t rope_paged_typed(const RopePagedArgs& a, cudaStream_t st) {
 cudaError_t page_tables_launch(const PageTablesArgs& a, cudaStream_t stream) {
   const size_t smem = 3 * (size_t)(a.n_req + 1) * sizeof(int);
   if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_smem<page_tables_kernel>(3 * (kPageTablesMaxReq + 1) * (int)sizeof(int));
     if (e != cudaSuccess) return e;
   }
   const unsigned cs = (a.max_tokens > 4096 || a.n_req > 1024) ? kPtCluster : 1;

@@ -9,8 +9,11 @@
 // requests load every SM alike, without the host knowing a length.  A CTA
 // walks its share as a stream: a (request, KV head) that lies inside it is
 // finished there; one that crosses a share's border leaves a partial (max,
-// sum, unnormalized output) in the workspace, and paged_join_kernel adds the
-// partials up.
+// sum, unnormalized output) in the workspace.  Partials are joined in a tree of
+// two levels: the CTA that finishes last among the (up to 16) neighbouring
+// shares of a group joins the group's partials, the one that finishes last
+// among the groups joins those.  Who is last decides only who adds, never in
+// what order, so the result does not depend on it.
 //
 // Inside a CTA each of four warps takes 16 of a unit's 64 keys, copies their
 // K and V rows into its own ring in shared memory (cp.async of 16 bytes, page
@@ -36,22 +39,35 @@ constexpr int kUnit = kWarps * kKeys;   // keys of a unit
 constexpr int kRows = 16;               // query heads of one MMA tile
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-template <typename T, int HD>
+constexpr int kGroup = 16;              // neighbouring shares whose partials are joined first
+constexpr int kMaxJoin = 64;            // partials of one join: kGroup, or the number of groups
+
+// R: query heads that a CTA carries through the join (8 where a KV head has no
+// more, which leaves room for another stage of the ring).
+template <typename T, int HD, int R>
 struct Cfg {
   static constexpr int kRowBytes = HD * (int)sizeof(T);
   static constexpr int kChunks = kRowBytes / 16;  // 16-byte chunks of a row
   static constexpr int kStageBytes = 2 * kKeys * kRowBytes;  // K and V rows of one warp
-  // CTAs per SM and ring depth: about 100 KB (two CTAs) of K/V in flight or at work
-  static constexpr int kStages = kRowBytes == 128 ? 5 : kRowBytes == 256 ? 2 : 2;
-  static constexpr int kCtas = kRowBytes == 512 ? 1 : 2;
   static constexpr int kQBytes = sizeof(T) == 4 ? 2 * kRows * kRowBytes : 0;  // tf32 hi and lo of Q
-  static constexpr int kMergeBytes = kWarps * kRows * HD * 4 + kWarps * kRows * 8;
+  static constexpr int kMergeBytes = kWarps * R * HD * 4 + kWarps * R * 8;
+  // two CTAs per SM, or one where two stages of the ring do not fit twice; the
+  // ring takes what is left of the SM's shared memory
+  static constexpr int kCtas = kRowBytes == 512 ? 1 : 2;
+  static constexpr int kBudget = kCtas == 1 ? 230000 : 113400;
+  static constexpr int kFit = (kBudget - kQBytes - kMergeBytes) / (kWarps * kStageBytes);
+  static constexpr int kStages = kFit > 6 ? 6 : kFit;
   static constexpr int kSmem = kWarps * kStages * kStageBytes + kQBytes + kMergeBytes;
+  static_assert(kStages >= 2, "a ring has two stages at least");
 };
 
-// The workspace: [0] total units (int64), then per request the first unit
-// (int64), then per CTA two partials: kRows (max, sum) pairs and kRows x HD.
-__host__ __device__ inline int64_t ws_part_offset(int n_req) { return ((int64_t)(n_req + 1) * 8 + 255) / 256 * 256; }
+// The workspace: counters (zero between calls; one per share for a piece that
+// starts in it, one per group for a piece that started before it, one per share
+// for the groups of a piece), then per share two partials, slot 1 for the piece
+// that starts in the share and slot 0 for the one that started before it: kRows
+// (max, sum) pairs and kRows x HD.
+constexpr int kMaxShares = kGroup * (kMaxJoin - 1);
+constexpr int64_t kPartOffset = ((2 * kMaxShares + kMaxShares / kGroup + 1) * 4 + 255) / 256 * 256;  // the same for every call
 __host__ __device__ inline int64_t ws_part_floats(int hd) { return (int64_t)kRows * (hd + 2); }
 
 // Units of a request; a length out of range counts as none.
@@ -150,10 +166,78 @@ __device__ __forceinline__ void walk_next(Walk& w, const PagedAttnArgs& a, int n
 __device__ __forceinline__ int share_count(int64_t total, int n_ctas) { return (int)min(total, (int64_t)n_ctas); }
 __device__ __forceinline__ int64_t share_begin(int64_t total, int c, int n) { return total * c / n; }
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD>::kCtas)
+// The share that holds unit x: the largest c with share_begin(c) <= x.
+__device__ __forceinline__ int share_of(int64_t x, int64_t total, int n) {
+  int c = (int)min((x * n) / total, (int64_t)n - 1);
+  while (c + 1 < n && share_begin(total, c + 1, n) <= x) ++c;
+  while (share_begin(total, c, n) > x) --c;
+  return c;
+}
+
+// Joins `count` partials in shared-memory order of `s_part` (their addresses):
+// weights first, then every thread four dims of a row at a time.  final: the
+// result goes to o and lse, else it replaces the first partial.  A sum below 0
+// marks a piece that met a bad page; it spoils the whole.  All threads.
+template <typename T, int HD, int R>
+__device__ void join_parts(const PagedAttnArgs& a, float* const* s_part, int count, int rows, bool final, T* o, float* lse,
+                           float (*s_w)[R], float2* s_ml, int* s_flag) {
+  const int tid = threadIdx.x;
+  if (tid == 0) *s_flag = 0;
+  __syncthreads();
+  if (tid < rows) {
+    float m = -INFINITY;
+    for (int i = 0; i < count; ++i) m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(s_part[i]) + tid).x);
+    const float z = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    bool bad = false;
+    for (int i = 0; i < count; ++i) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(s_part[i]) + tid);
+      const float c = ex2(ml.x - z);
+      bad |= ml.y < 0.f;
+      l = fmaf(ml.y, c, l);
+      s_w[i][tid] = c;
+    }
+    s_ml[tid] = make_float2(m, l);
+    if (bad) *s_flag = 1;
+  }
+  __syncthreads();
+  const bool bad = *s_flag != 0;
+  for (int i = tid; i < rows * HD / 4; i += kWarps * 32) {
+    const int row = i / (HD / 4);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int p = 0; p < count; ++p) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(s_part[p] + 2 * kRows) + i);
+      const float c = s_w[p][row];
+      acc.x = fmaf(x.x, c, acc.x);
+      acc.y = fmaf(x.y, c, acc.y);
+      acc.z = fmaf(x.z, c, acc.z);
+      acc.w = fmaf(x.w, c, acc.w);
+    }
+    if (!final) {
+      reinterpret_cast<float4*>(s_part[0] + 2 * kRows)[i] = acc;  // read by this thread alone
+    } else if (!bad) {
+      const float l = s_ml[row].y, f = l == 0.f ? 0.f : 1.f / l;
+      T* dst = o + i * 4;
+      store_as(dst, acc.x * f);
+      store_as(dst + 1, acc.y * f);
+      store_as(dst + 2, acc.z * f);
+      store_as(dst + 3, acc.w * f);
+    }
+  }
+  if (tid < rows) {
+    const float2 ml = s_ml[tid];
+    if (!final)
+      reinterpret_cast<float2*>(s_part[0])[tid] = make_float2(ml.x, bad ? -1.f : ml.y);
+    else if (!bad && lse)
+      lse[tid] = fmaf(ml.x, kLn2, logf(ml.y));
+  }
+}
+
+template <typename T, int HD, int R>
+__global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD, R>::kCtas)
     paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, int n_groups, float scale_log2) {
-  using C = Cfg<T, HD>;
+  using C = Cfg<T, HD, R>;
   constexpr bool kF32 = sizeof(T) == 4;
   constexpr int kSteps = C::kChunks / 2;  // MMA steps over the head's dims (two chunks each)
   constexpr int kTiles = HD / 8;          // n8 tiles of the output
@@ -161,64 +245,79 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD>::kCtas)
   __shared__ int64_t s_scan[kWarps];
   __shared__ Walk s_walk;
   __shared__ uint8_t s_bad[kWarps][C::kStages];
-  __shared__ int s_segbad[2];
+  __shared__ int s_segbad[2], s_last, s_flag;
+  __shared__ float* s_part[kMaxJoin];
+  __shared__ float s_w[kMaxJoin][R];
+  __shared__ float2 s_ml[R];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int P = a.c.page_size, cap = a.max_pages * P;
   const int G = a.nh / a.c.nkv, nv = a.c.nkv * n_groups;
-  int64_t* ws_units = static_cast<int64_t*>(a.ws);
-  float* ws_part = reinterpret_cast<float*>(static_cast<unsigned char*>(a.ws) + ws_part_offset(a.n_req));
+  unsigned* counters = static_cast<unsigned*>(a.ws);
+  float* ws_part = reinterpret_cast<float*>(static_cast<unsigned char*>(a.ws) + kPartOffset);
 
   pdl_trigger();
   pdl_wait();
 
-  // ---- this CTA's share: total units, then the request its first unit lies in
+  // ---- this CTA's share: thread t counts the units of `per` neighbouring
+  // requests; a scan gives the total and the request of the share's first unit
   if (tid < 2) s_segbad[tid] = 0;
+  const int per = (a.n_req + kWarps * 32 - 1) / (kWarps * 32), r_lo = min(tid * per, a.n_req), r_hi = min(r_lo + per, a.n_req);
   int64_t mine = 0;
-  for (int r = tid; r < a.n_req; r += kWarps * 32) mine += units_of(a.len[r], cap);
+#pragma unroll 4
+  for (int r = r_lo; r < r_hi; ++r) mine += units_of(a.len[r], cap);
+  int64_t incl = mine;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) s_scan[warp] = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_scan[warp] = incl;
   __syncthreads();
-  int64_t total = 0;
+  int64_t total = 0, before = incl - mine;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) total += s_scan[i];
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < warp) before += s_scan[i];
+    total += s_scan[i];
+  }
   total *= nv;
-  if (blockIdx.x == 0 && tid == 0) ws_units[0] = total;
-  const int n_shares = share_count(total, gridDim.x);
-  if ((int)blockIdx.x >= n_shares) return;
-  const int64_t begin = share_begin(total, blockIdx.x, n_shares);
-  const int count = (int)(share_begin(total, blockIdx.x + 1, n_shares) - begin);
-  {
-    // warp 0 scans the requests 32 at a time until the first unit is reached
-    if (warp == 0) {
-      int64_t base = 0;
-      for (int r0 = 0; r0 < a.n_req; r0 += 32) {
-        const int len = len_at(a, r0 + lane);
-        const int64_t own = r0 + lane < a.n_req ? (int64_t)units_of(len, cap) * nv : 0;
-        int64_t incl = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += y;
-        }
-        const int64_t lo = base + incl - own;
-        const bool here = begin >= lo && begin < lo + own;
-        if (here) {
-          const int units = units_of(len, cap);
-          const int off = (int)(begin - lo);
-          s_walk.r = r0 + lane;
-          s_walk.v = off / units;
-          s_walk.u = off - s_walk.v * units;
-          s_walk.units = units;
-          s_walk.len = len;
-          s_walk.next_len = len_at(a, r0 + lane + 1);
-        }
-        if (__any_sync(0xffffffffu, here)) break;
-        base += __shfl_sync(0xffffffffu, incl, 31);
+  // rows of requests without units: zeros for a length of 0, an error for one out of range
+  auto idle_requests = [&] {
+    for (int r = blockIdx.x; r < a.n_req; r += gridDim.x) {
+      const int len = a.len[r];
+      if (len == 0) {
+        for (int i = tid; i < a.nh * HD; i += kWarps * 32) store_as(static_cast<T*>(a.o) + (int64_t)r * a.o_stride + i, 0.f);
+        if (a.lse)
+          for (int i = tid; i < a.nh; i += kWarps * 32) a.lse[(int64_t)r * a.nh + i] = -INFINITY;
+      } else if ((len < 0 || len > cap) && tid == 0) {
+        set_error(a.status, MINFER_ERR_POS_OOB);
       }
     }
-    __syncthreads();
+  };
+  const int n_shares = share_count(total, gridDim.x);
+  if ((int)blockIdx.x >= n_shares) {
+    idle_requests();
+    return;
   }
+  const int64_t begin = share_begin(total, blockIdx.x, n_shares);
+  const int count = (int)(share_begin(total, blockIdx.x + 1, n_shares) - begin);
+  if (begin >= before * nv && begin < (before + mine) * nv) {
+    int64_t at = before * nv;
+    for (int r = r_lo; r < r_hi; ++r) {
+      const int len = a.len[r], units = units_of(len, cap);
+      if (begin < at + (int64_t)units * nv) {
+        const int off = (int)(begin - at);
+        s_walk.r = r;
+        s_walk.v = off / units;
+        s_walk.u = off - s_walk.v * units;
+        s_walk.units = units;
+        s_walk.len = len;
+        s_walk.next_len = len_at(a, r + 1);
+        break;
+      }
+      at += (int64_t)units * nv;
+    }
+  }
+  __syncthreads();
   Walk cw = s_walk;  // the unit being computed
   Walk lw = cw;      // the unit being loaded
 
@@ -275,8 +374,8 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD>::kCtas)
 
   // ---- one (request, head block) after another
   unsigned char* qs = smem + kWarps * C::kStages * C::kStageBytes;
-  float* m_out = reinterpret_cast<float*>(qs + C::kQBytes);  // [warp][kRows][HD]
-  float2* m_ml = reinterpret_cast<float2*>(m_out + kWarps * kRows * HD);  // [warp][kRows]
+  float* m_out = reinterpret_cast<float*>(qs + C::kQBytes);           // [warp][R][HD]
+  float2* m_ml = reinterpret_cast<float2*>(m_out + kWarps * R * HD);  // [warp][R]
   const int g4 = lane >> 2, t4 = lane & 3;
   int stage = 0, seg = 0;
   for (int done = 0; done < count;) {
@@ -476,15 +575,16 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD>::kCtas)
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
     if (t4 == 0) {
-      m_ml[warp * kRows + g4] = make_float2(m0, l0);
-      m_ml[warp * kRows + g4 + 8] = make_float2(m1, l1);
+      m_ml[warp * R + g4] = make_float2(m0, l0);
+      if constexpr (R > 8) m_ml[warp * R + g4 + 8] = make_float2(m1, l1);
     }
-    float* mo = m_out + warp * kRows * HD;
+    float* mo = m_out + warp * R * HD;
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) {
       const int d = n * 8 + t4 * 2;
       if (g4 < rows) *reinterpret_cast<float2*>(mo + g4 * HD + d) = make_float2(o[n][0], o[n][1]);
-      if (g4 + 8 < rows) *reinterpret_cast<float2*>(mo + (g4 + 8) * HD + d) = make_float2(o[n][2], o[n][3]);
+      if constexpr (R > 8)
+        if (g4 + 8 < rows) *reinterpret_cast<float2*>(mo + (g4 + 8) * HD + d) = make_float2(o[n][2], o[n][3]);
     }
     if (bad && lane == 0) s_segbad[seg & 1] = 1;
     __syncthreads();
@@ -492,21 +592,19 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD>::kCtas)
     const bool whole = from_start && to_end;
     if (seg_bad && tid == 0) set_error(a.status, MINFER_ERR_POS_OOB);
     float* part = ws_part + (int64_t)(blockIdx.x * 2 + (from_start ? 1 : 0)) * ws_part_floats(HD);
-    if (from_start && cw.v == 0 && tid == 0)
-      ws_units[1 + r] = begin + (done - seg_units);  // the request's first unit
     for (int i = tid; i < rows * HD; i += kWarps * 32) {
       const int row = i / HD, d = i % HD;
       float m = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, m_ml[w * kRows + row].x);
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, m_ml[w * R + row].x);
       const float z = m == -INFINITY ? 0.f : m;
       float l = 0.f, acc = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float2 ml = m_ml[w * kRows + row];
+        const float2 ml = m_ml[w * R + row];
         const float c = ex2(ml.x - z);
         l = fmaf(ml.y, c, l);
-        acc = fmaf(m_out[w * kRows * HD + i], c, acc);
+        acc = fmaf(m_out[w * R * HD + i], c, acc);
       }
       if (whole) {
         if (!seg_bad) {
@@ -518,117 +616,76 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD>::kCtas)
         part[2 * kRows + i] = acc;
       }
     }
-    // flag of the segment after the next, free since the barrier above
+    // flag of the next piece, free since the barrier above
     if (tid == 0) s_segbad[(seg + 1) & 1] = 0;
     __syncthreads();
     ++seg;
+    if (!whole) {
+      // the shares c0..c1 that hold this (request, head block), and their groups
+      const int64_t first = begin + (done - seg_units) - cw.u, last = first + cw.units - 1;
+      const int c0 = share_of(first, total, n_shares), c1 = share_of(last, total, n_shares);
+      const int g = blockIdx.x / kGroup, g0 = c0 / kGroup, g1 = c1 / kGroup;
+      const int lo = max(c0, g * kGroup), hi = min(c1, g * kGroup + kGroup - 1);
+      T* o_row = static_cast<T*>(a.o) + (int64_t)r * a.o_stride + (int64_t)head0 * HD;
+      float* lse_row = a.lse ? a.lse + (int64_t)r * a.nh + head0 : nullptr;
+      auto slot = [&](int c) { return ws_part + (int64_t)(c * 2 + (c == c0 ? 1 : 0)) * ws_part_floats(HD); };
+      // whether this CTA is the last of n to come to counter `at` (then zero again)
+      auto arrive = [&](int at, int n) {
+        if (n == 1) return true;
+        if (tid == 0) {
+          __threadfence();  // this CTA's partial, complete since the barrier above
+          s_last = atomicAdd(counters + at, 1u) == (unsigned)n - 1;
+          if (s_last) counters[at] = 0;
+          __threadfence();
+        }
+        __syncthreads();
+        return s_last != 0;
+      };
+      if (arrive(c0 >= g * kGroup ? c0 : (int)gridDim.x + g, hi - lo + 1)) {
+        if (hi > lo) {
+          if (tid <= hi - lo) s_part[tid] = slot(lo + tid);
+          join_parts<T, HD, R>(a, s_part, hi - lo + 1, rows, g0 == g1, o_row, lse_row, s_w, s_ml, &s_flag);
+        }
+        if (g0 != g1) {
+          __syncthreads();
+          if (arrive((int)gridDim.x + (int)gridDim.x / kGroup + 1 + c0, g1 - g0 + 1)) {
+            if (tid <= g1 - g0) s_part[tid] = slot(max(c0, (g0 + tid) * kGroup));
+            join_parts<T, HD, R>(a, s_part, g1 - g0 + 1, rows, true, o_row, lse_row, s_w, s_ml, &s_flag);
+          }
+        }
+      }
+      __syncthreads();  // s_last and the join's arrays are used again
+    }
     // on to the next (request, head block)
     cw.u = cw.units - 1;
     walk_next(cw, a, nv, cap);
   }
+  idle_requests();
 }
 
-// Adds up the partials of (request, query head)s whose units lie in more than
-// one share, and writes the rows of empty requests.  One CTA per (request,
-// query head): thread (g, d) takes partials g, g + kJoin, ... of dim d.
-constexpr int kJoin = 4;
-template <typename T, int HD>
-__global__ void __launch_bounds__(kJoin* HD) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, int n_groups, int n_ctas) {
-  __shared__ float s_m[kJoin], s_l[kJoin], s_o[kJoin][HD];
-  __shared__ int s_bad;
-  const int r = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, d = tid % HD, g = tid / HD;
-  const int G = a.nh / a.c.nkv, kvh = h / G, in = h - kvh * G, grp = in / kRows, row = in % kRows;
-  if (tid == 0) s_bad = 0;
-  pdl_trigger();
-  pdl_wait();
-  const int cap = a.max_pages * a.c.page_size;
-  const int len = a.len[r];
-  T* out = static_cast<T*>(a.o) + (int64_t)r * a.o_stride + (int64_t)h * HD;
-  if (len <= 0 || len > cap) {
-    if (len == 0) {
-      if (g == 0) store_as(out + d, 0.f);
-      if (tid == 0 && a.lse) a.lse[(int64_t)r * a.nh + h] = -INFINITY;
-    } else if (tid == 0) {
-      set_error(a.status, MINFER_ERR_POS_OOB);
-    }
-    return;
-  }
-  const int64_t* ws_units = static_cast<const int64_t*>(a.ws);
-  const float* ws_part = reinterpret_cast<const float*>(static_cast<const unsigned char*>(a.ws) + ws_part_offset(a.n_req));
-  const int64_t total = ws_units[0];
-  const int n_shares = share_count(total, n_ctas);
-  const int units = units_of(len, cap);
-  const int64_t first = ws_units[1 + r] + (int64_t)(kvh * n_groups + grp) * units, last = first + units - 1;
-  // the share that holds unit x: the largest c with share_begin(c) <= x
-  auto share_of = [&](int64_t x) {
-    int c = (int)min((x * n_shares) / total, (int64_t)n_shares - 1);
-    while (c + 1 < n_shares && share_begin(total, c + 1, n_shares) <= x) ++c;
-    while (share_begin(total, c, n_shares) > x) --c;
-    return c;
-  };
-  const int c0 = share_of(first), c1 = share_of(last);
-  if (c0 == c1) return;  // finished by the share that holds it
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  bool bad = false;
-  __syncthreads();  // s_bad is set
-  for (int c = c0 + g; c <= c1; c += kJoin) {
-    // a share that begins inside this head's units has it as its first piece
-    const int which = share_begin(total, c, n_shares) > first ? 0 : 1;
-    const float* part = ws_part + (int64_t)(c * 2 + which) * ws_part_floats(HD);
-    const float2 ml = reinterpret_cast<const float2*>(part)[row];
-    const float x = part[2 * kRows + row * HD + d];
-    bad |= ml.y < 0.f;
-    const float mn = fmaxf(m, ml.x), z = mn == -INFINITY ? 0.f : mn;
-    const float ca = ex2(m - z), cb = ex2(ml.x - z);
-    l = fmaf(l, ca, ml.y * cb);
-    o = fmaf(o, ca, x * cb);
-    m = mn;
-  }
-  if (bad) s_bad = 1;
-  if (d == 0) {
-    s_m[g] = m;
-    s_l[g] = l;
-  }
-  s_o[g][d] = o;
-  __syncthreads();
-  if (g != 0 || s_bad) return;
-  m = s_m[0];
-#pragma unroll
-  for (int i = 1; i < kJoin; ++i) m = fmaxf(m, s_m[i]);
-  const float z = m == -INFINITY ? 0.f : m;
-  l = o = 0.f;
-#pragma unroll
-  for (int i = 0; i < kJoin; ++i) {
-    const float c = ex2(s_m[i] - z);
-    l = fmaf(s_l[i], c, l);
-    o = fmaf(s_o[i][d], c, o);
-  }
-  store_as(out + d, l == 0.f ? 0.f : o / l);
-  if (d == 0 && a.lse) a.lse[(int64_t)r * a.nh + h] = fmaf(m, kLn2, logf(l));
+int shares(int hd, int type, int num_sms) {
+  return std::min(num_sms * (hd * (type == MINFER_F32 ? 4 : 2) == 512 ? 1 : 2), kMaxShares);
 }
 
-int row_bytes(int hd, int type) { return hd * (type == MINFER_F32 ? 4 : 2); }
-int shares(int hd, int type, int num_sms) { return num_sms * (row_bytes(hd, type) == 512 ? 1 : 2); }
-
+template <typename T, int HD, int R>
+cudaError_t launch(const PagedAttnArgs& a, int n, int n_groups, cudaStream_t st) {
+  using C = Cfg<T, HD, R>;
+  auto kernel = paged_attn_kernel<T, HD, R>;
+  cudaError_t e = allow_smem<paged_attn_kernel<T, HD, R>>(C::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3((unsigned)n), dim3(kWarps * 32), C::kSmem, st, a, n_groups, a.scale * kLog2e);
+}
 template <typename T, int HD>
 cudaError_t launch(const PagedAttnArgs& a, int type, int num_sms, cudaStream_t st) {
-  using C = Cfg<T, HD>;
-  const int G = a.nh / a.c.nkv, n_groups = (G + kRows - 1) / kRows;
-  const int n = shares(HD, type, num_sms);
-  auto kernel = paged_attn_kernel<T, HD>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(kernel, dim3((unsigned)n), dim3(kWarps * 32), C::kSmem, st, a, n_groups, a.scale * kLog2e);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(paged_join_kernel<T, HD>, dim3((unsigned)a.n_req, (unsigned)a.nh), dim3(kJoin * HD), 0, st, a, n_groups, n);
+  const int G = a.nh / a.c.nkv, n_groups = (G + kRows - 1) / kRows, n = shares(HD, type, num_sms);
+  return G <= 8 ? launch<T, HD, 8>(a, n, n_groups, st) : launch<T, HD, 16>(a, n, n_groups, st);
 }
 
 }  // namespace
 
-int64_t paged_attn_workspace(int n_req, int nh, int nkv, int hd, int type, int num_sms) {
-  (void)nh;
-  (void)nkv;
-  return ws_part_offset(n_req) + (int64_t)shares(hd, type, num_sms) * 2 * ws_part_floats(hd) * 4;
+int64_t paged_attn_workspace(int hd, int type, int num_sms) {
+  const int n = shares(hd, type, num_sms);
+  return kPartOffset + (int64_t)n * 2 * ws_part_floats(hd) * 4;
 }
 
 cudaError_t paged_attn_launch(const PagedAttnArgs& a, int type, int num_sms, cudaStream_t st) {

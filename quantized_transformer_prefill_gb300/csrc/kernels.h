@@ -30,6 +30,21 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// Let a kernel use `bytes` of dynamic shared memory on the current device: asked
+// for once per kernel and device (the call costs as much as a launch).
+template <auto kernel>
+cudaError_t allow_smem(int bytes) {
+  constexpr int kMaxDevices = 64;
+  static bool done[kMaxDevices];  // every thread writes the same value
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < kMaxDevices && __atomic_load_n(&done[dev], __ATOMIC_RELAXED)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < kMaxDevices) __atomic_store_n(&done[dev], true, __ATOMIC_RELAXED);
+  return e;
+}
+
 // ---------------------------------------------------------------- layouts
 //
 // GEMM operand planes (tensor-core path):
@@ -376,7 +391,7 @@ struct PagedAttnArgs {
   void* ws;
   int* status;
 };
-int64_t paged_attn_workspace(int n_req, int nh, int nkv, int hd, int type, int num_sms);
+int64_t paged_attn_workspace(int hd, int type, int num_sms);
 cudaError_t paged_attn_launch(const PagedAttnArgs& a, int type, int num_sms, cudaStream_t stream);
 
 // k_logprobs.cu: log probabilities, entropy and top k of logits rows.
