@@ -36,7 +36,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kChunk = 512;         // logits of a chunk
 constexpr int kPer = kChunk / 32;   // logits of a lane
-constexpr int kCtasPerSm = 24;
+constexpr int kCtasPerSm = 4;       // resident
+constexpr int kWaves = 4;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -186,7 +187,7 @@ struct Loader<__nv_bfloat16> {
 
 // How rows are cut, and where the workspace holds what: a counter per row (zero
 // between calls; only rows of several parts have one, and there are fewer than
-// num_sms * kCtasPerSm of those, so their place is the same in every call), a
+// num_sms * kCtasPerSm * kWaves of those, so their place is the same in every call), a
 // Stat per part, the largest key32 of every chunk.
 struct Plan {
   int chunks;  // of a row, at the worst alignment
@@ -221,7 +222,7 @@ __device__ __forceinline__ void load_chunk(const T* x, int head, int64_t vocab, 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constant__ LogprobsArgs a, const Plan plan) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __grid_constant__ LogprobsArgs a, const Plan plan) {
   using L = Loader<T>;
   constexpr int V = L::kVec;
   __shared__ uint64_t s_list[kWarps * 32];
@@ -260,9 +261,26 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
     t = c * fmaf(-d, s, t);
     s *= c;
   };
-  for (int c = part * plan.per + warp; c < c1; c += kWarps) {
+  constexpr int U = kPer / V;
+  // the next chunk's vectors are on their way while this one's are worked on
+  uint4 next[U];
+  auto inside = [&](int c) { return c > 0 && (int64_t)(c + 1) * kChunk - head <= a.vocab; };
+  auto fetch = [&](int c) {
+    const uint4* p = reinterpret_cast<const uint4*>(x + ((int64_t)c * kChunk - head)) + lane;
+#pragma unroll
+    for (int i = 0; i < U; ++i) next[i] = __ldcg(p + i * 32);
+  };
+  int c = part * plan.per + warp;
+  if (c < c1 && inside(c)) fetch(c);
+  for (; c < c1; c += kWarps) {
     float f[kPer];
-    load_chunk<T>(x, head, a.vocab, c, f);
+    if (inside(c)) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) L::get(next[i], f + i * V);
+    } else {
+      load_chunk<T>(x, head, a.vocab, c, f);
+    }
+    if (c + kWarps < c1 && inside(c + kWarps)) fetch(c + kWarps);
     float top = f[0];
 #pragma unroll
     for (int i = 1; i < kPer; ++i) top = max_nan(top, f[i]);
@@ -373,16 +391,18 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
   }
 }
 
-// Parts of a row: about kCtasPerSm CTAs per SM (four rounds of what is resident,
-// so the last round's idle share is small), none with less than a chunk per warp.
+// Parts of a row: with fewer rows than the GPU holds CTAs, as many as fill it
+// once; with more, so many that it is filled kWaves times, which keeps the last
+// round's idle share small.  None has less than a chunk per warp.
 Plan plan_of(int64_t rows, int64_t vocab, int vec, int k, int num_sms) {
   Plan p;
   p.chunks = (int)((vocab + vec - 1 + kChunk - 1) / kChunk);
-  const int64_t want = std::max<int64_t>(1, ((int64_t)num_sms * kCtasPerSm + rows - 1) / rows);
+  const int64_t resident = (int64_t)num_sms * kCtasPerSm;
+  const int64_t want = rows <= resident ? resident / rows : (resident * kWaves + rows - 1) / rows;
   const int64_t parts = std::min<int64_t>(want, (p.chunks + kWarps - 1) / kWarps);
   p.per = (int)((p.chunks + parts - 1) / parts);
   p.parts = (p.chunks + p.per - 1) / p.per;
-  p.stats = ((int64_t)num_sms * kCtasPerSm * 4 + 15) / 16 * 16;
+  p.stats = ((int64_t)num_sms * kCtasPerSm * kWaves * 4 + 15) / 16 * 16;
   p.keys = p.stats + rows * p.parts * 16;
   p.bytes = p.keys + (k > 0 ? rows * p.chunks * 4 : 0);
   return p;

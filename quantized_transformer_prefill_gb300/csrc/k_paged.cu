@@ -266,22 +266,43 @@ __device__ __forceinline__ void turn_cos_sin(uint64_t f, float* c, float* s) {
   *s = (quad >= 2) ? -ss : ss;
 }
 
-constexpr int kRpWarps = 8;
-constexpr int kRpHeads = 5;  // heads of a warp whose loads are in flight together
+constexpr int kRpHeads = 4;      // heads of a warp whose loads are in flight together
+constexpr int kRpMaxWarps = 16;
 
-// One CTA per token; warp w takes heads w, w + 8, ... of Q, K and V, lane l the
-// head's elements l*E..l*E+E-1.
+// One CTA per token, kRpHeads heads per warp: warp w of n takes heads w, w + n,
+// ... of Q, K and V, lane l the head's elements l*E..l*E+E-1.  The row, the
+// bias, the position and the slot are all loaded before the first of them is
+// looked at.
 template <typename TS, typename TD, int HD>
-__global__ void __launch_bounds__(kRpWarps * 32) rope_paged_kernel(const __grid_constant__ RopePagedArgs a) {
+__global__ void __launch_bounds__(kRpMaxWarps * 32, 2) rope_paged_kernel(const __grid_constant__ RopePagedArgs a) {
   constexpr int E = HD / 32;
   using VS = Vec<TS, E>;
   using VD = Vec<TD, E>;
   using VF = Vec<float, E>;
   __shared__ float s_cos[HD / 2], s_sin[HD / 2];
-  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  const int nqk = a.nh + a.c.nkv, heads = nqk + a.c.nkv;
+  const TS* row = static_cast<const TS*>(a.qkv) + (int64_t)t * a.row_stride + lane * E;
   pdl_trigger();
   pdl_wait();
+  VS x[kRpHeads];
+  VF b[kRpHeads];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < kRpHeads; ++i) {
+      const int h = h0 + i * warps;
+      if (h < heads) x[i] = *reinterpret_cast<const VS*>(row + (int64_t)h * HD);
+    }
+    if (a.bias) {
+#pragma unroll
+      for (int i = 0; i < kRpHeads; ++i) {
+        const int h = h0 + i * warps;
+        if (h < heads) b[i] = *reinterpret_cast<const VF*>(a.bias + (int64_t)h * HD + lane * E);
+      }
+    }
+  };
   const int slot = a.slot[t], pos = a.pos[t];
+  load(warp);
   if (slot < 0) return;  // padding
   if (slot >= a.c.n_pages * a.c.page_size || pos < 0) {
     if (tid == 0) set_error(a.status, MINFER_ERR_POS_OOB);
@@ -289,40 +310,28 @@ __global__ void __launch_bounds__(kRpWarps * 32) rope_paged_kernel(const __grid_
   }
   const int rot = a.rope.rot_dim, half = rot >> 1;
   const bool inter = a.rope.style == MINFER_ROPE_INTERLEAVED;
-  const int nqk = a.nh + a.c.nkv, heads = nqk + a.c.nkv;
-  const TS* row = static_cast<const TS*>(a.qkv) + (int64_t)t * a.row_stride;
   const int page = slot / a.c.page_size;
   const int64_t at = (int64_t)page * a.c.page_stride + (int64_t)(slot - page * a.c.page_size) * a.c.row_stride;
+  for (int i = tid; i < half; i += blockDim.x) {
+    float c, s;
+    turn_cos_sin((uint64_t)(uint32_t)pos * a.rope.turn[i], &c, &s);
+    s_cos[i] = c * a.rope.mscale;
+    s_sin[i] = s * a.rope.mscale;
+  }
+  __syncthreads();
 
-  bool first = true;
-  for (int h0 = warp; first || h0 < heads; h0 += kRpWarps * kRpHeads) {
-    VS x[kRpHeads];
+  for (int h0 = warp; h0 < heads; h0 += warps * kRpHeads) {
+    if (h0 != warp) load(h0);
 #pragma unroll
     for (int i = 0; i < kRpHeads; ++i) {
-      const int h = h0 + i * kRpWarps;
-      if (h < heads) x[i] = *reinterpret_cast<const VS*>(row + (int64_t)h * HD + lane * E);
-    }
-    if (first) {
-      if (tid < half) {
-        float c, s;
-        turn_cos_sin((uint64_t)(uint32_t)pos * a.rope.turn[tid], &c, &s);
-        s_cos[tid] = c * a.rope.mscale;
-        s_sin[tid] = s * a.rope.mscale;
-      }
-      __syncthreads();
-      first = false;
-    }
-#pragma unroll
-    for (int i = 0; i < kRpHeads; ++i) {
-      const int h = h0 + i * kRpWarps;
+      const int h = h0 + i * warps;
       if (h >= heads) break;
       float y[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) y[e] = to_f32<TS>(x[i].v[e]);
       if (a.bias) {
-        const VF b = *reinterpret_cast<const VF*>(a.bias + (int64_t)h * HD + lane * E);
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] += b.v[e];
+        for (int e = 0; e < E; ++e) y[e] += b[i].v[e];
       }
       if (h < nqk) {
         if (a.q_norm) {
@@ -385,9 +394,10 @@ __global__ void __launch_bounds__(kRpWarps * 32) rope_paged_kernel(const __grid_
 
 template <typename TS, typename TD>
 cudaError_t rope_paged_typed(const RopePagedArgs& a, cudaStream_t st) {
-  if (a.c.hd == 64)
-    return launch_pdl(rope_paged_kernel<TS, TD, 64>, dim3((unsigned)a.n_tokens), dim3(kRpWarps * 32), 0, st, a);
-  return launch_pdl(rope_paged_kernel<TS, TD, 128>, dim3((unsigned)a.n_tokens), dim3(kRpWarps * 32), 0, st, a);
+  const int heads = a.nh + 2 * a.c.nkv, warps = (heads + kRpHeads - 1) / kRpHeads;
+  const dim3 grid((unsigned)a.n_tokens), block(32 * (unsigned)(warps < kRpMaxWarps ? warps : kRpMaxWarps));
+  if (a.c.hd == 64) return launch_pdl(rope_paged_kernel<TS, TD, 64>, grid, block, 0, st, a);
+  return launch_pdl(rope_paged_kernel<TS, TD, 128>, grid, block, 0, st, a);
 }
 
 }  // namespace

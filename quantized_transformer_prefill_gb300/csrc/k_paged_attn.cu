@@ -9,11 +9,13 @@
 // requests load every SM alike, without the host knowing a length.  A CTA
 // walks its share as a stream: a (request, KV head) that lies inside it is
 // finished there; one that crosses a share's border leaves a partial (max,
-// sum, unnormalized output) in the workspace.  Partials are joined in a tree of
-// two levels: the CTA that finishes last among the (up to 16) neighbouring
-// shares of a group joins the group's partials, the one that finishes last
-// among the groups joins those.  Who is last decides only who adds, never in
-// what order, so the result does not depend on it.
+// sum, unnormalized output) in the workspace.  The CTA that finishes last among
+// the shares of a (request, KV head) joins the partials; where there are more
+// than kDirect of them, in a tree of two levels: first the last one of each
+// group of neighbouring shares, then the last one of the groups.  Who is last
+// decides only who adds, never in what order, so the result does not depend on
+// it.  A CTA reports its (at most two) partials after its last unit, so that no
+// unit waits for a fence.
 //
 // Inside a CTA each of four warps takes 16 of a unit's 64 keys, copies their
 // K and V rows into its own ring in shared memory (cp.async of 16 bytes, page
@@ -40,7 +42,8 @@ constexpr int kRows = 16;               // query heads of one MMA tile
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 constexpr int kGroup = 16;              // neighbouring shares whose partials are joined first
-constexpr int kMaxJoin = 64;            // partials of one join: kGroup, or the number of groups
+constexpr int kMaxJoin = 64;            // partials of one join: kDirect, kGroup, or the number of groups
+constexpr int kDirect = 32;             // partials that are joined in one step
 
 // R: query heads that a CTA carries through the join (8 where a KV head has no
 // more, which leaves room for another stage of the ring).
@@ -50,15 +53,15 @@ struct Cfg {
   static constexpr int kChunks = kRowBytes / 16;  // 16-byte chunks of a row
   static constexpr int kStageBytes = 2 * kKeys * kRowBytes;  // K and V rows of one warp
   static constexpr int kQBytes = sizeof(T) == 4 ? 2 * kRows * kRowBytes : 0;  // tf32 hi and lo of Q
-  static constexpr int kMergeBytes = kWarps * R * HD * 4 + kWarps * R * 8;
   // two CTAs per SM, or one where two stages of the ring do not fit twice; the
   // ring takes what is left of the SM's shared memory
   static constexpr int kCtas = kRowBytes == 512 ? 1 : 2;
-  static constexpr int kBudget = kCtas == 1 ? 230000 : 113400;
-  static constexpr int kFit = (kBudget - kQBytes - kMergeBytes) / (kWarps * kStageBytes);
+  static constexpr int kBudget = kCtas == 1 ? 222000 : R == 8 ? 109400 : 105000;
+  static constexpr int kFit = (kBudget - kQBytes) / (kWarps * kStageBytes);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
-  static constexpr int kSmem = kWarps * kStages * kStageBytes + kQBytes + kMergeBytes;
+  static constexpr int kSmem = kWarps * kStages * kStageBytes + kQBytes;
   static_assert(kStages >= 2, "a ring has two stages at least");
+  static_assert(R * HD * 4 <= kStageBytes, "a warp's output fits the stage it has just used");
 };
 
 // The workspace: counters (zero between calls; one per share for a piece that
@@ -174,50 +177,60 @@ __device__ __forceinline__ int share_of(int64_t x, int64_t total, int n) {
   return c;
 }
 
-// Joins `count` partials in shared-memory order of `s_part` (their addresses):
-// weights first, then every thread four dims of a row at a time.  final: the
-// result goes to o and lse, else it replaces the first partial.  A sum below 0
-// marks a piece that met a bad page; it spoils the whole.  All threads.
+// What the threads of a CTA share while they join partials.
+template <int R>
+struct JoinShared {
+  float* part[kMaxJoin];    // the partials, in the order of their shares
+  float2 ml[kMaxJoin][R];   // their (max, sum); then .x the weight
+  float2 out[R];            // the joined (max, sum)
+  int bad;
+};
+
+// Joins `count` partials: weights first, then every thread four dims of a row at
+// a time.  final: the result goes to o and lse, else it replaces the first
+// partial.  A sum below 0 marks a piece that met a bad page; it spoils the
+// whole.  All threads; s.part is written before a barrier of the caller's.
 template <typename T, int HD, int R>
-__device__ void join_parts(const PagedAttnArgs& a, float* const* s_part, int count, int rows, bool final, T* o, float* lse,
-                           float (*s_w)[R], float2* s_ml, int* s_flag) {
+__device__ void join_parts(JoinShared<R>& s, int count, int rows, bool final, T* o, float* lse) {
   const int tid = threadIdx.x;
-  if (tid == 0) *s_flag = 0;
+  for (int i = tid; i < count * R; i += kWarps * 32)
+    if (i % R < rows) s.ml[i / R][i % R] = __ldcg(reinterpret_cast<const float2*>(s.part[i / R]) + i % R);
+  if (tid == 0) s.bad = 0;
   __syncthreads();
   if (tid < rows) {
     float m = -INFINITY;
-    for (int i = 0; i < count; ++i) m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(s_part[i]) + tid).x);
+    for (int i = 0; i < count; ++i) m = fmaxf(m, s.ml[i][tid].x);
     const float z = m == -INFINITY ? 0.f : m;
     float l = 0.f;
     bool bad = false;
     for (int i = 0; i < count; ++i) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(s_part[i]) + tid);
+      const float2 ml = s.ml[i][tid];
       const float c = ex2(ml.x - z);
       bad |= ml.y < 0.f;
       l = fmaf(ml.y, c, l);
-      s_w[i][tid] = c;
+      s.ml[i][tid].x = c;
     }
-    s_ml[tid] = make_float2(m, l);
-    if (bad) *s_flag = 1;
+    s.out[tid] = make_float2(m, l);
+    if (bad) s.bad = 1;
   }
   __syncthreads();
-  const bool bad = *s_flag != 0;
+  const bool bad = s.bad != 0;
   for (int i = tid; i < rows * HD / 4; i += kWarps * 32) {
     const int row = i / (HD / 4);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
     for (int p = 0; p < count; ++p) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(s_part[p] + 2 * kRows) + i);
-      const float c = s_w[p][row];
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(s.part[p] + 2 * kRows) + i);
+      const float c = s.ml[p][row].x;
       acc.x = fmaf(x.x, c, acc.x);
       acc.y = fmaf(x.y, c, acc.y);
       acc.z = fmaf(x.z, c, acc.z);
       acc.w = fmaf(x.w, c, acc.w);
     }
     if (!final) {
-      reinterpret_cast<float4*>(s_part[0] + 2 * kRows)[i] = acc;  // read by this thread alone
+      reinterpret_cast<float4*>(s.part[0] + 2 * kRows)[i] = acc;  // read by this thread alone
     } else if (!bad) {
-      const float l = s_ml[row].y, f = l == 0.f ? 0.f : 1.f / l;
+      const float l = s.out[row].y, f = l == 0.f ? 0.f : 1.f / l;
       T* dst = o + i * 4;
       store_as(dst, acc.x * f);
       store_as(dst + 1, acc.y * f);
@@ -226,13 +239,18 @@ __device__ void join_parts(const PagedAttnArgs& a, float* const* s_part, int cou
     }
   }
   if (tid < rows) {
-    const float2 ml = s_ml[tid];
+    const float2 ml = s.out[tid];
     if (!final)
-      reinterpret_cast<float2*>(s_part[0])[tid] = make_float2(ml.x, bad ? -1.f : ml.y);
+      reinterpret_cast<float2*>(s.part[0])[tid] = make_float2(ml.x, bad ? -1.f : ml.y);
     else if (!bad && lse)
       lse[tid] = fmaf(ml.x, kLn2, logf(ml.y));
   }
 }
+
+// A piece of a (request, head block) that other shares hold pieces of too.
+struct Piece {
+  int r, head0, rows, c0, c1;  // c0..c1: the shares that hold one
+};
 
 template <typename T, int HD, int R>
 __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD, R>::kCtas)
@@ -245,10 +263,9 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD, R>::kCtas)
   __shared__ int64_t s_scan[kWarps];
   __shared__ Walk s_walk;
   __shared__ uint8_t s_bad[kWarps][C::kStages];
-  __shared__ int s_segbad[2], s_last, s_flag;
-  __shared__ float* s_part[kMaxJoin];
-  __shared__ float s_w[kMaxJoin][R];
-  __shared__ float2 s_ml[R];
+  __shared__ int s_segbad[2], s_last[2];
+  __shared__ JoinShared<R> s_join;
+  __shared__ float2 m_ml[kWarps * R];  // the warps' (max, sum) at the end of a piece
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int P = a.c.page_size, cap = a.max_pages * P;
   const int G = a.nh / a.c.nkv, nv = a.c.nkv * n_groups;
@@ -374,8 +391,8 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD, R>::kCtas)
 
   // ---- one (request, head block) after another
   unsigned char* qs = smem + kWarps * C::kStages * C::kStageBytes;
-  float* m_out = reinterpret_cast<float*>(qs + C::kQBytes);           // [warp][R][HD]
-  float2* m_ml = reinterpret_cast<float2*>(m_out + kWarps * R * HD);  // [warp][R]
+  Piece piece[2];  // [1]: the one that starts in this share, [0]: the one that started before
+  piece[0].rows = piece[1].rows = 0;
   const int g4 = lane >> 2, t4 = lane & 3;
   int stage = 0, seg = 0;
   for (int done = 0; done < count;) {
@@ -568,6 +585,11 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD, R>::kCtas)
       }
       if (++stage == C::kStages) stage = 0;
     }
+    // the outputs go to the stage that every warp has just used, which is
+    // filled again only after the barriers below
+    const int used = (stage == 0 ? C::kStages : stage) - 1;
+    float* m_out = reinterpret_cast<float*>(smem + used * C::kStageBytes);  // of warp 0
+    constexpr int kNext = C::kStages * C::kStageBytes / 4;                  // to the next warp's
 
     // ---- join the four warps; write the result or this share's partial
     l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
@@ -578,7 +600,8 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD, R>::kCtas)
       m_ml[warp * R + g4] = make_float2(m0, l0);
       if constexpr (R > 8) m_ml[warp * R + g4 + 8] = make_float2(m1, l1);
     }
-    float* mo = m_out + warp * R * HD;
+    float* mo = m_out + warp * kNext;
+    __syncwarp();
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) {
       const int d = n * 8 + t4 * 2;
@@ -604,7 +627,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD, R>::kCtas)
         const float2 ml = m_ml[w * R + row];
         const float c = ex2(ml.x - z);
         l = fmaf(ml.y, c, l);
-        acc = fmaf(m_out[w * R * HD + i], c, acc);
+        acc = fmaf(m_out[w * kNext + i], c, acc);
       }
       if (whole) {
         if (!seg_bad) {
@@ -621,44 +644,63 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD, R>::kCtas)
     __syncthreads();
     ++seg;
     if (!whole) {
-      // the shares c0..c1 that hold this (request, head block), and their groups
-      const int64_t first = begin + (done - seg_units) - cw.u, last = first + cw.units - 1;
-      const int c0 = share_of(first, total, n_shares), c1 = share_of(last, total, n_shares);
-      const int g = blockIdx.x / kGroup, g0 = c0 / kGroup, g1 = c1 / kGroup;
-      const int lo = max(c0, g * kGroup), hi = min(c1, g * kGroup + kGroup - 1);
-      T* o_row = static_cast<T*>(a.o) + (int64_t)r * a.o_stride + (int64_t)head0 * HD;
-      float* lse_row = a.lse ? a.lse + (int64_t)r * a.nh + head0 : nullptr;
-      auto slot = [&](int c) { return ws_part + (int64_t)(c * 2 + (c == c0 ? 1 : 0)) * ws_part_floats(HD); };
-      // whether this CTA is the last of n to come to counter `at` (then zero again)
-      auto arrive = [&](int at, int n) {
-        if (n == 1) return true;
-        if (tid == 0) {
-          __threadfence();  // this CTA's partial, complete since the barrier above
-          s_last = atomicAdd(counters + at, 1u) == (unsigned)n - 1;
-          if (s_last) counters[at] = 0;
-          __threadfence();
-        }
-        __syncthreads();
-        return s_last != 0;
-      };
-      if (arrive(c0 >= g * kGroup ? c0 : (int)gridDim.x + g, hi - lo + 1)) {
-        if (hi > lo) {
-          if (tid <= hi - lo) s_part[tid] = slot(lo + tid);
-          join_parts<T, HD, R>(a, s_part, hi - lo + 1, rows, g0 == g1, o_row, lse_row, s_w, s_ml, &s_flag);
-        }
-        if (g0 != g1) {
-          __syncthreads();
-          if (arrive((int)gridDim.x + (int)gridDim.x / kGroup + 1 + c0, g1 - g0 + 1)) {
-            if (tid <= g1 - g0) s_part[tid] = slot(max(c0, (g0 + tid) * kGroup));
-            join_parts<T, HD, R>(a, s_part, g1 - g0 + 1, rows, true, o_row, lse_row, s_w, s_ml, &s_flag);
-          }
-        }
-      }
-      __syncthreads();  // s_last and the join's arrays are used again
+      const int64_t first = begin + (done - seg_units) - cw.u;
+      Piece& p = piece[from_start ? 1 : 0];
+      p = Piece{r, head0, rows, share_of(first, total, n_shares), share_of(first + cw.units - 1, total, n_shares)};
     }
     // on to the next (request, head block)
     cw.u = cw.units - 1;
     walk_next(cw, a, nv, cap);
+  }
+
+  // ---- report the partials (complete since the last barrier) and join what is
+  // complete with them.  Thread 32 i takes piece i.
+  const int g = blockIdx.x / kGroup;
+  if (lane == 0 && warp < 2) {
+    const Piece& p = piece[warp];
+    bool last = false;
+    if (p.rows) {
+      const int all = p.c1 - p.c0 + 1;
+      const int lo = max(p.c0, g * kGroup), hi = min(p.c1, g * kGroup + kGroup - 1);
+      const int n = all <= kDirect ? all : hi - lo + 1;
+      unsigned* counter = counters + (all <= kDirect || p.c0 >= g * kGroup ? p.c0 : kMaxShares + g);
+      __threadfence();
+      last = n == 1 || atomicAdd(counter, 1u) == (unsigned)n - 1;
+      if (last && n > 1) *counter = 0;
+      __threadfence();
+    }
+    s_last[warp] = last;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    if (!s_last[i]) continue;
+    const Piece p = i ? piece[1] : piece[0];
+    T* o_row = static_cast<T*>(a.o) + (int64_t)p.r * a.o_stride + (int64_t)p.head0 * HD;
+    float* lse_row = a.lse ? a.lse + (int64_t)p.r * a.nh + p.head0 : nullptr;
+    auto slot = [&](int c) { return ws_part + (int64_t)(c * 2 + (c == p.c0 ? 1 : 0)) * ws_part_floats(HD); };
+    const bool direct = p.c1 - p.c0 + 1 <= kDirect;
+    const int lo = direct ? p.c0 : max(p.c0, g * kGroup), hi = direct ? p.c1 : min(p.c1, g * kGroup + kGroup - 1);
+    if (hi > lo) {
+      if (tid <= hi - lo) s_join.part[tid] = slot(lo + tid);
+      __syncthreads();
+      join_parts<T, HD, R>(s_join, hi - lo + 1, p.rows, direct, o_row, lse_row);
+      __syncthreads();
+    }
+    if (!direct) {
+      const int g0 = p.c0 / kGroup, g1 = p.c1 / kGroup;
+      if (tid == 0) {
+        unsigned* counter = counters + kMaxShares + kMaxShares / kGroup + 1 + p.c0;
+        __threadfence();
+        s_segbad[0] = atomicAdd(counter, 1u) == (unsigned)(g1 - g0);
+        if (s_segbad[0]) *counter = 0;
+        __threadfence();
+      }
+      if (tid <= g1 - g0) s_join.part[tid] = slot(max(p.c0, (g0 + tid) * kGroup));
+      __syncthreads();
+      if (s_segbad[0]) join_parts<T, HD, R>(s_join, g1 - g0 + 1, p.rows, true, o_row, lse_row);
+      __syncthreads();
+    }
   }
   idle_requests();
 }
