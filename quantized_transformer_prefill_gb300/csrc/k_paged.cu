@@ -266,39 +266,38 @@ __device__ __forceinline__ void turn_cos_sin(uint64_t f, float* c, float* s) {
   *s = (quad >= 2) ? -ss : ss;
 }
 
-constexpr int kRpHeads = 4;      // heads of a warp whose loads are in flight together
+constexpr int kRpInFlight = 16;  // elements of a lane whose loads are in flight together
 constexpr int kRpMaxWarps = 16;
 
-// One CTA per token, kRpHeads heads per warp: warp w of n takes heads w, w + n,
-// ... of Q, K and V, lane l the head's elements l*E..l*E+E-1.  The row, the
-// bias, the position and the slot are all loaded before the first of them is
-// looked at.
+// One CTA per token.  A lane takes E neighbouring elements of a head (one
+// 16-byte vector of the source type), so a unit of 32 lanes is 32 E / HD heads;
+// warp w of n takes units w, w + n, ...  The position, the slot and the
+// row are all loaded before the first of them is looked at.  The cosines and
+// sines of the lane's elements, with the rotation's signs in the sines, are the
+// same for every head: they are read into registers once.  The pair partner of
+// an element lies in the lane itself (interleaved pairs), in another lane at the
+// same place (half a rotation is a multiple of E), or anywhere (other rotated
+// sizes), where it is fetched through shared memory.
 template <typename TS, typename TD, int HD>
 __global__ void __launch_bounds__(kRpMaxWarps * 32, 2) rope_paged_kernel(const __grid_constant__ RopePagedArgs a) {
-  constexpr int E = HD / 32;
+  constexpr int E = 16 / sizeof(TS), kLanes = HD / E, kPer = 32 / kLanes;  // lanes of a head, heads of a unit
+  constexpr int kRpUnits = kRpInFlight / E;
   using VS = Vec<TS, E>;
   using VD = Vec<TD, E>;
-  using VF = Vec<float, E>;
   __shared__ float s_cos[HD / 2], s_sin[HD / 2];
+  extern __shared__ float s_swap[];  // [warp][32 E], only where partners lie anywhere
   const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const int nqk = a.nh + a.c.nkv, heads = nqk + a.c.nkv;
+  const int sub = lane / kLanes, d0 = (lane % kLanes) * E;  // head of the unit, first element of the head
   const TS* row = static_cast<const TS*>(a.qkv) + (int64_t)t * a.row_stride + lane * E;
   pdl_trigger();
   pdl_wait();
-  VS x[kRpHeads];
-  VF b[kRpHeads];
-  auto load = [&](int h0) {
+  VS x[kRpUnits];
+  auto load = [&](int u0) {
 #pragma unroll
-    for (int i = 0; i < kRpHeads; ++i) {
-      const int h = h0 + i * warps;
-      if (h < heads) x[i] = *reinterpret_cast<const VS*>(row + (int64_t)h * HD);
-    }
-    if (a.bias) {
-#pragma unroll
-      for (int i = 0; i < kRpHeads; ++i) {
-        const int h = h0 + i * warps;
-        if (h < heads) b[i] = *reinterpret_cast<const VF*>(a.bias + (int64_t)h * HD + lane * E);
-      }
+    for (int i = 0; i < kRpUnits; ++i) {
+      const int u = u0 + i * warps;
+      if (u * kPer + sub < heads) x[i] = *reinterpret_cast<const VS*>(row + u * (32 * E));
     }
   };
   const int slot = a.slot[t], pos = a.pos[t];
@@ -310,94 +309,118 @@ __global__ void __launch_bounds__(kRpMaxWarps * 32, 2) rope_paged_kernel(const _
   }
   const int rot = a.rope.rot_dim, half = rot >> 1;
   const bool inter = a.rope.style == MINFER_ROPE_INTERLEAVED;
-  const int page = slot / a.c.page_size;
-  const int64_t at = (int64_t)page * a.c.page_stride + (int64_t)(slot - page * a.c.page_size) * a.c.row_stride;
   for (int i = tid; i < half; i += blockDim.x) {
     float c, s;
     turn_cos_sin((uint64_t)(uint32_t)pos * a.rope.turn[i], &c, &s);
     s_cos[i] = c * a.rope.mscale;
     s_sin[i] = s * a.rope.mscale;
   }
+  const int page = slot / a.c.page_size;
+  const int64_t at = (int64_t)page * a.c.page_stride + (int64_t)(slot - page * a.c.page_size) * a.c.row_stride;
+  TD* qdst = static_cast<TD*>(a.q_out) + (int64_t)t * a.q_stride + d0;
+  TD* kdst = static_cast<TD*>(a.c.k) + at + d0;
+  TD* vdst = static_cast<TD*>(a.c.v) + at + d0;
   __syncthreads();
-
-  for (int h0 = warp; h0 < heads; h0 += warps * kRpHeads) {
-    if (h0 != warp) load(h0);
+  float cs[E], sn[E];
 #pragma unroll
-    for (int i = 0; i < kRpHeads; ++i) {
-      const int h = h0 + i * warps;
-      if (h >= heads) break;
+  for (int e = 0; e < E; ++e) {
+    const int d = d0 + e, p = inter ? d >> 1 : d < half ? d : d - half;
+    cs[e] = d < rot ? s_cos[p] : 1.f;
+    sn[e] = d < rot ? s_sin[p] : 0.f;
+    if (inter ? !(d & 1) : d < half) sn[e] = -sn[e];
+  }
+  const bool in_lane = inter, in_place = half % E == 0, some = d0 < rot;  // (uniform, uniform, per lane)
+  const int from = (d0 < half ? lane + half / E : lane - half / E) & 31;
+  float* swap = s_swap + warp * (32 * E);
+
+  for (int u0 = warp; u0 * kPer < heads; u0 += warps * kRpUnits) {
+    if (u0 != warp) load(u0);
+#pragma unroll
+    for (int i = 0; i < kRpUnits; ++i) {
+      const int u = u0 + i * warps, h = u * kPer + sub;
+      if (u * kPer >= heads) break;  // the whole warp
       float y[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) y[e] = to_f32<TS>(x[i].v[e]);
-      if (a.bias) {
+      if (a.bias && h < heads) {
+        const float4* b = reinterpret_cast<const float4*>(a.bias + h * HD + d0);
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] += b[i].v[e];
+        for (int j = 0; j < E / 4; ++j) {
+          const float4 f = b[j];
+          y[4 * j] += f.x;
+          y[4 * j + 1] += f.y;
+          y[4 * j + 2] += f.z;
+          y[4 * j + 3] += f.w;
+        }
       }
-      if (h < nqk) {
+      if (u * kPer < nqk) {  // some head of the unit is one of Q or K
         if (a.q_norm) {
           float ss = 0.f;
 #pragma unroll
           for (int e = 0; e < E; ++e) ss = fmaf(y[e], y[e], ss);
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          const float r = rsqrtf(ss * (1.f / HD) + a.eps);
-          const VF w = *reinterpret_cast<const VF*>((h < a.nh ? a.q_norm : a.k_norm) + lane * E);
+          for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          if (h < nqk) {
+            const float r = rsqrtf(ss * (1.f / HD) + a.eps);
+            const float4* w = reinterpret_cast<const float4*>((h < a.nh ? a.q_norm : a.k_norm) + d0);
 #pragma unroll
-          for (int e = 0; e < E; ++e) y[e] = y[e] * r * w.v[e];
-        }
-        // the pair partner of element i: i ^ 1, or i + half / i - half
-        float z[E];
-        if (inter) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) z[e] = y[e ^ 1];
-        } else if (half % E == 0) {
-          const int src = lane * E < half ? lane + half / E : lane - half / E;
-#pragma unroll
-          for (int e = 0; e < E; ++e) z[e] = __shfl_sync(0xffffffffu, y[e], src & 31);
-        } else {
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const int p = lane * E + e < half ? lane * E + e + half : lane * E + e - half;
-            z[e] = 0.f;
-#pragma unroll
-            for (int g = 0; g < E; ++g) {
-              const float w = __shfl_sync(0xffffffffu, y[g], (p / E) & 31);
-              if ((p & (E - 1)) == g) z[e] = w;
+            for (int j = 0; j < E / 4; ++j) {
+              const float4 f = w[j];
+              y[4 * j] *= r * f.x;
+              y[4 * j + 1] *= r * f.y;
+              y[4 * j + 2] *= r * f.z;
+              y[4 * j + 3] *= r * f.w;
             }
           }
         }
+        float z[E];
+        if (in_lane) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int d = lane * E + e;
-          if (d < rot) {
-            const int p = inter ? d >> 1 : (d < half ? d : d - half);
-            const bool lower = inter ? !(d & 1) : d < half;
-            const float s = lower ? -s_sin[p] : s_sin[p];
-            y[e] = fmaf(z[e], s, y[e] * s_cos[p]);
+          for (int e = 0; e < E; ++e) z[e] = y[e ^ 1];
+        } else if (in_place) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) z[e] = __shfl_sync(0xffffffffu, y[e], from);
+        } else {
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < E; ++e) swap[lane * E + e] = y[e];
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const int d = d0 + e;
+            z[e] = d < rot ? swap[sub * HD + (d < half ? d + half : d - half)] : 0.f;
           }
         }
-      }
-      VD out;
+        if (some && h < nqk) {
+          // (an element behind rot_dim in a lane that has some before it: y * 1 + z * 0 would lose
+          // it to an infinite z)
 #pragma unroll
-      for (int e = 0; e < E; ++e) out.v[e] = from_f32<TD>(y[e]);
-      TD* dst;
-      if (h < a.nh)
-        dst = static_cast<TD*>(a.q_out) + (int64_t)t * a.q_stride + (int64_t)h * HD;
-      else if (h < nqk)
-        dst = static_cast<TD*>(a.c.k) + at + (int64_t)(h - a.nh) * a.c.head_stride;
-      else
-        dst = static_cast<TD*>(a.c.v) + at + (int64_t)(h - nqk) * a.c.head_stride;
-      *reinterpret_cast<VD*>(dst + lane * E) = out;
+          for (int e = 0; e < E; ++e)
+            if (d0 + e < rot) y[e] = fmaf(z[e], sn[e], y[e] * cs[e]);
+        }
+      }
+      if (h < heads) {
+        VD out;
+#pragma unroll
+        for (int e = 0; e < E; ++e) out.v[e] = from_f32<TD>(y[e]);
+        TD* dst = h < a.nh ? qdst + h * HD : h < nqk ? kdst + (h - a.nh) * a.c.head_stride : vdst + (h - nqk) * a.c.head_stride;
+        *reinterpret_cast<VD*>(dst) = out;
+      }
     }
   }
 }
 
+template <typename TS, typename TD, int HD>
+cudaError_t rope_paged_sized(const RopePagedArgs& a, cudaStream_t st) {
+  constexpr int E = 16 / sizeof(TS), kPer = 32 * E / HD, kRpUnits = kRpInFlight / E;
+  const int units = (a.nh + 2 * a.c.nkv + kPer - 1) / kPer, warps = (units + kRpUnits - 1) / kRpUnits;
+  const unsigned n = warps < kRpMaxWarps ? warps : kRpMaxWarps;
+  const bool swap = a.rope.style == MINFER_ROPE_HALF && (a.rope.rot_dim / 2) % E != 0;
+  return launch_pdl(rope_paged_kernel<TS, TD, HD>, dim3((unsigned)a.n_tokens), dim3(32 * n), swap ? n * 32 * E * sizeof(float) : 0, st, a);
+}
 template <typename TS, typename TD>
 cudaError_t rope_paged_typed(const RopePagedArgs& a, cudaStream_t st) {
-  const int heads = a.nh + 2 * a.c.nkv, warps = (heads + kRpHeads - 1) / kRpHeads;
-  const dim3 grid((unsigned)a.n_tokens), block(32 * (unsigned)(warps < kRpMaxWarps ? warps : kRpMaxWarps));
-  if (a.c.hd == 64) return launch_pdl(rope_paged_kernel<TS, TD, 64>, grid, block, 0, st, a);
-  return launch_pdl(rope_paged_kernel<TS, TD, 128>, grid, block, 0, st, a);
+  return a.c.hd == 64 ? rope_paged_sized<TS, TD, 64>(a, st) : rope_paged_sized<TS, TD, 128>(a, st);
 }
 
 }  // namespace
