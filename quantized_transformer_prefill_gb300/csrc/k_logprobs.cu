@@ -36,8 +36,9 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kChunk = 512;         // logits of a chunk
 constexpr int kPer = kChunk / 32;   // logits of a lane
-constexpr int kCtasPerSm = 4;       // resident
-constexpr int kWaves = 4;
+constexpr int kCtasPerSm = 3;       // resident
+constexpr int kRing = 8192;         // bytes of a warp's ring: 3 CTAs of 8 warps have 192 KB in flight or at work
+constexpr int kWaves = 2;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -71,28 +72,21 @@ __device__ __forceinline__ uint32_t key_id(uint64_t k) { return ~(uint32_t)k; }
 struct Stat {
   float m, s, t;
 };
-__device__ __forceinline__ Stat join(const Stat& a, const Stat& b) {
-  Stat r;
-  r.m = max_nan(a.m, b.m);
-  // an empty side contributes nothing; its shift would be -inf
-  const float da = a.m == -INFINITY ? 0.f : (a.m - r.m) * kLog2e, db = b.m == -INFINITY ? 0.f : (b.m - r.m) * kLog2e;
-  const float ca = ex2(da), cb = ex2(db);
-  r.s = a.s * ca + b.s * cb;
-  // the terms' shift d moves t by d s; far below, c = 0 and d may overflow: no term
-  r.t = (ca == 0.f ? 0.f : ca * (a.t + da * a.s)) + (cb == 0.f ? 0.f : cb * (b.t + db * b.s));
-  return r;
-}
+// The joined sums of a warp's lanes, in every lane: all move to the largest
+// reference first.
 __device__ __forceinline__ Stat warp_join(Stat v) {
+  const float m = key_value(__reduce_max_sync(0xffffffffu, key32(v.m)));
+  // an empty side contributes nothing; its shift would be -inf
+  const float d = v.m == -INFINITY ? 0.f : (v.m - m) * kLog2e, c = ex2(d);
+  float s = v.s * c;
+  // the terms' shift d moves t by d s; far below, c = 0 and d may overflow: no term
+  float t = c == 0.f ? 0.f : c * fmaf(d, v.s, v.t);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    Stat w;
-    w.m = __shfl_xor_sync(0xffffffffu, v.m, o);
-    w.s = __shfl_xor_sync(0xffffffffu, v.s, o);
-    w.t = __shfl_xor_sync(0xffffffffu, v.t, o);
-    // both lanes of a pair join in the same order: the sum does not depend on the lane
-    v = (threadIdx.x & o) ? join(w, v) : join(v, w);
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    t += __shfl_xor_sync(0xffffffffu, t, o);
   }
-  return v;
+  return Stat{m, s, t};
 }
 
 // The warp's 32 keys in descending order of lanes (bitonic sort).
@@ -121,10 +115,22 @@ __device__ __forceinline__ uint64_t warp_merge(uint64_t a, uint64_t b) {
   }
   return v;
 }
-// Takes one new key per lane into the warp's list of the 32 largest.
+// Takes one new key per lane into the warp's list of the 32 largest, of which
+// the first k matter: a few keys one by one, many by sorting them.
 __device__ __forceinline__ void warp_take(uint64_t& list, uint64_t key, int k) {
+  const int lane = threadIdx.x & 31;
   const uint64_t kth = __shfl_sync(0xffffffffu, list, k - 1);
-  if (__any_sync(0xffffffffu, key > kth)) list = warp_merge(list, warp_sort(key));
+  unsigned come = __ballot_sync(0xffffffffu, key > kth);
+  if (__popc(come) > 6) {
+    list = warp_merge(list, warp_sort(key));
+    return;
+  }
+  for (; come; come &= come - 1) {
+    const uint64_t one = __shfl_sync(0xffffffffu, key, __ffs(come) - 1);
+    const int place = __popc(__ballot_sync(0xffffffffu, list > one));
+    const uint64_t up = __shfl_up_sync(0xffffffffu, list, 1);
+    list = lane < place ? list : lane == place ? one : up;
+  }
 }
 // The 32 largest of all warps' lists, in every warp.  s: [kWarps][32].
 __device__ __forceinline__ uint64_t block_merge(uint64_t list, uint64_t* s) {
@@ -225,9 +231,10 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __grid_constant__ LogprobsArgs a, const Plan plan) {
   using L = Loader<T>;
   constexpr int V = L::kVec;
+  extern __shared__ __align__(128) unsigned char lp_smem[];
   __shared__ uint64_t s_list[kWarps * 32];
   __shared__ Stat s_stat[kWarps];
-  __shared__ int s_last;
+  __shared__ int s_last, s_n;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = blockIdx.x / plan.parts;
   const int part = (int)(blockIdx.x - row * plan.parts);
@@ -237,15 +244,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
   uint32_t* keys = reinterpret_cast<uint32_t*>(ws + plan.keys) + row * plan.chunks;
   pdl_trigger();
   pdl_wait();
-  int id = -1;
-  if (a.ids) {
-    id = a.ids[row];
-    if (id < 0) return;  // padding
-    if (id >= a.vocab) {
-      if (part == 0 && tid == 0) set_error(a.status, MINFER_ERR_TOKEN_OOB);
-      return;
-    }
-  }
   const T* x = static_cast<const T*>(a.x) + row * a.row_stride;
   const int head = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
   const int chunks = (int)((a.vocab + head + kChunk - 1) / kChunk);
@@ -261,26 +259,53 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
     t = c * fmaf(-d, s, t);
     s *= c;
   };
-  constexpr int U = kPer / V;
-  // the next chunk's vectors are on their way while this one's are worked on
-  uint4 next[U];
-  auto inside = [&](int c) { return c > 0 && (int64_t)(c + 1) * kChunk - head <= a.vocab; };
-  auto fetch = [&](int c) {
-    const uint4* p = reinterpret_cast<const uint4*>(x + ((int64_t)c * kChunk - head)) + lane;
+  // Chunks that lie inside the row come through a ring in shared memory, kStages
+  // - 1 of them on their way.  A lane copies the 16-byte vectors that it reads
+  // itself, so a wait for its own copies is all the synchronization there is.
+  constexpr int U = kPer / V, kChunkBytes = kChunk * (int)sizeof(T), kStages = kRing / kChunkBytes;
+  const uint32_t ring = smem_u32(lp_smem) + warp * kRing + lane * 16;
+  auto inside = [&](int c) { return (c > 0 || head == 0) && (int64_t)(c + 1) * kChunk - head <= a.vocab; };
+  auto fetch = [&](int c, int stage) {
+    if (c < c1 && inside(c)) {
+      const unsigned char* p = reinterpret_cast<const unsigned char*>(x + ((int64_t)c * kChunk - head)) + lane * 16;
 #pragma unroll
-    for (int i = 0; i < U; ++i) next[i] = __ldcg(p + i * 32);
+      for (int i = 0; i < U; ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + stage * kChunkBytes + i * 512), "l"(p + i * 512) : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  int c = part * plan.per + warp;
-  if (c < c1 && inside(c)) fetch(c);
+  int c = part * plan.per + warp, stage = 0;
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(c + i * kWarps, i);
+  int id = -1;
+  if (a.ids) {
+    id = a.ids[row];
+    if (id < 0 || id >= a.vocab) {  // padding, or refused
+      if (id >= 0 && part == 0 && tid == 0) set_error(a.status, MINFER_ERR_TOKEN_OOB);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      return;
+    }
+  }
+  float given = 0.f;  // the given token's logit, on its way until the end
+  if (a.ids && tid == 0) given = L::one(x + id);
   for (; c < c1; c += kWarps) {
+    fetch(c + (kStages - 1) * kWarps, stage == 0 ? kStages - 1 : stage - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
     float f[kPer];
     if (inside(c)) {
 #pragma unroll
-      for (int i = 0; i < U; ++i) L::get(next[i], f + i * V);
+      for (int i = 0; i < U; ++i) {
+        uint4 u;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                     : "r"(ring + stage * kChunkBytes + i * 512)
+                     : "memory");
+        L::get(u, f + i * V);
+      }
     } else {
       load_chunk<T>(x, head, a.vocab, c, f);
     }
-    if (c + kWarps < c1 && inside(c + kWarps)) fetch(c + kWarps);
+    if (++stage == kStages) stage = 0;
     float top = f[0];
 #pragma unroll
     for (int i = 1; i < kPer; ++i) top = max_nan(top, f[i]);
@@ -323,20 +348,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
   }
   if (fabsf(r) <= 0x1p20f) exact();
 
-  auto block_join = [&](Stat v) {
-    v = warp_join(v);
-    if (lane == 0) s_stat[warp] = v;
-    __syncthreads();
-    v = s_stat[0];
-#pragma unroll
-    for (int i = 1; i < kWarps; ++i) v = join(v, s_stat[i]);
-    return v;
-  };
-  Stat v = block_join(Stat{r, s, t});
+  Stat v = warp_join(Stat{r, s, t});
+  if (lane == 0) s_stat[warp] = v;
+  __syncthreads();
+  // warp 0 has the row's sums (alone: it writes what depends on them)
+  if (warp == 0) v = warp_join(lane < kWarps ? s_stat[lane] : Stat{-INFINITY, 0.f, 0.f});
   if (plan.parts > 1) {
     if (tid == 0) {
       stats[part] = make_float4(v.m, v.s, v.t, 0.f);
-      __threadfence();  // also the other threads' keys: they came before block_join's barrier
+      __threadfence();  // also the other threads' keys: they came before the barrier
       unsigned* counter = reinterpret_cast<unsigned*>(ws) + row;
       s_last = atomicAdd(counter, 1u) == (unsigned)plan.parts - 1;
       if (s_last) *counter = 0;
@@ -344,20 +364,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
     }
     __syncthreads();
     if (!s_last) return;
-    v = Stat{-INFINITY, 0.f, 0.f};
-    for (int p = tid; p < plan.parts; p += kThreads) {
-      const float4 q = __ldcg(stats + p);
-      v = join(v, Stat{q.x, q.y, q.z});
+    if (warp == 0) {
+      v = Stat{-INFINITY, 0.f, 0.f};
+      for (int p0 = 0; p0 < plan.parts; p0 += 31) {  // the sums so far and 31 parts
+        if (lane < 31) {
+          v = Stat{-INFINITY, 0.f, 0.f};
+          if (p0 + lane < plan.parts) {
+            const float4 q = __ldcg(stats + p0 + lane);
+            v = Stat{q.x, q.y, q.z};
+          }
+        }
+        v = warp_join(v);
+      }
     }
-    v = block_join(v);
   }
 
-  const bool none = v.m == -INFINITY;
-  const float log2s = log2f(v.s);
-  auto logp = [&](float y) { return none ? -INFINITY : (y - v.m) - kLn2 * log2s; };
-  if (tid == 0) {
-    if (a.ids) a.logprob[row] = logp(L::one(x + id));
-    if (a.entropy) a.entropy[row] = none ? 0.f : kLn2 * (log2s - v.t / v.s);
+  if (warp == 0) {
+    const float log2s = log2f(v.s);
+    if (lane == 0) {
+      s_stat[0] = Stat{v.m, log2s, 0.f};  // for every warp, behind the barriers below
+      s_n = 0;
+      const bool none = v.m == -INFINITY;
+      if (a.ids) a.logprob[row] = none ? -INFINITY : (given - v.m) - kLn2 * log2s;
+      if (a.entropy) a.entropy[row] = none ? 0.f : kLn2 * (log2s - v.t / v.s);
+    }
   }
   if (k == 0) return;
 
@@ -370,25 +400,108 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
   const uint64_t picked = block_merge(list, s_list);
   // with fewer than k chunks the k-th key is 0 and everything counts
   const uint32_t floor = (uint32_t)(__shfl_sync(0xffffffffu, picked, k - 1) >> 32);
-  list = 0;
-  for (int j = warp; j < k; j += kWarps) {
-    const uint64_t pick = __shfl_sync(0xffffffffu, picked, j);
-    if (pick == 0) break;
-    const int c = (int)key_id(pick);
-    float f[kPer];
-    load_chunk<T>(x, head, a.vocab, c, f);
+  // every warp's chunks (4 at most) come into its ring together
+  constexpr int kPicks = kLogprobsMaxTop / kWarps;
+  static_assert(kPicks * kChunkBytes <= kRing, "a warp's picks fit its ring");
+  uint64_t pick[kPicks];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int64_t e = (int64_t)c * kChunk - head + ((i / V) * 32 + lane) * V + i % V;
-      const uint64_t key = e >= 0 && e < a.vocab ? make_key(f[i], (uint32_t)e) : 0;
-      warp_take(list, (uint32_t)(key >> 32) >= floor ? key : 0, k);
+  for (int j = 0; j < kPicks; ++j) {
+    const int at = warp + j * kWarps;
+    pick[j] = __shfl_sync(0xffffffffu, picked, at);
+    if (at >= k || pick[j] == 0) {
+      pick[j] = 0;
+      continue;
+    }
+    const int cp = (int)key_id(pick[j]);
+    if (inside(cp)) {
+      const unsigned char* p = reinterpret_cast<const unsigned char*>(x + ((int64_t)cp * kChunk - head)) + lane * 16;
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + j * kChunkBytes + i * 512), "l"(p + i * 512) : "memory");
+    } else {
+      T edge[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int64_t e = (int64_t)cp * kChunk - head + ((i / V) * 32 + lane) * V + i % V;
+        if (e >= 0 && e < a.vocab) edge[i] = x[e];
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        reinterpret_cast<T*>(lp_smem + warp * kRing + j * kChunkBytes + (i / V) * 512 + lane * 16)[i % V] = edge[i];
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  auto value = [&](int j, int i) {
+    return L::one(reinterpret_cast<const T*>(lp_smem + warp * kRing + j * kChunkBytes + (i / V) * 512 + lane * 16) + i % V);
+  };
+  auto place = [&](int j, int i) { return (int64_t)key_id(pick[j]) * kChunk - head + ((i / V) * 32 + lane) * V + i % V; };
+  // the logits that are large enough, about k of them, into s_list
+  unsigned large[kPicks];
+  int count = 0;
+#pragma unroll
+  for (int j = 0; j < kPicks; ++j) {
+    large[j] = 0;
+    if (pick[j] == 0) continue;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (key32(value(j, i)) >= floor && place(j, i) >= 0 && place(j, i) < a.vocab) large[j] |= 1u << i;
+    count += __popc(large[j]);
+  }
+  int at = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, at, o);
+    if (lane >= o) at += y;
+  }
+  const int all = __shfl_sync(0xffffffffu, at, 31);
+  int base = 0;
+  if (lane == 0 && all) base = atomicAdd(&s_n, all);
+  base = __shfl_sync(0xffffffffu, base, 0);
+  at += base - count;
+  if (base + all <= kThreads) {
+#pragma unroll
+    for (int j = 0; j < kPicks; ++j)
+      for (unsigned m = large[j]; m; m &= m - 1) {
+        const int i = __ffs(m) - 1;
+        s_list[at++] = make_key(value(j, i), (uint32_t)place(j, i));
+      }
+  }
+  __syncthreads();
+  const float m = s_stat[0].m, log2s = s_stat[0].s;
+  auto put = [&](uint64_t key, int at) {
+    a.top_ids[row * k + at] = (int32_t)key_id(key);
+    a.top_logprobs[row * k + at] = m == -INFINITY ? -INFINITY : (key_value((uint32_t)(key >> 32)) - m) - kLn2 * log2s;
+  };
+  const int n = s_n;
+  if (n <= kThreads) {
+    // a key's place is the number of keys above it
+    if (tid < n) {
+      const uint64_t own = s_list[tid];
+      int above = 0;
+      for (int i = 0; i < n; ++i) above += s_list[i] > own;
+      if (above < k) put(own, above);
+    }
+    return;
+  }
+  // many equal logits (rows of which a mask leaves little): the 32 largest so
+  // far in a list per warp, the chunks' logits in the order of their ids, so that
+  // equal ones fall behind at once
+  __syncthreads();
+  list = 0;
+#pragma unroll 1
+  for (int j = 0; j < kPicks; ++j) {
+    const int at_pick = warp + j * kWarps;
+    const uint64_t one = __shfl_sync(0xffffffffu, picked, at_pick);
+    if (at_pick >= k || one == 0) break;
+    const int64_t e0 = (int64_t)key_id(one) * kChunk - head;
+    const T* chunk = reinterpret_cast<const T*>(lp_smem + warp * kRing + j * kChunkBytes);
+    for (int i = lane; i < kChunk; i += 32) {
+      const uint64_t key = make_key(L::one(chunk + i), (uint32_t)(e0 + i));
+      warp_take(list, e0 + i >= 0 && e0 + i < a.vocab && (uint32_t)(key >> 32) >= floor ? key : 0, k);
     }
   }
   list = block_merge(list, s_list);
-  if (tid < k) {
-    a.top_ids[row * k + tid] = (int32_t)key_id(list);
-    a.top_logprobs[row * k + tid] = logp(key_value((uint32_t)(list >> 32)));
-  }
+  if (tid < k) put(list, tid);
 }
 
 // Parts of a row: with fewer rows than the GPU holds CTAs, as many as fill it
@@ -411,7 +524,9 @@ Plan plan_of(int64_t rows, int64_t vocab, int vec, int k, int num_sms) {
 template <typename T>
 cudaError_t launch(const LogprobsArgs& a, int num_sms, cudaStream_t st) {
   const Plan plan = plan_of(a.rows, a.vocab, Loader<T>::kVec, a.k, num_sms);
-  return launch_pdl(logprobs_kernel<T>, dim3((unsigned)(a.rows * plan.parts)), dim3(kThreads), 0, st, a, plan);
+  const cudaError_t e = allow_smem<logprobs_kernel<T>>(kWarps * kRing);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(logprobs_kernel<T>, dim3((unsigned)(a.rows * plan.parts)), dim3(kThreads), kWarps * kRing, st, a, plan);
 }
 
 }  // namespace
