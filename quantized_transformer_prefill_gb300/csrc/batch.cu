@@ -163,7 +163,7 @@ int minfer_op_paged_attention_workspace(int n_req, int n_head, const minfer_page
   if (!bytes || n_req <= 0 || n_head <= 0 || n_head % c.nkv != 0) return MINFER_ERR_ARG;
   const int sms = current_sms();
   if (sms == 0) return MINFER_ERR_CUDA;
-  *bytes = paged_attn_workspace(c.hd, cache->type, sms);
+  *bytes = paged_attn_workspace(n_head / c.nkv, c.hd, cache->type, sms);
   return MINFER_OK;
 }
 
@@ -185,7 +185,7 @@ int minfer_op_paged_attention(const void* d_q, int64_t q_stride, const minfer_pa
   if (!fits31(max_pages, cache->page_size) || n_head > 65535) return MINFER_ERR_TOO_LARGE;
   const int sms = current_sms();
   if (sms == 0) return MINFER_ERR_CUDA;
-  if (workspace_bytes < paged_attn_workspace(a.c.hd, cache->type, sms))
+  if (workspace_bytes < paged_attn_workspace(n_head / a.c.nkv, a.c.hd, cache->type, sms))
     return MINFER_ERR_TOO_LARGE;
   a.q = d_q;
   a.q_stride = q_stride;

@@ -17,14 +17,22 @@
 // it.  A CTA reports its (at most two) partials after its last unit, so that no
 // unit waits for a fence.
 //
-// Inside a CTA each of four warps takes 16 of a unit's 64 keys, copies their
-// K and V rows into its own ring in shared memory (cp.async of 16 bytes, page
-// by page; rows behind the request's last are filled with zeros) and runs an
-// online softmax of its own: no barrier before the end of the (request, KV
-// head).  The products are m16n8 MMAs with the query heads of the KV head as
-// the 16 rows.  One query token leaves the rows of a tcgen05 tile (128)
-// mostly empty and the bound is the bytes of K and V, so the accumulators stay
-// in registers, where the softmax needs them.
+// Inside a CTA every warp takes 16 keys of a unit, copies their K and V rows
+// into its own ring in shared memory (cp.async of 16 bytes, page by page; rows
+// behind the request's last are filled with zeros) and runs an online softmax of
+// its own: no barrier before the end of the (request, KV head).  The products
+// are m16n8 MMAs with the keys (S^T = K Q^T) and the head's dims (O^T = V^T P^T)
+// as the 16 rows and 8 query heads as the columns: with up to 8 query heads per
+// KV head no column is wasted more than the heads are few, and the accumulators
+// of a warp are HD / 2 x 8 / 32 registers.  One query token would leave the 128
+// rows of a tcgen05 tile of heads nearly empty, and with the keys as its rows the
+// scores would go through TMEM twice for a few flops per byte; the bound is the
+// bytes of K and V, so the accumulators stay in registers, where the softmax
+// needs them.
+//
+// f32 caches: every operand is split into two tf32 halves and three products are
+// taken (what is left out is 2^-22 of a product), and each unit's P V is added to
+// the running sum as an f32 addition of its own.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -35,31 +43,39 @@
 namespace minfer {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kKeys = 16;               // keys of a unit that one warp takes
-constexpr int kUnit = kWarps * kKeys;   // keys of a unit
-constexpr int kRows = 16;               // query heads of one MMA tile
+constexpr int kKeys = 16;  // keys of a unit that one warp takes
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 constexpr int kGroup = 16;              // neighbouring shares whose partials are joined first
 constexpr int kMaxJoin = 64;            // partials of one join: kDirect, kGroup, or the number of groups
 constexpr int kDirect = 32;             // partials that are joined in one step
 
-// R: query heads that a CTA carries through the join (8 where a KV head has no
-// more, which leaves room for another stage of the ring).
+// What the threads of a CTA share while they join partials.
+template <int R>
+struct JoinShared {
+  float* part[kMaxJoin];    // the partials, in the order of their shares
+  float2 ml[kMaxJoin][R];   // their (max, sum); then .x the weight
+  float2 out[R];            // the joined (max, sum)
+  int bad;
+};
+
+// R: query heads of a head block, one MMA tile of 8 or two.
 template <typename T, int HD, int R>
 struct Cfg {
+  static constexpr bool kF32 = sizeof(T) == 4;
   static constexpr int kRowBytes = HD * (int)sizeof(T);
-  static constexpr int kChunks = kRowBytes / 16;  // 16-byte chunks of a row
+  static constexpr int kChunks = kRowBytes / 16;             // 16-byte chunks of a row
   static constexpr int kStageBytes = 2 * kKeys * kRowBytes;  // K and V rows of one warp
-  static constexpr int kQBytes = sizeof(T) == 4 ? 2 * kRows * kRowBytes : 0;  // tf32 hi and lo of Q
-  // two CTAs per SM, or one where two stages of the ring do not fit twice; the
+  // as many CTAs per SM as their registers and two stages of the ring allow; the
   // ring takes what is left of the SM's shared memory
-  static constexpr int kCtas = kRowBytes == 512 ? 1 : 2;
-  static constexpr int kBudget = kCtas == 1 ? 222000 : R == 8 ? 109400 : 105000;
-  static constexpr int kFit = (kBudget - kQBytes) / (kWarps * kStageBytes);
+  static constexpr int kWarps = kRowBytes == 512 ? 2 : 4;
+  static constexpr int kCtas = kRowBytes == 128 ? 4 : R == 8 ? 3 : 2;
+  static constexpr int kUnit = kWarps * kKeys;  // keys of a unit
+  static constexpr int kPBytes = kF32 ? kWarps * kKeys * R * 4 : 0;  // softmax weights on their way to the other layout
+  static constexpr int kStatic = (int)sizeof(JoinShared<R>) + 768 + kWarps * R * 8;
+  static constexpr int kFit = (233472 / kCtas - 1024 - kStatic - kPBytes) / (kWarps * kStageBytes);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
-  static constexpr int kSmem = kWarps * kStages * kStageBytes + kQBytes;
+  static constexpr int kSmem = kWarps * kStages * kStageBytes + kPBytes;
   static_assert(kStages >= 2, "a ring has two stages at least");
   static_assert(R * HD * 4 <= kStageBytes, "a warp's output fits the stage it has just used");
 };
@@ -67,15 +83,16 @@ struct Cfg {
 // The workspace: counters (zero between calls; one per share for a piece that
 // starts in it, one per group for a piece that started before it, one per share
 // for the groups of a piece), then per share two partials, slot 1 for the piece
-// that starts in the share and slot 0 for the one that started before it: kRows
-// (max, sum) pairs and kRows x HD.
+// that starts in the share and slot 0 for the one that started before it: R
+// (max, sum) pairs and R x HD.
 constexpr int kMaxShares = kGroup * (kMaxJoin - 1);
 constexpr int64_t kPartOffset = ((2 * kMaxShares + kMaxShares / kGroup + 1) * 4 + 255) / 256 * 256;  // the same for every call
-__host__ __device__ inline int64_t ws_part_floats(int hd) { return (int64_t)kRows * (hd + 2); }
+__host__ __device__ constexpr int64_t part_floats(int rows, int hd) { return (int64_t)rows * (hd + 2); }
 
 // Units of a request; a length out of range counts as none.
+template <int kUnit>
 __device__ __forceinline__ int units_of(int len, int cap) {
-  return (len < 0 || len > cap) ? 0 : (len + kUnit - 1) / kUnit;
+  return (len < 0 || len > cap) ? 0 : (int)(((unsigned)len + kUnit - 1) / kUnit);
 }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
@@ -95,6 +112,13 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
+}
+// the 8 x 8 matrix of 16-bit values whose row lane / 4, columns 2 (lane % 4) and
+// the next a register holds, transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
@@ -145,12 +169,13 @@ __device__ __forceinline__ void store_as(__half* p, float x) { *p = __float2half
 __device__ __forceinline__ void store_as(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
 // Walks the units of the batch: request r, head block v (KV head and group of
-// kRows query heads), unit u of it.  The next request's length is read one
+// R query heads), unit u of it.  The next request's length is read one
 // request ahead.
 struct Walk {
   int r, v, u, units, len, next_len;
 };
 __device__ __forceinline__ int len_at(const PagedAttnArgs& a, int r) { return r < a.n_req ? a.len[r] : 0; }
+template <int kUnit>
 __device__ __forceinline__ void walk_next(Walk& w, const PagedAttnArgs& a, int nv, int cap) {
   if (++w.u < w.units) return;
   w.u = 0;
@@ -160,7 +185,7 @@ __device__ __forceinline__ void walk_next(Walk& w, const PagedAttnArgs& a, int n
     ++w.r;
     w.len = w.next_len;
     w.next_len = len_at(a, w.r + 1);
-    w.units = units_of(w.len, cap);
+    w.units = units_of<kUnit>(w.len, cap);
   } while (w.units == 0 && w.r < a.n_req);
 }
 
@@ -177,23 +202,14 @@ __device__ __forceinline__ int share_of(int64_t x, int64_t total, int n) {
   return c;
 }
 
-// What the threads of a CTA share while they join partials.
-template <int R>
-struct JoinShared {
-  float* part[kMaxJoin];    // the partials, in the order of their shares
-  float2 ml[kMaxJoin][R];   // their (max, sum); then .x the weight
-  float2 out[R];            // the joined (max, sum)
-  int bad;
-};
-
 // Joins `count` partials: weights first, then every thread four dims of a row at
 // a time.  final: the result goes to o and lse, else it replaces the first
 // partial.  A sum below 0 marks a piece that met a bad page; it spoils the
 // whole.  All threads; s.part is written before a barrier of the caller's.
-template <typename T, int HD, int R>
+template <typename T, int HD, int R, int kThreads>
 __device__ void join_parts(JoinShared<R>& s, int count, int rows, bool final, T* o, float* lse) {
   const int tid = threadIdx.x;
-  for (int i = tid; i < count * R; i += kWarps * 32)
+  for (int i = tid; i < count * R; i += kThreads)
     if (i % R < rows) s.ml[i / R][i % R] = __ldcg(reinterpret_cast<const float2*>(s.part[i / R]) + i % R);
   if (tid == 0) s.bad = 0;
   __syncthreads();
@@ -215,12 +231,12 @@ __device__ void join_parts(JoinShared<R>& s, int count, int rows, bool final, T*
   }
   __syncthreads();
   const bool bad = s.bad != 0;
-  for (int i = tid; i < rows * HD / 4; i += kWarps * 32) {
+  for (int i = tid; i < rows * HD / 4; i += kThreads) {
     const int row = i / (HD / 4);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
     for (int p = 0; p < count; ++p) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(s.part[p] + 2 * kRows) + i);
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(s.part[p] + 2 * R) + i);
       const float c = s.ml[p][row].x;
       acc.x = fmaf(x.x, c, acc.x);
       acc.y = fmaf(x.y, c, acc.y);
@@ -228,7 +244,7 @@ __device__ void join_parts(JoinShared<R>& s, int count, int rows, bool final, T*
       acc.w = fmaf(x.w, c, acc.w);
     }
     if (!final) {
-      reinterpret_cast<float4*>(s.part[0] + 2 * kRows)[i] = acc;  // read by this thread alone
+      reinterpret_cast<float4*>(s.part[0] + 2 * R)[i] = acc;  // read by this thread alone
     } else if (!bad) {
       const float l = s.out[row].y, f = l == 0.f ? 0.f : 1.f / l;
       T* dst = o + i * 4;
@@ -253,12 +269,14 @@ struct Piece {
 };
 
 template <typename T, int HD, int R>
-__global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD, R>::kCtas)
+__global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCtas)
     paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, int n_groups, float scale_log2) {
   using C = Cfg<T, HD, R>;
-  constexpr bool kF32 = sizeof(T) == 4;
+  constexpr bool kF32 = C::kF32;
+  constexpr int kWarps = C::kWarps, kUnit = C::kUnit;
   constexpr int kSteps = C::kChunks / 2;  // MMA steps over the head's dims (two chunks each)
-  constexpr int kTiles = HD / 8;          // n8 tiles of the output
+  constexpr int kTiles = HD / 16;         // m16 tiles of the output
+  constexpr int NH = R / 8;               // n8 tiles of query heads
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int64_t s_scan[kWarps];
   __shared__ Walk s_walk;
@@ -281,7 +299,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD, R>::kCtas)
   const int per = (a.n_req + kWarps * 32 - 1) / (kWarps * 32), r_lo = min(tid * per, a.n_req), r_hi = min(r_lo + per, a.n_req);
   int64_t mine = 0;
 #pragma unroll 4
-  for (int r = r_lo; r < r_hi; ++r) mine += units_of(a.len[r], cap);
+  for (int r = r_lo; r < r_hi; ++r) mine += units_of<kUnit>(a.len[r], cap);
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -320,7 +338,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD, R>::kCtas)
   if (begin >= before * nv && begin < (before + mine) * nv) {
     int64_t at = before * nv;
     for (int r = r_lo; r < r_hi; ++r) {
-      const int len = a.len[r], units = units_of(len, cap);
+      const int len = a.len[r], units = units_of<kUnit>(len, cap);
       if (begin < at + (int64_t)units * nv) {
         const int off = (int)(begin - at);
         s_walk.r = r;
@@ -338,45 +356,64 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD, R>::kCtas)
   Walk cw = s_walk;  // the unit being computed
   Walk lw = cw;      // the unit being loaded
 
-  // ---- loads: lane l < 16 looks up the page of key l, all lanes copy
+  // ---- loads: every lane looks up the page of the first key, or, where 16 keys may
+  // lie in several pages, lane l that of key l % 16; then all lanes copy
   const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStageBytes;
-  const bool pow2 = (P & (P - 1)) == 0;
+  const bool pow2 = (P & (P - 1)) == 0, one_page = (P & (kKeys - 1)) == 0;
   const int shift = __ffs(P) - 1;
-  int page_next = 0;  // page id of this lane's key of unit lw
+  int page_next = 0;  // page id that this lane looked up for unit lw
   auto lookup = [&](const Walk& w) {
-    const int key = w.u * kUnit + warp * kKeys + (lane & 15);
+    const int key = w.u * kUnit + warp * kKeys + (one_page ? 0 : lane & 15);
     if (key >= w.len) return 0;
     const int i = pow2 ? key >> shift : key / P;
     return a.table[(int64_t)w.r * a.table_stride + i];
   };
   page_next = lookup(lw);
+  constexpr int kRowsPer = 32 / C::kChunks;  // rows of one copy instruction
+  const int c = lane % C::kChunks, row0 = lane / C::kChunks;
   auto load_unit = [&](int stage) {
     const int key0 = lw.u * kUnit + warp * kKeys;
-    const int key = key0 + (lane & 15);
-    const int in_page = pow2 ? key & (P - 1) : key % P;
     const bool ok = (unsigned)page_next < (unsigned)a.c.n_pages;
-    const bool bad = key < lw.len && !ok;
-    int64_t off = 0;
-    if (key < lw.len && ok)
-      off = (int64_t)page_next * a.c.page_stride + (int64_t)in_page * a.c.row_stride +
-            (int64_t)(lw.v / n_groups) * a.c.head_stride;
-    const unsigned live = __ballot_sync(0xffffffffu, key < lw.len && ok);
-    const bool any_bad = __any_sync(0xffffffffu, bad);
-    if (lane == 0) s_bad[warp][stage] = any_bad;
-    // per instruction: 32 chunks = 32 / kChunks rows
-    constexpr int kRowsPer = 32 / C::kChunks > 0 ? 32 / C::kChunks : 1;
-    const int c = lane % C::kChunks;
     const uint32_t kdst = ring + stage * C::kStageBytes, vdst = kdst + kKeys * C::kRowBytes;
+    if (one_page) {
+      const int in_page = pow2 ? key0 & (P - 1) : key0 % P;
+      const int live = ok ? lw.len - key0 : 0;
+      int64_t off = 0;
+      if (live > 0)
+        off = (int64_t)page_next * a.c.page_stride + (int64_t)(in_page + row0) * a.c.row_stride + (int64_t)(lw.v / n_groups) * a.c.head_stride;
+      const unsigned char* kp = static_cast<const unsigned char*>(a.c.k) + off * (int64_t)sizeof(T) + c * 16;
+      const unsigned char* vp = static_cast<const unsigned char*>(a.c.v) + off * (int64_t)sizeof(T) + c * 16;
+      const int64_t step = kRowsPer * a.c.row_stride * (int64_t)sizeof(T);
+      if (lane == 0) s_bad[warp][stage] = key0 < lw.len && !ok;
 #pragma unroll
-    for (int j = 0; j < kKeys / kRowsPer; ++j) {
-      const int row = j * kRowsPer + lane / C::kChunks;
-      const int64_t o = __shfl_sync(0xffffffffu, off, row) * (int64_t)sizeof(T) + c * 16;
-      const int bytes = (live >> row) & 1 ? 16 : 0;
-      const uint32_t d = (uint32_t)(row * C::kRowBytes + ((c ^ (row & 7)) << 4));
-      cp16(kdst + d, static_cast<const unsigned char*>(a.c.k) + o, bytes);
-      cp16(vdst + d, static_cast<const unsigned char*>(a.c.v) + o, bytes);
+      for (int j = 0; j < kKeys / kRowsPer; ++j) {
+        const int row = j * kRowsPer + row0, bytes = row < live ? 16 : 0;
+        const uint32_t d = (uint32_t)(row * C::kRowBytes + ((c ^ (row & 7)) << 4));
+        cp16(kdst + d, kp, bytes);
+        cp16(vdst + d, vp, bytes);
+        kp += step;
+        vp += step;
+      }
+    } else {
+      const int key = key0 + (lane & 15);
+      const int in_page = pow2 ? key & (P - 1) : key % P;
+      int64_t off = 0;
+      if (key < lw.len && ok)
+        off = (int64_t)page_next * a.c.page_stride + (int64_t)in_page * a.c.row_stride + (int64_t)(lw.v / n_groups) * a.c.head_stride;
+      const unsigned live = __ballot_sync(0xffffffffu, key < lw.len && ok);
+      const bool any_bad = __any_sync(0xffffffffu, key < lw.len && !ok);
+      if (lane == 0) s_bad[warp][stage] = any_bad;
+#pragma unroll
+      for (int j = 0; j < kKeys / kRowsPer; ++j) {
+        const int row = j * kRowsPer + row0;
+        const int64_t o = __shfl_sync(0xffffffffu, off, row) * (int64_t)sizeof(T) + c * 16;
+        const int bytes = (live >> row) & 1 ? 16 : 0;
+        const uint32_t d = (uint32_t)(row * C::kRowBytes + ((c ^ (row & 7)) << 4));
+        cp16(kdst + d, static_cast<const unsigned char*>(a.c.k) + o, bytes);
+        cp16(vdst + d, static_cast<const unsigned char*>(a.c.v) + o, bytes);
+      }
     }
-    walk_next(lw, a, nv, cap);
+    walk_next<kUnit>(lw, a, nv, cap);
   };
 
   int issued = 0;
@@ -390,51 +427,51 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD, R>::kCtas)
   }
 
   // ---- one (request, head block) after another
-  unsigned char* qs = smem + kWarps * C::kStages * C::kStageBytes;
+  // f32: this warp's softmax weights [key][query head]
+  float* pbuf = reinterpret_cast<float*>(smem + kWarps * C::kStages * C::kStageBytes) + warp * (kKeys * R);
   Piece piece[2];  // [1]: the one that starts in this share, [0]: the one that started before
   piece[0].rows = piece[1].rows = 0;
   const int g4 = lane >> 2, t4 = lane & 3;
   int stage = 0, seg = 0;
   for (int done = 0; done < count;) {
     const int r = cw.r, kvh = cw.v / n_groups, grp = cw.v % n_groups;
-    const int rows = min(kRows, G - grp * kRows);
-    const int head0 = kvh * G + grp * kRows;
+    const int rows = min(R, G - grp * R);
+    const int head0 = kvh * G + grp * R;
     const bool from_start = cw.u == 0;
     const int seg_units = min(cw.units - cw.u, count - done);
     const bool to_end = cw.u + seg_units == cw.units;
     const int seg_len = cw.len;
     const T* qrow = static_cast<const T*>(a.q) + (int64_t)r * a.q_stride + (int64_t)head0 * HD;
 
-    // Q as the A operand: 16-bit types in registers, f32 as tf32 hi/lo in shared memory
-    uint32_t qa[kF32 ? 1 : kSteps][4];
-    if constexpr (!kF32) {
+    // Q as the B operand, in registers: two dims of a head (16-bit types), or a
+    // dim's tf32 halves; heads that the block does not have are zeros
+    uint32_t qb[NH][kSteps][2], ql[kF32 ? NH : 1][kF32 ? kSteps : 1][2];
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int d = s * 16 + t4 * 2;
-        const uint32_t* lo = reinterpret_cast<const uint32_t*>(qrow + (int64_t)g4 * HD + d);
-        const uint32_t* hi = reinterpret_cast<const uint32_t*>(qrow + (int64_t)(g4 + 8) * HD + d);
-        qa[s][0] = g4 < rows ? lo[0] : 0u;
-        qa[s][2] = g4 < rows ? lo[4] : 0u;
-        qa[s][1] = g4 + 8 < rows ? hi[0] : 0u;
-        qa[s][3] = g4 + 8 < rows ? hi[4] : 0u;
-      }
-    } else {
-      // the barrier at the end of the previous segment freed qs
-      for (int i = tid; i < kRows * HD; i += kWarps * 32) {
-        const int row = i / HD, d = i % HD;
-        uint32_t hi = 0, lo = 0;
-        if (row < rows) split_tf32(__float_as_uint(reinterpret_cast<const float*>(qrow)[i]), &hi, &lo);
-        const uint32_t at = (uint32_t)(row * C::kRowBytes + (((d >> 2) ^ (row & 7)) << 4) + (d & 3) * 4);
-        *reinterpret_cast<uint32_t*>(qs + at) = hi;
-        *reinterpret_cast<uint32_t*>(qs + kRows * C::kRowBytes + at) = lo;
-      }
-      __syncthreads();
+    for (int h = 0; h < NH; ++h) {
+      const bool there = g4 + 8 * h < rows;
+      const uint32_t* q32 = reinterpret_cast<const uint32_t*>(qrow + (int64_t)(g4 + 8 * h) * HD);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t x = there ? q32[s * 8 + j * 4 + t4] : 0u;
+          if constexpr (kF32)
+            split_tf32(x, &qb[h][s][j], &ql[h][s][j]);
+          else
+            qb[h][s][j] = x;
+        }
     }
 
-    float o[kTiles][4];
+    // the thread's query heads are 8 h + 2 t4 and the next, its keys g4 and g4 + 8,
+    // its dims 16 n + g4 and 16 n + g4 + 8
+    float o[kTiles][NH][4], m[NH][2], l[NH][2];
 #pragma unroll
-    for (int n = 0; n < kTiles; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // rows g4, g4 + 8
+    for (int h = 0; h < NH; ++h) {
+      m[h][0] = m[h][1] = -INFINITY;
+      l[h][0] = l[h][1] = 0.f;
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n) o[n][h][0] = o[n][h][1] = o[n][h][2] = o[n][h][3] = 0.f;
+    }
     bool bad = false;
 
 #pragma unroll 1
@@ -454,133 +491,137 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD, R>::kCtas)
       bad |= s_bad[warp][stage] != 0;
       const uint32_t ks = ring + stage * C::kStageBytes, vs = ks + kKeys * C::kRowBytes;
 
-      // S = Q K^T: two n8 tiles of keys
-      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+      // S^T = K Q^T, in two chains of accumulators
+      float sc[NH][4], se[NH][4];
+#pragma unroll
+      for (int h = 0; h < NH; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc[h][j] = se[h][j] = 0.f;
       {
-        const int key = ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
+        const int key = lane & 15, half = lane >> 4;
         const uint32_t kaddr = ks + key * C::kRowBytes;
-        if constexpr (!kF32) {
 #pragma unroll
-          for (int s = 0; s < kSteps; ++s) {
-            uint32_t b[4];
-            ldsm4(b, kaddr + (((s * 2 + half) ^ (key & 7)) << 4));
-            mma(s0, qa[s], b[0], b[1], T());
-            mma(s1, qa[s], b[2], b[3], T());
-          }
-        } else {
-          // three tf32 products of the hi/lo halves; the small ones in sums of
-          // their own, so the large sum takes kSteps tensor-core adds
-          float e0[4] = {0.f, 0.f, 0.f, 0.f}, e1[4] = {0.f, 0.f, 0.f, 0.f};
-          const int qr = lane & 15, qh = lane >> 4;
-          const uint32_t qaddr = smem_u32(qs) + qr * C::kRowBytes;
+        for (int s = 0; s < kSteps; ++s) {
+          uint32_t x[4];
+          ldsm4(x, kaddr + (((s * 2 + half) ^ (key & 7)) << 4));
+          if constexpr (!kF32) {
 #pragma unroll
-          for (int s = 0; s < kSteps; ++s) {
-            uint32_t b[4], bh[4], bl[4], ah[4], al[4];
-            ldsm4(b, kaddr + (((s * 2 + half) ^ (key & 7)) << 4));
-            const uint32_t qo = qaddr + (((s * 2 + qh) ^ (qr & 7)) << 4);
-            ldsm4(ah, qo);
-            ldsm4(al, qo + kRows * C::kRowBytes);
+            for (int h = 0; h < NH; ++h) mma(s & 1 ? se[h] : sc[h], x, qb[h][s][0], qb[h][s][1], T());
+          } else {
+            // the small products in a chain of their own, so the large ones take
+            // kSteps tensor-core adds
+            uint32_t xh[4], xl[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) split_tf32(b[j], &bh[j], &bl[j]);
-            mma(s0, ah, bh[0], bh[1], T());
-            mma(s1, ah, bh[2], bh[3], T());
-            mma(e0, ah, bl[0], bl[1], T());
-            mma(e1, ah, bl[2], bl[3], T());
-            mma(e0, al, bh[0], bh[1], T());
-            mma(e1, al, bh[2], bh[3], T());
-          }
+            for (int j = 0; j < 4; ++j) split_tf32(x[j], &xh[j], &xl[j]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            s0[j] += e0[j];
-            s1[j] += e1[j];
+            for (int h = 0; h < NH; ++h) {
+              mma(sc[h], xh, qb[h][s][0], qb[h][s][1], T());
+              mma(se[h], xh, ql[h][s][0], ql[h][s][1], T());
+              mma(se[h], xl, qb[h][s][0], qb[h][s][1], T());
+            }
           }
         }
       }
 
       // online softmax in log2 units
       const int live = seg_len - ((cw.u + i) * kUnit + warp * kKeys);  // keys of this warp's 16
+      float cf[NH][2];
+      bool moved = false;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = t4 * 2 + (j & 1);
-        s0[j] = k < live ? s0[j] * scale_log2 : -INFINITY;
-        s1[j] = k + 8 < live ? s1[j] * scale_log2 : -INFINITY;
+      for (int h = 0; h < NH; ++h) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc[h][j] = g4 + (j >> 1) * 8 < live ? (sc[h][j] + se[h][j]) * scale_log2 : -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float n = fmaxf(sc[h][j], sc[h][j + 2]);
+          n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 4));
+          n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 8));
+          n = fmaxf(m[h][j], fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 16)));
+          // nothing seen so far: any finite reference gives p = 0
+          const float z = n == -INFINITY ? 0.f : n;
+          cf[h][j] = ex2(m[h][j] - z);
+          moved |= n != m[h][j];
+          m[h][j] = n;
+          sc[h][j] = ex2(sc[h][j] - z);
+          sc[h][j + 2] = ex2(sc[h][j + 2] - z);
+          // the sums stay per thread until the end of the piece
+          l[h][j] = fmaf(l[h][j], cf[h][j], sc[h][j] + sc[h][j + 2]);
+        }
       }
-      float n0 = fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s1[0], s1[1]));
-      float n1 = fmaxf(fmaxf(s0[2], s0[3]), fmaxf(s1[2], s1[3]));
-      n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, 1));
-      n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, 1));
-      n0 = fmaxf(m0, fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, 2)));
-      n1 = fmaxf(m1, fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, 2)));
-      // nothing seen so far: any finite reference gives p = 0
-      const float z0 = n0 == -INFINITY ? 0.f : n0, z1 = n1 == -INFINITY ? 0.f : n1;
-      const float c0 = ex2(m0 - z0), c1 = ex2(m1 - z1);
-      m0 = n0;
-      m1 = n1;
-      s0[0] = ex2(s0[0] - z0);
-      s0[1] = ex2(s0[1] - z0);
-      s1[0] = ex2(s1[0] - z0);
-      s1[1] = ex2(s1[1] - z0);
-      s0[2] = ex2(s0[2] - z1);
-      s0[3] = ex2(s0[3] - z1);
-      s1[2] = ex2(s1[2] - z1);
-      s1[3] = ex2(s1[3] - z1);
-      // the row sums stay per thread until the end of the segment
-      l0 = fmaf(l0, c0, (s0[0] + s0[1]) + (s1[0] + s1[1]));
-      l1 = fmaf(l1, c1, (s0[2] + s0[3]) + (s1[2] + s1[3]));
 
-      // O = O * c + P V: every unit's product in a fresh accumulator, added in f32
+      // O^T = O^T c + V^T P^T
       if constexpr (!kF32) {
-        const uint32_t p[4] = {pack2(s0[0], s0[1], T()), pack2(s0[2], s0[3], T()), pack2(s1[0], s1[1], T()),
-                               pack2(s1[2], s1[3], T())};
-        const int key = (((lane >> 3) & 1) << 3) + (lane & 7), half = lane >> 4;
+        // The weights are rounded to the cache's type (half a step of it, against
+        // the result's own rounding of as much); 16-bit results can take the
+        // tensor core's truncating adds in place.
+        uint32_t p[NH][2];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          p[h][0] = transpose8(pack2(sc[h][0], sc[h][1], T()));
+          p[h][1] = transpose8(pack2(sc[h][2], sc[h][3], T()));
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+          for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[n][h][j] *= cf[h][j & 1];
+        }
+        const int key = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
         const uint32_t vaddr = vs + key * C::kRowBytes;
 #pragma unroll
-        for (int d = 0; d < HD / 16; ++d) {
-          uint32_t b[4];
-          ldsm4t(b, vaddr + (((d * 2 + half) ^ (key & 7)) << 4));
+        for (int n = 0; n < kTiles; ++n) {
+          uint32_t x[4];
+          ldsm4t(x, vaddr + (((n * 2 + half) ^ (key & 7)) << 4));
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float f[4] = {0.f, 0.f, 0.f, 0.f};
-            mma(f, p, b[2 * j], b[2 * j + 1], T());
-            float* q = o[2 * d + j];
-            q[0] = fmaf(q[0], c0, f[0]);
-            q[1] = fmaf(q[1], c0, f[1]);
-            q[2] = fmaf(q[2], c1, f[2]);
-            q[3] = fmaf(q[3], c1, f[3]);
-          }
+          for (int h = 0; h < NH; ++h) mma(o[n][h], x, p[h][0], p[h][1], T());
         }
       } else {
-        // the MMA's k index t stands for key 2t, t + 4 for key 2t + 1 of a tile
-        // of 8: S's accumulator layout is then P's operand layout
-        uint32_t ph[2][4], pl[2][4];
-        const float* st[2] = {s0, s1};
+        // The weights change their layout through shared memory.  The MMA's k
+        // index t stands for key 2t, t + 4 for key 2t + 1 of eight, which spreads
+        // a fragment's V values over the banks.
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          split_tf32(__float_as_uint(st[k][0]), &ph[k][0], &pl[k][0]);
-          split_tf32(__float_as_uint(st[k][2]), &ph[k][1], &pl[k][1]);
-          split_tf32(__float_as_uint(st[k][1]), &ph[k][2], &pl[k][2]);
-          split_tf32(__float_as_uint(st[k][3]), &ph[k][3], &pl[k][3]);
-        }
+        for (int h = 0; h < NH; ++h)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            *reinterpret_cast<float2*>(pbuf + (g4 + 8 * j) * R + 8 * h + 2 * t4) = make_float2(sc[h][2 * j], sc[h][2 * j + 1]);
+        __syncwarp();
+        uint32_t ph[NH][2][2], pl[NH][2][2];
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              split_tf32(__float_as_uint(pbuf[(k * 8 + t4 * 2 + j) * R + 8 * h + g4]), &ph[h][k][j], &pl[h][k][j]);
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) {
-          float f[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
+          float f[NH][4], e[NH][4];
+#pragma unroll
+          for (int h = 0; h < NH; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[h][j] = e[h][j] = 0.f;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            uint32_t bh[2], bl[2];
+            uint32_t xh[4], xl[4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int key = k * 8 + t4 * 2 + j;
-              const uint32_t v = lds32(vs + key * C::kRowBytes + (((n * 2 + (g4 >> 2)) ^ (key & 7)) << 4) + (g4 & 3) * 4);
-              split_tf32(v, &bh[j], &bl[j]);
+            for (int j = 0; j < 4; ++j) {
+              // a0: dim g4, first key; a1: dim g4 + 8; a2, a3: the same of the second key
+              const int key = k * 8 + t4 * 2 + (j >> 1), chunk = n * 4 + (j & 1) * 2 + (g4 >> 2);
+              split_tf32(lds32(vs + key * C::kRowBytes + ((chunk ^ (key & 7)) << 4) + (g4 & 3) * 4), &xh[j], &xl[j]);
             }
-            mma(f, ph[k], bh[0], bh[1], T());
-            mma(e, ph[k], bl[0], bl[1], T());
-            mma(e, pl[k], bh[0], bh[1], T());
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+              mma(f[h], xh, ph[h][k][0], ph[h][k][1], T());
+              mma(e[h], xh, pl[h][k][0], pl[h][k][1], T());
+              mma(e[h], xl, ph[h][k][0], ph[h][k][1], T());
+            }
           }
-          o[n][0] = fmaf(o[n][0], c0, f[0] + e[0]);
-          o[n][1] = fmaf(o[n][1], c0, f[1] + e[1]);
-          o[n][2] = fmaf(o[n][2], c1, f[2] + e[2]);
-          o[n][3] = fmaf(o[n][3], c1, f[3] + e[3]);
+#pragma unroll
+          for (int h = 0; h < NH; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[n][h][j] = fmaf(o[n][h][j], cf[h][j & 1], f[h][j] + e[h][j]);
         }
       }
       if (++stage == C::kStages) stage = 0;
@@ -591,30 +632,34 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD, R>::kCtas)
     float* m_out = reinterpret_cast<float*>(smem + used * C::kStageBytes);  // of warp 0
     constexpr int kNext = C::kStages * C::kStageBytes / 4;                  // to the next warp's
 
-    // ---- join the four warps; write the result or this share's partial
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-    if (t4 == 0) {
-      m_ml[warp * R + g4] = make_float2(m0, l0);
-      if constexpr (R > 8) m_ml[warp * R + g4 + 8] = make_float2(m1, l1);
-    }
+    // ---- join the warps; write the result or this share's partial
     float* mo = m_out + warp * kNext;
     __syncwarp();
 #pragma unroll
-    for (int n = 0; n < kTiles; ++n) {
-      const int d = n * 8 + t4 * 2;
-      if (g4 < rows) *reinterpret_cast<float2*>(mo + g4 * HD + d) = make_float2(o[n][0], o[n][1]);
-      if constexpr (R > 8)
-        if (g4 + 8 < rows) *reinterpret_cast<float2*>(mo + (g4 + 8) * HD + d) = make_float2(o[n][2], o[n][3]);
-    }
+    for (int h = 0; h < NH; ++h)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float sum = l[h][j];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        const int head = 8 * h + 2 * t4 + j;
+        if (g4 == 0) m_ml[warp * R + head] = make_float2(m[h][j], sum);
+        if (head < rows) {
+          // (dims of neighbouring head pairs are swapped in eights, for the banks)
+#pragma unroll
+          for (int n = 0; n < kTiles; ++n) {
+            mo[head * HD + ((n * 16 + g4) ^ (t4 * 8))] = o[n][h][j];
+            mo[head * HD + ((n * 16 + 8 + g4) ^ (t4 * 8))] = o[n][h][j + 2];
+          }
+        }
+      }
     if (bad && lane == 0) s_segbad[seg & 1] = 1;
     __syncthreads();
     const bool seg_bad = s_segbad[seg & 1] != 0;
     const bool whole = from_start && to_end;
     if (seg_bad && tid == 0) set_error(a.status, MINFER_ERR_POS_OOB);
-    float* part = ws_part + (int64_t)(blockIdx.x * 2 + (from_start ? 1 : 0)) * ws_part_floats(HD);
+    float* part = ws_part + (int64_t)(blockIdx.x * 2 + (from_start ? 1 : 0)) * part_floats(R, HD);
     for (int i = tid; i < rows * HD; i += kWarps * 32) {
       const int row = i / HD, d = i % HD;
       float m = -INFINITY;
@@ -627,7 +672,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD, R>::kCtas)
         const float2 ml = m_ml[w * R + row];
         const float c = ex2(ml.x - z);
         l = fmaf(ml.y, c, l);
-        acc = fmaf(m_out[w * kNext + i], c, acc);
+        acc = fmaf(m_out[w * kNext + row * HD + (d ^ (((row >> 1) & 3) * 8))], c, acc);
       }
       if (whole) {
         if (!seg_bad) {
@@ -636,7 +681,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD, R>::kCtas)
         }
       } else {
         if (d == 0) reinterpret_cast<float2*>(part)[row] = make_float2(m, seg_bad ? -1.f : l);
-        part[2 * kRows + i] = acc;
+        part[2 * R + i] = acc;
       }
     }
     // flag of the next piece, free since the barrier above
@@ -650,7 +695,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD, R>::kCtas)
     }
     // on to the next (request, head block)
     cw.u = cw.units - 1;
-    walk_next(cw, a, nv, cap);
+    walk_next<kUnit>(cw, a, nv, cap);
   }
 
   // ---- report the partials (complete since the last barrier) and join what is
@@ -678,13 +723,13 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD, R>::kCtas)
     const Piece p = i ? piece[1] : piece[0];
     T* o_row = static_cast<T*>(a.o) + (int64_t)p.r * a.o_stride + (int64_t)p.head0 * HD;
     float* lse_row = a.lse ? a.lse + (int64_t)p.r * a.nh + p.head0 : nullptr;
-    auto slot = [&](int c) { return ws_part + (int64_t)(c * 2 + (c == p.c0 ? 1 : 0)) * ws_part_floats(HD); };
+    auto slot = [&](int c) { return ws_part + (int64_t)(c * 2 + (c == p.c0 ? 1 : 0)) * part_floats(R, HD); };
     const bool direct = p.c1 - p.c0 + 1 <= kDirect;
     const int lo = direct ? p.c0 : max(p.c0, g * kGroup), hi = direct ? p.c1 : min(p.c1, g * kGroup + kGroup - 1);
     if (hi > lo) {
       if (tid <= hi - lo) s_join.part[tid] = slot(lo + tid);
       __syncthreads();
-      join_parts<T, HD, R>(s_join, hi - lo + 1, p.rows, direct, o_row, lse_row);
+      join_parts<T, HD, R, kWarps * 32>(s_join, hi - lo + 1, p.rows, direct, o_row, lse_row);
       __syncthreads();
     }
     if (!direct) {
@@ -698,45 +743,62 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<T, HD, R>::kCtas)
       }
       if (tid <= g1 - g0) s_join.part[tid] = slot(max(p.c0, (g0 + tid) * kGroup));
       __syncthreads();
-      if (s_segbad[0]) join_parts<T, HD, R>(s_join, g1 - g0 + 1, p.rows, true, o_row, lse_row);
+      if (s_segbad[0]) join_parts<T, HD, R, kWarps * 32>(s_join, g1 - g0 + 1, p.rows, true, o_row, lse_row);
       __syncthreads();
     }
   }
   idle_requests();
 }
 
-int shares(int hd, int type, int num_sms) {
-  return std::min(num_sms * (hd * (type == MINFER_F32 ? 4 : 2) == 512 ? 1 : 2), kMaxShares);
+template <typename T, int HD, int R>
+int shares(int num_sms) {
+  return std::min(num_sms * Cfg<T, HD, R>::kCtas, kMaxShares);
 }
 
-template <typename T, int HD, int R>
-cudaError_t launch(const PagedAttnArgs& a, int n, int n_groups, cudaStream_t st) {
-  using C = Cfg<T, HD, R>;
-  auto kernel = paged_attn_kernel<T, HD, R>;
-  cudaError_t e = allow_smem<paged_attn_kernel<T, HD, R>>(C::kSmem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3((unsigned)n), dim3(kWarps * 32), C::kSmem, st, a, n_groups, a.scale * kLog2e);
+// Runs f with the type, head size and heads of a block that the call's sizes
+// pick: blocks of 16 heads where a KV head has more than 8 and the cache is
+// 16-bit (an f32 block of 16 does not fit the registers; its blocks of 8 read K
+// and V again, out of L2 for the most part).
+template <typename F>
+auto with_config(int type, int hd, int G, F f) {
+  auto sized = [&](auto t) {
+    using T = decltype(t);
+    if constexpr (sizeof(T) == 2)
+      if (G > 8)
+        return hd == 64 ? f.template operator()<T, 64, 16>() : f.template operator()<T, 128, 16>();
+    return hd == 64 ? f.template operator()<T, 64, 8>() : f.template operator()<T, 128, 8>();
+  };
+  return type == MINFER_F32 ? sized(float()) : type == MINFER_F16 ? sized(__half()) : sized(__nv_bfloat16());
 }
-template <typename T, int HD>
-cudaError_t launch(const PagedAttnArgs& a, int type, int num_sms, cudaStream_t st) {
-  const int G = a.nh / a.c.nkv, n_groups = (G + kRows - 1) / kRows, n = shares(HD, type, num_sms);
-  return G <= 8 ? launch<T, HD, 8>(a, n, n_groups, st) : launch<T, HD, 16>(a, n, n_groups, st);
-}
+
+struct Launch {
+  const PagedAttnArgs& a;
+  int num_sms;
+  cudaStream_t st;
+  template <typename T, int HD, int R>
+  cudaError_t operator()() {
+    using C = Cfg<T, HD, R>;
+    const int G = a.nh / a.c.nkv, n_groups = (G + R - 1) / R;
+    const cudaError_t e = allow_smem<paged_attn_kernel<T, HD, R>>(C::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(paged_attn_kernel<T, HD, R>, dim3((unsigned)shares<T, HD, R>(num_sms)), dim3(C::kWarps * 32), C::kSmem, st, a,
+                      n_groups, a.scale * kLog2e);
+  }
+};
+struct Bytes {
+  int num_sms;
+  template <typename T, int HD, int R>
+  int64_t operator()() {
+    return kPartOffset + (int64_t)shares<T, HD, R>(num_sms) * 2 * part_floats(R, HD) * 4;
+  }
+};
 
 }  // namespace
 
-int64_t paged_attn_workspace(int hd, int type, int num_sms) {
-  const int n = shares(hd, type, num_sms);
-  return kPartOffset + (int64_t)n * 2 * ws_part_floats(hd) * 4;
-}
+int64_t paged_attn_workspace(int G, int hd, int type, int num_sms) { return with_config(type, hd, G, Bytes{num_sms}); }
 
 cudaError_t paged_attn_launch(const PagedAttnArgs& a, int type, int num_sms, cudaStream_t st) {
-  if (type == MINFER_F32)
-    return a.c.hd == 64 ? launch<float, 64>(a, type, num_sms, st) : launch<float, 128>(a, type, num_sms, st);
-  if (type == MINFER_F16)
-    return a.c.hd == 64 ? launch<__half, 64>(a, type, num_sms, st) : launch<__half, 128>(a, type, num_sms, st);
-  return a.c.hd == 64 ? launch<__nv_bfloat16, 64>(a, type, num_sms, st)
-                      : launch<__nv_bfloat16, 128>(a, type, num_sms, st);
+  return with_config(type, a.c.hd, a.nh / a.c.nkv, Launch{a, num_sms, st});
 }
 
 }  // namespace minfer

@@ -391,7 +391,7 @@ struct PagedAttnArgs {
   void* ws;
   int* status;
 };
-int64_t paged_attn_workspace(int hd, int type, int num_sms);
+int64_t paged_attn_workspace(int G, int hd, int type, int num_sms);
 cudaError_t paged_attn_launch(const PagedAttnArgs& a, int type, int num_sms, cudaStream_t stream);
 
 // k_logprobs.cu: log probabilities, entropy and top k of logits rows.
