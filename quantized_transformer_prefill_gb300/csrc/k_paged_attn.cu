@@ -53,9 +53,9 @@ constexpr int kDirect = 32;             // partials that are joined in one step
 // What the threads of a CTA share while they join partials.
 template <int R>
 struct JoinShared {
-  float* part[kMaxJoin];    // the partials, in the order of their shares
-  float2 ml[kMaxJoin][R];   // their (max, sum); then .x the weight
-  float2 out[R];            // the joined (max, sum)
+  float* part[kMaxJoin];  // the partials, in the order of their shares
+  float w[kMaxJoin][R];   // their weights
+  float2 out[R];          // the joined (max, sum)
   int bad;
 };
 
@@ -72,7 +72,7 @@ struct Cfg {
   static constexpr int kCtas = kRowBytes == 128 ? 4 : R == 8 ? 3 : 2;
   static constexpr int kUnit = kWarps * kKeys;  // keys of a unit
   static constexpr int kPBytes = kF32 ? kWarps * kKeys * R * 4 : 0;  // softmax weights on their way to the other layout
-  static constexpr int kStatic = (int)sizeof(JoinShared<R>) + 768 + kWarps * R * 8;
+  static constexpr int kStatic = (int)sizeof(JoinShared<R>) + 512 + kWarps * R * 8 + R * 16;
   static constexpr int kFit = (233472 / kCtas - 1024 - kStatic - kPBytes) / (kWarps * kStageBytes);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
   static constexpr int kSmem = kWarps * kStages * kStageBytes + kPBytes;
@@ -189,69 +189,118 @@ __device__ __forceinline__ void walk_next(Walk& w, const PagedAttnArgs& a, int n
   } while (w.units == 0 && w.r < a.n_req);
 }
 
-// The units are cut into as many shares as there are CTAs, but no empty ones;
-// share c begins at share_begin(c).
-__device__ __forceinline__ int share_count(int64_t total, int n_ctas) { return (int)min(total, (int64_t)n_ctas); }
-__device__ __forceinline__ int64_t share_begin(int64_t total, int c, int n) { return total * c / n; }
+// How the units are cut into shares: as many as there are CTAs, but none with
+// less than kLeast units (a share more costs a join, which takes as long as a few
+// units); the first `more` of them hold one unit more than the others.
+constexpr int kLeast = 1;
+struct Shares {
+  int64_t total, each;
+  int n, more;
+  __device__ __forceinline__ Shares(int64_t units, int n_ctas) {
+    total = units;
+    n = (int)max((int64_t)1, min(units / kLeast, (int64_t)n_ctas));
+    // (64-bit divisions are long; few batches need one)
+    each = total >> 32 ? total / n : (int64_t)((uint32_t)total / (uint32_t)n);
+    more = (int)(total - each * n);
+  }
+  __device__ __forceinline__ int64_t begin(int c) const { return each * c + min(c, more); }
+  // the share that holds unit x
+  __device__ __forceinline__ int of(int64_t x) const {
+    const int64_t low = (each + 1) * more, y = x < low ? x : x - low, d = x < low ? each + 1 : each;
+    return (x < low ? 0 : more) + (int)(y >> 32 ? y / d : (int64_t)((uint32_t)y / (uint32_t)d));
+  }
+};
 
-// The share that holds unit x: the largest c with share_begin(c) <= x.
-__device__ __forceinline__ int share_of(int64_t x, int64_t total, int n) {
-  int c = (int)min((x * n) / total, (int64_t)n - 1);
-  while (c + 1 < n && share_begin(total, c + 1, n) <= x) ++c;
-  while (share_begin(total, c, n) > x) --c;
-  return c;
-}
-
-// Joins `count` partials: weights first, then every thread four dims of a row at
-// a time.  final: the result goes to o and lse, else it replaces the first
+// Joins `count` partials.  Their outputs are copied to shared memory (ring, all
+// of them at once or as many as fit) while the weights are worked out, a warp
+// per row and a lane per partial; then every thread adds up four dims of a row
+// at a time.  final: the result goes to o and lse, else it replaces the first
 // partial.  A sum below 0 marks a piece that met a bad page; it spoils the
 // whole.  All threads; s.part is written before a barrier of the caller's.
-template <typename T, int HD, int R, int kThreads>
-__device__ void join_parts(JoinShared<R>& s, int count, int rows, bool final, T* o, float* lse) {
-  const int tid = threadIdx.x;
-  for (int i = tid; i < count * R; i += kThreads)
-    if (i % R < rows) s.ml[i / R][i % R] = __ldcg(reinterpret_cast<const float2*>(s.part[i / R]) + i % R);
+template <typename T, int HD, int R, int kWarps>
+__device__ void join_parts(JoinShared<R>& s, unsigned char* ring, int ring_bytes, int count, int rows, bool final, T* o, float* lse) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int items = rows * HD / 4, fit = min(count, ring_bytes / (items * 16));
+  auto copy = [&](int p0) {
+    const int n = min(fit, count - p0);
+    for (int i = tid; i < n * items; i += kWarps * 32) {
+      const int p = i / items;
+      cp16(smem_u32(ring) + i * 16, reinterpret_cast<const float4*>(s.part[p0 + p] + 2 * R) + (i - p * items), 16);
+    }
+    cp_commit();
+  };
+  copy(0);
   if (tid == 0) s.bad = 0;
   __syncthreads();
-  if (tid < rows) {
+  for (int row = warp; row < rows; row += kWarps) {
+    float2 ml[kMaxJoin / 32];
     float m = -INFINITY;
-    for (int i = 0; i < count; ++i) m = fmaxf(m, s.ml[i][tid].x);
+#pragma unroll
+    for (int j = 0; j < kMaxJoin / 32; ++j) {
+      ml[j] = make_float2(-INFINITY, 0.f);
+      if (lane + 32 * j < count) ml[j] = __ldcg(reinterpret_cast<const float2*>(s.part[lane + 32 * j]) + row);
+      m = fmaxf(m, ml[j].x);
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
     const float z = m == -INFINITY ? 0.f : m;
     float l = 0.f;
     bool bad = false;
-    for (int i = 0; i < count; ++i) {
-      const float2 ml = s.ml[i][tid];
-      const float c = ex2(ml.x - z);
-      bad |= ml.y < 0.f;
-      l = fmaf(ml.y, c, l);
-      s.ml[i][tid].x = c;
+#pragma unroll
+    for (int j = 0; j < kMaxJoin / 32; ++j) {
+      const float c = ex2(ml[j].x - z);
+      if (lane + 32 * j < count) s.w[lane + 32 * j][row] = c;
+      bad |= ml[j].y < 0.f;
+      l = fmaf(ml[j].y, c, l);
     }
-    s.out[tid] = make_float2(m, l);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
     if (bad) s.bad = 1;
+    if (lane == 0) s.out[row] = make_float2(m, l);
   }
-  __syncthreads();
-  const bool bad = s.bad != 0;
-  for (int i = tid; i < rows * HD / 4; i += kThreads) {
-    const int row = i / (HD / 4);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int p = 0; p < count; ++p) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(s.part[p] + 2 * R) + i);
-      const float c = s.ml[p][row].x;
-      acc.x = fmaf(x.x, c, acc.x);
-      acc.y = fmaf(x.y, c, acc.y);
-      acc.z = fmaf(x.z, c, acc.z);
-      acc.w = fmaf(x.w, c, acc.w);
+  constexpr int kItems = (R * HD / 4 + kWarps * 32 - 1) / (kWarps * 32);  // of a thread
+  float4 acc[kItems];
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p0 = 0; p0 < count; p0 += fit) {
+    cp_wait<0>();
+    __syncthreads();  // the copies of all threads; the weights
+    const int n = min(fit, count - p0);
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const int i = tid + k * kWarps * 32;
+      if (i >= items) break;
+      const float4* x = reinterpret_cast<const float4*>(ring) + i;
+      const int row = i / (HD / 4);
+#pragma unroll 4
+      for (int p = 0; p < n; ++p) {
+        const float4 v = x[p * items];
+        const float c = s.w[p0 + p][row];
+        acc[k].x = fmaf(v.x, c, acc[k].x);
+        acc[k].y = fmaf(v.y, c, acc[k].y);
+        acc[k].z = fmaf(v.z, c, acc[k].z);
+        acc[k].w = fmaf(v.w, c, acc[k].w);
+      }
     }
+    if (p0 + fit < count) {
+      __syncthreads();
+      copy(p0 + fit);
+    }
+  }
+  const bool bad = s.bad != 0;
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    const int i = tid + k * kWarps * 32;
+    if (i >= items) break;
     if (!final) {
-      reinterpret_cast<float4*>(s.part[0] + 2 * R)[i] = acc;  // read by this thread alone
+      reinterpret_cast<float4*>(s.part[0] + 2 * R)[i] = acc[k];
     } else if (!bad) {
-      const float l = s.out[row].y, f = l == 0.f ? 0.f : 1.f / l;
+      const float l = s.out[i / (HD / 4)].y, f = l == 0.f ? 0.f : 1.f / l;
       T* dst = o + i * 4;
-      store_as(dst, acc.x * f);
-      store_as(dst + 1, acc.y * f);
-      store_as(dst + 2, acc.z * f);
-      store_as(dst + 3, acc.w * f);
+      store_as(dst, acc[k].x * f);
+      store_as(dst + 1, acc[k].y * f);
+      store_as(dst + 2, acc[k].z * f);
+      store_as(dst + 3, acc[k].w * f);
     }
   }
   if (tid < rows) {
@@ -261,6 +310,14 @@ __device__ void join_parts(JoinShared<R>& s, int count, int rows, bool final, T*
     else if (!bad && lse)
       lse[tid] = fmaf(ml.x, kLn2, logf(ml.y));
   }
+}
+
+// Counts this CTA's arrival: its writes before the last barrier are released, and
+// what the CTAs released that came before is acquired.
+__device__ __forceinline__ unsigned arrive(unsigned* counter) {
+  unsigned before;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+  return before;
 }
 
 // A piece of a (request, head block) that other shares hold pieces of too.
@@ -284,6 +341,8 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
   __shared__ int s_segbad[2], s_last[2];
   __shared__ JoinShared<R> s_join;
   __shared__ float2 m_ml[kWarps * R];  // the warps' (max, sum) at the end of a piece
+  __shared__ float4 m_w[R];            // their weights
+  static_assert(kWarps <= 4, "a float4 of weights");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int P = a.c.page_size, cap = a.max_pages * P;
   const int G = a.nh / a.c.nkv, nv = a.c.nkv * n_groups;
@@ -328,13 +387,13 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
       }
     }
   };
-  const int n_shares = share_count(total, gridDim.x);
-  if ((int)blockIdx.x >= n_shares) {
+  const Shares shares(total, gridDim.x);
+  if (total == 0 || (int)blockIdx.x >= shares.n) {
     idle_requests();
     return;
   }
-  const int64_t begin = share_begin(total, blockIdx.x, n_shares);
-  const int count = (int)(share_begin(total, blockIdx.x + 1, n_shares) - begin);
+  const int64_t begin = shares.begin(blockIdx.x);
+  const int count = (int)(shares.begin(blockIdx.x + 1) - begin);
   if (begin >= before * nv && begin < (before + mine) * nv) {
     int64_t at = before * nv;
     for (int r = r_lo; r < r_hi; ++r) {
@@ -433,34 +492,44 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
   piece[0].rows = piece[1].rows = 0;
   const int g4 = lane >> 2, t4 = lane & 3;
   int stage = 0, seg = 0;
+  // Q's words of the (request, head block) that comes next, loaded while the one
+  // before is being joined; heads that the block does not have are zeros
+  uint32_t qx[NH][kSteps][2];
+  auto load_q = [&] {
+    const int grp = cw.v % n_groups, rows = min(R, G - grp * R), head0 = cw.v / n_groups * G + grp * R;
+    const T* qrow = static_cast<const T*>(a.q) + (int64_t)cw.r * a.q_stride + (int64_t)head0 * HD;
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      const uint32_t* q32 = reinterpret_cast<const uint32_t*>(qrow + (int64_t)(g4 + 8 * h) * HD);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) qx[h][s][j] = g4 + 8 * h < rows ? q32[s * 8 + j * 4 + t4] : 0u;
+    }
+  };
+  load_q();
   for (int done = 0; done < count;) {
     const int r = cw.r, kvh = cw.v / n_groups, grp = cw.v % n_groups;
     const int rows = min(R, G - grp * R);
     const int head0 = kvh * G + grp * R;
     const bool from_start = cw.u == 0;
     const int seg_units = min(cw.units - cw.u, count - done);
-    const bool to_end = cw.u + seg_units == cw.units;
+    const bool whole = from_start && cw.u + seg_units == cw.units;
     const int seg_len = cw.len;
-    const T* qrow = static_cast<const T*>(a.q) + (int64_t)r * a.q_stride + (int64_t)head0 * HD;
-
-    // Q as the B operand, in registers: two dims of a head (16-bit types), or a
-    // dim's tf32 halves; heads that the block does not have are zeros
+    const int first_unit = cw.u, all_units = cw.units;
+    // Q as the B operand: two dims of a head (16-bit types), or a dim's tf32 halves
     uint32_t qb[NH][kSteps][2], ql[kF32 ? NH : 1][kF32 ? kSteps : 1][2];
 #pragma unroll
-    for (int h = 0; h < NH; ++h) {
-      const bool there = g4 + 8 * h < rows;
-      const uint32_t* q32 = reinterpret_cast<const uint32_t*>(qrow + (int64_t)(g4 + 8 * h) * HD);
+    for (int h = 0; h < NH; ++h)
 #pragma unroll
       for (int s = 0; s < kSteps; ++s)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const uint32_t x = there ? q32[s * 8 + j * 4 + t4] : 0u;
           if constexpr (kF32)
-            split_tf32(x, &qb[h][s][j], &ql[h][s][j]);
+            split_tf32(qx[h][s][j], &qb[h][s][j], &ql[h][s][j]);
           else
-            qb[h][s][j] = x;
+            qb[h][s][j] = qx[h][s][j];
         }
-    }
 
     // the thread's query heads are 8 h + 2 t4 and the next, its keys g4 and g4 + 8,
     // its dims 16 n + g4 and 16 n + g4 + 8
@@ -524,7 +593,7 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
       }
 
       // online softmax in log2 units
-      const int live = seg_len - ((cw.u + i) * kUnit + warp * kKeys);  // keys of this warp's 16
+      const int live = seg_len - ((first_unit + i) * kUnit + warp * kKeys);  // keys of this warp's 16
       float cf[NH][2];
       bool moved = false;
 #pragma unroll
@@ -626,6 +695,11 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
       }
       if (++stage == C::kStages) stage = 0;
     }
+    // on to the next (request, head block)
+    cw.u = all_units - 1;
+    walk_next<kUnit>(cw, a, nv, cap);
+    if (done < count) load_q();
+
     // the outputs go to the stage that every warp has just used, which is
     // filled again only after the barriers below
     const int used = (stage == 0 ? C::kStages : stage) - 1;
@@ -657,31 +731,53 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
     if (bad && lane == 0) s_segbad[seg & 1] = 1;
     __syncthreads();
     const bool seg_bad = s_segbad[seg & 1] != 0;
-    const bool whole = from_start && to_end;
-    if (seg_bad && tid == 0) set_error(a.status, MINFER_ERR_POS_OOB);
     float* part = ws_part + (int64_t)(blockIdx.x * 2 + (from_start ? 1 : 0)) * part_floats(R, HD);
-    for (int i = tid; i < rows * HD; i += kWarps * 32) {
-      const int row = i / HD, d = i % HD;
-      float m = -INFINITY;
+    if (tid < rows) {
+      // the warps' weights of a row; of a whole piece with 1 / sum in them
+      float mx = -INFINITY, sum = 0.f, c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, m_ml[w * R + row].x);
-      const float z = m == -INFINITY ? 0.f : m;
-      float l = 0.f, acc = 0.f;
+      for (int k = 0; k < kWarps; ++k) mx = fmaxf(mx, m_ml[k * R + tid].x);
+      const float z = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 ml = m_ml[w * R + row];
-        const float c = ex2(ml.x - z);
-        l = fmaf(ml.y, c, l);
-        acc = fmaf(m_out[w * kNext + row * HD + (d ^ (((row >> 1) & 3) * 8))], c, acc);
+      for (int k = 0; k < kWarps; ++k) {
+        const float2 ml = m_ml[k * R + tid];
+        c[k] = ex2(ml.x - z);
+        sum = fmaf(ml.y, c[k], sum);
       }
-      if (whole) {
-        if (!seg_bad) {
-          store_as(static_cast<T*>(a.o) + (int64_t)r * a.o_stride + (int64_t)head0 * HD + i, l == 0.f ? 0.f : acc / l);
-          if (d == 0 && a.lse) a.lse[(int64_t)r * a.nh + head0 + row] = fmaf(m, kLn2, logf(l));
-        }
+      if (!whole) {
+        reinterpret_cast<float2*>(part)[tid] = make_float2(mx, seg_bad ? -1.f : sum);
       } else {
-        if (d == 0) reinterpret_cast<float2*>(part)[row] = make_float2(m, seg_bad ? -1.f : l);
-        part[2 * R + i] = acc;
+        const float f = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) c[k] *= f;
+        if (!seg_bad && a.lse) a.lse[(int64_t)r * a.nh + head0 + tid] = fmaf(mx, kLn2, logf(sum));
+      }
+      m_w[tid] = make_float4(c[0], c[1], c[2], c[3]);
+    }
+    __syncthreads();
+    if (seg_bad && tid == 0) set_error(a.status, MINFER_ERR_POS_OOB);
+    // four dims of a row at a time
+    for (int i = tid; i < rows * HD / 4; i += kWarps * 32) {
+      const int row = i / (HD / 4), d = (i - row * (HD / 4)) * 4;
+      const float4 w = m_w[row];
+      const float c[4] = {w.x, w.y, w.z, w.w};
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        const float4 x = *reinterpret_cast<const float4*>(m_out + k * kNext + row * HD + (d ^ (((row >> 1) & 3) * 8)));
+        acc.x = fmaf(x.x, c[k], acc.x);
+        acc.y = fmaf(x.y, c[k], acc.y);
+        acc.z = fmaf(x.z, c[k], acc.z);
+        acc.w = fmaf(x.w, c[k], acc.w);
+      }
+      if (!whole) {
+        reinterpret_cast<float4*>(part + 2 * R)[i] = acc;
+      } else if (!seg_bad) {
+        T* dst = static_cast<T*>(a.o) + (int64_t)r * a.o_stride + (int64_t)head0 * HD + i * 4;
+        store_as(dst, acc.x);
+        store_as(dst + 1, acc.y);
+        store_as(dst + 2, acc.z);
+        store_as(dst + 3, acc.w);
       }
     }
     // flag of the next piece, free since the barrier above
@@ -689,13 +785,10 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
     __syncthreads();
     ++seg;
     if (!whole) {
-      const int64_t first = begin + (done - seg_units) - cw.u;
+      const int64_t first = begin + (done - seg_units) - first_unit;
       Piece& p = piece[from_start ? 1 : 0];
-      p = Piece{r, head0, rows, share_of(first, total, n_shares), share_of(first + cw.units - 1, total, n_shares)};
+      p = Piece{r, head0, rows, shares.of(first), shares.of(first + all_units - 1)};
     }
-    // on to the next (request, head block)
-    cw.u = cw.units - 1;
-    walk_next<kUnit>(cw, a, nv, cap);
   }
 
   // ---- report the partials (complete since the last barrier) and join what is
@@ -709,10 +802,8 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
       const int lo = max(p.c0, g * kGroup), hi = min(p.c1, g * kGroup + kGroup - 1);
       const int n = all <= kDirect ? all : hi - lo + 1;
       unsigned* counter = counters + (all <= kDirect || p.c0 >= g * kGroup ? p.c0 : kMaxShares + g);
-      __threadfence();
-      last = n == 1 || atomicAdd(counter, 1u) == (unsigned)n - 1;
+      last = n == 1 || arrive(counter) == (unsigned)n - 1;
       if (last && n > 1) *counter = 0;
-      __threadfence();
     }
     s_last[warp] = last;
   }
@@ -729,21 +820,19 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
     if (hi > lo) {
       if (tid <= hi - lo) s_join.part[tid] = slot(lo + tid);
       __syncthreads();
-      join_parts<T, HD, R, kWarps * 32>(s_join, hi - lo + 1, p.rows, direct, o_row, lse_row);
+      join_parts<T, HD, R, kWarps>(s_join, smem, kWarps * C::kStages * C::kStageBytes, hi - lo + 1, p.rows, direct, o_row, lse_row);
       __syncthreads();
     }
     if (!direct) {
       const int g0 = p.c0 / kGroup, g1 = p.c1 / kGroup;
       if (tid == 0) {
         unsigned* counter = counters + kMaxShares + kMaxShares / kGroup + 1 + p.c0;
-        __threadfence();
-        s_segbad[0] = atomicAdd(counter, 1u) == (unsigned)(g1 - g0);
+        s_segbad[0] = arrive(counter) == (unsigned)(g1 - g0);
         if (s_segbad[0]) *counter = 0;
-        __threadfence();
       }
       if (tid <= g1 - g0) s_join.part[tid] = slot(max(p.c0, (g0 + tid) * kGroup));
       __syncthreads();
-      if (s_segbad[0]) join_parts<T, HD, R, kWarps * 32>(s_join, g1 - g0 + 1, p.rows, true, o_row, lse_row);
+      if (s_segbad[0]) join_parts<T, HD, R, kWarps>(s_join, smem, kWarps * C::kStages * C::kStageBytes, g1 - g0 + 1, p.rows, true, o_row, lse_row);
       __syncthreads();
     }
   }
@@ -751,7 +840,7 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
 }
 
 template <typename T, int HD, int R>
-int shares(int num_sms) {
+int ctas(int num_sms) {
   return std::min(num_sms * Cfg<T, HD, R>::kCtas, kMaxShares);
 }
 
@@ -781,7 +870,7 @@ struct Launch {
     const int G = a.nh / a.c.nkv, n_groups = (G + R - 1) / R;
     const cudaError_t e = allow_smem<paged_attn_kernel<T, HD, R>>(C::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(paged_attn_kernel<T, HD, R>, dim3((unsigned)shares<T, HD, R>(num_sms)), dim3(C::kWarps * 32), C::kSmem, st, a,
+    return launch_pdl(paged_attn_kernel<T, HD, R>, dim3((unsigned)ctas<T, HD, R>(num_sms)), dim3(C::kWarps * 32), C::kSmem, st, a,
                       n_groups, a.scale * kLog2e);
   }
 };
@@ -789,7 +878,7 @@ struct Bytes {
   int num_sms;
   template <typename T, int HD, int R>
   int64_t operator()() {
-    return kPartOffset + (int64_t)shares<T, HD, R>(num_sms) * 2 * part_floats(R, HD) * 4;
+    return kPartOffset + (int64_t)ctas<T, HD, R>(num_sms) * 2 * part_floats(R, HD) * 4;
   }
 };
 
