@@ -220,12 +220,17 @@ struct Shares {
 template <typename T, int HD, int R, int kWarps>
 __device__ void join_parts(JoinShared<R>& s, unsigned char* ring, int ring_bytes, int count, int rows, bool final, T* o, float* lse) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kItems = (R * HD / 4 + kWarps * 32 - 1) / (kWarps * 32);  // of a thread
   const int items = rows * HD / 4, fit = min(count, ring_bytes / (items * 16));
   auto copy = [&](int p0) {
     const int n = min(fit, count - p0);
-    for (int i = tid; i < n * items; i += kWarps * 32) {
-      const int p = i / items;
-      cp16(smem_u32(ring) + i * 16, reinterpret_cast<const float4*>(s.part[p0 + p] + 2 * R) + (i - p * items), 16);
+    uint32_t dst = smem_u32(ring) + tid * 16;
+#pragma unroll 4
+    for (int p = 0; p < n; ++p, dst += items * 16) {
+      const float4* src = reinterpret_cast<const float4*>(s.part[p0 + p] + 2 * R) + tid;
+#pragma unroll
+      for (int k = 0; k < kItems; ++k)
+        if (tid + k * kWarps * 32 < items) cp16(dst + k * kWarps * 512, src + k * kWarps * 32, 16);
     }
     cp_commit();
   };
@@ -258,7 +263,6 @@ __device__ void join_parts(JoinShared<R>& s, unsigned char* ring, int ring_bytes
     if (bad) s.bad = 1;
     if (lane == 0) s.out[row] = make_float2(m, l);
   }
-  constexpr int kItems = (R * HD / 4 + kWarps * 32 - 1) / (kWarps * 32);  // of a thread
   float4 acc[kItems];
 #pragma unroll
   for (int k = 0; k < kItems; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
