@@ -56,7 +56,6 @@ struct JoinShared {
   float* part[kMaxJoin];  // the partials, in the order of their shares
   float w[kMaxJoin][R];   // their weights
   float2 out[R];          // the joined (max, sum)
-  int bad;
 };
 
 // R: query heads of a head block, one MMA tile of 8 or two.
@@ -97,6 +96,17 @@ __device__ __forceinline__ int units_of(int len, int cap) {
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// The same for data that is read once: first to leave L2, where the page tables,
+// the partials and the code of the join stay.
+__device__ __forceinline__ uint64_t stream_policy() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void cp16_stream(uint32_t dst, const void* src, int bytes, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(bytes), "l"(policy)
+               : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -234,35 +244,41 @@ __device__ void join_parts(JoinShared<R>& s, unsigned char* ring, int ring_bytes
     }
     cp_commit();
   };
-  copy(0);
-  if (tid == 0) s.bad = 0;
-  __syncthreads();
-  for (int row = warp; row < rows; row += kWarps) {
-    float2 ml[kMaxJoin / 32];
-    float m = -INFINITY;
+  // lane (j, partial) of warp w has the (max, sum) of row w + kWarps i: all loads first
+  constexpr int kSeries = kMaxJoin / 32, kOwn = R / kWarps;
+  float2 ml[kOwn][kSeries];
 #pragma unroll
-    for (int j = 0; j < kMaxJoin / 32; ++j) {
-      ml[j] = make_float2(-INFINITY, 0.f);
-      if (lane + 32 * j < count) ml[j] = __ldcg(reinterpret_cast<const float2*>(s.part[lane + 32 * j]) + row);
-      m = fmaxf(m, ml[j].x);
+  for (int i = 0; i < kOwn; ++i)
+#pragma unroll
+    for (int j = 0; j < kSeries; ++j) {
+      const int row = warp + i * kWarps, p = lane + 32 * j;
+      ml[i][j] = make_float2(-INFINITY, 0.f);
+      if (p < count && row < rows) ml[i][j] = __ldcg(reinterpret_cast<const float2*>(s.part[p]) + row);
     }
+  copy(0);
+  bool bad_row = false;
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const int row = warp + i * kWarps;
+    float m = ml[i][0].x;
+#pragma unroll
+    for (int j = 1; j < kSeries; ++j) m = fmaxf(m, ml[i][j].x);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
     const float z = m == -INFINITY ? 0.f : m;
     float l = 0.f;
-    bool bad = false;
 #pragma unroll
-    for (int j = 0; j < kMaxJoin / 32; ++j) {
-      const float c = ex2(ml[j].x - z);
+    for (int j = 0; j < kSeries; ++j) {
+      const float c = ex2(ml[i][j].x - z);
       if (lane + 32 * j < count) s.w[lane + 32 * j][row] = c;
-      bad |= ml[j].y < 0.f;
-      l = fmaf(ml[j].y, c, l);
+      bad_row |= ml[i][j].y < 0.f;
+      l = fmaf(ml[i][j].y, c, l);
     }
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-    if (bad) s.bad = 1;
     if (lane == 0) s.out[row] = make_float2(m, l);
   }
+  const bool bad = __syncthreads_or(bad_row);
   float4 acc[kItems];
 #pragma unroll
   for (int k = 0; k < kItems; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -291,7 +307,6 @@ __device__ void join_parts(JoinShared<R>& s, unsigned char* ring, int ring_bytes
       copy(p0 + fit);
     }
   }
-  const bool bad = s.bad != 0;
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
     const int i = tid + k * kWarps * 32;
@@ -433,6 +448,7 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
   };
   page_next = lookup(lw);
   constexpr int kRowsPer = 32 / C::kChunks;  // rows of one copy instruction
+  const uint64_t policy = stream_policy();
   const int c = lane % C::kChunks, row0 = lane / C::kChunks;
   auto load_unit = [&](int stage) {
     const int key0 = lw.u * kUnit + warp * kKeys;
@@ -452,8 +468,8 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
       for (int j = 0; j < kKeys / kRowsPer; ++j) {
         const int row = j * kRowsPer + row0, bytes = row < live ? 16 : 0;
         const uint32_t d = (uint32_t)(row * C::kRowBytes + ((c ^ (row & 7)) << 4));
-        cp16(kdst + d, kp, bytes);
-        cp16(vdst + d, vp, bytes);
+        cp16_stream(kdst + d, kp, bytes, policy);
+        cp16_stream(vdst + d, vp, bytes, policy);
         kp += step;
         vp += step;
       }
@@ -472,8 +488,8 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
         const int64_t o = __shfl_sync(0xffffffffu, off, row) * (int64_t)sizeof(T) + c * 16;
         const int bytes = (live >> row) & 1 ? 16 : 0;
         const uint32_t d = (uint32_t)(row * C::kRowBytes + ((c ^ (row & 7)) << 4));
-        cp16(kdst + d, static_cast<const unsigned char*>(a.c.k) + o, bytes);
-        cp16(vdst + d, static_cast<const unsigned char*>(a.c.v) + o, bytes);
+        cp16_stream(kdst + d, static_cast<const unsigned char*>(a.c.k) + o, bytes, policy);
+        cp16_stream(vdst + d, static_cast<const unsigned char*>(a.c.v) + o, bytes, policy);
       }
     }
     walk_next<kUnit>(lw, a, nv, cap);
