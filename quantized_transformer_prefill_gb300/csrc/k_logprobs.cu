@@ -265,12 +265,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
   constexpr int U = kPer / V, kChunkBytes = kChunk * (int)sizeof(T), kStages = kRing / kChunkBytes;
   const uint32_t ring = smem_u32(lp_smem) + warp * kRing + lane * 16;
   auto inside = [&](int c) { return (c > 0 || head == 0) && (int64_t)(c + 1) * kChunk - head <= a.vocab; };
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
   auto fetch = [&](int c, int stage) {
     if (c < c1 && inside(c)) {
       const unsigned char* p = reinterpret_cast<const unsigned char*>(x + ((int64_t)c * kChunk - head)) + lane * 16;
 #pragma unroll
       for (int i = 0; i < U; ++i)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + stage * kChunkBytes + i * 512), "l"(p + i * 512) : "memory");
+        asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(ring + stage * kChunkBytes + i * 512),
+                     "l"(p + i * 512), "l"(policy)
+                     : "memory");
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
