@@ -138,6 +138,8 @@ int minfer_op_rope_paged_store(const void* d_qkv, int type, int64_t row_stride,
       !aligned16(d_knorm) || !stride_ok(row_stride, type) || !stride_ok(q_stride, cache->type) ||
       (n_tokens > 1 && (row_stride < q + 2 * kv || q_stride < q)))
     return MINFER_ERR_ARG;
+  const int sms = current_sms();
+  if (sms == 0) return MINFER_ERR_CUDA;
   a.qkv = d_qkv;
   a.row_stride = row_stride;
   a.bias = d_bias;
@@ -152,7 +154,7 @@ int minfer_op_rope_paged_store(const void* d_qkv, int type, int64_t row_stride,
   a.q_stride = q_stride;
   a.status = d_status;
   a.rope = *rope;
-  return from_cuda(rope_paged_launch(a, type, cache->type, static_cast<cudaStream_t>(stream)));
+  return from_cuda(rope_paged_launch(a, type, cache->type, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int minfer_op_paged_attention_workspace(int n_req, int n_head, const minfer_paged_cache* cache,

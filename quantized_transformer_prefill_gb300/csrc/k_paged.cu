@@ -3,6 +3,8 @@
 // Q|K|V rows with K and V written to their slots.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -254,96 +256,153 @@ struct alignas(E * sizeof(T)) Vec {
   T v[E];
 };
 
-// cos and sin of 2 pi * f / 2^64.  The quadrant comes off in integers, so the
-// rest r (in half turns, |r| <= 1/4) keeps its relative precision in f32.
+// cos and sin of 2 pi * f / 2^64.  The quadrant comes off in integers; the rest,
+// at most an eighth of a turn, is taken to 2^-34 of a turn (an angle of 4e-10,
+// below f32's step for a sine or cosine), and its sine and cosine are the Taylor
+// polynomials to the 9th and 10th degree: the first terms left out, x^11 / 11!
+// and x^12 / 12! at pi / 4, are 1.8e-9 and 1.1e-10.
 __device__ __forceinline__ void turn_cos_sin(uint64_t f, float* c, float* s) {
-  const uint32_t quad = (uint32_t)((f + (1ull << 61)) >> 62);
-  const int64_t rest = (int64_t)(f - ((uint64_t)quad << 62));
-  float sr, cr;
-  sincospif(__ll2float_rn(rest) * 0x1p-63f, &sr, &cr);
+  const uint64_t g = f + (1ull << 61);
+  const uint32_t quad = (uint32_t)(g >> 62);
+  const int32_t rest = (int32_t)((uint32_t)(g >> 30) - 0x80000000u);  // 2^-34 turns
+  const float x = (float)rest * (float)(6.283185307179586 / 17179869184.0), q = x * x;
+  float sr = fmaf(q, 1.f / 362880, -1.f / 5040);
+  sr = fmaf(q, sr, 1.f / 120);
+  sr = fmaf(q, sr, -1.f / 6);
+  sr = fmaf(q * x, sr, x);
+  float cr = fmaf(q, -1.f / 3628800, 1.f / 40320);
+  cr = fmaf(q, cr, -1.f / 720);
+  cr = fmaf(q, cr, 1.f / 24);
+  cr = fmaf(q, cr, -0.5f);
+  cr = fmaf(q, cr, 1.f);
   const float cc = (quad & 1) ? sr : cr, ss = (quad & 1) ? cr : sr;
   *c = (quad == 1 || quad == 2) ? -cc : cc;
   *s = (quad >= 2) ? -ss : ss;
 }
 
-constexpr int kRpInFlight = 16;  // elements of a lane whose loads are in flight together
-constexpr int kRpMaxWarps = 16;
+constexpr int kRpWarps = 8;
+constexpr int kRpTokens = 4;     // of a CTA, at most
+constexpr int kRpFill = 2;       // CTAs per SM that more tokens per CTA must leave
+constexpr int kRpMaxBias = 24576;  // values that are kept in shared memory
+constexpr int kRpRing = 8;       // units of a warp on their way or at work
 
-// One CTA per token.  A lane takes E neighbouring elements of a head (one
-// 16-byte vector of the source type), so a unit of 32 lanes is 32 E / HD heads;
-// warp w of n takes units w, w + n, ...  The position, the slot and the
-// row are all loaded before the first of them is looked at.  The cosines and
-// sines of the lane's elements, with the rotation's signs in the sines, are the
-// same for every head: they are read into registers once.  The pair partner of
-// an element lies in the lane itself (interleaved pairs), in another lane at the
-// same place (half a rotation is a multiple of E), or anywhere (other rotated
-// sizes), where it is fetched through shared memory.
+// A CTA takes 1, 2 or 4 tokens.  Its threads work out the tokens' cosines and
+// sines, one pair each, while the rows are on the way; then 8, 4 or 2 warps go
+// over a token's heads.  A lane takes E neighbouring elements of a head (one
+// 16-byte vector of the source type), so a unit of 32 lanes is 32 E / HD heads,
+// and the lane's cosines and signed sines are the same for every unit.  The pair
+// partner of an element lies in the lane itself (interleaved pairs), in another
+// lane at the same place (half a rotation is a multiple of E), or, with rotated
+// sizes that are no multiples of E, anywhere, and comes through shared memory.
 template <typename TS, typename TD, int HD>
-__global__ void __launch_bounds__(kRpMaxWarps * 32, 2) rope_paged_kernel(const __grid_constant__ RopePagedArgs a) {
+__global__ void __launch_bounds__(kRpWarps * 32) rope_paged_kernel(const __grid_constant__ RopePagedArgs a, int tokens, int swap_floats, int bias_floats) {
   constexpr int E = 16 / sizeof(TS), kLanes = HD / E, kPer = 32 / kLanes;  // lanes of a head, heads of a unit
-  constexpr int kRpUnits = kRpInFlight / E;
   using VS = Vec<TS, E>;
   using VD = Vec<TD, E>;
-  __shared__ float s_cos[HD / 2], s_sin[HD / 2];
-  extern __shared__ float s_swap[];  // [warp][32 E], only where partners lie anywhere
-  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  const int nqk = a.nh + a.c.nkv, heads = nqk + a.c.nkv;
+  __shared__ uint64_t s_turn[64];
+  __shared__ float s_cos[kRpTokens][64], s_sin[kRpTokens][64];
+  // [warp][32 E], only where partners lie anywhere; then the bias (read for every
+  // unit: from here, or from global memory where it is too large)
+  extern __shared__ __align__(16) float rp_smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = kRpWarps / tokens, mine = warp / per, first = warp % per;  // warps of a token, token, first unit
+  const int t = blockIdx.x * tokens + mine;
+  const int nqk = a.nh + a.c.nkv, heads = nqk + a.c.nkv, units = (heads + kPer - 1) / kPer;
   const int sub = lane / kLanes, d0 = (lane % kLanes) * E;  // head of the unit, first element of the head
-  const TS* row = static_cast<const TS*>(a.qkv) + (int64_t)t * a.row_stride + lane * E;
+  const int rot = a.rope.rot_dim, half = rot >> 1, slots = a.c.n_pages * a.c.page_size;
+  const bool inter = a.rope.style == MINFER_ROPE_INTERLEAVED;
+  const bool in_lane = inter && rot % E == 0, in_place = !inter && half % E == 0;
+
   pdl_trigger();
   pdl_wait();
-  VS x[kRpUnits];
-  auto load = [&](int u0) {
-#pragma unroll
-    for (int i = 0; i < kRpUnits; ++i) {
-      const int u = u0 + i * warps;
-      if (u * kPer + sub < heads) x[i] = *reinterpret_cast<const VS*>(row + u * (32 * E));
-    }
+  const TS* row = static_cast<const TS*>(a.qkv) + (int64_t)t * a.row_stride + lane * E;
+  // The rows come through a ring in shared memory (a lane copies the vectors that
+  // it reads itself): what is on its way takes no registers, so more warps fit.
+  __shared__ __align__(16) unsigned char s_ring[kRpWarps][kRpRing][512];
+  const uint32_t ring = smem_u32(s_ring[warp]) + lane * 16;
+  auto fetch = [&](int u, int stage) {
+    if (u * kPer + sub < heads)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + stage * 512), "l"(row + u * (32 * E)) : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  const int slot = a.slot[t], pos = a.pos[t];
-  load(warp);
+  for (int i = tid * 4; i < bias_floats; i += kRpWarps * 128)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(rp_smem + swap_floats + i)), "l"(a.bias + i) : "memory");
+  __shared__ __align__(16) float s_norm[2][HD];
+  if (a.q_norm && tid < HD / 2)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&s_norm[0][0] + tid * 4)),
+                 "l"((tid < HD / 4 ? a.q_norm : a.k_norm - HD) + tid * 4)
+                 : "memory");
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  int slot = -1, pos = 0;
+  if (t < a.n_tokens) {
+    slot = a.slot[t];
+    pos = a.pos[t];
+#pragma unroll
+    for (int i = 0; i < kRpRing - 1; ++i) fetch(first + i * per, i);
+  } else {
+    for (int i = 0; i < kRpRing - 1; ++i) asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // (a parameter is read fast at one address per warp, and very slowly at 32)
+  static_assert(kRpWarps * 8 == 64, "eight entries per warp");
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s_turn[warp * 8 + i] = a.rope.turn[warp * 8 + i];
+  }
+  {
+    const int j = tid >> 6, pair = tid & 63, tj = blockIdx.x * tokens + j;
+    const bool there = j < tokens && pair < half && tj < a.n_tokens;
+    const int p = there ? a.pos[tj] : 0;
+    __syncthreads();
+    if (there) {
+      float c, s;
+      turn_cos_sin((uint64_t)(uint32_t)p * s_turn[pair], &c, &s);
+      s_cos[j][pair] = c * a.rope.mscale;
+      s_sin[j][pair] = s * a.rope.mscale;
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRpRing - 1) : "memory");  // bias and norm weights, the oldest group
+    __syncthreads();
+  }
   if (slot < 0) return;  // padding
-  if (slot >= a.c.n_pages * a.c.page_size || pos < 0) {
-    if (tid == 0) set_error(a.status, MINFER_ERR_POS_OOB);
+  if (slot >= slots || pos < 0) {
+    if (first == 0 && lane == 0) set_error(a.status, MINFER_ERR_POS_OOB);
     return;
   }
-  const int rot = a.rope.rot_dim, half = rot >> 1;
-  const bool inter = a.rope.style == MINFER_ROPE_INTERLEAVED;
-  for (int i = tid; i < half; i += blockDim.x) {
-    float c, s;
-    turn_cos_sin((uint64_t)(uint32_t)pos * a.rope.turn[i], &c, &s);
-    s_cos[i] = c * a.rope.mscale;
-    s_sin[i] = s * a.rope.mscale;
-  }
-  const int page = slot / a.c.page_size;
-  const int64_t at = (int64_t)page * a.c.page_stride + (int64_t)(slot - page * a.c.page_size) * a.c.row_stride;
-  TD* qdst = static_cast<TD*>(a.q_out) + (int64_t)t * a.q_stride + d0;
-  TD* kdst = static_cast<TD*>(a.c.k) + at + d0;
-  TD* vdst = static_cast<TD*>(a.c.v) + at + d0;
-  __syncthreads();
   float cs[E], sn[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const int d = d0 + e, p = inter ? d >> 1 : d < half ? d : d - half;
-    cs[e] = d < rot ? s_cos[p] : 1.f;
-    sn[e] = d < rot ? s_sin[p] : 0.f;
+    const int d = d0 + e, p = d >= rot ? 0 : inter ? d >> 1 : d < half ? d : d - half;
+    cs[e] = s_cos[mine][p];
+    sn[e] = s_sin[mine][p];
     if (inter ? !(d & 1) : d < half) sn[e] = -sn[e];
   }
-  const bool in_lane = inter, in_place = half % E == 0, some = d0 < rot;  // (uniform, uniform, per lane)
   const int from = (d0 < half ? lane + half / E : lane - half / E) & 31;
-  float* swap = s_swap + warp * (32 * E);
+  const bool turned = d0 < rot;
+  float* swap = rp_smem + warp * (32 * E);
+  const int page = slot / a.c.page_size;
+  const int64_t at = (int64_t)page * a.c.page_stride + (int64_t)(slot - page * a.c.page_size) * a.c.row_stride;
+  TD* const qdst = static_cast<TD*>(a.q_out) + (int64_t)t * a.q_stride + d0;
+  TD* const kdst = static_cast<TD*>(a.c.k) + (at + d0 - a.nh * a.c.head_stride);
+  TD* const vdst = static_cast<TD*>(a.c.v) + (at + d0 - nqk * a.c.head_stride);
+  const float* const bias = !a.bias ? nullptr : (bias_floats ? rp_smem + swap_floats : a.bias) + lane * E;
 
-  for (int u0 = warp; u0 * kPer < heads; u0 += warps * kRpUnits) {
-    if (u0 != warp) load(u0);
-#pragma unroll
-    for (int i = 0; i < kRpUnits; ++i) {
-      const int u = u0 + i * warps, h = u * kPer + sub;
-      if (u * kPer >= heads) break;  // the whole warp
+  int stage = 0;
+  for (int u = first; u < units; u += per) {
+    {
+      const int h = u * kPer + sub;
+      fetch(u + (kRpRing - 1) * per, (stage + kRpRing - 1) % kRpRing);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRpRing - 1) : "memory");
+      VS x;
+      {
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(ring + stage * 512) : "memory");
+        x = *reinterpret_cast<const VS*>(&v);
+      }
+      stage = (stage + 1) % kRpRing;
       float y[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) y[e] = to_f32<TS>(x[i].v[e]);
-      if (a.bias && h < heads) {
-        const float4* b = reinterpret_cast<const float4*>(a.bias + h * HD + d0);
+      for (int e = 0; e < E; ++e) y[e] = to_f32<TS>(x.v[e]);
+      if (bias && h < heads) {
+        const float4* b = reinterpret_cast<const float4*>(bias + u * (32 * E));
 #pragma unroll
         for (int j = 0; j < E / 4; ++j) {
           const float4 f = b[j];
@@ -354,15 +413,16 @@ __global__ void __launch_bounds__(kRpMaxWarps * 32, 2) rope_paged_kernel(const _
         }
       }
       if (u * kPer < nqk) {  // some head of the unit is one of Q or K
+        const bool qk = h < nqk;
         if (a.q_norm) {
           float ss = 0.f;
 #pragma unroll
           for (int e = 0; e < E; ++e) ss = fmaf(y[e], y[e], ss);
 #pragma unroll
           for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          if (h < nqk) {
+          if (qk) {
             const float r = rsqrtf(ss * (1.f / HD) + a.eps);
-            const float4* w = reinterpret_cast<const float4*>((h < a.nh ? a.q_norm : a.k_norm) + d0);
+            const float4* w = reinterpret_cast<const float4*>(s_norm[h < a.nh ? 0 : 1] + d0);
 #pragma unroll
             for (int j = 0; j < E / 4; ++j) {
               const float4 f = w[j];
@@ -374,36 +434,35 @@ __global__ void __launch_bounds__(kRpMaxWarps * 32, 2) rope_paged_kernel(const _
           }
         }
         float z[E];
-        if (in_lane) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) z[e] = y[e ^ 1];
-        } else if (in_place) {
+        if (in_place) {
 #pragma unroll
           for (int e = 0; e < E; ++e) z[e] = __shfl_sync(0xffffffffu, y[e], from);
+        } else if (in_lane) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) z[e] = y[e ^ 1];
         } else {
           __syncwarp();
 #pragma unroll
           for (int e = 0; e < E; ++e) swap[lane * E + e] = y[e];
           __syncwarp();
+          if (qk) {
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const int d = d0 + e;
-            z[e] = d < rot ? swap[sub * HD + (d < half ? d + half : d - half)] : 0.f;
+            for (int e = 0; e < E; ++e) {
+              const int d = d0 + e, p = inter ? d ^ 1 : d < half ? d + half : d - half;
+              if (d < rot) y[e] = fmaf(swap[sub * HD + p], sn[e], y[e] * cs[e]);
+            }
           }
         }
-        if (some && h < nqk) {
-          // (an element behind rot_dim in a lane that has some before it: y * 1 + z * 0 would lose
-          // it to an infinite z)
+        if ((in_place || in_lane) && turned && qk) {
 #pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (d0 + e < rot) y[e] = fmaf(z[e], sn[e], y[e] * cs[e]);
+          for (int e = 0; e < E; ++e) y[e] = fmaf(z[e], sn[e], y[e] * cs[e]);
         }
       }
       if (h < heads) {
         VD out;
 #pragma unroll
         for (int e = 0; e < E; ++e) out.v[e] = from_f32<TD>(y[e]);
-        TD* dst = h < a.nh ? qdst + h * HD : h < nqk ? kdst + (h - a.nh) * a.c.head_stride : vdst + (h - nqk) * a.c.head_stride;
+        TD* dst = h < a.nh ? qdst + h * HD : (h < nqk ? kdst : vdst) + h * a.c.head_stride;
         *reinterpret_cast<VD*>(dst) = out;
       }
     }
@@ -411,16 +470,23 @@ __global__ void __launch_bounds__(kRpMaxWarps * 32, 2) rope_paged_kernel(const _
 }
 
 template <typename TS, typename TD, int HD>
-cudaError_t rope_paged_sized(const RopePagedArgs& a, cudaStream_t st) {
-  constexpr int E = 16 / sizeof(TS), kPer = 32 * E / HD, kRpUnits = kRpInFlight / E;
-  const int units = (a.nh + 2 * a.c.nkv + kPer - 1) / kPer, warps = (units + kRpUnits - 1) / kRpUnits;
-  const unsigned n = warps < kRpMaxWarps ? warps : kRpMaxWarps;
-  const bool swap = a.rope.style == MINFER_ROPE_HALF && (a.rope.rot_dim / 2) % E != 0;
-  return launch_pdl(rope_paged_kernel<TS, TD, HD>, dim3((unsigned)a.n_tokens), dim3(32 * n), swap ? n * 32 * E * sizeof(float) : 0, st, a);
+cudaError_t rope_paged_sized(const RopePagedArgs& a, int num_sms, cudaStream_t st) {
+  constexpr int E = 16 / sizeof(TS);
+  // One token per CTA while that keeps the GPU from being full, for its eight
+  // warps finish sooner; else up to four, which share the work before the heads.
+  int tokens = 1;
+  while (tokens < kRpTokens && a.n_tokens / (2 * tokens) >= num_sms * kRpFill) tokens *= 2;
+  const bool swap = a.rope.style == MINFER_ROPE_HALF ? (a.rope.rot_dim / 2) % E != 0 : a.rope.rot_dim % E != 0;
+  const int swap_floats = swap ? kRpWarps * 32 * E : 0, width = (a.nh + 2 * a.c.nkv) * HD;
+  const int bias_floats = a.bias && width <= kRpMaxBias ? width : 0, smem = (swap_floats + bias_floats) * (int)sizeof(float);
+  const cudaError_t e = allow_smem<rope_paged_kernel<TS, TD, HD>>((kRpWarps * 32 * E + kRpMaxBias) * (int)sizeof(float));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(rope_paged_kernel<TS, TD, HD>, dim3((unsigned)((a.n_tokens - 1) / tokens + 1)), dim3(32 * kRpWarps), smem, st, a, tokens,
+                    swap_floats, bias_floats);
 }
 template <typename TS, typename TD>
-cudaError_t rope_paged_typed(const RopePagedArgs& a, cudaStream_t st) {
-  return a.c.hd == 64 ? rope_paged_sized<TS, TD, 64>(a, st) : rope_paged_sized<TS, TD, 128>(a, st);
+cudaError_t rope_paged_typed(const RopePagedArgs& a, int num_sms, cudaStream_t st) {
+  return a.c.hd == 64 ? rope_paged_sized<TS, TD, 64>(a, num_sms, st) : rope_paged_sized<TS, TD, 128>(a, num_sms, st);
 }
 
 }  // namespace
@@ -449,12 +515,13 @@ cudaError_t page_tables_launch(const PageTablesArgs& a, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, page_tables_kernel, a);
 }
 
-cudaError_t rope_paged_launch(const RopePagedArgs& a, int src_type, int cache_type, cudaStream_t st) {
-  if (cache_type == MINFER_F32) return rope_paged_typed<float, float>(a, st);
+cudaError_t rope_paged_launch(const RopePagedArgs& a, int src_type, int cache_type, int num_sms, cudaStream_t st) {
+  if (cache_type == MINFER_F32) return rope_paged_typed<float, float>(a, num_sms, st);
   if (cache_type == MINFER_F16)
-    return src_type == MINFER_F32 ? rope_paged_typed<float, __half>(a, st) : rope_paged_typed<__half, __half>(a, st);
-  return src_type == MINFER_F32 ? rope_paged_typed<float, __nv_bfloat16>(a, st)
-                                : rope_paged_typed<__nv_bfloat16, __nv_bfloat16>(a, st);
+    return src_type == MINFER_F32 ? rope_paged_typed<float, __half>(a, num_sms, st)
+                                  : rope_paged_typed<__half, __half>(a, num_sms, st);
+  return src_type == MINFER_F32 ? rope_paged_typed<float, __nv_bfloat16>(a, num_sms, st)
+                                : rope_paged_typed<__nv_bfloat16, __nv_bfloat16>(a, num_sms, st);
 }
 
 }  // namespace minfer

@@ -371,7 +371,7 @@ struct RopePagedArgs {
   int* status;
   minfer_rope_table rope;
 };
-cudaError_t rope_paged_launch(const RopePagedArgs& a, int src_type, int cache_type,
+cudaError_t rope_paged_launch(const RopePagedArgs& a, int src_type, int cache_type, int num_sms,
                               cudaStream_t stream);
 
 // k_paged_attn.cu: one query row per request over its pages.
