@@ -46,7 +46,7 @@ int check_cache(const minfer_paged_cache* c, PagedCache* out) {
     return MINFER_ERR_ARG;
   if (!fits31(c->n_pages, c->page_size)) return MINFER_ERR_TOO_LARGE;
   *out = PagedCache{c->k, c->v, c->n_pages, c->page_size, c->n_head_kv, c->head_dim,
-                    c->page_stride, c->row_stride, c->head_stride};
+                    c->page_stride, c->row_stride, c->head_stride, PageDiv(c->page_size)};
   return MINFER_OK;
 }
 
@@ -114,7 +114,7 @@ int minfer_op_page_tables(const int32_t* d_len, const int32_t* d_target, int n_r
       !fits31(n_pages, page_size) || max_tokens >= (1 << 30))
     return MINFER_ERR_TOO_LARGE;
   const PageTablesArgs a{d_len,   d_target, n_req,    page_size,    n_pages, max_pages, max_tokens, d_table,
-                         d_free,  d_n_free, d_n_free_out, d_start, d_pos,   d_slot,    d_status};
+                         d_free,  d_n_free, d_n_free_out, d_start, d_pos,   d_slot,    d_status, PageDiv(page_size)};
   return from_cuda(page_tables_launch(a, static_cast<cudaStream_t>(stream)));
 }
 

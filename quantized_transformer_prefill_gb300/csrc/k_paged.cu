@@ -39,17 +39,23 @@ __device__ __forceinline__ void pt_cluster_sync() {
                    : "memory");
 }
 
-// Largest i in [0, n) with a[i] <= x (a ascending, a[0] <= x < a[n]).
-__device__ __forceinline__ int pt_find(const int* a, int n, int x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a[mid] <= x)
-      lo = mid;
-    else
-      hi = mid;
+// Largest i in [0, n) with a[i] <= x (a ascending, a[0] <= x < a[n]), for Q values
+// at once: the same number of steps for all, their loads side by side.
+template <int Q>
+__device__ __forceinline__ void pt_find(const int* a, int n, const int (&x)[Q], int (&i)[Q]) {
+#pragma unroll
+  for (int q = 0; q < Q; ++q) i[q] = 0;
+  for (int w = 1 << (31 - __clz(n)); w > 0; w >>= 1) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if (i[q] + w < n && a[i[q] + w] <= x[q]) i[q] += w;
   }
-  return lo;
+}
+__device__ __forceinline__ int pt_find(const int* a, int n, int x) {
+  const int y[1] = {x};
+  int i[1];
+  pt_find<1>(a, n, y, i);
+  return i[0];
 }
 
 __global__ void __launch_bounds__(kPtThreads, 1) page_tables_kernel(const PageTablesArgs a) {
@@ -74,6 +80,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_tables_kernel(const PageTa
     __syncthreads();
 
   const int cap = a.max_pages * P;
+  auto pages = [&](int rows) { return rows == 0 ? 0 : a.div.of(rows - 1) + 1; };
   const int n_free = *a.n_free;
   int err = 0;
   int base0 = 0, base1 = 0, base2 = 0;
@@ -85,8 +92,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_tables_kernel(const PageTa
       if (L < 0 || T < 0 || L > cap || T > cap) {
         err |= kBadLen;
       } else {
-        const int held = (int)(((unsigned)L + P - 1) / (unsigned)P);
-        const int need = (int)(((unsigned)T + P - 1) / (unsigned)P);
+        const int held = pages(L), need = pages(T);
         v0 = max(0, T - L);
         v1 = max(0, need - held);
         v2 = max(0, held - need);
@@ -161,25 +167,30 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_tables_kernel(const PageTa
   // k-th returned page, and entry i of the stack with the returned pages on top
   auto returned = [&](int k) {
     const int r = pt_find(s_back, n, k);
-    const int first = (int)(((unsigned)a.target[r] + P - 1) / (unsigned)P);
-    return a.table[(int64_t)r * a.max_pages + first + (k - s_back[r])];
+    return a.table[(int64_t)r * a.max_pages + pages(a.target[r]) + (k - s_back[r])];
   };
   auto new_page = [&](int j) {
     const int64_t i = depth - 1 - j;
     return i < n_free ? a.free_pages[i] : returned((int)(i - n_free));
   };
 
+  // A thread's first grown page, returned page and shared page (the one that a
+  // request's next row shares with its last one), loaded side by side; checked
+  // here, and the grown one kept for when it is entered.
+  int page0 = 0;
   if (!err) {
     const unsigned np = (unsigned)a.n_pages;
-    bool bad = false;
-    for (int j = gtid; j < grown; j += gn) bad |= (unsigned)new_page(j) >= np;
-    for (int k = gtid; k < back; k += gn) bad |= (unsigned)returned(k) >= np;
-    for (int r = gtid; r < n; r += gn) {
-      // the page that a request's next row shares with its last one
-      const int L = a.len[r], p = L / P;
-      if (s_start[r + 1] > s_start[r] && L > p * P)
-        bad |= (unsigned)a.table[(int64_t)r * a.max_pages + p] >= np;
-    }
+    auto shared_page = [&](int r) {  // 0 where there is none
+      const int L = a.len[r], p = a.div.of(L);
+      return s_start[r + 1] > s_start[r] && L > p * P ? a.table[(int64_t)r * a.max_pages + p] : 0;
+    };
+    const int back0 = gtid < back ? returned(gtid) : 0;
+    const int shared0 = gtid < n ? shared_page(gtid) : 0;
+    page0 = gtid < grown ? new_page(gtid) : 0;
+    bool bad = (unsigned)page0 >= np || (unsigned)back0 >= np || (unsigned)shared0 >= np;
+    for (int j = gtid + gn; j < grown; j += gn) bad |= (unsigned)new_page(j) >= np;
+    for (int k = gtid + gn; k < back; k += gn) bad |= (unsigned)returned(k) >= np;
+    for (int r = gtid + gn; r < n; r += gn) bad |= (unsigned)shared_page(r) >= np;
     if (__syncthreads_or(bad)) err |= kBadPage;
   }
   if (nrank > 1) {
@@ -209,24 +220,35 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_tables_kernel(const PageTa
   for (int r = gtid; r <= n; r += gn) a.start[r] = s_start[r];
   for (int j = gtid; j < grown; j += gn) {
     const int r = pt_find(s_grow, n, j);
-    const int held = (int)(((unsigned)a.len[r] + P - 1) / (unsigned)P);
-    a.table[(int64_t)r * a.max_pages + held + (j - s_grow[r])] = new_page(j);
+    const int held = pages(a.len[r]);
+    a.table[(int64_t)r * a.max_pages + held + (j - s_grow[r])] = j == gtid ? page0 : new_page(j);
   }
   const int pushed = (int)(depth - grown) - n_free;
   for (int k = gtid; k < pushed; k += gn) a.free_pages[n_free + k] = returned(k);
-  for (int t = gtid; t < a.max_tokens; t += gn) {
-    int pos = -1, slot = -1;
-    if (t < tokens) {
-      const int r = pt_find(s_start, n, t);
-      const int L = a.len[r];
-      pos = L + (t - s_start[r]);
-      const int p = (int)((unsigned)pos / (unsigned)P);
-      const int held = (int)(((unsigned)L + P - 1) / (unsigned)P);
-      const int page = p < held ? a.table[(int64_t)r * a.max_pages + p] : new_page(s_grow[r] + (p - held));
-      slot = page * P + (pos - p * P);
+  constexpr int Q = 4;  // tokens of a thread at a time
+  for (int t0 = gtid; t0 < a.max_tokens; t0 += Q * gn) {
+    int t[Q], r[Q], pos[Q], page[Q], off[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) t[q] = min(t0 + q * gn, tokens - 1);
+    if (t0 < tokens) pt_find<Q>(s_start, n, t, r);
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      pos[q] = page[q] = -1;
+      off[q] = P - 1;  // slot -1
+      if (t0 + q * gn >= tokens) continue;
+      const int L = a.len[r[q]];
+      pos[q] = L + (t[q] - s_start[r[q]]);
+      const int p = a.div.of(pos[q]), held = pages(L);
+      off[q] = pos[q] - p * P;
+      page[q] = p < held ? a.table[(int64_t)r[q] * a.max_pages + p] : new_page(s_grow[r[q]] + (p - held));
     }
-    a.pos[t] = pos;
-    a.slot[t] = slot;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int at = t0 + q * gn;
+      if (at >= a.max_tokens) break;
+      a.pos[at] = pos[q];
+      a.slot[at] = page[q] * P + off[q];
+    }
   }
   if (gtid == 0) *a.n_free_out = (int)(depth - grown);
 }
@@ -378,7 +400,7 @@ __global__ void __launch_bounds__(kRpWarps * 32) rope_paged_kernel(const __grid_
   const int from = (d0 < half ? lane + half / E : lane - half / E) & 31;
   const bool turned = d0 < rot;
   float* swap = rp_smem + warp * (32 * E);
-  const int page = slot / a.c.page_size;
+  const int page = a.c.div.of(slot);
   const int64_t at = (int64_t)page * a.c.page_stride + (int64_t)(slot - page * a.c.page_size) * a.c.row_stride;
   TD* const qdst = static_cast<TD*>(a.q_out) + (int64_t)t * a.q_stride + d0;
   TD* const kdst = static_cast<TD*>(a.c.k) + (at + d0 - a.nh * a.c.head_stride);

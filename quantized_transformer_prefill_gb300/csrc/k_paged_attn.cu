@@ -437,14 +437,12 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
   // ---- loads: every lane looks up the page of the first key, or, where 16 keys may
   // lie in several pages, lane l that of key l % 16; then all lanes copy
   const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStageBytes;
-  const bool pow2 = (P & (P - 1)) == 0, one_page = (P & (kKeys - 1)) == 0;
-  const int shift = __ffs(P) - 1;
+  const bool one_page = (P & (kKeys - 1)) == 0;
   int page_next = 0;  // page id that this lane looked up for unit lw
   auto lookup = [&](const Walk& w) {
     const int key = w.u * kUnit + warp * kKeys + (one_page ? 0 : lane & 15);
     if (key >= w.len) return 0;
-    const int i = pow2 ? key >> shift : key / P;
-    return a.table[(int64_t)w.r * a.table_stride + i];
+    return a.table[(int64_t)w.r * a.table_stride + a.c.div.of(key)];
   };
   page_next = lookup(lw);
   constexpr int kRowsPer = 32 / C::kChunks;  // rows of one copy instruction
@@ -455,7 +453,7 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
     const bool ok = (unsigned)page_next < (unsigned)a.c.n_pages;
     const uint32_t kdst = ring + stage * C::kStageBytes, vdst = kdst + kKeys * C::kRowBytes;
     if (one_page) {
-      const int in_page = pow2 ? key0 & (P - 1) : key0 % P;
+      const int in_page = key0 - a.c.div.of(key0) * P;
       const int live = ok ? lw.len - key0 : 0;
       int64_t off = 0;
       if (live > 0)
@@ -475,7 +473,7 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
       }
     } else {
       const int key = key0 + (lane & 15);
-      const int in_page = pow2 ? key & (P - 1) : key % P;
+      const int in_page = key - a.c.div.of(key) * P;
       int64_t off = 0;
       if (key < lw.len && ok)
         off = (int64_t)page_next * a.c.page_stride + (int64_t)in_page * a.c.row_stride + (int64_t)(lw.v / n_groups) * a.c.head_stride;

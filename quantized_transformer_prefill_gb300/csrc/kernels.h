@@ -329,6 +329,25 @@ cudaError_t sum_splits_launch(const float* partials, int nsplit, int64_t split_s
 // ---------------------------------------------------------------- batch operators
 // Their launchers take checked arguments (batch.cu checks them).
 
+// Division by a page size: x / d = x * mul >> shift for 0 <= x < 2^31, with shift
+// = 31 + ceil(log2 d) and mul = floor(2^shift / d) + 1 (so mul * d exceeds 2^shift
+// by at most 2^(shift - 31), and the error x brings stays below 1 / d).
+struct PageDiv {
+  uint32_t mul;
+  int shift, d;
+  PageDiv() = default;
+  explicit PageDiv(int d_) : d(d_) {
+    int l = 0;
+    while ((1ll << l) < d_) ++l;
+    shift = 31 + l;
+    mul = (uint32_t)((1ull << shift) / (unsigned)d_ + 1);
+  }
+#ifdef __CUDACC__
+  __host__ __device__
+#endif
+      int of(int x) const { return (int)(((uint64_t)(uint32_t)x * mul) >> shift); }
+};
+
 // k_paged.cu: block tables and slot maps from request lengths.
 struct PageTablesArgs {
   const int32_t* len;
@@ -342,6 +361,7 @@ struct PageTablesArgs {
   int32_t* pos;
   int32_t* slot;
   int* status;
+  PageDiv div;  // by page_size
 };
 constexpr int kPageTablesMaxReq = 16384;  // three prefix arrays of n_req + 1 ints in shared memory
 cudaError_t page_tables_launch(const PageTablesArgs& a, cudaStream_t stream);
@@ -352,6 +372,7 @@ struct PagedCache {
   void* v;
   int n_pages, page_size, nkv, hd;
   int64_t page_stride, row_stride, head_stride;
+  PageDiv div;  // by page_size
 };
 
 // k_paged.cu: bias + QK-norm + RoPE + paged store of fused Q|K|V rows.
