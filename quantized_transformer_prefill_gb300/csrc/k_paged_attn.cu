@@ -159,11 +159,14 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x = hi + lo, two tf32 values (11 significant bits each; the rest is below 2^-22 |x|)
+// x = hi + lo: hi is x rounded to tf32 (11 significant bits), ties away from
+// zero, in integer arithmetic (the conversion instruction has a quarter of its
+// rate); lo = x - hi is exact and at most 2^-11 |x|, and the MMA takes its upper
+// 11 bits, which leaves out less than 2^-21 |x|.  (A NaN may lose its bits in hi;
+// lo keeps it.)
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t* hi, uint32_t* lo) {
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(*hi) : "f"(__uint_as_float(x)));
-  const float rest = __uint_as_float(x) - __uint_as_float(*hi);
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(*lo) : "f"(rest));
+  *hi = (x + 0x1000u) & 0xFFFFE000u;
+  *lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(*hi));
 }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
