@@ -465,8 +465,8 @@ int minfer_op_page_tables(const int32_t* d_len, const int32_t* d_target, int n_r
  * (f32 [head_dim], both or neither) every head of Q and K is RMS-normalized;
  * Q and K are rotated by d_pos[t]; Q goes to d_q_out (the cache's type, rows of
  * n_head*head_dim values q_stride apart), K and V to slot d_slot[t].  A row
- * with a negative slot is padding: it is neither read nor written.  Slots of
- * one call are distinct.  `type` is MINFER_F32 or the cache's type; all
+ * with a negative slot is padding: nothing is written for it, whatever it
+ * holds.  Slots of one call are distinct.  n_head <= 65535 (here and below).  `type` is MINFER_F32 or the cache's type; all
  * arithmetic is f32, rounded once.  Device errors: MINFER_ERR_POS_OOB for a
  * slot past the pool or a negative position of a stored row (that row is not
  * written). */

@@ -12,6 +12,7 @@ using namespace minfer;
 namespace {
 
 constexpr int kMaxDevices = 64;
+constexpr int kMaxHeads = 65535;  // a row of heads is indexed with 32 bits
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool type_ok(int t) { return t == MINFER_F32 || t == MINFER_F16 || t == MINFER_BF16; }
@@ -130,6 +131,7 @@ int minfer_op_rope_paged_store(const void* d_qkv, int type, int64_t row_stride,
   if (!d_qkv || !rope || !d_pos || !d_slot || !d_q_out || n_tokens <= 0 || n_head <= 0 ||
       n_head % cache->n_head_kv != 0 || (d_qnorm == nullptr) != (d_knorm == nullptr) || !(eps >= 0))
     return MINFER_ERR_ARG;
+  if (n_head > kMaxHeads) return MINFER_ERR_TOO_LARGE;
   if ((type != MINFER_F32 && type != cache->type) || rope->head_dim != cache->head_dim ||
       rope->rot_dim < 2 || rope->rot_dim > cache->head_dim || rope->rot_dim % 2)
     return MINFER_ERR_SHAPE;
@@ -163,6 +165,7 @@ int minfer_op_paged_attention_workspace(int n_req, int n_head, const minfer_page
   const int rc = check_cache(cache, &c);
   if (rc != MINFER_OK) return rc;
   if (!bytes || n_req <= 0 || n_head <= 0 || n_head % c.nkv != 0) return MINFER_ERR_ARG;
+  if (n_head > kMaxHeads) return MINFER_ERR_TOO_LARGE;
   const int sms = current_sms();
   if (sms == 0) return MINFER_ERR_CUDA;
   *bytes = paged_attn_workspace(n_head / c.nkv, c.hd, cache->type, sms);
@@ -184,7 +187,7 @@ int minfer_op_paged_attention(const void* d_q, int64_t q_stride, const minfer_pa
   if (!aligned16(d_q) || !aligned16(d_o) || !aligned16(d_workspace) || !stride_ok(q_stride, cache->type) ||
       !stride_ok(o_stride, cache->type) || (n_req > 1 && (q_stride < q || o_stride < q || table_stride < max_pages)))
     return MINFER_ERR_ARG;
-  if (!fits31(max_pages, cache->page_size) || n_head > 65535) return MINFER_ERR_TOO_LARGE;
+  if (!fits31(max_pages, cache->page_size) || n_head > kMaxHeads) return MINFER_ERR_TOO_LARGE;
   const int sms = current_sms();
   if (sms == 0) return MINFER_ERR_CUDA;
   if (workspace_bytes < paged_attn_workspace(n_head / a.c.nkv, a.c.hd, cache->type, sms))

@@ -72,7 +72,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_tables_kernel(const PageTa
   enum { kBadLen = 1, kTooMany = 2, kNoPages = 4, kBadPage = 8 };
 
   if (tid == 0) s_local = s_err = 0;
-  pdl_trigger();
+  // No early launch of the next kernel: the forward's kernels read positions, which
+  // this one writes, before they wait for their predecessor.
   pdl_wait();
   if (nrank > 1)
     pt_cluster_sync();  // s_err is set in every CTA before a peer may OR into it

@@ -421,10 +421,9 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
     for (int r = r_lo; r < r_hi; ++r) {
       const int len = a.len[r], units = units_of<kUnit>(len, cap);
       if (begin < at + (int64_t)units * nv) {
-        const int off = (int)(begin - at);
         s_walk.r = r;
-        s_walk.v = off / units;
-        s_walk.u = off - s_walk.v * units;
+        s_walk.v = (int)((begin - at) / units);
+        s_walk.u = (int)(begin - at - (int64_t)s_walk.v * units);
         s_walk.units = units;
         s_walk.len = len;
         s_walk.next_len = len_at(a, r + 1);

@@ -87,7 +87,8 @@ def _store_args(qp, cache=None, rope=None):
     (dict(q_out=None), ARG), (dict(n_tokens=0), ARG), (dict(n_head=0), ARG), (dict(n_head=3), ARG), (dict(qnorm=PTR), ARG),
     (dict(knorm=PTR), ARG), (dict(eps=-1.0), ARG), (dict(eps=math.nan), ARG), (dict(type=F16), SHAPE), (dict(type=8), SHAPE),
     (dict(qkv=PTR + 2), ARG), (dict(q_out=PTR + 4), ARG), (dict(bias=PTR + 4), ARG), (dict(row_stride=516), ARG),
-    (dict(row_stride=504), ARG), (dict(q_stride=248), ARG), (dict(q_stride=260), ARG)])
+    (dict(row_stride=504), ARG), (dict(q_stride=248), ARG), (dict(q_stride=260), ARG),
+    (dict(n_head=65536, row_stride=2 ** 23, q_stride=2 ** 23), TOO_LARGE)])
 def test_rope_store_arguments(qp, change, code):
     keep, args = _store_args(qp)
     assert _call(qp.lib().minfer_op_rope_paged_store, args, **change) == code

@@ -245,6 +245,8 @@ ROPE_CASES = [
     (4, 4, 64, F32, F32, 7, "half", 2, "none", False, False),
     (5, 1, 128, BF16, BF16, 16, "half", 90, "linear", True, True),
     (40, 8, 128, F32, BF16, 16, "half", 128, "none", False, False),
+    (160, 32, 128, F32, F16, 16, "interleaved", 90, "yarn", False, True),
+    (3, 3, 64, F16, F16, 16, "half", 20, "none", True, True),
 ]
 
 
@@ -353,16 +355,20 @@ def attention_by_definition(q, k, v, table, length, nh, scale):
 
 def attention_tolerance(t, hd, length, want):
     """Score error: the MMA sums over the head's dims truncate (2^-23 of the
-    partial sum each, hd / 8 + 2 of them), f32 operands are split into two tf32
-    halves (3 * 2^-24); the scaled score's rounding and the exponential's 2 ulp
-    come on top.  Each weight's relative error is the score error twice (its own and
-    the sum's); 16-bit weights are rounded (half a step, or half of the smallest
-    subnormal under a sum that is at least 1); sums of up to 64 + units adds."""
+    partial sum each, hd / 8 + 2 of them); of f32 operands as hi + lo, |lo| <= 2^-11
+    of the value, the product of the two lo (2^-22) and the bits that the MMA cuts
+    from each lo (2^-10 of it, 2^-21) are left out: 2^-22 + 2 * 2^-21 = 20 U of a
+    product; the scaled score's rounding and the exponential's 2 ulp come on top.
+    Each weight's relative error is the score error twice (its own and the sum's);
+    16-bit weights are rounded (half a step, or half of the smallest subnormal under
+    a sum that is at least 1), f32 weights and values lose 20 U again; sums of up to
+    64 + units adds."""
     o, lse, mean, size, top = want
     steps = hd // 8 + 2
-    score = size * (steps * 2.0 ** -23 + 3 * U + 4 * U) + 8 * U
+    split = 20 * U if t == F32 else 0
+    score = size * (steps * 2.0 ** -23 + split + 4 * U) + 8 * U
     m = torch.tensor([max(x, 1) for x in length], dtype=torch.float64, device="cuda")[:, None, None]
-    rel = 2 * score + (32 + 6 * torch.log2(m) + m / 64) * U
+    rel = 2 * score + (32 + 6 * torch.log2(m) + m / 64) * U + split
     tol = rel * mean
     if t != F32:
         tol = tol + half(t) * (o.abs() + mean) + top * m * (2.0 ** -25 if t == F16 else 0)
@@ -421,7 +427,7 @@ def test_paged_attention(qp, t, nh, nkv, hd, length, P, order):
     check_attention(qp, t, nh, nkv, hd, P, length, order, seed=len(length) + nh)
 
 
-@pytest.mark.parametrize("t", [F32, BF16])
+@pytest.mark.parametrize("t", [F32, F16, BF16])
 @pytest.mark.parametrize("nh,nkv,hd", [(8, 1, 64), (9, 1, 128), (16, 1, 64), (17, 1, 128), (32, 1, 64), (64, 2, 64), (3, 1, 128)])
 def test_paged_attention_head_groups(qp, t, nh, nkv, hd):
     check_attention(qp, t, nh, nkv, hd, 8, [5, 130, 0, 67], seed=nh)
@@ -435,6 +441,13 @@ def test_paged_attention_page_sizes(qp, P):
 @pytest.mark.parametrize("t,length", [(BF16, [40001]), (F32, [9000, 1]), (F16, [131071])])
 def test_paged_attention_long(qp, t, length):
     check_attention(qp, t, 14, 2, 64, 64, length)
+
+
+@pytest.mark.parametrize("t", [F32, F16, BF16])
+@pytest.mark.parametrize("nh,nkv", [(7, 1), (12, 2), (32, 2)])
+@pytest.mark.parametrize("length", [[6000, 0, 2047], [30001]])
+def test_paged_attention_long_wide_heads(qp, t, nh, nkv, length):
+    check_attention(qp, t, nh, nkv, 128, 48, length, "heads")
 
 
 def test_paged_attention_many_ragged_requests(qp):
@@ -508,6 +521,44 @@ def test_paged_attention_refuses_requests_on_the_device(qp, t):
         tol, _ = attention_tolerance(t, hd, length, want)
         close(out[rest].view(-1, nh, hd), good[rest].view(-1, nh, hd), 2 * tol[rest])
         close(out[rest].view(-1, nh, hd), want[0][rest], tol[rest])
+
+
+@pytest.mark.parametrize("t,nh,nkv,hd", [(BF16, 14, 2, 64), (F16, 16, 1, 128), (F32, 12, 2, 128)])
+def test_paged_attention_refuses_a_long_request(qp, t, nh, nkv, hd):
+    """A bad page in one of many shares: the mark goes through both levels of the
+    join, and the next call with the same workspace is what it should be."""
+    length, P = [20000, 77], 16
+    q, k, v, table = attention_case(6, t, nh, nkv, hd, P, length)
+    cache = qp.PagedCache(k, v)
+    work = qp.op_paged_attention_workspace(cache, 2, nh)
+    good = qp.op_paged_attention(q, cache, table, dev(length), nh, workspace=work)
+    for page in (0, 600, 1249):
+        bad = table.clone()
+        bad[0, page] = -1
+        out, status = torch.full_like(q, 3.0), status_word()
+        qp.op_paged_attention(q, cache, bad, dev(length), nh, out=out, workspace=work, status=status)
+        assert int(status) == -2 and (out[0] == 3).all() and torch.equal(out[1], good[1])
+    assert torch.equal(good, qp.op_paged_attention(q, cache, table, dev(length), nh, workspace=work))
+    assert int(work.buffer[:4096].sum()) == 0  # the counters
+
+
+def test_workspaces_serve_calls_of_other_sizes(qp):
+    """One workspace for calls of several shapes in turn: what one leaves behind
+    does not reach the next."""
+    nh, nkv, hd = 14, 2, 64
+    cases = [attention_case(i, BF16, nh, nkv, hd, 16, length) + (length,) for i, length in enumerate(([5000], [3, 900, 0, 64], [1] * 40))]
+    work = qp.op_paged_attention_workspace(qp.PagedCache(cases[0][1], cases[0][2]), 40, nh)
+    g = gen(2)
+    logits = [torch.randn(r, v, generator=g, device="cuda").to(t) for r, v, t in ((300, 20000, F32), (7, 9999, BF16), (1, 151936, F32), (1200, 600, F16))]
+    lwork = max((qp.op_token_logprobs_workspace(x, 9) for x in logits), key=lambda w: w.nbytes)
+    for _ in range(2):
+        for q, k, v, table, length in cases:
+            cache = qp.PagedCache(k, v)
+            a = qp.op_paged_attention(q, cache, table, dev(length), nh, workspace=work)
+            assert torch.equal(a, qp.op_paged_attention(q, cache, table, dev(length), nh))
+        for x in logits:
+            a, b = (qp.op_token_logprobs(x, None, 9, workspace=w) for w in (lwork, None))
+            assert all(torch.equal(i, j) for i, j in zip(a[1:], b[1:]))
 
 
 def test_paged_attention_shared_pages_and_repeats(qp):
