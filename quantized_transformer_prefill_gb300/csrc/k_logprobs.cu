@@ -1,12 +1,8 @@
 // k_logprobs.cu -- log probabilities of given tokens, entropy and the k
 // largest of logits rows, in one pass over the logits.
 //
-//   m = max x,  s = sum e^(x-m),  t = sum e^(x-m) (x-m) log2 e
+//   s = sum e^(x-m),  t = sum e^(x-m) (x-m) log2 e,  m a logit near the largest
 //   log p_i = (x_i - m) - ln s,   H = ln 2 (log2 s - t / s)
-//
-// x - m is taken before the factor log2 e: one multiply-add with a rounded
-// m log2 e would be off by 2^-24 |m|, which for logits of 1e30, or for rows
-// masked with the type's lowest value, is any power of two.
 //
 // A row is cut into parts, one CTA each.  Every thread keeps a running
 // (reference, s, t); a warp reads chunks of 512 neighbouring logits and leaves
@@ -22,6 +18,12 @@
 // Pairs (value, id) are compared as one 64-bit key, the value's
 // order-preserving bits above the complemented id: keys are distinct, and equal
 // values rank by ascending id whatever the order in which they are met.
+//
+// Measured on a GB300 (us a call, device): 512 f32 rows of 151,936 59 (311 MB, 5.3
+// TB/s, 78% of the measured copy), without a top k 53; 65 bf16 rows of 150,001 15;
+// one f32 row 7.9, without a top k 4.5.  The stream is bound by HBM, with 6 or 7
+// instructions a logit next to it; a row's join adds 3 us of dependent steps, of
+// which the rows in flight hide a part.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -509,8 +511,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
 }
 
 // Parts of a row: with fewer rows than the GPU holds CTAs, as many as fill it
-// once; with more, so many that it is filled kWaves times, which keeps the last
-// round's idle share small.  None has less than a chunk per warp.
+// once (65 rows: 15.0 us; twice as many parts 19); with more, so many that it is
+// filled kWaves times, for the last round's idle share (512 rows: once 67 us, twice
+// 59, three times 61).  None has less than a chunk per warp.
 Plan plan_of(int64_t rows, int64_t vocab, int vec, int k, int num_sms) {
   Plan p;
   p.chunks = (int)((vocab + vec - 1 + kChunk - 1) / kChunk);

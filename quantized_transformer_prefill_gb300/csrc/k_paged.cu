@@ -13,7 +13,10 @@ namespace {
 
 // ================================================================ page tables
 //
-// One thread-block cluster does a step.  Every CTA scans all requests (new
+// One thread-block cluster does a step, or one CTA where there is little to write
+// (32 requests of one token 4.0 us against 5.1 with eight CTAs, 1,087 tokens 6.5
+// against 7.6, 2,164 tokens 7.7 against 7.4; 21,500 tokens of 1,023 requests take
+// 10.7 us with eight, and 9.6 with sixteen, which is no portable cluster size).  Every CTA scans all requests (new
 // tokens, grown pages, returned pages: three exclusive prefix sums in its own
 // shared memory), checks its share of the page ids the step will use, and
 // after one cluster barrier, at which the CTAs learn whether any of them found
@@ -305,10 +308,18 @@ __device__ __forceinline__ void turn_cos_sin(uint64_t f, float* c, float* s) {
 
 constexpr int kRpWarps = 8;
 constexpr int kRpTokens = 4;     // of a CTA, at most
-constexpr int kRpFill = 2;       // CTAs per SM that more tokens per CTA must leave
-constexpr int kRpMaxBias = 24576;  // values that are kept in shared memory
+// CTAs per SM that more tokens per CTA must leave (1: 1,001 rows 9.6 us, 500 rows
+// 6.3; 2: 7.3 and 5.2; 4: 8.4 and 5.1)
+constexpr int kRpFill = 2;
+// Values of the bias that are kept in shared memory; read from global memory for
+// every head instead, it made the 4096 rows 30 us.
+constexpr int kRpMaxBias = 24576;
 constexpr int kRpRing = 8;       // units of a warp on their way or at work
 
+// Bound by HBM: 4096 f32 rows of 36 heads of 128 into a bf16 cache, 113 MB, take
+// 20 us (5.7 TB/s, 84% of the measured copy); 1,001 f16 rows with QK-norm 6.2 us;
+// 64 rows 2.5 us, a launch.
+//
 // A CTA takes 1, 2 or 4 tokens.  Its threads work out the tokens' cosines and
 // sines, one pair each, while the rows are on the way; then 8, 4 or 2 warps go
 // over a token's heads.  A lane takes E neighbouring elements of a head (one
@@ -520,7 +531,7 @@ cudaError_t page_tables_launch(const PageTablesArgs& a, cudaStream_t stream) {
     const cudaError_t e = allow_smem<page_tables_kernel>(3 * (kPageTablesMaxReq + 1) * (int)sizeof(int));
     if (e != cudaSuccess) return e;
   }
-  const unsigned cs = (a.max_tokens > 4096 || a.n_req > 1024) ? kPtCluster : 1;
+  const unsigned cs = (a.max_tokens > 2048 || a.n_req > 1024) ? kPtCluster : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cs);
   cfg.blockDim = dim3(kPtThreads);

@@ -31,8 +31,17 @@
 // needs them.
 //
 // f32 caches: every operand is split into two tf32 halves and three products are
-// taken (what is left out is 2^-22 of a product), and each unit's P V is added to
-// the running sum as an f32 addition of its own.
+// taken (what is left out is at most 5 * 2^-22 of a product, of either sign), and
+// each unit's P V is added to the running sum as an f32 addition of its own.
+//
+// Measured on a GB300 (us a call, device; bytes of K and V at the measured copy
+// rate of 6.77 TB/s in brackets): 64 requests of up to 4096 rows, 28/4 heads of
+// 128, bf16: 52 (44); one of 131,071, 12/2 heads of 128, f16: 30 (20); 33 of up to
+// 2048, 14/2 heads of 64, f32: 15 (5); one of 513: 6.3.  While units are worked on
+// the rows come in at 7.1 TB/s; what is left is the start (lengths, page lookup,
+// first rows: 3 us), equal shares ending up to a tenth apart, and the join (report
+// 1 us, 2 to 3 us a level).  Small last shares for CTAs that start where one has
+// finished early made 64 x 4096 3% and the single long request 15% slower.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -48,7 +57,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 constexpr int kGroup = 16;              // neighbouring shares whose partials are joined first
 constexpr int kMaxJoin = 64;            // partials of one join: kDirect, kGroup, or the number of groups
-constexpr int kDirect = 32;             // partials that are joined in one step
+// Partials that are joined in one step (20 of them: 8.3 us a call, in two steps
+// 9.8; 32 of them: 10.2 either way).
+constexpr int kDirect = 32;
 
 // What the threads of a CTA share while they join partials.
 template <int R>
@@ -58,15 +69,21 @@ struct JoinShared {
   float2 out[R];          // the joined (max, sum)
 };
 
-// R: query heads of a head block, one MMA tile of 8 or two.
+// R: query heads of a head block, one MMA tile of 8, or two where a KV head of a
+// 16-bit cache has more than 8 (32/2 heads of 128, 64 requests of up to 4096: 35 us
+// against 40 with two blocks of 8, which read K and V twice, the second time for
+// the most part out of L2).  An f32 block of 16 would not fit the registers.
 template <typename T, int HD, int R>
 struct Cfg {
   static constexpr bool kF32 = sizeof(T) == 4;
   static constexpr int kRowBytes = HD * (int)sizeof(T);
   static constexpr int kChunks = kRowBytes / 16;             // 16-byte chunks of a row
   static constexpr int kStageBytes = 2 * kKeys * kRowBytes;  // K and V rows of one warp
-  // as many CTAs per SM as their registers and two stages of the ring allow; the
-  // ring takes what is left of the SM's shared memory
+  // As many CTAs per SM as their registers and two stages of the ring allow; the
+  // ring takes what is left of the SM's shared memory.  Rows of 512 bytes (f32,
+  // head size 128) have CTAs of two warps: three of them hold 6 warps where one
+  // CTA of four would fit (64 requests of up to 1024, 16/8 heads: 60 us against
+  // 72; 4 of up to 2048, 12/2 heads: 13 against 11, for its shares are smaller).
   static constexpr int kWarps = kRowBytes == 512 ? 2 : 4;
   static constexpr int kCtas = kRowBytes == 128 ? 4 : R == 8 ? 3 : 2;
   static constexpr int kUnit = kWarps * kKeys;  // keys of a unit
@@ -202,16 +219,16 @@ __device__ __forceinline__ void walk_next(Walk& w, const PagedAttnArgs& a, int n
   } while (w.units == 0 && w.r < a.n_req);
 }
 
-// How the units are cut into shares: as many as there are CTAs, but none with
-// less than kLeast units (a share more costs a join, which takes as long as a few
-// units); the first `more` of them hold one unit more than the others.
-constexpr int kLeast = 1;
+// How the units are cut into shares: as many as there are CTAs, none of them
+// empty; the first `more` of them hold one unit more than the others.  (At least
+// two units a share made a single request of 64 rows slower, 6.3 us against 4.2,
+// for its two KV heads then share a CTA.)
 struct Shares {
   int64_t total, each;
   int n, more;
   __device__ __forceinline__ Shares(int64_t units, int n_ctas) {
     total = units;
-    n = (int)max((int64_t)1, min(units / kLeast, (int64_t)n_ctas));
+    n = (int)max((int64_t)1, min(units, (int64_t)n_ctas));
     // (64-bit divisions are long; few batches need one)
     each = total >> 32 ? total / n : (int64_t)((uint32_t)total / (uint32_t)n);
     more = (int)(total - each * n);
@@ -455,6 +472,7 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
     const bool ok = (unsigned)page_next < (unsigned)a.c.n_pages;
     const uint32_t kdst = ring + stage * C::kStageBytes, vdst = kdst + kKeys * C::kRowBytes;
     if (one_page) {
+      // (no shuffles of addresses: f32 rows of 128 60 us against 64, 16-bit rows 1%)
       const int in_page = key0 - a.c.div.of(key0) * P;
       const int live = ok ? lw.len - key0 : 0;
       int64_t off = 0;
@@ -864,10 +882,7 @@ int ctas(int num_sms) {
   return std::min(num_sms * Cfg<T, HD, R>::kCtas, kMaxShares);
 }
 
-// Runs f with the type, head size and heads of a block that the call's sizes
-// pick: blocks of 16 heads where a KV head has more than 8 and the cache is
-// 16-bit (an f32 block of 16 does not fit the registers; its blocks of 8 read K
-// and V again, out of L2 for the most part).
+// Runs f with the type, head size and head block of a call.
 template <typename F>
 auto with_config(int type, int hd, int G, F f) {
   auto sized = [&](auto t) {
