@@ -15,8 +15,8 @@ namespace {
 //
 // One thread-block cluster does a step, or one CTA where there is little to write
 // (32 requests of one token 4.0 us against 5.1 with eight CTAs, 1,087 tokens 6.5
-// against 7.6, 2,164 tokens 7.7 against 7.4; 21,500 tokens of 1,023 requests take
-// 10.7 us with eight, and 9.6 with sixteen, which is no portable cluster size).  Every CTA scans all requests (new
+// against 7.6, 2,164 tokens 7.7 against 7.4; sixteen where there is much: 6,364
+// tokens 8.2 with either, 21,500 tokens of 1,023 requests 9.6 against 10.6).  Every CTA scans all requests (new
 // tokens, grown pages, returned pages: three exclusive prefix sums in its own
 // shared memory), checks its share of the page ids the step will use, and
 // after one cluster barrier, at which the CTAs learn whether any of them found
@@ -25,7 +25,7 @@ namespace {
 // CTA still reads is written after it: the entries that grow, the stack above
 // its old depth and the outputs are read by nobody.
 constexpr int kPtThreads = 1024;
-constexpr int kPtCluster = 8;
+constexpr int kPtMostSmem = 96 * 1024;  // of a CTA in a cluster of 16, so that two fit an SM
 
 __device__ __forceinline__ uint32_t pt_cluster_rank() {
   uint32_t r;
@@ -37,10 +37,8 @@ __device__ __forceinline__ uint32_t pt_cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void pt_cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
+__device__ __forceinline__ void pt_cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void pt_cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // Largest i in [0, n) with a[i] <= x (a ascending, a[0] <= x < a[n]), for Q values
 // at once: the same number of steps for all, their loads side by side.
@@ -75,13 +73,10 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_tables_kernel(const PageTa
   enum { kBadLen = 1, kTooMany = 2, kNoPages = 4, kBadPage = 8 };
 
   if (tid == 0) s_local = s_err = 0;
+  if (nrank > 1) pt_cluster_arrive();  // waited for before a peer's s_err is touched
   // No early launch of the next kernel: the forward's kernels read positions, which
   // this one writes, before they wait for their predecessor.
   pdl_wait();
-  if (nrank > 1)
-    pt_cluster_sync();  // s_err is set in every CTA before a peer may OR into it
-  else
-    __syncthreads();
 
   const int cap = a.max_pages * P;
   auto pages = [&](int rows) { return rows == 0 ? 0 : a.div.of(rows - 1) + 1; };
@@ -198,12 +193,14 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_tables_kernel(const PageTa
     if (__syncthreads_or(bad)) err |= kBadPage;
   }
   if (nrank > 1) {
+    pt_cluster_wait();
     if (err && tid < (int)nrank) {
       uint32_t addr;
       asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(&s_err)), "r"(tid));
       asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(err) : "memory");
     }
-    pt_cluster_sync();
+    pt_cluster_arrive();
+    pt_cluster_wait();
     err = s_err;
   }
 
@@ -531,7 +528,18 @@ cudaError_t page_tables_launch(const PageTablesArgs& a, cudaStream_t stream) {
     const cudaError_t e = allow_smem<page_tables_kernel>(3 * (kPageTablesMaxReq + 1) * (int)sizeof(int));
     if (e != cudaSuccess) return e;
   }
-  const unsigned cs = (a.max_tokens > 2048 || a.n_req > 1024) ? kPtCluster : 1;
+  unsigned cs = (a.max_tokens > 2048 || a.n_req > 1024) ? 8 : 1;
+  if (a.max_tokens > 8192 && smem <= kPtMostSmem) {
+    // more than the portable cluster size, where the device allows it
+    static int allowed = 0;  // 0: not asked yet, 1, or -1; every thread writes the same
+    int ok = __atomic_load_n(&allowed, __ATOMIC_RELAXED);
+    if (ok == 0) {
+      ok = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess ? 1 : -1;
+      if (ok < 0) (void)cudaGetLastError();
+      __atomic_store_n(&allowed, ok, __ATOMIC_RELAXED);
+    }
+    if (ok > 0) cs = 16;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cs);
   cfg.blockDim = dim3(kPtThreads);
