@@ -25,6 +25,7 @@ namespace {
 // CTA still reads is written after it: the entries that grow, the stack above
 // its old depth and the outputs are read by nobody.
 constexpr int kPtThreads = 1024;
+constexpr int kPtUnaskedSmem = 40 * 1024;  // with the kernel's static bytes below the 48 KB that need no leave
 constexpr int kPtMostSmem = 96 * 1024;  // of a CTA in a cluster of 16, so that two fit an SM
 
 __device__ __forceinline__ uint32_t pt_cluster_rank() {
@@ -524,7 +525,7 @@ cudaError_t rope_paged_typed(const RopePagedArgs& a, int num_sms, cudaStream_t s
 
 cudaError_t page_tables_launch(const PageTablesArgs& a, cudaStream_t stream) {
   const size_t smem = 3 * (size_t)(a.n_req + 1) * sizeof(int);
-  if (smem > 48 * 1024) {
+  if (smem > kPtUnaskedSmem) {
     const cudaError_t e = allow_smem<page_tables_kernel>(3 * (kPageTablesMaxReq + 1) * (int)sizeof(int));
     if (e != cudaSuccess) return e;
   }

@@ -118,6 +118,13 @@ def test_page_tables(qp, n, P, W, kinds):
         assert int(status) == 0
 
 
+@pytest.mark.parametrize("n", [3412, 3413, 4061, 4062, 4095, 4096])
+def test_page_tables_around_the_default_shared_memory(qp, n):
+    """Three counts of 4 bytes a request pass 40 KB at 3,413 requests and 48 KB, less the kernel's static bytes, from
+    about 4,062: on either side of both the step is done."""
+    test_page_tables(qp, n, 8, 2, ["one", "same", "back"])
+
+
 def test_page_tables_long_prompt_into_an_empty_pool(qp):
     P, W = 128, 1024
     ids = list(range(2 * W))
