@@ -25,8 +25,9 @@ namespace {
 // CTA still reads is written after it: the entries that grow, the stack above
 // its old depth and the outputs are read by nobody.
 constexpr int kPtThreads = 1024;
-constexpr int kPtUnaskedSmem = 40 * 1024;  // with the kernel's static bytes below the 48 KB that need no leave
-constexpr int kPtMostSmem = 96 * 1024;  // of a CTA in a cluster of 16, so that two fit an SM
+// What a launch gets unasked, 48 KB, less the kernel's static bytes: of that size
+// are also the CTAs of a cluster of 16 (3,412 requests).
+constexpr int kPtUnaskedSmem = 40 * 1024;
 
 __device__ __forceinline__ uint32_t pt_cluster_rank() {
   uint32_t r;
@@ -521,6 +522,36 @@ cudaError_t rope_paged_typed(const RopePagedArgs& a, int num_sms, cudaStream_t s
   return a.c.hd == 64 ? rope_paged_sized<TS, TD, 64>(a, num_sms, st) : rope_paged_sized<TS, TD, 128>(a, num_sms, st);
 }
 
+// Whether the current device runs a cluster of sixteen CTAs, more than the portable
+// size: asked for once per device.
+bool pt_sixteen_fit() {
+  constexpr int kMaxDevices = 64;
+  static int8_t known[kMaxDevices];  // 0: not asked yet, 1 or -1; every thread writes the same
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return false;
+  int8_t fit = __atomic_load_n(&known[dev], __ATOMIC_RELAXED);
+  if (fit == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(kPtThreads);
+    cfg.dynamicSmemBytes = kPtUnaskedSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 16;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    const bool ok = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                    cudaOccupancyMaxActiveClusters(&clusters, page_tables_kernel, &cfg) == cudaSuccess && clusters > 0;
+    if (!ok) (void)cudaGetLastError();  // a cluster of eight serves
+    fit = ok ? 1 : -1;
+    __atomic_store_n(&known[dev], fit, __ATOMIC_RELAXED);
+  }
+  return fit > 0;
+}
+
 }  // namespace
 
 cudaError_t page_tables_launch(const PageTablesArgs& a, cudaStream_t stream) {
@@ -530,17 +561,7 @@ cudaError_t page_tables_launch(const PageTablesArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   unsigned cs = (a.max_tokens > 2048 || a.n_req > 1024) ? 8 : 1;
-  if (a.max_tokens > 8192 && smem <= kPtMostSmem) {
-    // more than the portable cluster size, where the device allows it
-    static int allowed = 0;  // 0: not asked yet, 1, or -1; every thread writes the same
-    int ok = __atomic_load_n(&allowed, __ATOMIC_RELAXED);
-    if (ok == 0) {
-      ok = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess ? 1 : -1;
-      if (ok < 0) (void)cudaGetLastError();
-      __atomic_store_n(&allowed, ok, __ATOMIC_RELAXED);
-    }
-    if (ok > 0) cs = 16;
-  }
+  if (a.max_tokens > 8192 && smem <= kPtUnaskedSmem && pt_sixteen_fit()) cs = 16;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cs);
   cfg.blockDim = dim3(kPtThreads);
