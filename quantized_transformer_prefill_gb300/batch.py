@@ -8,9 +8,10 @@ tensor of one element in which the kernels leave the first error code they find
 (check_status reads it).
 
 A small call takes less time on the GPU than its arguments take to be checked
-in Python, so the checks are written out, cheapest expressions first, and an
-error message is put together only when one fails (measured on the host of a
-GB300: a helper per tensor with its message 1.2 us, written out 0.3 us).
+in Python, so the checks are written out, with the attributes that are cheapest
+to read (a vector is any contiguous tensor of so many elements), and an error
+message is put together only when one fails (measured on the host of a GB300: a
+helper per tensor with its message 1.2 us, written out 0.3 us).
 """
 from __future__ import annotations
 
@@ -110,20 +111,18 @@ def op_page_tables(length, target, page_size: int, table, free, n_free, n_pages:
     Returns (start [n_req + 1], pos [max_tokens], slot [max_tokens], n_free
     [1]), or fills `out`, four such tensors; the last may be n_free itself."""
     dev = length.get_device()
-    n = length.shape[0] if length.dim() == 1 else -1
-    of_n = (n,)
-    if not (length.dtype is _I32 and length.shape == of_n and length.is_contiguous()):
+    n = length.numel()
+    if not (length.dtype is _I32 and length.is_contiguous()):
         _refuse("length: int32 [n_req] wanted", length)
-    if not (target.dtype is _I32 and target.shape == of_n and target.is_contiguous() and target.get_device() == dev):
+    if not (target.dtype is _I32 and target.numel() == n and target.is_contiguous() and target.get_device() == dev):
         _refuse("target: int32 [n_req] wanted", target)
-    if not (table.dtype is _I32 and table.dim() == 2 and table.is_contiguous() and table.get_device() == dev):
+    shape = table.shape
+    if not (table.dtype is _I32 and len(shape) == 2 and shape[0] == n and table.is_contiguous()
+            and table.get_device() == dev):
         _refuse("table: int32 [n_req][max_pages] wanted", table)
-    rows, max_pages = table.shape
-    if rows != n:
-        _refuse("table: int32 [n_req][max_pages] wanted", table)
-    if not (free.dtype is _I32 and free.shape == (n_pages,) and free.is_contiguous() and free.get_device() == dev):
+    if not (free.dtype is _I32 and free.numel() == n_pages and free.is_contiguous() and free.get_device() == dev):
         _refuse("free: int32 [n_pages] wanted", free)
-    if not (n_free.dtype is _I32 and n_free.shape == (1,) and n_free.get_device() == dev):
+    if not (n_free.dtype is _I32 and n_free.numel() == 1 and n_free.get_device() == dev):
         _refuse("n_free: int32 [1] wanted", n_free)
     if status is not None and not (status.dtype is _I32 and status.numel() == 1 and status.get_device() == dev):
         _refuse("status: int32 [1] wanted", status)
@@ -137,15 +136,15 @@ def op_page_tables(length, target, page_size: int, table, free, n_free, n_pages:
         start, pos, slot, left = out
     else:
         start, pos, slot, left = out
-        if not (start.dtype is _I32 and start.shape == (n + 1,) and start.is_contiguous() and start.get_device() == dev):
+        if not (start.dtype is _I32 and start.numel() == n + 1 and start.is_contiguous() and start.get_device() == dev):
             _refuse("start: int32 [n_req + 1] wanted", start)
-        if not (pos.dtype is _I32 and pos.shape == (max_tokens,) and pos.is_contiguous() and pos.get_device() == dev):
+        if not (pos.dtype is _I32 and pos.numel() == max_tokens and pos.is_contiguous() and pos.get_device() == dev):
             _refuse("pos: int32 [max_tokens] wanted", pos)
-        if not (slot.dtype is _I32 and slot.shape == (max_tokens,) and slot.is_contiguous() and slot.get_device() == dev):
+        if not (slot.dtype is _I32 and slot.numel() == max_tokens and slot.is_contiguous() and slot.get_device() == dev):
             _refuse("slot: int32 [max_tokens] wanted", slot)
-        if not (left.dtype is _I32 and left.shape == (1,) and left.get_device() == dev):
+        if not (left.dtype is _I32 and left.numel() == 1 and left.get_device() == dev):
             _refuse("n_free of out: int32 [1] wanted", left)
-    rc = _page_tables(length.data_ptr(), target.data_ptr(), n, page_size, n_pages, table.data_ptr(), max_pages,
+    rc = _page_tables(length.data_ptr(), target.data_ptr(), n, page_size, n_pages, table.data_ptr(), shape[1],
                       free.data_ptr(), n_free.data_ptr(), left.data_ptr(), start.data_ptr(), pos.data_ptr(),
                       slot.data_ptr(), max_tokens, None if status is None else status.data_ptr(), _stream_of(dev))
     if rc:
@@ -162,22 +161,22 @@ def op_rope_paged_store(qkv, rope: RopeTable, pos, slot, cache: PagedCache, n_he
     they are zero)."""
     dev, hd = qkv.get_device(), cache.head_dim
     width = (n_head + 2 * cache.n_head_kv) * hd
-    n = qkv.shape[0] if qkv.dim() == 2 else -1
-    if not (qkv.shape == (n, width) and dev == cache.index):
+    shape = qkv.shape
+    if not (len(shape) == 2 and shape[1] == width and dev == cache.index):
         _refuse(f"qkv: rows of {width} on the cache's device wanted", qkv)
+    n = shape[0]
     row_stride, one = qkv.stride()
     if one != 1:
         _refuse("qkv: contiguous rows wanted", qkv)
-    of_n = (n,)
-    if not (pos.dtype is _I32 and pos.shape == of_n and pos.is_contiguous() and pos.get_device() == dev):
+    if not (pos.dtype is _I32 and pos.numel() == n and pos.is_contiguous() and pos.get_device() == dev):
         _refuse("pos: int32 [n] wanted", pos)
-    if not (slot.dtype is _I32 and slot.shape == of_n and slot.is_contiguous() and slot.get_device() == dev):
+    if not (slot.dtype is _I32 and slot.numel() == n and slot.is_contiguous() and slot.get_device() == dev):
         _refuse("slot: int32 [n] wanted", slot)
-    if bias is not None and not (bias.dtype is _F32 and bias.shape == (width,) and bias.is_contiguous()
+    if bias is not None and not (bias.dtype is _F32 and bias.numel() == width and bias.is_contiguous()
                                  and bias.get_device() == dev):
         _refuse(f"bias: float32 [{width}] wanted", bias)
     for w in (q_norm, k_norm):
-        if w is not None and not (w.dtype is _F32 and w.shape == (hd,) and w.is_contiguous() and w.get_device() == dev):
+        if w is not None and not (w.dtype is _F32 and w.numel() == hd and w.is_contiguous() and w.get_device() == dev):
             _refuse(f"q_norm, k_norm: float32 [{hd}] wanted", w)
     if status is not None and not (status.dtype is _I32 and status.numel() == 1 and status.get_device() == dev):
         _refuse("status: int32 [1] wanted", status)
@@ -222,20 +221,21 @@ def op_paged_attention(q, cache: PagedCache, table, length, n_head: int, scale: 
     new one included.  Returns o like q; `lse` (float32 [n_req][n_head]), when
     given, gets ln sum exp(scale q.k)."""
     dev, width = q.get_device(), n_head * cache.head_dim
-    n = q.shape[0] if q.dim() == 2 else -1
-    of_q = (n, width)
-    if not (q.dtype is cache.dtype and q.shape == of_q and dev == cache.index):
+    shape = q.shape
+    if not (q.dtype is cache.dtype and len(shape) == 2 and shape[1] == width and dev == cache.index):
         _refuse(f"q: rows of {width} {cache.dtype} on {cache.device} wanted", q)
+    n = shape[0]
     q_stride, one = q.stride()
     if one != 1:
         _refuse("q: contiguous rows wanted", q)
-    if not (table.dtype is _I32 and table.dim() == 2 and table.get_device() == dev):
+    pages = table.shape
+    if not (table.dtype is _I32 and len(pages) == 2 and pages[0] == n and table.get_device() == dev):
         _refuse("table: int32 [n_req][max_pages] wanted", table)
-    rows, max_pages = table.shape
     table_stride, one = table.stride()
-    if rows != n or (one != 1 and max_pages > 1):
-        _refuse("table: int32 [n_req][max_pages] with contiguous rows wanted", table)
-    if not (length.dtype is _I32 and length.shape == (n,) and length.is_contiguous() and length.get_device() == dev):
+    max_pages = pages[1]
+    if one != 1 and max_pages > 1:
+        _refuse("table: contiguous rows wanted", table)
+    if not (length.dtype is _I32 and length.numel() == n and length.is_contiguous() and length.get_device() == dev):
         _refuse("length: int32 [n_req] wanted", length)
     if lse is not None and not (lse.dtype is _F32 and lse.shape == (n, n_head) and lse.is_contiguous()
                                 and lse.get_device() == dev):
@@ -248,10 +248,10 @@ def op_paged_attention(q, cache: PagedCache, table, length, n_head: int, scale: 
         with torch.cuda.device(dev):
             return op_paged_attention(q, cache, table, length, n_head, scale, out, lse, workspace, status)
     if out is None:
-        out = torch.empty(of_q, dtype=q.dtype, device=q.device)
+        out = torch.empty((n, width), dtype=q.dtype, device=q.device)
         o_stride = width
     else:
-        if not (out.dtype is cache.dtype and out.shape == of_q and out.get_device() == dev):
+        if not (out.dtype is cache.dtype and out.shape == shape and out.get_device() == dev):
             _refuse("out: like q wanted", out)
         o_stride, one = out.stride()
         if one != 1:
@@ -287,41 +287,42 @@ def op_token_logprobs(logits, ids=None, k: int = 0, out=None, workspace: Workspa
     top_logprobs), or fills `out`, four such tensors (logprob without ids,
     entropy, and the last two with k = 0 may be None); logprob is None without
     ids."""
-    dev = logits.get_device()
-    if logits.dim() != 2:
+    dev, shape = logits.get_device(), logits.shape
+    if len(shape) != 2:
         _refuse("logits: [rows][vocab] wanted", logits)
-    rows, vocab = logits.shape
+    rows, vocab = shape
     row_stride, one = logits.stride()
     if one != 1 and vocab > 1:
         _refuse("logits: contiguous rows wanted", logits)
-    of_rows, of_top = (rows,), (rows, k)
-    if ids is not None and not (ids.dtype is _I32 and ids.shape == of_rows and ids.is_contiguous()
+    if ids is not None and not (ids.dtype is _I32 and ids.numel() == rows and ids.is_contiguous()
                                 and ids.get_device() == dev):
         _refuse("ids: int32 [rows] wanted", ids)
     if status is not None and not (status.dtype is _I32 and status.numel() == 1 and status.get_device() == dev):
         _refuse("status: int32 [1] wanted", status)
     if dev < 0:
         _refuse("a CUDA device wanted", logits)
+    if k < 0:
+        _refuse(f"k: {k}")
     if dev != _current():
         with torch.cuda.device(dev):
             return op_token_logprobs(logits, ids, k, out, workspace, status)
     if out is None:
         new = lambda shape, t: torch.empty(shape, dtype=t, device=logits.device)  # noqa: E731
-        out = (None if ids is None else new(rows, _F32), new(rows, _F32), new(of_top, _I32), new(of_top, _F32))
+        out = (None if ids is None else new(rows, _F32), new(rows, _F32), new((rows, k), _I32), new((rows, k), _F32))
         logprob, entropy, top_ids, top_logprobs = out
     else:
         logprob, entropy, top_ids, top_logprobs = out
-        if logprob is not None and not (logprob.dtype is _F32 and logprob.shape == of_rows and logprob.is_contiguous()
+        if logprob is not None and not (logprob.dtype is _F32 and logprob.numel() == rows and logprob.is_contiguous()
                                         and logprob.get_device() == dev):
             _refuse("logprob: float32 [rows] wanted", logprob)
-        if entropy is not None and not (entropy.dtype is _F32 and entropy.shape == of_rows and entropy.is_contiguous()
+        if entropy is not None and not (entropy.dtype is _F32 and entropy.numel() == rows and entropy.is_contiguous()
                                         and entropy.get_device() == dev):
             _refuse("entropy: float32 [rows] wanted", entropy)
         if k > 0:
-            if top_ids is None or not (top_ids.dtype is _I32 and top_ids.shape == of_top and top_ids.is_contiguous()
+            if top_ids is None or not (top_ids.dtype is _I32 and top_ids.shape == (rows, k) and top_ids.is_contiguous()
                                        and top_ids.get_device() == dev):
                 _refuse("top_ids: int32 [rows][k] wanted", top_ids)
-            if top_logprobs is None or not (top_logprobs.dtype is _F32 and top_logprobs.shape == of_top
+            if top_logprobs is None or not (top_logprobs.dtype is _F32 and top_logprobs.shape == (rows, k)
                                             and top_logprobs.is_contiguous() and top_logprobs.get_device() == dev):
                 _refuse("top_logprobs: float32 [rows][k] wanted", top_logprobs)
     if workspace is None:

@@ -891,3 +891,24 @@ def test_logits_rows_of_a_model_are_scored(qp):
     assert m.prefill_device_n(kv, ids.data_ptr(), pos.data_ptr(), 32, 32, logits.data_ptr()) == 0
     assert m.sync_status() == 0
     check_logprobs(qp, logits, torch.cat([ids[1:], ids[:1]]), 5)
+
+
+def test_outputs_of_another_layout_are_refused(qp):
+    """An output with as many elements as wanted, laid out otherwise, is refused before any launch."""
+    cache = qp.PagedCache(torch.zeros(4, 16, 2, 64, device="cuda"), torch.zeros(4, 16, 2, 64, device="cuda"))
+    q, length, table = torch.zeros(3, 256, device="cuda"), dev([1, 1, 1]), dev([[0], [1], [2]])
+    with pytest.raises(qp.MinferError, match="lse"):
+        qp.op_paged_attention(q, cache, table, length, 4, lse=torch.zeros(4, 3, device="cuda"))
+    with pytest.raises(qp.MinferError, match="out"):
+        qp.op_paged_attention(q, cache, table, length, 4, out=torch.zeros(256, 3, device="cuda"))
+    x, ids = torch.zeros(3, 50, device="cuda"), dev([1, 2, 3])
+    out = [torch.zeros(3, device="cuda"), torch.zeros(3, device="cuda"), torch.zeros(3, 2, dtype=I32, device="cuda"),
+           torch.zeros(3, 2, device="cuda")]
+    qp.op_token_logprobs(x, ids, 2, out=tuple(out))
+    for i in (2, 3):
+        wrong = list(out)
+        wrong[i] = torch.zeros(2, 3, dtype=out[i].dtype, device="cuda")
+        with pytest.raises(qp.MinferError, match="top"):
+            qp.op_token_logprobs(x, ids, 2, out=tuple(wrong))
+    with pytest.raises(qp.MinferError, match="k: -1"):
+        qp.op_token_logprobs(x, ids, -1)
