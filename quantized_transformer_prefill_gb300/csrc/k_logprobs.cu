@@ -7,13 +7,13 @@
 // A row is cut into parts, one CTA each.  Every thread keeps a running
 // (reference, s, t); a warp reads chunks of 512 neighbouring logits and leaves
 // each chunk's largest one in the workspace.  The CTA that finishes a row last
-// (a counter per row) joins the parts' sums and finds the k largest logits:
-// they lie in the k chunks with the largest maxima (each of those holds a logit
-// at least as large as the k-th of these maxima; among equal maxima the chunks
-// with lower ids count first, as the order of the result wants it).  Those k
-// chunks are read again, 512 k of the row's logits, out of L2.  The streaming
-// part so carries one warp-wide maximum per 512 logits and nothing else for
-// the top k, whatever the values are.
+// (a counter per row) joins the parts' sums and finds the k largest logits.
+// A bound that at least k chunks' maxima reach is reached by at least k logits,
+// all of them in those chunks; halving finds one that few more than k chunks
+// reach, without a sort.  These chunks are read again, 512 k of the row's logits,
+// out of L2, and those of their logits that reach the bound are ranked by
+// counting.  The streaming part so carries one warp-wide maximum per 512 logits
+// and nothing else for the top k, whatever the values are.
 //
 // Pairs (value, id) are compared as one 64-bit key, the value's
 // order-preserving bits above the complemented id: keys are distinct, and equal
@@ -91,65 +91,12 @@ __device__ __forceinline__ Stat warp_join(Stat v) {
   return Stat{m, s, t};
 }
 
-// The warp's 32 keys in descending order of lanes (bitonic sort).
-__device__ __forceinline__ uint64_t warp_sort(uint64_t v) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int k = 2; k <= 32; k <<= 1)
-#pragma unroll
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      const uint64_t w = __shfl_xor_sync(0xffffffffu, v, j);
-      const bool desc = (lane & k) == 0, low = (lane & j) == 0;
-      v = (desc == low) == (w > v) ? w : v;
-    }
-  return v;
-}
-// The 32 largest of two descending lists, descending: the larger one of each
-// key and its mirror image is a bitonic sequence of them.
-__device__ __forceinline__ uint64_t warp_merge(uint64_t a, uint64_t b) {
-  const int lane = threadIdx.x & 31;
-  const uint64_t r = __shfl_sync(0xffffffffu, b, 31 - lane);
-  uint64_t v = r > a ? r : a;
-#pragma unroll
-  for (int j = 16; j > 0; j >>= 1) {
-    const uint64_t w = __shfl_xor_sync(0xffffffffu, v, j);
-    v = ((lane & j) == 0) == (w > v) ? w : v;
-  }
-  return v;
-}
-// Takes one new key per lane into the warp's list of the 32 largest, of which
-// the first k matter: a few keys one by one, many by sorting them.
-__device__ __forceinline__ void warp_take(uint64_t& list, uint64_t key, int k) {
-  const int lane = threadIdx.x & 31;
-  const uint64_t kth = __shfl_sync(0xffffffffu, list, k - 1);
-  unsigned come = __ballot_sync(0xffffffffu, key > kth);
-  if (__popc(come) > 6) {
-    list = warp_merge(list, warp_sort(key));
-    return;
-  }
-  for (; come; come &= come - 1) {
-    const uint64_t one = __shfl_sync(0xffffffffu, key, __ffs(come) - 1);
-    const int place = __popc(__ballot_sync(0xffffffffu, list > one));
-    const uint64_t up = __shfl_up_sync(0xffffffffu, list, 1);
-    list = lane < place ? list : lane == place ? one : up;
-  }
-}
-// The 32 largest of all warps' lists, in every warp.  s: [kWarps][32].
-__device__ __forceinline__ uint64_t block_merge(uint64_t list, uint64_t* s) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  s[warp * 32 + lane] = list;
-  __syncthreads();
-#pragma unroll
-  for (int n = kWarps / 2; n > 0; n >>= 1) {
-    if (warp < n) {
-      list = warp_merge(list, s[(warp + n) * 32 + lane]);
-      s[warp * 32 + lane] = list;
-    }
-    __syncthreads();
-  }
-  list = s[lane];
-  __syncthreads();
-  return list;
+// Two sets' sums in one (as warp_join, without the lanes).
+__device__ __forceinline__ Stat join2(Stat a, Stat b) {
+  const float m = max_nan(a.m, b.m);
+  const float da = a.m == -INFINITY ? 0.f : (a.m - m) * kLog2e, ca = ex2(da);
+  const float db = b.m == -INFINITY ? 0.f : (b.m - m) * kLog2e, cb = ex2(db);
+  return Stat{m, a.s * ca + b.s * cb, (ca == 0.f ? 0.f : ca * fmaf(da, a.s, a.t)) + (cb == 0.f ? 0.f : cb * fmaf(db, b.s, b.t))};
 }
 
 template <typename T>
@@ -234,9 +181,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
   using L = Loader<T>;
   constexpr int V = L::kVec;
   extern __shared__ __align__(128) unsigned char lp_smem[];
-  __shared__ uint64_t s_list[kWarps * 32];
+  __shared__ uint64_t s_list[kThreads];
+  __shared__ int s_pick[kWarps][kLogprobsMaxTop];
   __shared__ Stat s_stat[kWarps];
-  __shared__ int s_last, s_n;
+  __shared__ int s_last, s_n, s_count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = blockIdx.x / plan.parts;
   const int part = (int)(blockIdx.x - row * plan.parts);
@@ -293,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
     }
   }
   float given = 0.f;  // the given token's logit, on its way until the end
-  if (a.ids && tid == 0) given = L::one(x + id);
+  if (a.ids && tid == kThreads - 32) given = L::one(x + id);
   for (; c < c1; c += kWarps) {
     fetch(c + (kStages - 1) * kWarps, stage == 0 ? kStages - 1 : stage - 1);
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
@@ -357,10 +305,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
   Stat v = warp_join(Stat{r, s, t});
   if (lane == 0) s_stat[warp] = v;
   __syncthreads();
-  // warp 0 has the row's sums (alone: it writes what depends on them)
-  if (warp == 0) v = warp_join(lane < kWarps ? s_stat[lane] : Stat{-INFINITY, 0.f, 0.f});
+  // the last warp has the row's sums (alone: it writes what depends on them)
+  constexpr int kSumWarp = kWarps - 1;
+  if (warp == kSumWarp) v = warp_join(lane < kWarps ? s_stat[lane] : Stat{-INFINITY, 0.f, 0.f});
   if (plan.parts > 1) {
-    if (tid == 0) {
+    if (tid == kSumWarp * 32) {
       stats[part] = make_float4(v.m, v.s, v.t, 0.f);
       __threadfence();  // also the other threads' keys: they came before the barrier
       unsigned* counter = reinterpret_cast<unsigned*>(ws) + row;
@@ -370,55 +319,95 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
     }
     __syncthreads();
     if (!s_last) return;
-    if (warp == 0) {
-      v = Stat{-INFINITY, 0.f, 0.f};
-      for (int p0 = 0; p0 < plan.parts; p0 += 31) {  // the sums so far and 31 parts
-        if (lane < 31) {
-          v = Stat{-INFINITY, 0.f, 0.f};
-          if (p0 + lane < plan.parts) {
-            const float4 q = __ldcg(stats + p0 + lane);
-            v = Stat{q.x, q.y, q.z};
-          }
-        }
-        v = warp_join(v);
-      }
-    }
   }
 
-  if (warp == 0) {
+  // The chunks' maxima, in every warp: the first kHeld * 32 in registers, further
+  // ones (of vocabularies past 262,144) are read again whenever they are counted.
+  constexpr int kHeld = 16;
+  uint32_t held[kHeld];
+  auto each = [&](auto f) {  // f(chunk of this lane, its maximum; 0 behind the last chunk), in the order of the chunks
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (i * 32 < chunks) f(i * 32 + lane, held[i]);
+    for (int c0 = kHeld * 32; c0 < chunks; c0 += 32) f(c0 + lane, c0 + lane < chunks ? __ldcg(keys + c0 + lane) : 0u);
+  };
+  if (k > 0) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) held[i] = i * 32 + lane < chunks ? __ldcg(keys + i * 32 + lane) : 0;
+  }
+
+  if (warp == kSumWarp) {
+    if (plan.parts > 1) {
+      v = Stat{-INFINITY, 0.f, 0.f};
+      for (int p = lane; p < plan.parts; p += 32) {
+        const float4 q = __ldcg(stats + p);
+        v = join2(v, Stat{q.x, q.y, q.z});
+      }
+      v = warp_join(v);
+    }
     const float log2s = log2f(v.s);
     if (lane == 0) {
       s_stat[0] = Stat{v.m, log2s, 0.f};  // for every warp, behind the barriers below
-      s_n = 0;
       const bool none = v.m == -INFINITY;
       if (a.ids) a.logprob[row] = none ? -INFINITY : (given - v.m) - kLn2 * log2s;
       if (a.entropy) a.entropy[row] = none ? 0.f : kLn2 * (log2s - v.t / v.s);
     }
   }
   if (k == 0) return;
+  if (tid == 0) s_n = s_count = 0;
 
-  // the k chunks with the largest maxima (an id is a chunk here)
-  uint64_t list = 0;
-  for (int c0 = warp * 32; c0 < chunks; c0 += kThreads) {
-    const int c = c0 + lane;
-    warp_take(list, c < chunks ? ((uint64_t)__ldcg(keys + c) << 32) | (uint32_t)~c : 0, k);
-  }
-  const uint64_t picked = block_merge(list, s_list);
-  // with fewer than k chunks the k-th key is 0 and everything counts
-  const uint32_t floor = (uint32_t)(__shfl_sync(0xffffffffu, picked, k - 1) >> 32);
-  // every warp's chunks (4 at most) come into its ring together
+  // A bound `floor` that at least k chunks' maxima reach, but few more: halving
+  // between the least of the lanes' largest (32 chunks reach it) and the largest.
+  // With fewer than k chunks all count.
   constexpr int kPicks = kLogprobsMaxTop / kWarps;
+  auto reach = [&](uint32_t bound) {
+    int n = 0;
+    each([&](int, uint32_t key) { n += key >= bound; });
+    return (int)__reduce_add_sync(0xffffffffu, n);
+  };
+  uint32_t most = 0;
+  each([&](int, uint32_t key) { most = max(most, key); });
+  uint32_t floor = 1, above = __reduce_max_sync(0xffffffffu, most) + 1;
+  int picks = chunks;
+  if (chunks > k) {
+    const int enough = min((k + 3 + kWarps - 1) / kWarps * kWarps, kLogprobsMaxTop);  // as many for every warp
+    floor = max(floor, __reduce_min_sync(0xffffffffu, most));
+    uint32_t hi = above;
+    picks = reach(floor);
+    while (picks > enough && hi - floor > 1) {
+      const uint32_t mid = floor + (hi - floor) / 2;
+      const int n = reach(mid);
+      if (n >= k) {
+        floor = mid;
+        picks = n;
+      } else {
+        hi = mid;
+      }
+    }
+  }
+  // Those chunks, in the order of their ids.  If more than kLogprobsMaxTop have
+  // the same maximum, the first of them do: each holds one such logit, fewer than
+  // k chunks have a larger maximum, and equal logits rank by their ids.
+  int equals = picks > kLogprobsMaxTop ? kLogprobsMaxTop - reach(floor + 1) : kLogprobsMaxTop;
+  int taken = 0;
+  each([&](int c, uint32_t key) {
+    const unsigned lower = (1u << lane) - 1, eq = __ballot_sync(0xffffffffu, key == floor);
+    const bool take = key > floor || (key == floor && __popc(eq & lower) < equals);
+    const unsigned all = __ballot_sync(0xffffffffu, take);
+    if (take) s_pick[warp][taken + __popc(all & lower)] = c;
+    taken += __popc(all);
+    equals -= min(__popc(eq), equals);
+  });
+  __syncwarp();
+  // every warp's chunks (4 at most) come into its ring together
   static_assert(kPicks * kChunkBytes <= kRing, "a warp's picks fit its ring");
-  uint64_t pick[kPicks];
+  int pick[kPicks];
 #pragma unroll
   for (int j = 0; j < kPicks; ++j) {
     const int at = warp + j * kWarps;
-    pick[j] = __shfl_sync(0xffffffffu, picked, at);
-    if (at >= k || pick[j] == 0) {
-      pick[j] = 0;
-      continue;
-    }
-    const int cp = (int)key_id(pick[j]);
+    pick[j] = -1;
+    if (at >= taken) continue;
+    const int cp = pick[j] = s_pick[warp][at];
     if (inside(cp)) {
       const unsigned char* p = reinterpret_cast<const unsigned char*>(x + ((int64_t)cp * kChunk - head)) + lane * 16;
 #pragma unroll
@@ -440,74 +429,125 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
   auto value = [&](int j, int i) {
     return L::one(reinterpret_cast<const T*>(lp_smem + warp * kRing + j * kChunkBytes + (i / V) * 512 + lane * 16) + i % V);
   };
-  auto place = [&](int j, int i) { return (int64_t)key_id(pick[j]) * kChunk - head + ((i / V) * 32 + lane) * V + i % V; };
-  // the logits that are large enough, about k of them, into s_list
+  auto place = [&](int j, int i) { return (int64_t)pick[j] * kChunk - head + ((i / V) * 32 + lane) * V + i % V; };
+  // this lane's logits that reach a bound, a mask per pick; how many
   unsigned large[kPicks];
-  int count = 0;
+  auto mark = [&](uint32_t bound) {
+    int n = 0;
 #pragma unroll
-  for (int j = 0; j < kPicks; ++j) {
-    large[j] = 0;
-    if (pick[j] == 0) continue;
+    for (int j = 0; j < kPicks; ++j) {
+      large[j] = 0;
+      if (pick[j] < 0) continue;
+      unsigned m = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (key32(value(j, i)) >= floor && place(j, i) >= 0 && place(j, i) < a.vocab) large[j] |= 1u << i;
-    count += __popc(large[j]);
-  }
-  int at = count;
+      for (int i = 0; i < U; ++i) {
+        float f[V];
+        L::get(*reinterpret_cast<const uint4*>(lp_smem + warp * kRing + j * kChunkBytes + i * 512 + lane * 16), f);
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, at, o);
-    if (lane >= o) at += y;
-  }
-  const int all = __shfl_sync(0xffffffffu, at, 31);
-  int base = 0;
-  if (lane == 0 && all) base = atomicAdd(&s_n, all);
-  base = __shfl_sync(0xffffffffu, base, 0);
-  at += base - count;
-  if (base + all <= kThreads) {
-#pragma unroll
-    for (int j = 0; j < kPicks; ++j)
-      for (unsigned m = large[j]; m; m &= m - 1) {
-        const int i = __ffs(m) - 1;
-        s_list[at++] = make_key(value(j, i), (uint32_t)place(j, i));
+        for (int e = 0; e < V; ++e) m |= (unsigned)(key32(f[e]) >= bound) << (i * V + e);
       }
-  }
-  __syncthreads();
-  const float m = s_stat[0].m, log2s = s_stat[0].s;
-  auto put = [&](uint64_t key, int at) {
-    a.top_ids[row * k + at] = (int32_t)key_id(key);
-    a.top_logprobs[row * k + at] = m == -INFINITY ? -INFINITY : (key_value((uint32_t)(key >> 32)) - m) - kLn2 * log2s;
+      if (!inside(pick[j])) {
+        for (unsigned all = m; all; all &= all - 1) {
+          const int64_t e = place(j, __ffs(all) - 1);
+          if (e < 0 || e >= a.vocab) m &= ~(all & -all);
+        }
+      }
+      large[j] = m;
+      n += __popc(m);
+    }
+    return n;
   };
-  const int n = s_n;
-  if (n <= kThreads) {
-    // a key's place is the number of keys above it
-    if (tid < n) {
-      const uint64_t own = s_list[tid];
-      int above = 0;
-      for (int i = 0; i < n; ++i) above += s_list[i] > own;
-      if (above < k) put(own, above);
+  // those marked, `count` in this lane, into s_list; none of a warp's beyond its end
+  auto list = [&](int count) {
+    int at = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) at += y;
     }
-    return;
-  }
-  // many equal logits (rows of which a mask leaves little): the 32 largest so
-  // far in a list per warp, the chunks' logits in the order of their ids, so that
-  // equal ones fall behind at once
+    const int all = __shfl_sync(0xffffffffu, at, 31);
+    int base = 0;
+    if (lane == 0 && all) base = atomicAdd(&s_n, all);
+    base = __shfl_sync(0xffffffffu, base, 0);
+    at += base - count;
+    if (base + all <= kThreads) {
+#pragma unroll
+      for (int j = 0; j < kPicks; ++j)
+        for (unsigned m = large[j]; m; m &= m - 1) {
+          const int i = __ffs(m) - 1;
+          s_list[at++] = make_key(value(j, i), (uint32_t)place(j, i));
+        }
+    }
+  };
+  const int count = mark(floor);
+  __syncthreads();  // s_n is zero
+  list(count);
   __syncthreads();
-  list = 0;
-#pragma unroll 1
-  for (int j = 0; j < kPicks; ++j) {
-    const int at_pick = warp + j * kWarps;
-    const uint64_t one = __shfl_sync(0xffffffffu, picked, at_pick);
-    if (at_pick >= k || one == 0) break;
-    const int64_t e0 = (int64_t)key_id(one) * kChunk - head;
-    const T* chunk = reinterpret_cast<const T*>(lp_smem + warp * kRing + j * kChunkBytes);
-    for (int i = lane; i < kChunk; i += 32) {
-      const uint64_t key = make_key(L::one(chunk + i), (uint32_t)(e0 + i));
-      warp_take(list, e0 + i >= 0 && e0 + i < a.vocab && (uint32_t)(key >> 32) >= floor ? key : 0, k);
+  int n = s_n;
+  if (n > kThreads) {
+    // Many logits reach the floor: equal ones (rows of which a mask leaves little),
+    // or large ones side by side.  The least bound above it that no more than
+    // kThreads reach; if fewer than k do, those equal to the bound below follow in
+    // the order of their ids.
+    auto total = [&](uint32_t bound) {
+      const int own = (int)__reduce_add_sync(0xffffffffu, mark(bound));
+      if (lane == 0 && own) atomicAdd(&s_count, own);
+      __syncthreads();
+      const int sum = s_count;
+      __syncthreads();
+      if (tid == 0) s_count = 0;
+      __syncthreads();
+      return sum;
+    };
+    uint32_t hi = floor + 1;
+    n = hi == above ? 0 : total(hi);
+    if (n > kThreads) {
+      floor = hi;
+      hi = above;
+      n = 0;
+      while (hi - floor > 1) {
+        const uint32_t mid = floor + (hi - floor) / 2;
+        const int at_mid = total(mid);
+        if (at_mid > kThreads) {
+          floor = mid;
+        } else {
+          hi = mid;
+          n = at_mid;
+          if (n >= k) break;
+        }
+      }
+    }
+    if (tid == 0) s_n = 0;
+    __syncthreads();
+    if (n > 0) list(mark(hi));
+    if (n < k && warp == 0) {
+      int at = n;
+      for (int p = 0; p < taken && at < k; ++p) {
+        const int64_t e0 = (int64_t)s_pick[0][p] * kChunk - head;
+        const T* chunk = reinterpret_cast<const T*>(lp_smem + (p % kWarps) * kRing + (p / kWarps) * kChunkBytes);
+        for (int i = lane; i < kChunk && at < k; i += 32) {
+          const bool eq = key32(L::one(chunk + i)) == floor && e0 + i >= 0 && e0 + i < a.vocab;
+          const unsigned all = __ballot_sync(0xffffffffu, eq);
+          const int to = at + __popc(all & ((1u << lane) - 1));
+          if (eq && to < k) s_list[to] = make_key(L::one(chunk + i), (uint32_t)(e0 + i));
+          at += __popc(all);
+        }
+      }
+    }
+    n = max(n, k);
+    __syncthreads();
+  }
+  // a key's place is the number of keys above it
+  if (tid < n) {
+    const uint64_t own = s_list[tid];
+    int at = 0;
+    for (int i = 0; i < n; ++i) at += s_list[i] > own;
+    if (at < k) {
+      const float m = s_stat[0].m, log2s = s_stat[0].s;
+      a.top_ids[row * k + at] = (int32_t)key_id(own);
+      a.top_logprobs[row * k + at] = m == -INFINITY ? -INFINITY : (key_value((uint32_t)(own >> 32)) - m) - kLn2 * log2s;
     }
   }
-  list = block_merge(list, s_list);
-  if (tid < k) put(list, tid);
 }
 
 // Parts of a row: with fewer rows than the GPU holds CTAs, as many as fill it

@@ -687,6 +687,26 @@ def test_token_logprobs_hard_rows(qp, kind, V, k):
     check_logprobs(qp, x, ids, k)
 
 
+@pytest.mark.parametrize("t", [F32, F16])
+@pytest.mark.parametrize("kind", ["random", "side by side", "few levels", "two left", "none left"])
+@pytest.mark.parametrize("k", [1, 9, 32])
+def test_token_logprobs_wide_vocabularies(qp, t, kind, k):
+    """Chunk maxima beyond the 512 that a join holds in registers; large values that share chunks."""
+    g = gen(k)
+    for V in (262143, 262145, 400003):
+        x = torch.randn(2, V, generator=g, device="cuda")
+        if kind == "side by side":  # one chunk and a half hold everything large, more than fits the list
+            x[:, V - 800:] = 20 + x[:, V - 800:]
+        elif kind == "few levels":
+            x = (4 * x).round() / 4
+        elif kind == "two left":
+            x[:, 2:V - 1] = -math.inf
+        elif kind == "none left":
+            x[0].fill_(-math.inf)
+        x = x.to(t)
+        check_logprobs(qp, x, dev([0, V - 1]), k)
+
+
 def test_token_logprobs_nan_and_infinity(qp):
     x = torch.randn(4, 3000, device="cuda")
     x[0, 0], x[0, 2999] = math.nan, math.inf
