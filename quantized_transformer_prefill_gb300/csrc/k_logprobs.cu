@@ -19,11 +19,12 @@
 // order-preserving bits above the complemented id: keys are distinct, and equal
 // values rank by ascending id whatever the order in which they are met.
 //
-// Measured on a GB300 (us a call, device): 512 f32 rows of 151,936 59 (311 MB, 5.3
-// TB/s, 78% of the measured copy), without a top k 53; 65 bf16 rows of 150,001 15;
-// one f32 row 7.9, without a top k 4.5.  The stream is bound by HBM, with 6 or 7
-// instructions a logit next to it; a row's join adds 3 us of dependent steps, of
-// which the rows in flight hide a part.
+// Measured on a GB300 (us a call, device): 512 f32 rows of 151,936, k = 20, 56 (311
+// MB, 5.6 TB/s, 82% of the measured copy), without a top k 49; 65 bf16 rows of
+// 150,001, k = 8, 13.7; one f32 row, k = 5, 7.2, without a top k 4.4.  The stream
+// is bound by HBM, with 6 or 7 instructions a logit next to it; a row's join adds
+// 3 us of dependent steps, of which the rows in flight hide a part.  With a ring
+// of 8 KB a warp and three CTAs per SM the 512 rows took 60 and 53.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -38,8 +39,9 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kChunk = 512;         // logits of a chunk
 constexpr int kPer = kChunk / 32;   // logits of a lane
-constexpr int kCtasPerSm = 3;       // resident
-constexpr int kRing = 8192;         // bytes of a warp's ring: 3 CTAs of 8 warps have 192 KB in flight or at work
+constexpr int kCtasPerSm = 4;       // resident
+constexpr int kRing = 6144;         // bytes of a warp's ring: 4 CTAs of 8 warps have 192 KB in flight or at work
+constexpr int kHeld = 512;          // chunk maxima that a CTA, or a warp's registers, hold
 constexpr int kWaves = 2;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -111,6 +113,7 @@ struct Loader<float> {
     x[3] = __uint_as_float(u.w);
   }
   __device__ static float one(const float* p) { return *p; }
+  __device__ static float from(float x) { return x; }
 };
 template <>
 struct Loader<__half> {
@@ -125,6 +128,7 @@ struct Loader<__half> {
     }
   }
   __device__ static float one(const __half* p) { return __half2float(*p); }
+  __device__ static __half from(float x) { return __float2half_rn(x); }
 };
 template <>
 struct Loader<__nv_bfloat16> {
@@ -138,6 +142,7 @@ struct Loader<__nv_bfloat16> {
     }
   }
   __device__ static float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  __device__ static __nv_bfloat16 from(float x) { return __float2bfloat16_rn(x); }
 };
 
 // How rows are cut, and where the workspace holds what: a counter per row (zero
@@ -182,9 +187,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
   constexpr int V = L::kVec;
   extern __shared__ __align__(128) unsigned char lp_smem[];
   __shared__ uint64_t s_list[kThreads];
-  __shared__ int s_pick[kWarps][kLogprobsMaxTop];
+  __shared__ uint32_t s_keys[kHeld];
+  __shared__ int s_pick[kLogprobsMaxTop];
   __shared__ Stat s_stat[kWarps];
-  __shared__ int s_last, s_n, s_count;
+  __shared__ int s_last, s_n, s_count, s_taken;
+  __shared__ uint32_t s_floor, s_above;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = blockIdx.x / plan.parts;
   const int part = (int)(blockIdx.x - row * plan.parts);
@@ -198,6 +205,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
   const int head = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
   const int chunks = (int)((a.vocab + head + kChunk - 1) / kChunk);
   const int c1 = min(chunks, (part + 1) * plan.per);
+  // the maxima of a row that this CTA has alone stay in shared memory, if they fit
+  // (512 rows: 2 us less than with a store of 4 bytes per chunk)
+  const bool alone = plan.parts == 1 && plan.per <= kHeld;
 
   // r: the reference, a logit near the largest so far (-inf: none yet).  Up to
   // |r| = 2^20 the terms are 2^(x L - z), one multiply-add each, with z = r L
@@ -265,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
     for (int i = 1; i < kPer; ++i) top = max_nan(top, f[i]);
     if (k > 0) {
       const uint32_t best = __reduce_max_sync(0xffffffffu, key32(top));
-      if (lane == 0) keys[c] = best;
+      if (lane == 0) *(alone ? s_keys + c : keys + c) = best;
     }
     // a new reference only when the terms get large: 2^(4 L) at most
     if (!(top <= r + 4.f)) {
@@ -321,21 +331,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
     if (!s_last) return;
   }
 
-  // The chunks' maxima, in every warp: the first kHeld * 32 in registers, further
-  // ones (of vocabularies past 262,144) are read again whenever they are counted.
-  constexpr int kHeld = 16;
-  uint32_t held[kHeld];
-  auto each = [&](auto f) {  // f(chunk of this lane, its maximum; 0 behind the last chunk), in the order of the chunks
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-      if (i * 32 < chunks) f(i * 32 + lane, held[i]);
-    for (int c0 = kHeld * 32; c0 < chunks; c0 += 32) f(c0 + lane, c0 + lane < chunks ? __ldcg(keys + c0 + lane) : 0u);
-  };
-  if (k > 0) {
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) held[i] = i * 32 + lane < chunks ? __ldcg(keys + i * 32 + lane) : 0;
-  }
-
   if (warp == kSumWarp) {
     if (plan.parts > 1) {
       v = Stat{-INFINITY, 0.f, 0.f};
@@ -354,134 +349,162 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
     }
   }
   if (k == 0) return;
-  if (tid == 0) s_n = s_count = 0;
 
-  // A bound `floor` that at least k chunks' maxima reach, but few more: halving
-  // between the least of the lanes' largest (32 chunks reach it) and the largest.
-  // With fewer than k chunks all count.
-  constexpr int kPicks = kLogprobsMaxTop / kWarps;
-  auto reach = [&](uint32_t bound) {
-    int n = 0;
-    each([&](int, uint32_t key) { n += key >= bound; });
-    return (int)__reduce_add_sync(0xffffffffu, n);
-  };
-  uint32_t most = 0;
-  each([&](int, uint32_t key) { most = max(most, key); });
-  uint32_t floor = 1, above = __reduce_max_sync(0xffffffffu, most) + 1;
-  int picks = chunks;
-  if (chunks > k) {
-    const int enough = min((k + 3 + kWarps - 1) / kWarps * kWarps, kLogprobsMaxTop);  // as many for every warp
-    floor = max(floor, __reduce_min_sync(0xffffffffu, most));
-    uint32_t hi = above;
-    picks = reach(floor);
-    while (picks > enough && hi - floor > 1) {
-      const uint32_t mid = floor + (hi - floor) / 2;
-      const int n = reach(mid);
-      if (n >= k) {
-        floor = mid;
-        picks = n;
-      } else {
-        hi = mid;
-      }
-    }
-  }
-  // Those chunks, in the order of their ids.  If more than kLogprobsMaxTop have
-  // the same maximum, the first of them do: each holds one such logit, fewer than
-  // k chunks have a larger maximum, and equal logits rank by their ids.
-  int equals = picks > kLogprobsMaxTop ? kLogprobsMaxTop - reach(floor + 1) : kLogprobsMaxTop;
-  int taken = 0;
-  each([&](int c, uint32_t key) {
-    const unsigned lower = (1u << lane) - 1, eq = __ballot_sync(0xffffffffu, key == floor);
-    const bool take = key > floor || (key == floor && __popc(eq & lower) < equals);
-    const unsigned all = __ballot_sync(0xffffffffu, take);
-    if (take) s_pick[warp][taken + __popc(all & lower)] = c;
-    taken += __popc(all);
-    equals -= min(__popc(eq), equals);
-  });
-  __syncwarp();
-  // every warp's chunks (4 at most) come into its ring together
-  static_assert(kPicks * kChunkBytes <= kRing, "a warp's picks fit its ring");
-  int pick[kPicks];
+  // Meanwhile one warp finds a bound `floor` that at least k chunks' maxima reach, but
+  // few more: halving between the least of the lanes' largest (32 chunks reach it)
+  // and the largest.  With fewer than k chunks all count.  (In every warp, which
+  // saves a barrier, it cost 512 rows 3 us of issue slots.)
+  if (warp == 0) {
+    // the first maxima in registers, further ones (of vocabularies past 262,144)
+    // are read again whenever they are counted
+    uint32_t held[kHeld / 32];
+    if (alone) {
 #pragma unroll
-  for (int j = 0; j < kPicks; ++j) {
-    const int at = warp + j * kWarps;
-    pick[j] = -1;
-    if (at >= taken) continue;
-    const int cp = pick[j] = s_pick[warp][at];
-    if (inside(cp)) {
-      const unsigned char* p = reinterpret_cast<const unsigned char*>(x + ((int64_t)cp * kChunk - head)) + lane * 16;
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + j * kChunkBytes + i * 512), "l"(p + i * 512) : "memory");
+      for (int i = 0; i < kHeld / 32; ++i) held[i] = i * 32 + lane < chunks ? s_keys[i * 32 + lane] : 0u;
     } else {
-      T edge[kPer];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int64_t e = (int64_t)cp * kChunk - head + ((i / V) * 32 + lane) * V + i % V;
-        if (e >= 0 && e < a.vocab) edge[i] = x[e];
-      }
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        reinterpret_cast<T*>(lp_smem + warp * kRing + j * kChunkBytes + (i / V) * 512 + lane * 16)[i % V] = edge[i];
+      for (int i = 0; i < kHeld / 32; ++i) held[i] = i * 32 + lane < chunks ? __ldcg(keys + i * 32 + lane) : 0u;
     }
-  }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  auto value = [&](int j, int i) {
-    return L::one(reinterpret_cast<const T*>(lp_smem + warp * kRing + j * kChunkBytes + (i / V) * 512 + lane * 16) + i % V);
-  };
-  auto place = [&](int j, int i) { return (int64_t)pick[j] * kChunk - head + ((i / V) * 32 + lane) * V + i % V; };
-  // this lane's logits that reach a bound, a mask per pick; how many
-  unsigned large[kPicks];
-  auto mark = [&](uint32_t bound) {
-    int n = 0;
+    auto each = [&](auto f) {  // f(chunk of this lane, its maximum; 0 behind the last chunk), in the order of the chunks
 #pragma unroll
-    for (int j = 0; j < kPicks; ++j) {
-      large[j] = 0;
-      if (pick[j] < 0) continue;
-      unsigned m = 0;
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        float f[V];
-        L::get(*reinterpret_cast<const uint4*>(lp_smem + warp * kRing + j * kChunkBytes + i * 512 + lane * 16), f);
-#pragma unroll
-        for (int e = 0; e < V; ++e) m |= (unsigned)(key32(f[e]) >= bound) << (i * V + e);
-      }
-      if (!inside(pick[j])) {
-        for (unsigned all = m; all; all &= all - 1) {
-          const int64_t e = place(j, __ffs(all) - 1);
-          if (e < 0 || e >= a.vocab) m &= ~(all & -all);
+      for (int i = 0; i < kHeld / 32; ++i)
+        if (i * 32 < chunks) f(i * 32 + lane, held[i]);
+      for (int c = kHeld; c < chunks; c += 32) f(c + lane, c + lane < chunks ? __ldcg(keys + c + lane) : 0u);
+    };
+    auto reach = [&](uint32_t bound) {
+      int n = 0;
+      each([&](int, uint32_t key) { n += key >= bound; });
+      return (int)__reduce_add_sync(0xffffffffu, n);
+    };
+    uint32_t most = 0;
+    each([&](int, uint32_t key) { most = max(most, key); });
+    const uint32_t above = __reduce_max_sync(0xffffffffu, most) + 1;
+    uint32_t floor = 1;
+    int picks = chunks;
+    if (chunks > k) {
+      const int enough = min((k + 3 + kWarps - 1) / kWarps * kWarps, kLogprobsMaxTop);  // as many for every warp
+      floor = max(floor, __reduce_min_sync(0xffffffffu, most));
+      uint32_t hi = above;
+      picks = reach(floor);
+      while (picks > enough && hi - floor > 1) {
+        const uint32_t mid = floor + (hi - floor) / 2;
+        const int n = reach(mid);
+        if (n >= k) {
+          floor = mid;
+          picks = n;
+        } else {
+          hi = mid;
         }
       }
-      large[j] = m;
-      n += __popc(m);
+    }
+    // Those chunks, in the order of their ids.  If more than kLogprobsMaxTop have
+    // the same maximum, the first of them do: each holds one such logit, fewer than
+    // k chunks have a larger maximum, and equal logits rank by their ids.
+    int equals = picks > kLogprobsMaxTop ? kLogprobsMaxTop - reach(floor + 1) : kLogprobsMaxTop;
+    int taken = 0;
+    each([&](int c, uint32_t key) {
+      const unsigned lower = (1u << lane) - 1, eq = __ballot_sync(0xffffffffu, key == floor);
+      const bool take = key > floor || (key == floor && __popc(eq & lower) < equals);
+      const unsigned all = __ballot_sync(0xffffffffu, take);
+      if (take) s_pick[taken + __popc(all & lower)] = c;
+      taken += __popc(all);
+      equals -= min(__popc(eq), equals);
+    });
+    if (lane == 0) {
+      s_taken = taken;
+      s_floor = floor;
+      s_above = above;
+      s_n = s_count = 0;
+    }
+  }
+  __syncthreads();
+  const int taken = s_taken;
+
+  // Those chunks come into the warps' rings, kPicks a warp together (all of them, but
+  // of more than 24 f32 chunks).
+  constexpr int kPicks = kRing / kChunkBytes * kWarps < kLogprobsMaxTop ? kRing / kChunkBytes : kLogprobsMaxTop / kWarps;
+  // The warp's logits that reach a bound: their number, and, with `list`, they
+  // themselves at the end of s_list as long as there is room (in an order of
+  // arrival: the ranks do not depend on it).
+  bool resident = false;
+  auto sweep = [&](uint32_t bound, bool list) {
+    int n = 0;
+    for (int p0 = warp; p0 < taken; p0 += kPicks * kWarps) {
+      if (!resident) {
+#pragma unroll
+        for (int j = 0; j < kPicks; ++j) {
+          if (p0 + j * kWarps >= taken) break;
+          const int cp = s_pick[p0 + j * kWarps];
+          if (inside(cp)) {
+            const unsigned char* p = reinterpret_cast<const unsigned char*>(x + ((int64_t)cp * kChunk - head)) + lane * 16;
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + j * kChunkBytes + i * 512), "l"(p + i * 512)
+                           : "memory");
+          } else {
+            float edge[kPer];
+            load_chunk<T>(x, head, a.vocab, cp, edge);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+              reinterpret_cast<T*>(lp_smem + warp * kRing + j * kChunkBytes + (i / V) * 512 + lane * 16)[i % V] = L::from(edge[i]);
+          }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        resident = taken <= kPicks * kWarps;
+      }
+      unsigned large[kPicks];
+      int own = 0;
+      const unsigned char* mine = lp_smem + warp * kRing + lane * 16;
+      auto id_of = [&](int j, int i) {
+        return (int64_t)s_pick[p0 + j * kWarps] * kChunk - head + ((i / V) * 32 + lane) * V + i % V;
+      };
+#pragma unroll
+      for (int j = 0; j < kPicks; ++j) {
+        large[j] = 0;
+        if (p0 + j * kWarps >= taken) continue;
+        unsigned m = 0;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          float y[V];
+          L::get(*reinterpret_cast<const uint4*>(mine + j * kChunkBytes + i * 512), y);
+#pragma unroll
+          for (int e = 0; e < V; ++e) m |= (unsigned)(key32(y[e]) >= bound) << (i * V + e);
+        }
+        if (!inside(s_pick[p0 + j * kWarps])) {
+          for (unsigned all = m; all; all &= all - 1) {
+            const int64_t id = id_of(j, __ffs(all) - 1);
+            if (id < 0 || id >= a.vocab) m &= ~(all & -all);
+          }
+        }
+        large[j] = m;
+        own += __popc(m);
+      }
+      int at = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += y;
+      }
+      const int all = __shfl_sync(0xffffffffu, at, 31);
+      n += all;
+      if (!list) continue;
+      int base = 0;
+      if (lane == 0 && all) base = atomicAdd(&s_n, all);
+      base = __shfl_sync(0xffffffffu, base, 0);
+      at += base - own;
+      if (base + all <= kThreads) {
+#pragma unroll
+        for (int j = 0; j < kPicks; ++j)
+          for (unsigned m = large[j]; m; m &= m - 1, ++at) {
+            const int i = __ffs(m) - 1;
+            s_list[at] = make_key(L::one(reinterpret_cast<const T*>(mine + j * kChunkBytes + (i / V) * 512) + i % V), (uint32_t)id_of(j, i));
+          }
+      }
     }
     return n;
   };
-  // those marked, `count` in this lane, into s_list; none of a warp's beyond its end
-  auto list = [&](int count) {
-    int at = count;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, at, o);
-      if (lane >= o) at += y;
-    }
-    const int all = __shfl_sync(0xffffffffu, at, 31);
-    int base = 0;
-    if (lane == 0 && all) base = atomicAdd(&s_n, all);
-    base = __shfl_sync(0xffffffffu, base, 0);
-    at += base - count;
-    if (base + all <= kThreads) {
-#pragma unroll
-      for (int j = 0; j < kPicks; ++j)
-        for (unsigned m = large[j]; m; m &= m - 1) {
-          const int i = __ffs(m) - 1;
-          s_list[at++] = make_key(value(j, i), (uint32_t)place(j, i));
-        }
-    }
-  };
-  const int count = mark(floor);
-  __syncthreads();  // s_n is zero
-  list(count);
+  uint32_t floor = s_floor;
+  sweep(floor, true);
   __syncthreads();
   int n = s_n;
   if (n > kThreads) {
@@ -490,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
     // kThreads reach; if fewer than k do, those equal to the bound below follow in
     // the order of their ids.
     auto total = [&](uint32_t bound) {
-      const int own = (int)__reduce_add_sync(0xffffffffu, mark(bound));
+      const int own = sweep(bound, false);
       if (lane == 0 && own) atomicAdd(&s_count, own);
       __syncthreads();
       const int sum = s_count;
@@ -499,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
       __syncthreads();
       return sum;
     };
+    const uint32_t above = s_above;
     uint32_t hi = floor + 1;
     n = hi == above ? 0 : total(hi);
     if (n > kThreads) {
@@ -517,20 +541,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
         }
       }
     }
+    __syncthreads();  // s_n has been read
     if (tid == 0) s_n = 0;
     __syncthreads();
-    if (n > 0) list(mark(hi));
+    if (n > 0) sweep(hi, true);
     if (n < k && warp == 0) {
       int at = n;
       for (int p = 0; p < taken && at < k; ++p) {
-        const int64_t e0 = (int64_t)s_pick[0][p] * kChunk - head;
-        const T* chunk = reinterpret_cast<const T*>(lp_smem + (p % kWarps) * kRing + (p / kWarps) * kChunkBytes);
-        for (int i = lane; i < kChunk && at < k; i += 32) {
-          const bool eq = key32(L::one(chunk + i)) == floor && e0 + i >= 0 && e0 + i < a.vocab;
-          const unsigned all = __ballot_sync(0xffffffffu, eq);
-          const int to = at + __popc(all & ((1u << lane) - 1));
-          if (eq && to < k) s_list[to] = make_key(L::one(chunk + i), (uint32_t)(e0 + i));
-          at += __popc(all);
+        float f[kPer];
+        load_chunk<T>(x, head, a.vocab, s_pick[p], f);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {  // a vector of every lane: neighbouring logits
+          const int64_t e0 = (int64_t)s_pick[p] * kChunk - head + (i * 32 + lane) * V;
+          unsigned eq = 0;
+#pragma unroll
+          for (int e = 0; e < V; ++e) eq |= (unsigned)(key32(f[i * V + e]) == floor && e0 + e >= 0 && e0 + e < a.vocab) << e;
+          int to = __popc(eq);
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, to, o);
+            if (lane >= o) to += y;
+          }
+          const int all = __shfl_sync(0xffffffffu, to, 31);
+          to += at - __popc(eq);
+          for (; eq && to < k; eq &= eq - 1) s_list[to++] = (uint64_t)floor << 32 | (uint32_t)~(uint32_t)(e0 + __ffs(eq) - 1);
+          at += all;
         }
       }
     }
@@ -550,10 +585,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
   }
 }
 
-// Parts of a row: with fewer rows than the GPU holds CTAs, as many as fill it
-// once (65 rows: 15.0 us; twice as many parts 19); with more, so many that it is
-// filled kWaves times, for the last round's idle share (512 rows: once 67 us, twice
-// 59, three times 61).  None has less than a chunk per warp.
+// Parts of a row: with fewer rows than the GPU holds CTAs, as many as it holds (340
+// rows: 42 us; one part more, so that a second round begins, 45; 65 rows 14.2
+// against 16.3); with more, so many that it is filled kWaves times, for the last
+// round's idle share (620 rows: once 60 us, twice 53).  None has less than a chunk
+// per warp.
 Plan plan_of(int64_t rows, int64_t vocab, int vec, int k, int num_sms) {
   Plan p;
   p.chunks = (int)((vocab + vec - 1 + kChunk - 1) / kChunk);
