@@ -43,6 +43,7 @@ constexpr int kCtasPerSm = 4;       // resident
 constexpr int kRing = 6144;         // bytes of a warp's ring: 4 CTAs of 8 warps have 192 KB in flight or at work
 constexpr int kHeld = 512;          // chunk maxima that a CTA, or a warp's registers, hold
 constexpr int kWaves = 2;
+constexpr int kWorth = 64;          // chunks of a part, at least, where the rows alone fill the GPU
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -144,6 +145,42 @@ struct Loader<__nv_bfloat16> {
   __device__ static float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
   __device__ static __nv_bfloat16 from(float x) { return __float2bfloat16_rn(x); }
 };
+
+// Keys held by a warp, `Regs` in every lane (0: none); each(f) calls f(number, key)
+// for one key per lane, in the order of the numbers.  The search finds a bound that
+// at least k of all `count` keys reach, but no more than `enough` if it can: halving
+// between the least of the lanes' largest (32 keys reach it, or all) and the largest.
+struct Bound {
+  uint32_t floor, above;  // above: larger than every key
+  int reach;              // keys that reach the floor
+};
+template <typename Each>
+__device__ __forceinline__ int keys_reach(Each each, uint32_t bound) {
+  int n = 0;
+  each([&](int, uint32_t key) { n += key >= bound; });
+  return (int)__reduce_add_sync(0xffffffffu, n);
+}
+template <typename Each>
+__device__ __forceinline__ Bound find_bound(Each each, int count, int k, int enough) {
+  uint32_t most = 0;
+  each([&](int, uint32_t key) { most = max(most, key); });
+  Bound b{1u, __reduce_max_sync(0xffffffffu, most) + 1, count};
+  if (count < k) return b;
+  b.floor = __reduce_min_sync(0xffffffffu, most ? most : 0xFFFFFFFFu);
+  b.reach = keys_reach(each, b.floor);
+  uint32_t hi = b.above;
+  while (b.reach > enough && hi - b.floor > 1) {
+    const uint32_t mid = b.floor + (hi - b.floor) / 2;
+    const int n = keys_reach(each, mid);
+    if (n >= k) {
+      b.floor = mid;
+      b.reach = n;
+    } else {
+      hi = mid;
+    }
+  }
+  return b;
+}
 
 // How rows are cut, and where the workspace holds what: a counter per row (zero
 // between calls; only rows of several parts have one, and there are fewer than
@@ -351,9 +388,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
   if (k == 0) return;
 
   // Meanwhile one warp finds a bound `floor` that at least k chunks' maxima reach, but
-  // few more: halving between the least of the lanes' largest (32 chunks reach it)
-  // and the largest.  With fewer than k chunks all count.  (In every warp, which
-  // saves a barrier, it cost 512 rows 3 us of issue slots.)
+  // few more.  With fewer than k chunks all count.  (In every warp, which saves a
+  // barrier, it cost 512 rows 3 us of issue slots.)
   if (warp == 0) {
     // the first maxima in registers, further ones (of vocabularies past 262,144)
     // are read again whenever they are counted
@@ -365,46 +401,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
 #pragma unroll
       for (int i = 0; i < kHeld / 32; ++i) held[i] = i * 32 + lane < chunks ? __ldcg(keys + i * 32 + lane) : 0u;
     }
-    auto each = [&](auto f) {  // f(chunk of this lane, its maximum; 0 behind the last chunk), in the order of the chunks
+    auto each = [&](auto f) {  // the chunks' maxima
 #pragma unroll
       for (int i = 0; i < kHeld / 32; ++i)
         if (i * 32 < chunks) f(i * 32 + lane, held[i]);
       for (int c = kHeld; c < chunks; c += 32) f(c + lane, c + lane < chunks ? __ldcg(keys + c + lane) : 0u);
     };
-    auto reach = [&](uint32_t bound) {
-      int n = 0;
-      each([&](int, uint32_t key) { n += key >= bound; });
-      return (int)__reduce_add_sync(0xffffffffu, n);
-    };
-    uint32_t most = 0;
-    each([&](int, uint32_t key) { most = max(most, key); });
-    const uint32_t above = __reduce_max_sync(0xffffffffu, most) + 1;
-    uint32_t floor = 1;
-    int picks = chunks;
-    if (chunks > k) {
-      const int enough = min((k + 3 + kWarps - 1) / kWarps * kWarps, kLogprobsMaxTop);  // as many for every warp
-      floor = max(floor, __reduce_min_sync(0xffffffffu, most));
-      uint32_t hi = above;
-      picks = reach(floor);
-      while (picks > enough && hi - floor > 1) {
-        const uint32_t mid = floor + (hi - floor) / 2;
-        const int n = reach(mid);
-        if (n >= k) {
-          floor = mid;
-          picks = n;
-        } else {
-          hi = mid;
-        }
-      }
-    }
+    // (as many picks for every warp)
+    const Bound b = find_bound(each, chunks, k, min((k + 3 + kWarps - 1) / kWarps * kWarps, kLogprobsMaxTop));
     // Those chunks, in the order of their ids.  If more than kLogprobsMaxTop have
     // the same maximum, the first of them do: each holds one such logit, fewer than
     // k chunks have a larger maximum, and equal logits rank by their ids.
-    int equals = picks > kLogprobsMaxTop ? kLogprobsMaxTop - reach(floor + 1) : kLogprobsMaxTop;
+    int equals = b.reach > kLogprobsMaxTop ? kLogprobsMaxTop - keys_reach(each, b.floor + 1) : kLogprobsMaxTop;
     int taken = 0;
     each([&](int c, uint32_t key) {
-      const unsigned lower = (1u << lane) - 1, eq = __ballot_sync(0xffffffffu, key == floor);
-      const bool take = key > floor || (key == floor && __popc(eq & lower) < equals);
+      const unsigned lower = (1u << lane) - 1, eq = __ballot_sync(0xffffffffu, key == b.floor);
+      const bool take = key > b.floor || (key == b.floor && __popc(eq & lower) < equals);
       const unsigned all = __ballot_sync(0xffffffffu, take);
       if (take) s_pick[taken + __popc(all & lower)] = c;
       taken += __popc(all);
@@ -412,8 +424,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
     });
     if (lane == 0) {
       s_taken = taken;
-      s_floor = floor;
-      s_above = above;
+      s_floor = b.floor;
+      s_above = b.above;
       s_n = s_count = 0;
     }
   }
@@ -423,38 +435,39 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
   // Those chunks come into the warps' rings, kPicks a warp together (all of them, but
   // of more than 24 f32 chunks).
   constexpr int kPicks = kRing / kChunkBytes * kWarps < kLogprobsMaxTop ? kRing / kChunkBytes : kLogprobsMaxTop / kWarps;
+  bool resident = false;
+  const unsigned char* const mine = lp_smem + warp * kRing + lane * 16;
+  auto fetch_picks = [&](int p0) {
+    if (resident) return;
+#pragma unroll
+    for (int j = 0; j < kPicks; ++j) {
+      if (p0 + j * kWarps >= taken) break;
+      const int cp = s_pick[p0 + j * kWarps];
+      if (inside(cp)) {
+        const unsigned char* p = reinterpret_cast<const unsigned char*>(x + ((int64_t)cp * kChunk - head)) + lane * 16;
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + j * kChunkBytes + i * 512), "l"(p + i * 512) : "memory");
+      } else {
+        float edge[kPer];
+        load_chunk<T>(x, head, a.vocab, cp, edge);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          reinterpret_cast<T*>(lp_smem + warp * kRing + j * kChunkBytes + (i / V) * 512 + lane * 16)[i % V] = L::from(edge[i]);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    resident = taken <= kPicks * kWarps;
+  };
   // The warp's logits that reach a bound: their number, and, with `list`, they
   // themselves at the end of s_list as long as there is room (in an order of
   // arrival: the ranks do not depend on it).
-  bool resident = false;
   auto sweep = [&](uint32_t bound, bool list) {
     int n = 0;
     for (int p0 = warp; p0 < taken; p0 += kPicks * kWarps) {
-      if (!resident) {
-#pragma unroll
-        for (int j = 0; j < kPicks; ++j) {
-          if (p0 + j * kWarps >= taken) break;
-          const int cp = s_pick[p0 + j * kWarps];
-          if (inside(cp)) {
-            const unsigned char* p = reinterpret_cast<const unsigned char*>(x + ((int64_t)cp * kChunk - head)) + lane * 16;
-#pragma unroll
-            for (int i = 0; i < U; ++i)
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + j * kChunkBytes + i * 512), "l"(p + i * 512)
-                           : "memory");
-          } else {
-            float edge[kPer];
-            load_chunk<T>(x, head, a.vocab, cp, edge);
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-              reinterpret_cast<T*>(lp_smem + warp * kRing + j * kChunkBytes + (i / V) * 512 + lane * 16)[i % V] = L::from(edge[i]);
-          }
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        resident = taken <= kPicks * kWarps;
-      }
+      fetch_picks(p0);
       unsigned large[kPicks];
       int own = 0;
-      const unsigned char* mine = lp_smem + warp * kRing + lane * 16;
       auto id_of = [&](int j, int i) {
         return (int64_t)s_pick[p0 + j * kWarps] * kChunk - head + ((i / V) * 32 + lane) * V + i % V;
       };
@@ -504,9 +517,50 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
     return n;
   };
   uint32_t floor = s_floor;
-  sweep(floor, true);
+  const bool all_count = floor == 1 && a.vocab > kThreads;  // fewer than k chunks: no use in a list of everything
+  if (!all_count) sweep(floor, true);
   __syncthreads();
-  int n = s_n;
+  int n = all_count ? kThreads + 1 : s_n;
+  const uint32_t above = s_above;
+  if (n > kThreads && floor + 1 < above) {
+    // A better floor from the largest logit of every thread's share of the chunks:
+    // at least 32 threads have one.  (What is -inf behind a row's ends counts only
+    // for a floor that every logit reaches.)
+    uint32_t best = 0;
+    for (int p0 = warp; p0 < taken; p0 += kPicks * kWarps) {
+      fetch_picks(p0);
+#pragma unroll 1
+      for (int j = 0; j < kPicks && p0 + j * kWarps < taken; ++j)
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          float y[V];
+          L::get(*reinterpret_cast<const uint4*>(mine + j * kChunkBytes + i * 512), y);
+#pragma unroll
+          for (int e = 0; e < V; ++e) best = max(best, key32(y[e]));
+        }
+    }
+    s_keys[tid] = best;
+    __syncthreads();
+    if (warp == 0) {
+      uint32_t held[kWarps];
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) held[i] = s_keys[i * 32 + lane];
+      auto each = [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) f(i * 32 + lane, held[i]);
+      };
+      const Bound b = find_bound(each, kThreads, k, k + 8);
+      if (lane == 0) {
+        s_floor = b.floor;
+        s_n = 0;
+      }
+    }
+    __syncthreads();
+    floor = s_floor;
+    sweep(floor, true);
+    __syncthreads();
+    n = s_n;
+  }
   if (n > kThreads) {
     // Many logits reach the floor: equal ones (rows of which a mask leaves little),
     // or large ones side by side.  The least bound above it that no more than
@@ -522,7 +576,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
       __syncthreads();
       return sum;
     };
-    const uint32_t above = s_above;
     uint32_t hi = floor + 1;
     n = hi == above ? 0 : total(hi);
     if (n > kThreads) {
@@ -588,14 +641,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
 // Parts of a row: with fewer rows than the GPU holds CTAs, as many as it holds (340
 // rows: 42 us; one part more, so that a second round begins, 45; 65 rows 14.2
 // against 16.3); with more, so many that it is filled kWaves times, for the last
-// round's idle share (620 rows: once 60 us, twice 53).  None has less than a chunk
-// per warp.
+// round's idle share (620 rows: once 60 us, twice 53) as long as a part is worth its
+// join (1,000 bf16 rows of 18,000: 15 us whole, 20 in halves).  None has less than a
+// chunk per warp.
 Plan plan_of(int64_t rows, int64_t vocab, int vec, int k, int num_sms) {
   Plan p;
   p.chunks = (int)((vocab + vec - 1 + kChunk - 1) / kChunk);
   const int64_t resident = (int64_t)num_sms * kCtasPerSm;
   const int64_t want = rows <= resident ? resident / rows : (resident * kWaves + rows - 1) / rows;
-  const int64_t parts = std::min<int64_t>(want, (p.chunks + kWarps - 1) / kWarps);
+  const int64_t most = rows <= resident ? (p.chunks + kWarps - 1) / kWarps : std::max(1, p.chunks / kWorth);
+  const int64_t parts = std::min(want, most);
   p.per = (int)((p.chunks + parts - 1) / parts);
   p.parts = (p.chunks + p.per - 1) / p.per;
   p.stats = ((int64_t)num_sms * kCtasPerSm * kWaves * 4 + 15) / 16 * 16;
