@@ -19,12 +19,14 @@
 // order-preserving bits above the complemented id: keys are distinct, and equal
 // values rank by ascending id whatever the order in which they are met.
 //
-// Measured on a GB300 (us a call, device): 512 f32 rows of 151,936, k = 20, 56 (311
-// MB, 5.6 TB/s, 82% of the measured copy), without a top k 49; 65 bf16 rows of
-// 150,001, k = 8, 13.7; one f32 row, k = 5, 7.2, without a top k 4.4.  The stream
-// is bound by HBM, with 6 or 7 instructions a logit next to it; a row's join adds
-// 3 us of dependent steps, of which the rows in flight hide a part.  With a ring
-// of 8 KB a warp and three CTAs per SM the 512 rows took 60 and 53.
+// Measured on a GB300 (us a call, device): 512 f32 rows of 151,936, k = 20, 54.3 (311
+// MB, 5.7 TB/s, 85% of the measured copy), without a top k 47.9 (96%); as many bf16
+// rows 43 and 32; 65 bf16 rows of 150,001, k = 8, 13.2; one f32 row, k = 5, 7.2,
+// without a top k 4.4.  f32 streams are bound by HBM, 16-bit ones by 11 instructions
+// a logit (two logits in one multiply-add and three in one maximum: 15% less time
+// than one by one).  A row's join adds 4 us of dependent steps, and 16 MB that have
+// left L2 for 512 rows; rows that end together hide nothing of it.  With a ring of
+// 8 KB a warp and three CTAs per SM the 512 f32 rows took 60 and 53.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -55,6 +57,29 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float max_nan(float a, float b) {
   float y;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Two f32 values in one register pair: one instruction for two logits.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t y;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float* a, float* b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(x)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t y;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
+  return y;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t y;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
   return y;
 }
 
@@ -250,34 +275,51 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
   // |r| = 2^20 the terms are 2^(x L - z), one multiply-add each, with z = r L
   // rounded: z stands for itself and the sums are corrected by 2^(z - r L) at
   // the end.  Beyond, where that factor is no longer near 1, x - r comes first.
-  float r = -INFINITY, z = 0.f, s = 0.f, t = 0.f;
-  auto exact = [&] {  // s, t from reference z to reference r
-    const float d = fmaf(r, kLog2e, -z), c = ex2(-d);
-    t = c * fmaf(-d, s, t);
-    s *= c;
+  float r = -INFINITY, z = 0.f;
+  bool near = true;              // |r| <= 2^20, or no reference yet
+  uint64_t s2 = 0, t2 = 0;       // s and t, the logits of even and of odd places apart
+  auto scale = [&](float d, float c) {  // from one reference to another that is d above: c = 2^d
+    float s0, s1, t0, t1;
+    unpair(s2, &s0, &s1);
+    unpair(t2, &t0, &t1);
+    t0 = c == 0.f ? 0.f : c * fmaf(d, s0, t0);
+    t1 = c == 0.f ? 0.f : c * fmaf(d, s1, t1);
+    s2 = pair(s0 * c, s1 * c);
+    t2 = pair(t0, t1);
+  };
+  auto exact = [&] {  // from reference z to reference r
+    const float d = -fmaf(r, kLog2e, -z);
+    scale(d, ex2(d));
   };
   // Chunks that lie inside the row come through a ring in shared memory, kStages
   // - 1 of them on their way.  A lane copies the 16-byte vectors that it reads
   // itself, so a wait for its own copies is all the synchronization there is.
   constexpr int U = kPer / V, kChunkBytes = kChunk * (int)sizeof(T), kStages = kRing / kChunkBytes;
-  const uint32_t ring = smem_u32(lp_smem) + warp * kRing + lane * 16;
-  auto inside = [&](int c) { return (c > 0 || head == 0) && (int64_t)(c + 1) * kChunk - head <= a.vocab; };
+  const uint32_t ring = smem_u32(lp_smem) + warp * kRing + lane * 16, ring_end = ring + kStages * kChunkBytes;
+  const int in0 = head ? 1 : 0, in1 = (int)((a.vocab + head) / kChunk), inside_end = min(in1, c1);
+  auto inside = [&](int c) { return c >= in0 && c < in1; };
   uint64_t policy;
   asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
-  auto fetch = [&](int c, int stage) {
-    if (c < c1 && inside(c)) {
-      const unsigned char* p = reinterpret_cast<const unsigned char*>(x + ((int64_t)c * kChunk - head)) + lane * 16;
+  int c = part * plan.per + warp;
+  // the chunk that is fetched next: its number, this lane's first vector, its place
+  int fc = c;
+  const unsigned char* from = reinterpret_cast<const unsigned char*>(x - head + (int64_t)c * kChunk) + lane * 16;
+  uint32_t to = ring;
+  auto fetch = [&] {
+    if (fc >= in0 && fc < inside_end) {
 #pragma unroll
       for (int i = 0; i < U; ++i)
-        asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(ring + stage * kChunkBytes + i * 512),
-                     "l"(p + i * 512), "l"(policy)
+        asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to + i * 512), "l"(from + i * 512), "l"(policy)
                      : "memory");
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+    fc += kWarps;
+    from += kWarps * kChunkBytes;
+    to += kChunkBytes;
+    if (to == ring_end) to = ring;
   };
-  int c = part * plan.per + warp, stage = 0;
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(c + i * kWarps, i);
+  for (int i = 0; i < kStages - 1; ++i) fetch();
   int id = -1;
   if (a.ids) {
     id = a.ids[row];
@@ -289,8 +331,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
   }
   float given = 0.f;  // the given token's logit, on its way until the end
   if (a.ids && tid == kThreads - 32) given = L::one(x + id);
+  uint32_t at = ring;
+#pragma unroll 1
   for (; c < c1; c += kWarps) {
-    fetch(c + (kStages - 1) * kWarps, stage == 0 ? kStages - 1 : stage - 1);
+    fetch();
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
     float f[kPer];
     if (inside(c)) {
@@ -299,17 +343,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
         uint4 u;
         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-                     : "r"(ring + stage * kChunkBytes + i * 512)
+                     : "r"(at + i * 512)
                      : "memory");
         L::get(u, f + i * V);
       }
     } else {
       load_chunk<T>(x, head, a.vocab, c, f);
     }
-    if (++stage == kStages) stage = 0;
-    float top = f[0];
+    at += kChunkBytes;
+    if (at == ring_end) at = ring;
+    float top = max_nan(f[0], f[1]);
 #pragma unroll
-    for (int i = 1; i < kPer; ++i) top = max_nan(top, f[i]);
+    for (int i = 2; i < kPer; i += 2) top = max_nan(top, f[i], f[i + 1]);
     if (k > 0) {
       const uint32_t best = __reduce_max_sync(0xffffffffu, key32(top));
       if (lane == 0) *(alone ? s_keys + c : keys + c) = best;
@@ -317,39 +362,44 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
     // a new reference only when the terms get large: 2^(4 L) at most
     if (!(top <= r + 4.f)) {
       if (r != -INFINITY) {
-        if (fabsf(r) <= 0x1p20f) exact();
-        const float d = (r - top) * kLog2e, w = ex2(d);
-        t = w == 0.f ? 0.f : w * fmaf(d, s, t);
-        s *= w;
+        if (near) exact();
+        const float d = (r - top) * kLog2e;
+        scale(d, ex2(d));
       }
       r = top;
       z = r * kLog2e;
-      if (fabsf(r) <= 0x1p20f) {
-        const float d = fmaf(r, kLog2e, -z), w = ex2(d);
-        t = w * fmaf(d, s, t);
-        s *= w;
+      near = fabsf(r) <= 0x1p20f;
+      if (near) {
+        const float d = fmaf(r, kLog2e, -z);
+        scale(d, ex2(d));
       }
     }
     // 2^-200 is 0 in f32: the clamp changes no sum and keeps 0 * -inf out of t
-    if (r == -INFINITY || fabsf(r) <= 0x1p20f) {
+    auto add = [&](float d0, float d1) {
+      d0 = max_nan(d0, -200.f);
+      d1 = max_nan(d1, -200.f);
+      const uint64_t e2 = pair(ex2(d0), ex2(d1));
+      s2 = add2(s2, e2);
+      t2 = fma2(e2, pair(d0, d1), t2);
+    };
+    if (near) {
+      const uint64_t scale2 = pair(kLog2e, kLog2e), minus2 = pair(-z, -z);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const float d = max_nan(fmaf(f[i], kLog2e, -z), -200.f), e = ex2(d);
-        s += e;
-        t = fmaf(e, d, t);
+      for (int i = 0; i < kPer; i += 2) {
+        float d0, d1;
+        unpair(fma2(pair(f[i], f[i + 1]), scale2, minus2), &d0, &d1);
+        add(d0, d1);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const float d = max_nan((f[i] - r) * kLog2e, -200.f), e = ex2(d);
-        s += e;
-        t = fmaf(e, d, t);
-      }
+      for (int i = 0; i < kPer; i += 2) add((f[i] - r) * kLog2e, (f[i + 1] - r) * kLog2e);
     }
   }
-  if (fabsf(r) <= 0x1p20f) exact();
-
-  Stat v = warp_join(Stat{r, s, t});
+  if (near && r != -INFINITY) exact();
+  float s0, s1, t0, t1;
+  unpair(s2, &s0, &s1);
+  unpair(t2, &t0, &t1);
+  Stat v = warp_join(Stat{r, s0 + s1, t0 + t1});
   if (lane == 0) s_stat[warp] = v;
   __syncthreads();
   // the last warp has the row's sums (alone: it writes what depends on them)
