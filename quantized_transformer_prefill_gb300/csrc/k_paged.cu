@@ -14,16 +14,17 @@ namespace {
 // ================================================================ page tables
 //
 // One thread-block cluster does a step, or one CTA where there is little to write
-// (32 requests of one token 4.0 us against 5.1 with eight CTAs, 1,087 tokens 6.5
-// against 7.6, 2,164 tokens 7.7 against 7.4; sixteen where there is much: 6,364
-// tokens 8.2 with either, 21,500 tokens of 1,023 requests 9.6 against 10.6).  Every CTA scans all requests (new
-// tokens, grown pages, returned pages: three exclusive prefix sums in its own
-// shared memory), checks its share of the page ids the step will use, and
-// after one cluster barrier, at which the CTAs learn whether any of them found
-// an error, writes its share of the outputs.  Nothing is written before the
-// barrier, so an error leaves everything as it was, and nothing that another
-// CTA still reads is written after it: the entries that grow, the stack above
-// its old depth and the outputs are read by nobody.
+// (32 requests of one token 3.8 us against 4.5 with eight CTAs, 1,087 tokens 5.2
+// against 5.8, 2,164 tokens 6.0 against 5.8; sixteen where there is much: 6,364
+// tokens 6.3 with either, 21,500 tokens of 1,023 requests 7.1 against 8.6).  Every
+// CTA scans all requests (new tokens, grown pages, returned pages: three exclusive
+// prefix sums in its own shared memory), checks its share of the page ids the step
+// will use, works out its share of the outputs, and writes it after one cluster
+// barrier, at which the CTAs learn whether any of them found an error.  Nothing is
+// written before the barrier, so an error leaves everything as it was, and nothing
+// that is read is written: the entries that grow, the stack above its old depth and
+// the outputs are read by nobody.  What is left is a chain: the lengths (1.2 us),
+// the searches and page loads (1.7), the barrier (0.8), the stores.
 constexpr int kPtThreads = 1024;
 // What a launch gets unasked, 48 KB, less the kernel's static bytes: of that size
 // are also the CTAs of a cluster of 16 (3,412 requests).
@@ -71,7 +72,12 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_tables_kernel(const PageTa
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = a.n_req, P = a.page_size;
   const uint32_t rank = pt_cluster_rank(), nrank = pt_cluster_size();
+  // A thread's number for what is written side by side; and its numbers for grown,
+  // shared and returned pages, of which there are fewer than threads: every CTA has its
+  // share of them, in warps of their own.
   const int gtid = (int)rank * kPtThreads + tid, gn = (int)nrank * kPtThreads;
+  auto number = [&](int at) { return at * (int)nrank + (int)rank; };
+  const int j0 = number(tid), r0_shared = number((tid + kPtThreads / 2) % kPtThreads), k0 = number(kPtThreads - 1 - tid);
   enum { kBadLen = 1, kTooMany = 2, kNoPages = 4, kBadPage = 8 };
 
   if (tid == 0) s_local = s_err = 0;
@@ -165,33 +171,81 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_tables_kernel(const PageTa
       err |= kBadPage;
   }
 
-  // k-th returned page, and entry i of the stack with the returned pages on top
-  auto returned = [&](int k) {
+  // where the k-th returned page is, and the j-th new one: the stack from its top,
+  // with the returned pages on it
+  auto returned_at = [&](int k) -> const int* {
     const int r = pt_find(s_back, n, k);
-    return a.table[(int64_t)r * a.max_pages + pages(a.target[r]) + (k - s_back[r])];
+    return a.table + (int64_t)r * a.max_pages + pages(a.target[r]) + (k - s_back[r]);
   };
-  auto new_page = [&](int j) {
+  auto new_at = [&](int j) -> const int* {
     const int64_t i = depth - 1 - j;
-    return i < n_free ? a.free_pages[i] : returned((int)(i - n_free));
+    return i < n_free ? a.free_pages + i : returned_at((int)(i - n_free));
+  };
+
+  // positions and slots of the tokens t0, t0 + gn, ..; -1 behind the last
+  constexpr int Q = 2;
+  auto tokens_at = [&](int t0, int (&pos)[Q], int (&slot)[Q]) {
+    int t[Q], r[Q], off[Q];
+    const int* from[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) t[q] = min(t0 + q * gn, tokens - 1);
+    if (t0 < tokens) pt_find<Q>(s_start, n, t, r);
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      pos[q] = -1;
+      off[q] = 0;
+      from[q] = nullptr;
+      if (t0 + q * gn >= tokens) continue;
+      const int L = a.len[r[q]];
+      pos[q] = L + (t[q] - s_start[r[q]]);
+      const int p = a.div.of(pos[q]), held = pages(L);
+      off[q] = pos[q] - p * P;
+      from[q] = p < held ? a.table + (int64_t)r[q] * a.max_pages + p : new_at(s_grow[r[q]] + (p - held));
+    }
+    int page[Q];  // the loads side by side
+#pragma unroll
+    for (int q = 0; q < Q; ++q) page[q] = from[q] ? *from[q] : 0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) slot[q] = from[q] ? (int)((unsigned)page[q] * (unsigned)P + (unsigned)off[q]) : -1;
+  };
+  auto put_tokens = [&](int t0, const int (&pos)[Q], const int (&slot)[Q]) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int at = t0 + q * gn;
+      if (at >= a.max_tokens) break;
+      a.pos[at] = pos[q];
+      a.slot[at] = slot[q];
+    }
+  };
+  auto entry_of = [&](int j) {  // where the j-th new page is entered
+    const int r = pt_find(s_grow, n, j);
+    return a.table + (int64_t)r * a.max_pages + pages(a.len[r]) + (j - s_grow[r]);
   };
 
   // A thread's first grown page, returned page and shared page (the one that a
-  // request's next row shares with its last one), loaded side by side; checked
-  // here, and the grown one kept for when it is entered.
-  int page0 = 0;
+  // request's next row shares with its last one) are checked here, and all that a
+  // thread will write first is worked out before the barrier, whose wait hides it
+  // (after the barrier, the mixed step took 8.6 us).  Nothing that is read here is
+  // written by this step.
+  int page0 = 0, back0 = 0, *entry0 = nullptr;
+  int pos0[Q], slot0[Q];
   if (!err) {
     const unsigned np = (unsigned)a.n_pages;
     auto shared_page = [&](int r) {  // 0 where there is none
       const int L = a.len[r], p = a.div.of(L);
       return s_start[r + 1] > s_start[r] && L > p * P ? a.table[(int64_t)r * a.max_pages + p] : 0;
     };
-    const int back0 = gtid < back ? returned(gtid) : 0;
-    const int shared0 = gtid < n ? shared_page(gtid) : 0;
-    page0 = gtid < grown ? new_page(gtid) : 0;
+    if (k0 < back) back0 = *returned_at(k0);
+    const int shared0 = r0_shared < n ? shared_page(r0_shared) : 0;
+    if (j0 < grown) {
+      page0 = *new_at(j0);
+      entry0 = entry_of(j0);
+    }
+    tokens_at(gtid, pos0, slot0);
     bool bad = (unsigned)page0 >= np || (unsigned)back0 >= np || (unsigned)shared0 >= np;
-    for (int j = gtid + gn; j < grown; j += gn) bad |= (unsigned)new_page(j) >= np;
-    for (int k = gtid + gn; k < back; k += gn) bad |= (unsigned)returned(k) >= np;
-    for (int r = gtid + gn; r < n; r += gn) bad |= (unsigned)shared_page(r) >= np;
+    for (int j = j0 + gn; j < grown; j += gn) bad |= (unsigned)*new_at(j) >= np;
+    for (int k = k0 + gn; k < back; k += gn) bad |= (unsigned)*returned_at(k) >= np;
+    for (int r = r0_shared + gn; r < n; r += gn) bad |= (unsigned)shared_page(r) >= np;
     if (__syncthreads_or(bad)) err |= kBadPage;
   }
   if (nrank > 1) {
@@ -221,37 +275,15 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_tables_kernel(const PageTa
   }
 
   for (int r = gtid; r <= n; r += gn) a.start[r] = s_start[r];
-  for (int j = gtid; j < grown; j += gn) {
-    const int r = pt_find(s_grow, n, j);
-    const int held = pages(a.len[r]);
-    a.table[(int64_t)r * a.max_pages + held + (j - s_grow[r])] = j == gtid ? page0 : new_page(j);
-  }
+  put_tokens(gtid, pos0, slot0);
+  if (j0 < grown) *entry0 = page0;
+  for (int j = j0 + gn; j < grown; j += gn) *entry_of(j) = *new_at(j);
   const int pushed = (int)(depth - grown) - n_free;
-  for (int k = gtid; k < pushed; k += gn) a.free_pages[n_free + k] = returned(k);
-  constexpr int Q = 4;  // tokens of a thread at a time
-  for (int t0 = gtid; t0 < a.max_tokens; t0 += Q * gn) {
-    int t[Q], r[Q], pos[Q], page[Q], off[Q];
-#pragma unroll
-    for (int q = 0; q < Q; ++q) t[q] = min(t0 + q * gn, tokens - 1);
-    if (t0 < tokens) pt_find<Q>(s_start, n, t, r);
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      pos[q] = page[q] = -1;
-      off[q] = P - 1;  // slot -1
-      if (t0 + q * gn >= tokens) continue;
-      const int L = a.len[r[q]];
-      pos[q] = L + (t[q] - s_start[r[q]]);
-      const int p = a.div.of(pos[q]), held = pages(L);
-      off[q] = pos[q] - p * P;
-      page[q] = p < held ? a.table[(int64_t)r[q] * a.max_pages + p] : new_page(s_grow[r[q]] + (p - held));
-    }
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int at = t0 + q * gn;
-      if (at >= a.max_tokens) break;
-      a.pos[at] = pos[q];
-      a.slot[at] = page[q] * P + off[q];
-    }
+  if (k0 < pushed) a.free_pages[n_free + k0] = back0;
+  for (int k = k0 + gn; k < pushed; k += gn) a.free_pages[n_free + k] = *returned_at(k);
+  for (int t0 = gtid + Q * gn; t0 < a.max_tokens; t0 += Q * gn) {
+    tokens_at(t0, pos0, slot0);
+    put_tokens(t0, pos0, slot0);
   }
   if (gtid == 0) *a.n_free_out = (int)(depth - grown);
 }
