@@ -427,9 +427,9 @@ __global__ void __launch_bounds__(kRpWarps * 32) rope_paged_kernel(const __grid_
     asm volatile("cp.async.wait_group %0;" ::"n"(kRpRing - 1) : "memory");  // bias and norm weights, the oldest group
     __syncthreads();
   }
-  if (slot < 0) return;  // padding
-  if (slot >= slots || pos < 0) {
-    if (first == 0 && lane == 0) set_error(a.status, MINFER_ERR_POS_OOB);
+  if (slot < 0 || slot >= slots || pos < 0) {  // padding, or refused
+    if (slot >= 0 && first == 0 && lane == 0) set_error(a.status, MINFER_ERR_POS_OOB);
+    asm volatile("cp.async.wait_all;" ::: "memory");
     return;
   }
   float cs[E], sn[E];
