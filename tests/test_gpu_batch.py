@@ -707,6 +707,28 @@ def test_token_logprobs_wide_vocabularies(qp, t, kind, k):
         check_logprobs(qp, x, dev([0, V - 1]), k)
 
 
+@pytest.mark.parametrize("V", [151936, 262145, 300001])
+def test_token_logprobs_many_whole_rows(qp, V):
+    """More rows than the GPU holds CTAs twice: every row is one CTA's, with its chunk maxima in shared memory or, past
+    512 chunks, in the workspace."""
+    rows = 2 * 4 * torch.cuda.get_device_properties(0).multi_processor_count + 7
+    x = torch.randn(rows, V, generator=gen(V), device="cuda", dtype=F16)
+    x[3].fill_(-math.inf)
+    ids = (torch.arange(rows, device="cuda") * 37 % V).to(I32)
+    status = status_word()
+    got = qp.op_token_logprobs(x, ids, 9, status=status)
+    assert int(status) == 0
+    some = [0, 3, 4, rows // 2, rows - 1]
+    for r in some:
+        lp, h, order, tl = logprobs_by_definition(x[r:r + 1], ids[r:r + 1], 9)
+        assert torch.equal(got[2][r], order[0])
+        close(got[0][r:r + 1], lp, logprobs_tolerance(x, lp))
+        close(got[3][r], tl[0], logprobs_tolerance(x, tl[0]))
+        close(got[1][r:r + 1], h, 2 * logprobs_tolerance(x, h + math.log(V)) * (1 + h.abs() + math.log(V)))
+    again = qp.op_token_logprobs(x, ids, 9, status=status)
+    assert all(torch.equal(p, q) for p, q in zip(got, again))
+
+
 def test_token_logprobs_nan_and_infinity(qp):
     x = torch.randn(4, 3000, device="cuda")
     x[0, 0], x[0, 2999] = math.nan, math.inf
