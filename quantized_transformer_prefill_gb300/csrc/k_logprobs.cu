@@ -5,8 +5,8 @@
 //   log p_i = (x_i - m) - ln s,   H = ln 2 (log2 s - t / s)
 //
 // A row is cut into parts, one CTA each.  Every thread keeps a running
-// (reference, s, t); a warp reads chunks of 512 neighbouring logits and leaves
-// each chunk's largest one in the workspace.  The CTA that finishes a row last
+// (reference, s, t); a warp reads blocks of 2 KB and keeps the largest logit of
+// each chunk of 512.  The CTA that finishes a row last
 // (a counter per row) joins the parts' sums and finds the k largest logits.
 // A bound that at least k chunks' maxima reach is reached by at least k logits,
 // all of them in those chunks; halving finds one that few more than k chunks
@@ -19,14 +19,16 @@
 // order-preserving bits above the complemented id: keys are distinct, and equal
 // values rank by ascending id whatever the order in which they are met.
 //
-// Measured on a GB300 (us a call, device): 512 f32 rows of 151,936, k = 20, 54.3 (311
-// MB, 5.7 TB/s, 85% of the measured copy), without a top k 47.9 (96%); as many bf16
-// rows 43 and 32; 65 bf16 rows of 150,001, k = 8, 13.2; one f32 row, k = 5, 7.2,
-// without a top k 4.4.  f32 streams are bound by HBM, 16-bit ones by 11 instructions
-// a logit (two logits in one multiply-add and three in one maximum: 15% less time
-// than one by one).  A row's join adds 4 us of dependent steps, and 16 MB that have
-// left L2 for 512 rows; rows that end together hide nothing of it.  With a ring of
-// 8 KB a warp and three CTAs per SM the 512 f32 rows took 60 and 53.
+// Measured on a GB300 (us a call, device): 512 f32 rows of 151,936, k = 20, 54 (311
+// MB, 5.8 TB/s, 85% of the measured copy), without a top k 47.5 (97%); as many bf16
+// rows 36 and 28 (5.6 TB/s); 65 bf16 rows of 150,001, k = 8, 12.3; one f32 row, k =
+// 5, 7.2, without a top k 4.3.  f32 streams are bound by HBM, 16-bit ones by 7
+// instructions a logit next to it: two logits in a multiply-add, maxima and clamps
+// of two 16-bit or three f32 values, and blocks of two 16-bit chunks, over which a
+// step's 60 other instructions are spread (logit by logit and chunk by chunk the
+// bf16 rows took 48 and 36).  A row's join adds 4 us of dependent steps, and for the
+// 512 f32 rows 16 MB that have left L2; rows that end together hide nothing of it.
+// With a ring of 8 KB a warp and three CTAs per SM the 512 f32 rows took 60 and 53.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -39,13 +41,15 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kChunk = 512;         // logits of a chunk
-constexpr int kPer = kChunk / 32;   // logits of a lane
+constexpr int kChunk = 512;         // logits of a chunk, of which the maximum is kept
+constexpr int kVecs = 4;            // 16-byte vectors of a lane in a block: one f32 chunk or two 16-bit ones
+constexpr int kBlockBytes = kVecs * 512;
 constexpr int kCtasPerSm = 4;       // resident
 constexpr int kRing = 6144;         // bytes of a warp's ring: 4 CTAs of 8 warps have 192 KB in flight or at work
+constexpr int kMostPicks = kLogprobsMaxTop + kWarps;  // chunks that are read again
 constexpr int kHeld = 512;          // chunk maxima that a CTA, or a warp's registers, hold
 constexpr int kWaves = 2;
-constexpr int kWorth = 64;          // chunks of a part, at least, where the rows alone fill the GPU
+constexpr int kWorth = 64;          // blocks of a part, at least, where the rows alone fill the GPU
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -127,11 +131,27 @@ __device__ __forceinline__ Stat join2(Stat a, Stat b) {
   return Stat{m, a.s * ca + b.s * cb, (ca == 0.f ? 0.f : ca * fmaf(da, a.s, a.t)) + (cb == 0.f ? 0.f : cb * fmaf(db, b.s, b.t))};
 }
 
+// 16-byte vectors of T.  top: the largest value of a lane's vectors of a chunk; clamp: values
+// raised to kLow, where infinities would make 0 * -inf of a term; pairs: two values
+// each as f32.  kNear: up to this size of the reference, what kLow stands for is so
+// far below it that its terms are 0.
 template <typename T>
-struct Loader;  // 16-byte vectors of T as floats
+struct Loader;
 template <>
 struct Loader<float> {
   static constexpr int kVec = 4;
+  static constexpr float kNear = 0x1p20f;
+  __device__ static float top(const uint4* u) {
+    float y = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kChunk / 32 / kVec; ++i)
+      y = max_nan(max_nan(y, __uint_as_float(u[i].x), __uint_as_float(u[i].y)), __uint_as_float(u[i].z), __uint_as_float(u[i].w));
+    return y;
+  }
+  __device__ static void pairs(const uint4& u, uint64_t* p) {  // raised to -2^100
+    p[0] = pair(max_nan(__uint_as_float(u.x), -0x1p100f), max_nan(__uint_as_float(u.y), -0x1p100f));
+    p[1] = pair(max_nan(__uint_as_float(u.z), -0x1p100f), max_nan(__uint_as_float(u.w), -0x1p100f));
+  }
   __device__ static void get(const uint4& u, float* x) {
     x[0] = __uint_as_float(u.x);
     x[1] = __uint_as_float(u.y);
@@ -139,36 +159,81 @@ struct Loader<float> {
     x[3] = __uint_as_float(u.w);
   }
   __device__ static float one(const float* p) { return *p; }
-  __device__ static float from(float x) { return x; }
+  __device__ static float none() { return -INFINITY; }
 };
 template <>
 struct Loader<__half> {
   static constexpr int kVec = 8;
+  static constexpr float kNear = 0x1p15f;
+  __device__ static uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t y;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+  }
+  __device__ static float2 two(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+  __device__ static float top(const uint4* u) {
+    uint32_t y = max2(max2(u[0].x, u[0].y), max2(u[0].z, u[0].w));
+#pragma unroll
+    for (int i = 1; i < kChunk / 32 / kVec; ++i) y = max2(y, max2(max2(u[i].x, u[i].y), max2(u[i].z, u[i].w)));
+    const float2 f = two(y);
+    return max_nan(f.x, f.y);
+  }
+  __device__ static void pairs(const uint4& u, uint64_t* p) {  // raised to -65504
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = two(max2(w[i], 0xFBFFFBFFu));
+      p[i] = pair(f.x, f.y);
+    }
+  }
   __device__ static void get(const uint4& u, float* x) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      const float2 f = two(w[i]);
       x[2 * i] = f.x;
       x[2 * i + 1] = f.y;
     }
   }
   __device__ static float one(const __half* p) { return __half2float(*p); }
-  __device__ static __half from(float x) { return __float2half_rn(x); }
+  __device__ static __half none() { return __ushort_as_half(0xFC00); }
 };
 template <>
 struct Loader<__nv_bfloat16> {
   static constexpr int kVec = 8;
+  static constexpr float kNear = 0x1p20f;
+  __device__ static uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t y;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+  }
+  __device__ static float2 two(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+  __device__ static float top(const uint4* u) {
+    uint32_t y = max2(max2(u[0].x, u[0].y), max2(u[0].z, u[0].w));
+#pragma unroll
+    for (int i = 1; i < kChunk / 32 / kVec; ++i) y = max2(y, max2(max2(u[i].x, u[i].y), max2(u[i].z, u[i].w)));
+    const float2 f = two(y);
+    return max_nan(f.x, f.y);
+  }
+  __device__ static void pairs(const uint4& u, uint64_t* p) {  // raised to -2^100
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = two(max2(w[i], 0xF180F180u));
+      p[i] = pair(f.x, f.y);
+    }
+  }
   __device__ static void get(const uint4& u, float* x) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      const float2 f = two(w[i]);
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
     }
   }
   __device__ static float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-  __device__ static __nv_bfloat16 from(float x) { return __float2bfloat16_rn(x); }
+  __device__ static __nv_bfloat16 none() { return __ushort_as_bfloat16(0xFF80); }
 };
 
 // Keys held by a warp, `Regs` in every lane (0: none); each(f) calls f(number, key)
@@ -212,33 +277,33 @@ __device__ __forceinline__ Bound find_bound(Each each, int count, int k, int eno
 // num_sms * kCtasPerSm * kWaves of those, so their place is the same in every call), a
 // Stat per part, the largest key32 of every chunk.
 struct Plan {
-  int chunks;  // of a row, at the worst alignment
+  int chunks;  // of a row's blocks, at the worst alignment
   int parts;   // of a row
-  int per;     // chunks of a part
+  int per;     // blocks of a part
   int64_t stats, keys, bytes;  // offsets and size
 };
 
-// One lane's 16 logits of chunk c of a row: vectors of 16 bytes, lane after
-// lane.  Vector v holds the values [v*V - head, (v+1)*V - head): the row's first
-// address rounded down to 16 bytes is vector 0.  -inf outside of the row.
-template <typename T>
-__device__ __forceinline__ void load_chunk(const T* x, int head, int64_t vocab, int64_t c, float* f) {
+// One lane's N vectors of those from element e0 on, lane after lane; e0 plus the row's
+// first address is a multiple of 16 bytes.  -inf outside of the row.
+template <typename T, int N>
+__device__ __forceinline__ void load_vectors(const T* x, int64_t vocab, int64_t e0, uint4* u) {
   using L = Loader<T>;
-  constexpr int V = L::kVec, U = kPer / V;
+  constexpr int V = L::kVec;
   const int lane = threadIdx.x & 31;
-  const int64_t e0 = c * kChunk - head;
-  if (e0 >= 0 && e0 + kChunk <= vocab) {
+  if (e0 >= 0 && e0 + N * 32 * V <= vocab) {
     const uint4* p = reinterpret_cast<const uint4*>(x + e0) + lane;
-    uint4 u[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) u[i] = __ldcg(p + i * 32);
-#pragma unroll
-    for (int i = 0; i < U; ++i) L::get(u[i], f + i * V);
+    for (int i = 0; i < N; ++i) u[i] = __ldcg(p + i * 32);
   } else {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int64_t e = e0 + ((i / V) * 32 + lane) * V + i % V;
-      f[i] = e >= 0 && e < vocab ? L::one(x + e) : -INFINITY;
+    for (int i = 0; i < N; ++i) {
+      alignas(16) T t[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const int64_t e = e0 + (i * 32 + lane) * V + k;
+        t[k] = e >= 0 && e < vocab ? x[e] : L::none();
+      }
+      u[i] = *reinterpret_cast<const uint4*>(t);
     }
   }
 }
@@ -246,11 +311,12 @@ __device__ __forceinline__ void load_chunk(const T* x, int head, int64_t vocab, 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __grid_constant__ LogprobsArgs a, const Plan plan) {
   using L = Loader<T>;
-  constexpr int V = L::kVec;
+  // values of a vector, logits of a block, its chunks, a lane's vectors of a chunk
+  constexpr int V = L::kVec, kBlock = 32 * kVecs * V, S = kBlock / kChunk, U = kVecs / S;
   extern __shared__ __align__(128) unsigned char lp_smem[];
   __shared__ uint64_t s_list[kThreads];
   __shared__ uint32_t s_keys[kHeld];
-  __shared__ int s_pick[kLogprobsMaxTop];
+  __shared__ int s_pick[kMostPicks];
   __shared__ Stat s_stat[kWarps];
   __shared__ int s_last, s_n, s_count, s_taken;
   __shared__ uint32_t s_floor, s_above;
@@ -266,17 +332,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
   const T* x = static_cast<const T*>(a.x) + row * a.row_stride;
   const int head = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
   const int chunks = (int)((a.vocab + head + kChunk - 1) / kChunk);
-  const int c1 = min(chunks, (part + 1) * plan.per);
+  const int b1 = min((chunks + S - 1) / S, (part + 1) * plan.per);
   // the maxima of a row that this CTA has alone stay in shared memory, if they fit
   // (512 rows: 2 us less than with a store of 4 bytes per chunk)
-  const bool alone = plan.parts == 1 && plan.per <= kHeld;
+  const bool alone = plan.parts == 1 && plan.chunks <= kHeld;
 
   // r: the reference, a logit near the largest so far (-inf: none yet).  Up to
-  // |r| = 2^20 the terms are 2^(x L - z), one multiply-add each, with z = r L
+  // |r| = kNear the terms are 2^(x L - z), one multiply-add each, with z = r L
   // rounded: z stands for itself and the sums are corrected by 2^(z - r L) at
   // the end.  Beyond, where that factor is no longer near 1, x - r comes first.
   float r = -INFINITY, z = 0.f;
-  bool near = true;              // |r| <= 2^20, or no reference yet
+  bool near = true;              // |r| <= kNear, or no reference yet
   uint64_t s2 = 0, t2 = 0;       // s and t, the logits of even and of odd places apart
   auto scale = [&](float d, float c) {  // from one reference to another that is d above: c = 2^d
     float s0, s1, t0, t1;
@@ -291,31 +357,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
     const float d = -fmaf(r, kLog2e, -z);
     scale(d, ex2(d));
   };
-  // Chunks that lie inside the row come through a ring in shared memory, kStages
+  // Blocks that lie inside the row come through a ring in shared memory, kStages
   // - 1 of them on their way.  A lane copies the 16-byte vectors that it reads
   // itself, so a wait for its own copies is all the synchronization there is.
-  constexpr int U = kPer / V, kChunkBytes = kChunk * (int)sizeof(T), kStages = kRing / kChunkBytes;
-  const uint32_t ring = smem_u32(lp_smem) + warp * kRing + lane * 16, ring_end = ring + kStages * kChunkBytes;
-  const int in0 = head ? 1 : 0, in1 = (int)((a.vocab + head) / kChunk), inside_end = min(in1, c1);
-  auto inside = [&](int c) { return c >= in0 && c < in1; };
+  constexpr int kStages = kRing / kBlockBytes;
+  const uint32_t ring = smem_u32(lp_smem) + warp * kRing + lane * 16, ring_end = ring + kStages * kBlockBytes;
+  const int in0 = head ? 1 : 0, in1 = min((int)((a.vocab + head) / kBlock), b1);
   uint64_t policy;
   asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
-  int c = part * plan.per + warp;
-  // the chunk that is fetched next: its number, this lane's first vector, its place
-  int fc = c;
-  const unsigned char* from = reinterpret_cast<const unsigned char*>(x - head + (int64_t)c * kChunk) + lane * 16;
+  int b = part * plan.per + warp;
+  // the block that is fetched next: its number, this lane's first vector, its place
+  int fb = b;
+  const unsigned char* from = reinterpret_cast<const unsigned char*>(x - head + (int64_t)b * kBlock) + lane * 16;
   uint32_t to = ring;
   auto fetch = [&] {
-    if (fc >= in0 && fc < inside_end) {
+    if (fb >= in0 && fb < in1) {
 #pragma unroll
-      for (int i = 0; i < U; ++i)
+      for (int i = 0; i < kVecs; ++i)
         asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to + i * 512), "l"(from + i * 512), "l"(policy)
                      : "memory");
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    fc += kWarps;
-    from += kWarps * kChunkBytes;
-    to += kChunkBytes;
+    fb += kWarps;
+    from += kWarps * kBlockBytes;
+    to += kBlockBytes;
     if (to == ring_end) to = ring;
   };
 #pragma unroll
@@ -333,32 +398,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
   if (a.ids && tid == kThreads - 32) given = L::one(x + id);
   uint32_t at = ring;
 #pragma unroll 1
-  for (; c < c1; c += kWarps) {
+  for (; b < b1; b += kWarps) {
     fetch();
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-    float f[kPer];
-    if (inside(c)) {
+    uint4 u[kVecs];
+    if (b >= in0 && b < in1) {
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        uint4 u;
+      for (int i = 0; i < kVecs; ++i)
         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                     : "=r"(u[i].x), "=r"(u[i].y), "=r"(u[i].z), "=r"(u[i].w)
                      : "r"(at + i * 512)
                      : "memory");
-        L::get(u, f + i * V);
-      }
     } else {
-      load_chunk<T>(x, head, a.vocab, c, f);
+      load_vectors<T, kVecs>(x, a.vocab, (int64_t)b * kBlock - head, u);
     }
-    at += kChunkBytes;
+    at += kBlockBytes;
     if (at == ring_end) at = ring;
-    float top = max_nan(f[0], f[1]);
-#pragma unroll
-    for (int i = 2; i < kPer; i += 2) top = max_nan(top, f[i], f[i + 1]);
+    float top = L::top(u), top1 = S > 1 ? L::top(u + kVecs - U) : top;
     if (k > 0) {
-      const uint32_t best = __reduce_max_sync(0xffffffffu, key32(top));
-      if (lane == 0) *(alone ? s_keys + c : keys + c) = best;
+      uint32_t best = __reduce_max_sync(0xffffffffu, key32(top));
+      if (S > 1) {
+        const uint32_t best1 = __reduce_max_sync(0xffffffffu, key32(top1));
+        if (lane == 1) best = best1;
+      }
+      const int c = b * S + lane;
+      if (lane < S && c < chunks) *(alone ? s_keys + c : keys + c) = best;
     }
+    if (S > 1) top = max_nan(top, top1);
     // a new reference only when the terms get large: 2^(4 L) at most
     if (!(top <= r + 4.f)) {
       if (r != -INFINITY) {
@@ -368,16 +434,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
       }
       r = top;
       z = r * kLog2e;
-      near = fabsf(r) <= 0x1p20f;
+      near = fabsf(r) <= L::kNear;
       if (near) {
         const float d = fmaf(r, kLog2e, -z);
         scale(d, ex2(d));
       }
     }
-    // 2^-200 is 0 in f32: the clamp changes no sum and keeps 0 * -inf out of t
     auto add = [&](float d0, float d1) {
-      d0 = max_nan(d0, -200.f);
-      d1 = max_nan(d1, -200.f);
       const uint64_t e2 = pair(ex2(d0), ex2(d1));
       s2 = add2(s2, e2);
       t2 = fma2(e2, pair(d0, d1), t2);
@@ -385,14 +448,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
     if (near) {
       const uint64_t scale2 = pair(kLog2e, kLog2e), minus2 = pair(-z, -z);
 #pragma unroll
-      for (int i = 0; i < kPer; i += 2) {
-        float d0, d1;
-        unpair(fma2(pair(f[i], f[i + 1]), scale2, minus2), &d0, &d1);
-        add(d0, d1);
+      for (int i = 0; i < kVecs; ++i) {
+        uint64_t f[V / 2];
+        L::pairs(u[i], f);
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+          float d0, d1;
+          unpair(fma2(f[e], scale2, minus2), &d0, &d1);
+          add(d0, d1);
+        }
       }
     } else {
+      // 2^-200 is 0 in f32: the clamp changes no sum and keeps 0 * -inf out of t
 #pragma unroll
-      for (int i = 0; i < kPer; i += 2) add((f[i] - r) * kLog2e, (f[i + 1] - r) * kLog2e);
+      for (int i = 0; i < kVecs; ++i) {
+        float f[V];
+        L::get(u[i], f);
+#pragma unroll
+        for (int e = 0; e < V; e += 2) add(max_nan((f[e] - r) * kLog2e, -200.f), max_nan((f[e + 1] - r) * kLog2e, -200.f));
+      }
     }
   }
   if (near && r != -INFINITY) exact();
@@ -457,12 +531,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
         if (i * 32 < chunks) f(i * 32 + lane, held[i]);
       for (int c = kHeld; c < chunks; c += 32) f(c + lane, c + lane < chunks ? __ldcg(keys + c + lane) : 0u);
     };
-    // (as many picks for every warp)
-    const Bound b = find_bound(each, chunks, k, min((k + 3 + kWarps - 1) / kWarps * kWarps, kLogprobsMaxTop));
-    // Those chunks, in the order of their ids.  If more than kLogprobsMaxTop have
+    // (as many picks for every warp, kMostPicks for k = kLogprobsMaxTop)
+    const Bound b = find_bound(each, chunks, k, (k + 3 + kWarps - 1) / kWarps * kWarps);
+    // Those chunks, in the order of their ids.  If more than kMostPicks have
     // the same maximum, the first of them do: each holds one such logit, fewer than
     // k chunks have a larger maximum, and equal logits rank by their ids.
-    int equals = b.reach > kLogprobsMaxTop ? kLogprobsMaxTop - keys_reach(each, b.floor + 1) : kLogprobsMaxTop;
+    int equals = b.reach > kMostPicks ? kMostPicks - keys_reach(each, b.floor + 1) : kMostPicks;
     int taken = 0;
     each([&](int c, uint32_t key) {
       const unsigned lower = (1u << lane) - 1, eq = __ballot_sync(0xffffffffu, key == b.floor);
@@ -484,7 +558,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
 
   // Those chunks come into the warps' rings, kPicks a warp together (all of them, but
   // of more than 24 f32 chunks).
-  constexpr int kPicks = kRing / kChunkBytes * kWarps < kLogprobsMaxTop ? kRing / kChunkBytes : kLogprobsMaxTop / kWarps;
+  constexpr int kChunkBytes = kChunk * (int)sizeof(T);
+  const int cin1 = (int)((a.vocab + head) / kChunk);
+  auto inside = [&](int c) { return c >= in0 && c < cin1; };
+  constexpr int kPicks = kRing / kChunkBytes * kWarps < kMostPicks ? kRing / kChunkBytes : kMostPicks / kWarps;
   bool resident = false;
   const unsigned char* const mine = lp_smem + warp * kRing + lane * 16;
   auto fetch_picks = [&](int p0) {
@@ -499,11 +576,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
         for (int i = 0; i < U; ++i)
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + j * kChunkBytes + i * 512), "l"(p + i * 512) : "memory");
       } else {
-        float edge[kPer];
-        load_chunk<T>(x, head, a.vocab, cp, edge);
+        uint4 edge[U];
+        load_vectors<T, U>(x, a.vocab, (int64_t)cp * kChunk - head, edge);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          reinterpret_cast<T*>(lp_smem + warp * kRing + j * kChunkBytes + (i / V) * 512 + lane * 16)[i % V] = L::from(edge[i]);
+        for (int i = 0; i < U; ++i) *reinterpret_cast<uint4*>(lp_smem + warp * kRing + j * kChunkBytes + i * 512 + lane * 16) = edge[i];
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -651,14 +727,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
     if (n < k && warp == 0) {
       int at = n;
       for (int p = 0; p < taken && at < k; ++p) {
-        float f[kPer];
-        load_chunk<T>(x, head, a.vocab, s_pick[p], f);
+        uint4 u[U];
+        load_vectors<T, U>(x, a.vocab, (int64_t)s_pick[p] * kChunk - head, u);
 #pragma unroll
         for (int i = 0; i < U; ++i) {  // a vector of every lane: neighbouring logits
           const int64_t e0 = (int64_t)s_pick[p] * kChunk - head + (i * 32 + lane) * V;
           unsigned eq = 0;
+          float f[V];
+          L::get(u[i], f);
 #pragma unroll
-          for (int e = 0; e < V; ++e) eq |= (unsigned)(key32(f[i * V + e]) == floor && e0 + e >= 0 && e0 + e < a.vocab) << e;
+          for (int e = 0; e < V; ++e) eq |= (unsigned)(key32(f[e]) == floor && e0 + e >= 0 && e0 + e < a.vocab) << e;
           int to = __popc(eq);
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -693,16 +771,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const __
 // against 16.3); with more, so many that it is filled kWaves times, for the last
 // round's idle share (620 rows: once 60 us, twice 53) as long as a part is worth its
 // join (1,000 bf16 rows of 18,000: 15 us whole, 20 in halves).  None has less than a
-// chunk per warp.
+// block per warp.
 Plan plan_of(int64_t rows, int64_t vocab, int vec, int k, int num_sms) {
   Plan p;
-  p.chunks = (int)((vocab + vec - 1 + kChunk - 1) / kChunk);
+  const int block = 32 * kVecs * vec;  // logits
+  const int blocks = (int)((vocab + vec - 1 + block - 1) / block);
   const int64_t resident = (int64_t)num_sms * kCtasPerSm;
   const int64_t want = rows <= resident ? resident / rows : (resident * kWaves + rows - 1) / rows;
-  const int64_t most = rows <= resident ? (p.chunks + kWarps - 1) / kWarps : std::max(1, p.chunks / kWorth);
+  const int64_t most = rows <= resident ? (blocks + kWarps - 1) / kWarps : std::max(1, blocks / kWorth);
   const int64_t parts = std::min(want, most);
-  p.per = (int)((p.chunks + parts - 1) / parts);
-  p.parts = (p.chunks + p.per - 1) / p.per;
+  p.per = (int)((blocks + parts - 1) / parts);
+  p.parts = (blocks + p.per - 1) / p.per;
+  p.chunks = blocks * (block / kChunk);
   p.stats = ((int64_t)num_sms * kCtasPerSm * kWaves * 4 + 15) / 16 * 16;
   p.keys = p.stats + rows * p.parts * 16;
   p.bytes = p.keys + (k > 0 ? rows * p.chunks * 4 : 0);
