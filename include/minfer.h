@@ -497,7 +497,8 @@ int minfer_op_paged_attention_workspace(int n_req, int n_head, const minfer_page
  * scale 0 means 1/sqrt(head_dim).  A request of length 0 gets zeros and -inf.
  * What lies in the pages behind a request's last row is never used, whatever
  * its bits.  Scores, softmax statistics and sums are f32; with a 16-bit cache
- * the softmax weights are rounded to its type for their product with V, and with
+ * each softmax weight is held in two numbers of its type for the product with V
+ * (to 2^-15 of it; f16: to 2^-20, or 2^-39 of the largest so far), and with
  * an f32 cache the products are those of tf32 halves (an infinity among the K and
  * V values that a request sees makes its result NaN there).  The
  * result of a call depends on its inputs alone, bit for bit on one device

@@ -30,6 +30,11 @@
 // bytes of K and V, so the accumulators stay in registers, where the softmax
 // needs them.
 //
+// 16-bit caches: Q, K and V are exact in an MMA; a weight goes through two of them, as
+// the sum of two 16-bit numbers (split2), which costs 1% of a call bound by its bytes,
+// 8% of one of many heads (64 of up to 4096, 32/2 heads of 64: 23.7 us against 21.9),
+// and keeps 15 bits and more of it instead of 8 (bf16) or 11 (f16).
+//
 // f32 caches: every operand is split into two tf32 halves and three products are
 // taken (what is left out is at most 5 * 2^-22 of a product, of either sign), and
 // each unit's P V is added to the running sum as an f32 addition of its own.
@@ -70,9 +75,9 @@ struct JoinShared {
 };
 
 // R: query heads of a head block, one MMA tile of 8, or two where a KV head of a
-// 16-bit cache has more than 8 (32/2 heads of 128, 64 requests of up to 4096: 35 us
-// against 40 with two blocks of 8, which read K and V twice, the second time for
-// the most part out of L2).  An f32 block of 16 would not fit the registers.
+// 16-bit cache has more than 8 (32/2 heads of 128, 64 requests of up to 4096, with one
+// MMA for the weights: 35 us against 40 with two blocks of 8, which read K and V twice,
+// the second time for the most part out of L2; with two MMAs 36).  An f32 block of 16 would not fit the registers.
 template <typename T, int HD, int R>
 struct Cfg {
   static constexpr bool kF32 = sizeof(T) == 4;
@@ -186,13 +191,36 @@ __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t* hi, uint32_t* l
   *lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(*hi));
 }
 
-__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
+// Two weights 0 <= a, b <= 1, each as the sum of an upper and a lower 16-bit number,
+// times kWeightScale.  The upper one is cut off below the weight, never equal to it,
+// so that the lower one is positive as well: an infinite value times the weight is
+// then infinite and never 0 * inf.
+//  bf16: the upper 16 bits of the f32 before the weight; what is left is at most
+//    2^-7 of the weight and rounded to 2^-8 of itself.  A weight of 0 counts as the
+//    least normal number, 2^-126.
+//  f16: weights are raised by 2^15, since f16 ends at 2^-24; the upper number is the
+//    weight less 2^-12 of it, cut off; what is left, at most 1.25 * 2^-10, is rounded
+//    to 2^-11 of itself, or to a step of 2^-24 (2^-39 of the largest weight), which it
+//    keeps if the weight has one.
+template <typename T>
+constexpr float kWeightScale = 1.f;
+template <>
+constexpr float kWeightScale<__half> = 32768.f;
+__device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t* lo, __nv_bfloat16) {
+  a = fmaxf(a, 0x1p-126f);
+  b = fmaxf(b, 0x1p-126f);
+  const uint32_t ua = (__float_as_uint(a) - 1) & 0xFFFF0000u, ub = (__float_as_uint(b) - 1) & 0xFFFF0000u;
+  const __nv_bfloat162 l = __floats2bfloat162_rn(a - __uint_as_float(ua), b - __uint_as_float(ub));
+  *hi = ua >> 16 | ub;
+  *lo = *reinterpret_cast<const uint32_t*>(&l);
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
+__device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t* lo, __half) {
+  constexpr float kS = kWeightScale<__half>, kBelow = kS * (1.f - 0x1p-12f);
+  asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(*hi) : "f"(b * kBelow), "f"(a * kBelow));
+  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(hi));
+  constexpr float kStep = 0x1.01p-25f;  // rounds to a step
+  const __half2 l = __floats2half2_rn(fmaxf(fmaf(a, kS, -h.x), fminf(a * kS, kStep)), fmaxf(fmaf(b, kS, -h.y), fminf(b * kS, kStep)));
+  *lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 __device__ __forceinline__ void store_as(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_as(__half* p, float x) { *p = __float2half_rn(x); }
@@ -658,15 +686,19 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
 
       // O^T = O^T c + V^T P^T
       if constexpr (!kF32) {
-        // The weights are rounded to the cache's type (half a step of it, against
-        // the result's own rounding of as much); 16-bit results can take the
-        // tensor core's truncating adds in place.
-        uint32_t p[NH][2];
+        // Two MMAs, on the upper and on the lower halves of the weights: what is
+        // lost of a weight, 2^-15 of it at most, lies far below the result's own
+        // rounding, and 16-bit results can take the tensor core's truncating adds
+        // in place.
+        uint32_t p[NH][2], pl[NH][2];
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          p[h][0] = transpose8(pack2(sc[h][0], sc[h][1], T()));
-          p[h][1] = transpose8(pack2(sc[h][2], sc[h][3], T()));
-        }
+        for (int h = 0; h < NH; ++h)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            split2(sc[h][2 * j], sc[h][2 * j + 1], &p[h][j], &pl[h][j], T());
+            p[h][j] = transpose8(p[h][j]);
+            pl[h][j] = transpose8(pl[h][j]);
+          }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
           for (int n = 0; n < kTiles; ++n)
@@ -682,7 +714,10 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
           uint32_t x[4];
           ldsm4t(x, vaddr + (((n * 2 + half) ^ (key & 7)) << 4));
 #pragma unroll
-          for (int h = 0; h < NH; ++h) mma(o[n][h], x, p[h][0], p[h][1], T());
+          for (int h = 0; h < NH; ++h) {
+            mma(o[n][h], x, p[h][0], p[h][1], T());
+            mma(o[n][h], x, pl[h][0], pl[h][1], T());
+          }
         }
       } else {
         // The weights change their layout through shared memory.  The MMA's k
@@ -790,7 +825,8 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
         for (int k = 0; k < kWarps; ++k) c[k] *= f;
         if (!seg_bad && a.lse) a.lse[(int64_t)r * a.nh + head0 + tid] = fmaf(mx, kLn2, logf(sum));
       }
-      m_w[tid] = make_float4(c[0], c[1], c[2], c[3]);
+      constexpr float kDown = 1.f / kWeightScale<T>;  // a power of two
+      m_w[tid] = make_float4(c[0] * kDown, c[1] * kDown, c[2] * kDown, c[3] * kDown);
     }
     __syncthreads();
     if (seg_bad && tid == 0) set_error(a.status, MINFER_ERR_POS_OOB);

@@ -1,0 +1,100 @@
+"""The batch operators on the GPU at their edges: values, sizes, layouts and
+refusals that the plain cases do not reach, against 64-bit definitions."""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+from test_gpu_batch import (BF16, F16, F32, U, attention_by_definition, attention_case, close, dev, gen, half, qp,  # noqa: E402, F401
+                            status_word)
+
+
+# ------------------------------------------------------------------ paged attention: the weights' bits
+def weight_tolerance(t, want, m, units):
+    """As attention_tolerance for the scores and sums, with what two 16-bit
+    numbers hold of a weight.  The upper one is at most p and leaves at most
+    2^-7 p (bf16, truncated) or 1.25 * 2^-10 p (f16); the lower one is rounded,
+    by half a step: 2^-15 p, or 1.25 * 2^-21 p and a step of f16's smallest numbers
+    under weights raised by 2^15, 2^-39.  A warp adds its `units` units with two MMAs each, whose sums of 17 terms are
+    truncated to 24 bits or more."""
+    o, lse, mean, size, top = want
+    hd = o.shape[-1]
+    score = size * ((hd // 8 + 2) * 2.0 ** -23 + 4 * U) + 8 * U
+    weight = 2.0 ** -15 if t == BF16 else 1.25 * 2.0 ** -21
+    rel = 2 * score + weight + (32 + 6 * math.log2(max(m, 2))) * U + 2 * units * 17 * 2.0 ** -23
+    return half(t) * o.abs() + rel * mean + (m * 2.0 ** -39 * top + 2.0 ** -25 if t == F16 else 0)
+
+
+@pytest.mark.parametrize("t", [F16, BF16])
+@pytest.mark.parametrize("m", [2, 33, 600])
+def test_paged_attention_weights_between_two_16_bit_numbers(qp, t, m):
+    """Every other key's weight lies between two neighbours of the cache's type,
+    and values of opposite sign leave little but what its rounding moves."""
+    nh, nkv, hd, P = 4, 2, 64, 16
+    q, k, v, table = attention_case(1, t, nh, nkv, hd, P, [m], poison=False)
+    q.zero_(), k.zero_()
+    q[:, ::hd] = 1.0
+    pages = table[0].long()
+    kk, vv = (torch.zeros(len(pages) * P, nkv, hd, device="cuda") for _ in range(2))
+    kk[1::2, :, 0] = -1.0
+    vv[0::2], vv[1::2] = 1.0, -1.0
+    k[pages], v[pages] = (x.view(-1, P, nkv, hd).to(t) for x in (kk, vv))
+    for scale in (2.0 ** -9, 2.0 ** -12, 0.7, 1.9):
+        o = qp.op_paged_attention(q, qp.PagedCache(k, v), table, dev([m]), nh, scale=scale)
+        want = attention_by_definition(q, k, v, table, [m], nh, scale)
+        close(o.view(1, nh, hd), want[0], weight_tolerance(t, want, m, 2))
+
+
+@pytest.mark.parametrize("t", [F16, BF16])
+@pytest.mark.parametrize("m", [70, 2000])
+@pytest.mark.parametrize("gap", [9.0, 14.0, 18.0, 21.0])
+@pytest.mark.parametrize("sink", [0, 40])
+def test_paged_attention_tail_beside_a_dominant_key(qp, t, m, gap, sink):
+    """One key holds nearly all of the weight and a value of zero: the result is the sum of the others' small weights."""
+    nh, nkv, hd, P = 14, 2, 64, 16
+    q, k, v, table = attention_case(2, t, nh, nkv, hd, P, [m], poison=False)
+    q.zero_()
+    q[:, ::hd] = 1.0
+    pages = table[0].long()
+    kk, vv = (x[pages].reshape(-1, nkv, hd).float() for x in (k, v))
+    kk[:, :, 0] = torch.rand(kk.shape[0], nkv, generator=gen(m), device="cuda")
+    kk[sink, :, 0] = gap + 1
+    vv = 1000 + 100 * vv
+    vv[sink] = 0
+    k[pages], v[pages] = (x.view(-1, P, nkv, hd).to(t) for x in (kk, vv))
+    lse = torch.empty(1, nh, device="cuda")
+    o = qp.op_paged_attention(q, qp.PagedCache(k, v), table, dev([m]), nh, scale=1.0, lse=lse)
+    want = attention_by_definition(q, k, v, table, [m], nh, 1.0)
+    close(o.view(1, nh, hd), want[0], weight_tolerance(t, want, m, 2))
+    # an infinity under a weight of either size is one
+    k2, v2 = k.clone(), v.clone()
+    v2[int(pages[1]), 3, :, 5], v2[int(pages[sink // P]), sink % P, :, 6] = math.inf, -math.inf
+    o2 = qp.op_paged_attention(q, qp.PagedCache(k2, v2), table, dev([m]), nh, scale=1.0).view(nh, hd)
+    assert (o2[:, 5] == math.inf).all() and (o2[:, 6] == -math.inf).all()
+    keep = [d for d in range(hd) if d not in (5, 6)]
+    assert torch.equal(o2[:, keep], o.view(nh, hd)[:, keep])
+
+
+@pytest.mark.parametrize("m", [131071])
+def test_paged_attention_long_request_with_large_results(qp, m):
+    """Values around 1, so that a part of the keys left out would show: the result stands far above its tolerance."""
+    nh, nkv, hd, P = 14, 2, 64, 64
+    q, k, v, table = attention_case(3, F16, nh, nkv, hd, P, [m])
+    q *= 0.5
+    v[table[0].long()] = (1 + 0.5 * v[table[0].long()].float()).to(F16)
+    v[int(table[0, -1]), m % P:] = math.nan
+    cache = qp.PagedCache(k, v)
+    work = qp.op_paged_attention_workspace(cache, 1, nh)
+    lse = torch.empty(1, nh, device="cuda")
+    o = qp.op_paged_attention(q, cache, table, dev([m]), nh, lse=lse, workspace=work)
+    want = attention_by_definition(q, k, v, table, [m], nh, 1 / 8)
+    tol = weight_tolerance(F16, want, m, 12)
+    assert float((tol / want[0].abs()).max()) < 2.0 ** -9
+    close(o.view(1, nh, hd), want[0], tol)
+    # counters of shares, of groups, of the second level: all back at zero
+    shares = 16 * 63
+    assert int(work.buffer[:4 * (2 * shares + shares // 16 + 1)].max()) == 0
+    assert torch.equal(o, qp.op_paged_attention(q, cache, table, dev([m]), nh, workspace=work))
