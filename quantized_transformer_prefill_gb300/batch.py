@@ -109,7 +109,9 @@ def op_page_tables(length, target, page_size: int, table, free, n_free, n_pages:
     holding `length` rows are to hold `target`.  int32 tensors; `table`
     [n_req][max_pages] and the stack `free` [n_pages] are updated in place.
     Returns (start [n_req + 1], pos [max_tokens], slot [max_tokens], n_free
-    [1]), or fills `out`, four such tensors; the last may be n_free itself."""
+    [1]), or fills `out`, four such tensors; the last may be n_free itself.
+    After a refused step the returned n_free is the old one, and that of `out`
+    is as it was."""
     dev = length.get_device()
     n = length.numel()
     if not (length.dtype is _I32 and length.is_contiguous()):
@@ -132,8 +134,9 @@ def op_page_tables(length, target, page_size: int, table, free, n_free, n_pages:
         with torch.cuda.device(dev):
             return op_page_tables(length, target, page_size, table, free, n_free, n_pages, max_tokens, out, status)
     if out is None:
-        out = tuple(torch.empty(m, dtype=_I32, device=length.device) for m in (n + 1, max_tokens, max_tokens, 1))
-        start, pos, slot, left = out
+        start, pos, slot = (torch.empty(m, dtype=_I32, device=length.device) for m in (n + 1, max_tokens, max_tokens))
+        left = n_free.reshape(1).clone()  # what a refused step leaves
+        out = start, pos, slot, left
     else:
         start, pos, slot, left = out
         if not (start.dtype is _I32 and start.numel() == n + 1 and start.is_contiguous() and start.get_device() == dev):

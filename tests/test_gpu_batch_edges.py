@@ -8,8 +8,8 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_batch import (BF16, F16, F32, U, attention_by_definition, attention_case, close, dev, gen, half, qp,  # noqa: E402, F401
-                            status_word)
+from test_gpu_batch import (BF16, F16, F32, I32, U, attention_by_definition, attention_case, close, dev, gen, half, qp,  # noqa: E402, F401
+                            status_word, tables_by_hand)
 
 
 # ------------------------------------------------------------------ paged attention: the weights' bits
@@ -98,3 +98,27 @@ def test_paged_attention_long_request_with_large_results(qp, m):
     shares = 16 * 63
     assert int(work.buffer[:4 * (2 * shares + shares // 16 + 1)].max()) == 0
     assert torch.equal(o, qp.op_paged_attention(q, cache, table, dev([m]), nh, workspace=work))
+
+
+# ------------------------------------------------------------------ refused steps
+def litter(value, dtype, sizes):
+    """Freed memory of these sizes that holds `value`: what a fresh tensor that nobody fills is likely to show."""
+    junk = [torch.full((n,), value, dtype=dtype, device="cuda") for n in sizes for _ in range(8)]
+    torch.cuda.synchronize()
+    del junk
+
+
+def test_a_refused_page_tables_step_returns_the_old_depth(qp):
+    """Without `out`, as a loop that rebinds n_free to what it gets: a step that finds too few pages, then one that fits."""
+    P, W, n_pages = 16, 4, 6
+    table, free, n_free = dev([[0, -1, -1, -1], [1, 2, -1, -1]]), dev([3, 4, 5, -1, -1, -1]), dev([3])
+    litter(2, I32, (1, 3, 80))
+    status = status_word()
+    start, pos, slot, n_free = qp.op_page_tables(dev([16, 32]), dev([64, 49]), P, table, free, n_free, n_pages, 80, status=status)
+    assert int(status) == -7 and n_free.tolist() == [3]
+    assert start.tolist() == [0, 0, 0] and set(pos.tolist()) == set(slot.tolist()) == {-1}
+    status.zero_()
+    got = qp.op_page_tables(dev([16, 32]), dev([17, 0]), P, table, free, n_free, n_pages, 80, status=status)
+    want = tables_by_hand([16, 32], [17, 0], P, [[0, -1, -1, -1], [1, 2, -1, -1]], [3, 4, 5, -1, -1, -1], 3, 80)
+    assert int(status) == 0
+    assert (table.tolist(), free.tolist(), int(got[3]), *(x.tolist() for x in got[:3])) == want
