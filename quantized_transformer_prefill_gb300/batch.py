@@ -222,7 +222,8 @@ def op_paged_attention(q, cache: PagedCache, table, length, n_head: int, scale: 
     (minfer_op_paged_attention): q [n_req][n_head*head_dim] in the cache's type,
     table int32 [n_req][max_pages], length int32 [n_req] rows to attend to, the
     new one included.  Returns o like q; `lse` (float32 [n_req][n_head]), when
-    given, gets ln sum exp(scale q.k)."""
+    given, gets ln sum exp(scale q.k).  Rows of refused requests are not written
+    (without `out` they are zero)."""
     dev, width = q.get_device(), n_head * cache.head_dim
     shape = q.shape
     if not (q.dtype is cache.dtype and len(shape) == 2 and shape[1] == width and dev == cache.index):
@@ -251,7 +252,7 @@ def op_paged_attention(q, cache: PagedCache, table, length, n_head: int, scale: 
         with torch.cuda.device(dev):
             return op_paged_attention(q, cache, table, length, n_head, scale, out, lse, workspace, status)
     if out is None:
-        out = torch.empty((n, width), dtype=q.dtype, device=q.device)
+        out = torch.zeros((n, width), dtype=q.dtype, device=q.device)
         o_stride = width
     else:
         if not (out.dtype is cache.dtype and out.shape == shape and out.get_device() == dev):
@@ -289,7 +290,8 @@ def op_token_logprobs(logits, ids=None, k: int = 0, out=None, workspace: Workspa
     (minfer_op_token_logprobs).  Returns (logprob, entropy, top_ids,
     top_logprobs), or fills `out`, four such tensors (logprob without ids,
     entropy, and the last two with k = 0 may be None); logprob is None without
-    ids."""
+    ids.  Skipped and refused rows are not written (without `out` they are zero,
+    with top_ids of -1)."""
     dev, shape = logits.get_device(), logits.shape
     if len(shape) != 2:
         _refuse("logits: [rows][vocab] wanted", logits)
@@ -310,9 +312,15 @@ def op_token_logprobs(logits, ids=None, k: int = 0, out=None, workspace: Workspa
         with torch.cuda.device(dev):
             return op_token_logprobs(logits, ids, k, out, workspace, status)
     if out is None:
-        new = lambda shape, t: torch.empty(shape, dtype=t, device=logits.device)  # noqa: E731
-        out = (None if ids is None else new(rows, _F32), new(rows, _F32), new((rows, k), _I32), new((rows, k), _F32))
-        logprob, entropy, top_ids, top_logprobs = out
+        if ids is None:  # every row is written
+            logprob, new = None, torch.empty(rows * (1 + k), dtype=_F32, device=logits.device)
+            top_ids = torch.empty((rows, k), dtype=_I32, device=logits.device)
+        else:
+            new = torch.zeros(rows * (2 + k), dtype=_F32, device=logits.device)
+            top_ids = torch.full((rows, k), -1, dtype=_I32, device=logits.device)
+            logprob, new = new[:rows], new[rows:]
+        entropy, top_logprobs = new[:rows], new[rows:].view(rows, k)
+        out = logprob, entropy, top_ids, top_logprobs
     else:
         logprob, entropy, top_ids, top_logprobs = out
         if logprob is not None and not (logprob.dtype is _F32 and logprob.numel() == rows and logprob.is_contiguous()

@@ -122,3 +122,30 @@ def test_a_refused_page_tables_step_returns_the_old_depth(qp):
     want = tables_by_hand([16, 32], [17, 0], P, [[0, -1, -1, -1], [1, 2, -1, -1]], [3, 4, 5, -1, -1, -1], 3, 80)
     assert int(status) == 0
     assert (table.tolist(), free.tolist(), int(got[3]), *(x.tolist() for x in got[:3])) == want
+
+
+def test_fresh_outputs_of_skipped_rows(qp):
+    """Without `out`, rows that are not written are zero (token ids -1), so sums over a padded batch hold."""
+    x, k = torch.randn(6, 500, device="cuda"), 4
+    for t in (F32, I32):
+        litter(9, t, (6, 24, 36))
+    status = status_word()
+    logprob, entropy, top_ids, top_logprobs = qp.op_token_logprobs(x, dev([3, -1, 500, 7, -5, 499]), k, status=status)
+    assert int(status) == -3
+    skipped, live = [1, 2, 4], [0, 3, 5]
+    assert (logprob[skipped] == 0).all() and (entropy[skipped] == 0).all()
+    assert (top_ids[skipped] == -1).all() and (top_logprobs[skipped] == 0).all()
+    for got, want in zip((logprob, entropy, top_ids, top_logprobs), qp.op_token_logprobs(x[live], dev([3, 7, 499]), k)):
+        assert torch.equal(got[live], want)
+    none, entropy0, top_ids0, top_logprobs0 = qp.op_token_logprobs(x, None, k)
+    assert none is None and torch.equal(top_ids0[live], top_ids[live]) and torch.equal(top_logprobs0[live], top_logprobs[live])
+    assert torch.equal(entropy0[live], entropy[live]) and qp.op_token_logprobs(x, dev([1] * 6), 0)[2].shape == (6, 0)
+    nh, nkv, hd, length = 4, 2, 64, [30, 40, 0]
+    for t in (F32, F16, BF16):
+        q, kk, v, table = attention_case(7, t, nh, nkv, hd, 16, length)
+        cache = qp.PagedCache(kk, v)
+        table[1, 1] = -1
+        litter(9, t, (3 * nh * hd,))
+        status.zero_()
+        o = qp.op_paged_attention(q, cache, table, dev(length), nh, status=status)
+        assert int(status) == -2 and (o[1:] == 0).all() and (o[0] != 0).any()
