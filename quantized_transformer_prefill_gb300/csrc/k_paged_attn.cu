@@ -191,25 +191,28 @@ __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t* hi, uint32_t* l
   *lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(*hi));
 }
 
-// Two weights 0 <= a, b <= 1, each as the sum of an upper and a lower 16-bit number,
-// times kWeightScale.  The upper one is cut off below the weight, never equal to it,
-// so that the lower one is positive as well: an infinite value times the weight is
-// then infinite and never 0 * inf.
-//  bf16: the upper 16 bits of the f32 before the weight; what is left is at most
-//    2^-7 of the weight and rounded to 2^-8 of itself.  A weight of 0 counts as the
-//    least normal number, 2^-126.
-//  f16: weights are raised by 2^15, since f16 ends at 2^-24; the upper number is the
-//    weight less 2^-12 of it, cut off; what is left, at most 1.25 * 2^-10, is rounded
-//    to 2^-11 of itself, or to a step of 2^-24 (2^-39 of the largest weight), which it
-//    keeps if the weight has one.
+// Weights, at most 1, go into the sums of values times this, and results are divided by
+// it: 2^31 keys of the largest finite f32 or bf16 value do not overflow (a warp's sum,
+// under its own maximum, may be one of keys that weigh nothing in the end), and f16
+// weights stand well above 2^-24, where f16 ends.
 template <typename T>
-constexpr float kWeightScale = 1.f;
+constexpr float kWeightScale = 0x1p-31f;
 template <>
-constexpr float kWeightScale<__half> = 32768.f;
+constexpr float kWeightScale<__half> = 0x1p15f;
+
+// Two weights, each times kWeightScale the sum of an upper and a lower 16-bit number.
+// The upper one is cut off below the weight, equal to it only for a weight of 0, so
+// that the lower one is positive as well: an infinite value times the weight is then
+// infinite and not 0 * inf.
+//  bf16: the upper 16 bits of the f32 before the weight; what is left is at most
+//    2^-7 of the weight and rounded to 2^-8 of itself.
+//  f16: the upper number is the weight less 2^-12 of it, cut off; what is left, at
+//    most 1.25 * 2^-10, is rounded to 2^-11 of itself, or to a step of 2^-24 (2^-39 of
+//    the largest weight), which it keeps if the weight has one.
 __device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t* lo, __nv_bfloat16) {
-  a = fmaxf(a, 0x1p-126f);
-  b = fmaxf(b, 0x1p-126f);
-  const uint32_t ua = (__float_as_uint(a) - 1) & 0xFFFF0000u, ub = (__float_as_uint(b) - 1) & 0xFFFF0000u;
+  a *= kWeightScale<__nv_bfloat16>;
+  b *= kWeightScale<__nv_bfloat16>;
+  const uint32_t ua = (max(__float_as_uint(a), 1u) - 1) & 0xFFFF0000u, ub = (max(__float_as_uint(b), 1u) - 1) & 0xFFFF0000u;
   const __nv_bfloat162 l = __floats2bfloat162_rn(a - __uint_as_float(ua), b - __uint_as_float(ub));
   *hi = ua >> 16 | ub;
   *lo = *reinterpret_cast<const uint32_t*>(&l);
@@ -362,7 +365,7 @@ __device__ void join_parts(JoinShared<R>& s, unsigned char* ring, int ring_bytes
     if (!final) {
       reinterpret_cast<float4*>(s.part[0] + 2 * R)[i] = acc[k];
     } else if (!bad) {
-      const float l = s.out[i / (HD / 4)].y, f = l == 0.f ? 0.f : 1.f / l;
+      const float l = s.out[i / (HD / 4)].y, f = l == 0.f ? 0.f : 1.f / (l * kWeightScale<T>);
       T* dst = o + i * 4;
       store_as(dst, acc[k].x * f);
       store_as(dst + 1, acc[k].y * f);
@@ -727,7 +730,8 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
         for (int h = 0; h < NH; ++h)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            *reinterpret_cast<float2*>(pbuf + (g4 + 8 * j) * R + 8 * h + 2 * t4) = make_float2(sc[h][2 * j], sc[h][2 * j + 1]);
+            *reinterpret_cast<float2*>(pbuf + (g4 + 8 * j) * R + 8 * h + 2 * t4) =
+                make_float2(sc[h][2 * j] * kWeightScale<T>, sc[h][2 * j + 1] * kWeightScale<T>);
         __syncwarp();
         uint32_t ph[NH][2][2], pl[NH][2][2];
 #pragma unroll
@@ -820,13 +824,12 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
       if (!whole) {
         reinterpret_cast<float2*>(part)[tid] = make_float2(mx, seg_bad ? -1.f : sum);
       } else {
-        const float f = sum == 0.f ? 0.f : 1.f / sum;
+        const float f = sum == 0.f ? 0.f : 1.f / (sum * kWeightScale<T>);
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) c[k] *= f;
         if (!seg_bad && a.lse) a.lse[(int64_t)r * a.nh + head0 + tid] = fmaf(mx, kLn2, logf(sum));
       }
-      constexpr float kDown = 1.f / kWeightScale<T>;  // a power of two
-      m_w[tid] = make_float4(c[0] * kDown, c[1] * kDown, c[2] * kDown, c[3] * kDown);
+      m_w[tid] = make_float4(c[0], c[1], c[2], c[3]);
     }
     __syncthreads();
     if (seg_bad && tid == 0) set_error(a.status, MINFER_ERR_POS_OOB);

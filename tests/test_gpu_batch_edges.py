@@ -78,6 +78,20 @@ def test_paged_attention_tail_beside_a_dominant_key(qp, t, m, gap, sink):
     assert torch.equal(o2[:, keep], o.view(nh, hd)[:, keep])
 
 
+@pytest.mark.parametrize("t", [F32, F16, BF16])
+def test_paged_attention_weights_of_zero(qp, t):
+    """Keys a thousand below the largest score weigh nothing, however large their values."""
+    nh, nkv, hd, P, m = 4, 2, 64, 16, 50
+    q, k, v, table = attention_case(4, t, nh, nkv, hd, P, [m], poison=False)
+    q.zero_(), k.zero_()
+    q[:, ::hd] = 1.0
+    v[:] = torch.finfo(t).max / 2
+    k[int(table[0, 1]), 2, :, 0] = 1000
+    v[int(table[0, 1]), 2] = 0.25
+    o = qp.op_paged_attention(q, qp.PagedCache(k, v), table, dev([m]), nh, scale=1.0)
+    assert (o == 0.25).all()
+
+
 @pytest.mark.parametrize("m", [131071])
 def test_paged_attention_long_request_with_large_results(qp, m):
     """Values around 1, so that a part of the keys left out would show: the result stands far above its tolerance."""
