@@ -499,8 +499,8 @@ int minfer_op_paged_attention_workspace(int n_req, int n_head, const minfer_page
  * its bits.  Scores, softmax statistics and sums are f32; with a 16-bit cache
  * each softmax weight is held in two numbers of its type for the product with V
  * (to 2^-15 of it; f16: to 2^-20, or 2^-39 of the largest so far), and with
- * an f32 cache the products are those of tf32 halves (an infinity among the K and
- * V values that a request sees makes its result NaN there).  The
+ * an f32 cache the products are those of tf32 halves.  Scores of -inf weigh
+ * nothing; a request of which every score is -inf gets zeros and -inf.  The
  * result of a call depends on its inputs alone, bit for bit on one device
  * type.  Device errors: MINFER_ERR_POS_OOB for a length outside
  * 0..max_pages*page_size or a page id outside the pool (that request's row of

@@ -87,8 +87,8 @@ struct Cfg {
   // As many CTAs per SM as their registers and two stages of the ring allow; the
   // ring takes what is left of the SM's shared memory.  Rows of 512 bytes (f32,
   // head size 128) have CTAs of two warps: three of them hold 6 warps where one
-  // CTA of four would fit (64 requests of up to 1024, 16/8 heads: 60 us against
-  // 72; 4 of up to 2048, 12/2 heads: 13 against 11, for its shares are smaller).
+  // CTA of four would fit (64 requests of up to 1024, 16/8 heads: a sixth less time,
+  // 63 us now; 4 of up to 2048, 12/2 heads: 13 against 11, for its shares are smaller).
   static constexpr int kWarps = kRowBytes == 512 ? 2 : 4;
   static constexpr int kCtas = kRowBytes == 128 ? 4 : R == 8 ? 3 : 2;
   static constexpr int kUnit = kWarps * kKeys;  // keys of a unit
@@ -183,11 +183,14 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 }
 // x = hi + lo: hi is x rounded to tf32 (11 significant bits), ties away from
 // zero, in integer arithmetic (the conversion instruction has a quarter of its
-// rate); lo = x - hi is exact and at most 2^-11 |x|, and the MMA takes its upper
-// 11 bits, which leaves out less than 2^-21 |x|.  (A NaN may lose its bits in hi;
-// lo keeps it.)
+// rate), and at most the largest finite tf32 in size, to which the topmost f32 values
+// and infinities are cut; lo = x - hi is exact and at most 2^-11 |x| (of the topmost
+// values 2^-11 and a step), and the MMA takes its upper 11 bits, which leaves out less
+// than 2^-21 |x|.  An infinity or a NaN lies in lo.  (The cut costs 2% of a call of
+// ordinary length and 4% of 64 x 1024, 16/8 heads of 128.)
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t* hi, uint32_t* lo) {
-  *hi = (x + 0x1000u) & 0xFFFFE000u;
+  const uint32_t near = (x + 0x1000u) & 0xFFFFE000u;
+  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=r"(*hi) : "r"(near), "r"(0x7F7FE000u));
   *lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(*hi));
 }
 
@@ -503,7 +506,7 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
     const bool ok = (unsigned)page_next < (unsigned)a.c.n_pages;
     const uint32_t kdst = ring + stage * C::kStageBytes, vdst = kdst + kKeys * C::kRowBytes;
     if (one_page) {
-      // (no shuffles of addresses: f32 rows of 128 60 us against 64, 16-bit rows 1%)
+      // (no shuffles of addresses: f32 rows of 128 6% less time, 16-bit rows 1%)
       const int in_page = key0 - a.c.div.of(key0) * P;
       const int live = ok ? lw.len - key0 : 0;
       int64_t off = 0;

@@ -19,11 +19,12 @@ def weight_tolerance(t, want, m, units):
     2^-7 p (bf16, truncated) or 1.25 * 2^-10 p (f16); the lower one is rounded,
     by half a step: 2^-15 p, or 1.25 * 2^-21 p and a step of f16's smallest numbers
     under weights raised by 2^15, 2^-39.  A warp adds its `units` units with two MMAs each, whose sums of 17 terms are
-    truncated to 24 bits or more."""
+    truncated to 24 bits or more.  f32: the halves' 20 U, in scores and weights."""
     o, lse, mean, size, top = want
     hd = o.shape[-1]
-    score = size * ((hd // 8 + 2) * 2.0 ** -23 + 4 * U) + 8 * U
-    weight = 2.0 ** -15 if t == BF16 else 1.25 * 2.0 ** -21
+    split = 20 * U if t == F32 else 0
+    score = size * ((hd // 8 + 2) * 2.0 ** -23 + split + 4 * U) + 8 * U
+    weight = {BF16: 2.0 ** -15, F16: 1.25 * 2.0 ** -21, F32: 20 * U}[t]
     rel = 2 * score + weight + (32 + 6 * math.log2(max(m, 2))) * U + 2 * units * 17 * 2.0 ** -23
     return half(t) * o.abs() + rel * mean + (m * 2.0 ** -39 * top + 2.0 ** -25 if t == F16 else 0)
 
@@ -90,6 +91,85 @@ def test_paged_attention_weights_of_zero(qp, t):
     v[int(table[0, 1]), 2] = 0.25
     o = qp.op_paged_attention(q, qp.PagedCache(k, v), table, dev([m]), nh, scale=1.0)
     assert (o == 0.25).all()
+
+
+@pytest.mark.parametrize("t", [F32, F16, BF16])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_paged_attention_largest_values(qp, t, sign):
+    """Values, and keys and queries, at and next to the largest finite one of the type, weights from 1 to small ones."""
+    nh, nkv, hd, P, m = 4, 2, 64, 16, 90
+    top = torch.finfo(t).max
+    q, k, v, table = attention_case(4, t, nh, nkv, hd, P, [m])
+    v[table[0].long()] = sign * top
+    v[int(table[0, 2]), 5] = sign * top * (1 - torch.finfo(t).eps)
+    v[int(table[0, -1]), m % P:] = math.nan
+    o = qp.op_paged_attention(q, qp.PagedCache(k, v), table, dev([m]), nh).view(nh, hd)
+    # a mean of equal numbers: their roundings, and the last one may reach the type's infinity
+    assert ((o.double() * sign >= top * (1 - 2.0 ** -7)) & ((o * sign).float() > 0)).all() and not o.isnan().any()
+    # one key of the largest size in a dim where the query is tiny: scores stay ordinary
+    q, k, v, table = attention_case(5, t, nh, nkv, hd, P, [m])
+    q[:, ::hd] = float(torch.finfo(t).tiny)
+    k[int(table[0, 1]), 7, :, 0] = sign * top
+    o = qp.op_paged_attention(q, qp.PagedCache(k, v), table, dev([m]), nh)
+    want = attention_by_definition(q, k, v, table, [m], nh, 1 / 8)
+    close(o.view(1, nh, hd), want[0], weight_tolerance(t, want, m, 2))
+    # the same size in the query
+    q, k, v, table = attention_case(6, t, nh, nkv, hd, P, [m], poison=False)
+    k[..., 0] = 0
+    k[int(table[0, 1]), 7, :, 0] = float(torch.finfo(t).tiny)
+    q[:, ::hd] = sign * top
+    o = qp.op_paged_attention(q, qp.PagedCache(k, v), table, dev([m]), nh)
+    want = attention_by_definition(q, k, v, table, [m], nh, 1 / 8)
+    close(o.view(1, nh, hd), want[0], weight_tolerance(t, want, m, 2))
+
+
+@pytest.mark.parametrize("t", [F32, F16, BF16])
+def test_paged_attention_infinite_keys_and_values(qp, t):
+    """A score of -inf weighs nothing: the result is that without the key.  A value of +-inf that weighs something makes
+    its dim infinite, and nothing else.  A request of which every score is -inf has zeros and an lse of -inf."""
+    nh, nkv, hd, P, m = 4, 2, 64, 16, 100
+    q, k, v, table = attention_case(6, t, nh, nkv, hd, P, [m, m], poison=False)
+    q[:, ::hd] = 1.0
+    drop = [0, 17, 18, 60, 99]
+    keep = [j for j in range(m) if j not in drop]
+    k2, v2 = torch.zeros_like(k), torch.zeros_like(v)
+    n = -(-len(keep) // P)
+    for x, x2 in ((k, k2), (v, v2)):
+        rows = x[table[0].long()].reshape(-1, nkv, hd)[keep]
+        x2[table[0, :n].long()] = torch.cat([rows, rows.new_zeros(n * P - len(keep), nkv, hd)]).view(n, P, nkv, hd)
+    want = attention_by_definition(q[:1], k2, v2, table[:1, :n], [len(keep)], nh, 1 / 8)
+    for j in drop:
+        k[int(table[0, j // P]), j % P, :, 0] = -math.inf
+    lse = torch.empty(2, nh, device="cuda")
+    cache = qp.PagedCache(k, v)
+    o = qp.op_paged_attention(q, cache, table, dev([m, m]), nh, lse=lse)
+    close(o[:1].view(1, nh, hd), want[0], weight_tolerance(t, want, m, 2))
+    v[int(table[0, 3]), 4, :, 5], v[int(table[0, 2]), 4, :, 9] = math.inf, -math.inf
+    o2 = qp.op_paged_attention(q, cache, table, dev([m, m]), nh).view(2, nh, hd)
+    assert (o2[0, :, 5] == math.inf).all() and (o2[0, :, 9] == -math.inf).all()
+    o2[0, :, [5, 9]] = o.view(2, nh, hd)[0, :, [5, 9]]
+    assert torch.equal(o2.view(2, -1), o)
+    k[table[0].long(), :, :, 0] = -math.inf
+    v[table[0].long()] = 1.0
+    o3 = qp.op_paged_attention(q, cache, table, dev([m, m]), nh, lse=lse)
+    assert (o3[0] == 0).all() and (lse[0] == -math.inf).all() and torch.equal(o3[1], o[1])
+
+
+@pytest.mark.parametrize("t", [F32, F16, BF16])
+@pytest.mark.parametrize("m", [1500, 33])
+def test_paged_attention_rising_and_falling_scores(qp, t, m):
+    """Scores that rise along the request by 60 in all, or fall: the first, or last, keys' weights vanish."""
+    nh, nkv, hd, P = 7, 1, 64, 16
+    for lo, hi in ((-30.0, 30.0), (30.0, -30.0)):
+        q, k, v, table = attention_case(5, t, nh, nkv, hd, P, [m], poison=False)
+        q.zero_()
+        q[:, ::hd] = 1.0
+        k[table[0].long(), :, 0, 0] = torch.linspace(lo, hi, table.shape[1] * P, device="cuda").view(-1, P).to(t)
+        lse = torch.empty(1, nh, device="cuda")
+        o = qp.op_paged_attention(q, qp.PagedCache(k, v), table, dev([m]), nh, scale=1.0, lse=lse)
+        want = attention_by_definition(q, k, v, table, [m], nh, 1.0)
+        close(o.view(1, nh, hd), want[0], weight_tolerance(t, want, m, 2))
+        close(lse, want[1], 2 * want[3][..., 0] * (10 * 2.0 ** -23 + 24 * U) + 2.0 ** -18)
 
 
 @pytest.mark.parametrize("m", [131071])
