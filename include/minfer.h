@@ -449,7 +449,10 @@ int minfer_rope_prepare(const minfer_rope_spec* spec, minfer_rope_table* out);
  * 0..max_pages*page_size; MINFER_ERR_TOO_LARGE: more than max_tokens new
  * tokens; MINFER_ERR_OOM: too few free pages; MINFER_ERR_ARG: a page id in use
  * or a depth out of range) table, stack and *d_n_free_out stay as they were,
- * and the step has no token: d_start is 0 and d_pos, d_slot are -1.
+ * and the step has no token: d_start is 0 and d_pos, d_slot are -1.  Entries of a
+ * request's table behind its pages may name pages of other requests, so after a
+ * refused step nothing may read up to d_target: the rows that a request holds in
+ * either case are min(target, len + start[r+1] - start[r]).
  * n_req <= 16384; n_req*max_pages, max_pages*page_size and n_pages*page_size
  * fit 31 bits (MINFER_ERR_TOO_LARGE otherwise). */
 int minfer_op_page_tables(const int32_t* d_len, const int32_t* d_target, int n_req, int page_size,

@@ -1,6 +1,8 @@
 """The batch operators on the GPU at their edges: values, sizes, layouts and
 refusals that the plain cases do not reach, against 64-bit definitions."""
 import math
+import os
+import re
 
 import pytest
 
@@ -243,3 +245,46 @@ def test_fresh_outputs_of_skipped_rows(qp):
         status.zero_()
         o = qp.op_paged_attention(q, cache, table, dev(length), nh, status=status)
         assert int(status) == -2 and (o[1:] == 0).all() and (o[0] != 0).any()
+
+
+def readme_step():
+    """The README's step of a batch, from its page tables on."""
+    text = open(os.path.join(os.path.dirname(__file__), "..", "README.md")).read()
+    block = next(b for b in re.findall(r"```python\n(.*?)```", text, re.S) if "op_page_tables" in b)
+    return block[block.index("start, pos, slot"):]
+
+
+@pytest.mark.parametrize("refused", [False, True])
+def test_the_readmes_step(qp, refused):
+    """A request is rolled back and its page goes to another one; then it is to grow again, and the other one too, which
+    is done, or refused for want of a page.  Attention sees each request's own rows in both cases."""
+    nh, nkv, hd, P, V = 4, 2, 64, 16, 300
+    n_pages = 3 if refused else 6
+    cache = qp.PagedCache(*(torch.full((n_pages, P, nkv, hd), math.nan, device="cuda") for _ in range(2)))
+    s = dict(qp=qp, torch=torch, cache=cache, rope=qp.RopeTable(head_dim=hd, theta=1e4), page_size=P, n_pages=n_pages, n_head=nh, bias=None,
+             table=torch.full((2, 4), -1, dtype=I32, device="cuda"), free=torch.arange(n_pages, dtype=I32, device="cuda"), n_free=dev([n_pages]),
+             logits=torch.randn(2, V, device="cuda"), ids=dev([5, 7]), max_tokens=44)
+    g = gen(1)
+    have, keys = [0, 0], [[], []]  # the K and V rows of each request, by the positions and slots of its steps
+    for want, ok in (([20, 12], True), ([10, 12], True), ([11, 22], True), ([27, 38], not refused)):
+        s.update(length=dev(have), target=dev(want), status=status_word(), qkv=torch.randn(44, (nh + 2 * nkv) * hd, generator=g, device="cuda"))
+        exec(readme_step().replace("qp.check_status(status)", ""), s)
+        assert int(s["status"]) == (0 if ok else -7)
+        if ok:
+            at = 0
+            for r in range(2):
+                new = max(0, want[r] - have[r])
+                slots = s["slot"][at:at + new].long()
+                at += new
+                # the step's rows, from the cache as the store left them
+                rows = torch.stack([x[slots // P, slots % P] for x in (cache.k, cache.v)], 1)
+                keys[r] = torch.cat([keys[r][:min(have[r], want[r])], rows]) if len(keys[r]) else rows
+            have = want
+        held = [min(a, b) for a, b in zip(have, want)]
+        for r in range(2):
+            k, v = keys[r][:held[r]].unbind(1)
+            n = -(-held[r] // P)
+            k, v = (torch.cat([x, x.new_zeros(n * P - held[r], nkv, hd)]).view(n, P, nkv, hd) for x in (k, v))
+            tb = torch.arange(n, dtype=I32, device="cuda")[None]
+            o = attention_by_definition(s["newest"][r:r + 1], k, v, tb, [held[r]], nh, 1 / 8)
+            close(s["o"][r:r + 1].view(1, nh, hd), o[0], weight_tolerance(F32, o, held[r], 2))
