@@ -381,7 +381,9 @@ int minfer_op_gemm_noalloc(const int8_t* d_xq, const uint16_t* d_xd, int64_t M,
  *    MINFER_ERR_* code in *d_status (int, never cleared by the library; may be
  *    NULL) and what the error belongs to (a request, a token's row) is not
  *    written.
- *  - Types: MINFER_F32, MINFER_F16, MINFER_BF16.  Strides count elements. */
+ *  - Types: MINFER_F32, MINFER_F16, MINFER_BF16.  Strides count elements.
+ *    n_req, n_tokens and rows are at least 1 (MINFER_ERR_ARG otherwise): a step
+ *    without any makes no call. */
 
 /* A pool of n_pages pages of page_size K/V rows each; row s of page p, head h
  * starts at p*page_stride + s*row_stride + h*head_stride in both k and v, its

@@ -5,7 +5,8 @@ The calls enqueue on the current stream of the tensors' device, wait for
 nothing, and can be captured into a CUDA graph.  `out`, `lse`, `workspace` and
 the like may be given, so that a loop allocates nothing; `status` is an int32
 tensor of one element in which the kernels leave the first error code they find
-(check_status reads it).
+(check_status reads it).  A step without rows (no requests, no tokens) is done
+without a kernel.
 
 A small call takes less time on the GPU than its arguments take to be checked
 in Python, so the checks are written out, with the attributes that are cheapest
@@ -147,6 +148,9 @@ def op_page_tables(length, target, page_size: int, table, free, n_free, n_pages:
             _refuse("slot: int32 [max_tokens] wanted", slot)
         if not (left.dtype is _I32 and left.numel() == 1 and left.get_device() == dev):
             _refuse("n_free of out: int32 [1] wanted", left)
+    if n == 0:
+        start.zero_(), pos.fill_(-1), slot.fill_(-1), left.reshape(1).copy_(n_free.reshape(1))
+        return out
     rc = _page_tables(length.data_ptr(), target.data_ptr(), n, page_size, n_pages, table.data_ptr(), shape[1],
                       free.data_ptr(), n_free.data_ptr(), left.data_ptr(), start.data_ptr(), pos.data_ptr(),
                       slot.data_ptr(), max_tokens, None if status is None else status.data_ptr(), _stream_of(dev))
@@ -197,6 +201,8 @@ def op_rope_paged_store(qkv, rope: RopeTable, pos, slot, cache: PagedCache, n_he
         q_stride, one = out.stride()
         if one != 1:
             _refuse("out: contiguous rows wanted", out)
+    if n == 0:
+        return out
     rc = _rope_paged_store(qkv.data_ptr(), _type_of(qkv, "qkv"), row_stride, None if bias is None else bias.data_ptr(),
                            None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
                            eps, rope.ptr, pos.data_ptr(), slot.data_ptr(), n, n_head, cache.ptr, out.data_ptr(), q_stride,
@@ -260,6 +266,8 @@ def op_paged_attention(q, cache: PagedCache, table, length, n_head: int, scale: 
         o_stride, one = out.stride()
         if one != 1:
             _refuse("out: contiguous rows wanted", out)
+    if n == 0:
+        return out
     if workspace is None:
         workspace = op_paged_attention_workspace(cache, n, n_head)
     elif workspace.index != dev:
@@ -336,6 +344,8 @@ def op_token_logprobs(logits, ids=None, k: int = 0, out=None, workspace: Workspa
             if top_logprobs is None or not (top_logprobs.dtype is _F32 and top_logprobs.shape == (rows, k)
                                             and top_logprobs.is_contiguous() and top_logprobs.get_device() == dev):
                 _refuse("top_logprobs: float32 [rows][k] wanted", top_logprobs)
+    if rows == 0:
+        return out
     if workspace is None:
         workspace = op_token_logprobs_workspace(logits, k)
     elif workspace.index != dev:

@@ -288,3 +288,19 @@ def test_the_readmes_step(qp, refused):
             tb = torch.arange(n, dtype=I32, device="cuda")[None]
             o = attention_by_definition(s["newest"][r:r + 1], k, v, tb, [held[r]], nh, 1 / 8)
             close(s["o"][r:r + 1].view(1, nh, hd), o[0], weight_tolerance(F32, o, held[r], 2))
+
+
+def test_a_step_without_rows(qp):
+    """No requests, no tokens, no logits rows: empty results of the right shapes, and outputs that are set as a step without tokens sets them."""
+    nh, nkv, hd, P = 4, 2, 64, 16
+    cache = qp.PagedCache(torch.zeros(3, P, nkv, hd, device="cuda"), torch.zeros(3, P, nkv, hd, device="cuda"))
+    none, free, n_free = dev([]), dev([2, 1, 0]), dev([3])
+    for out in (None, tuple(torch.full((m,), 9, dtype=I32, device="cuda") for m in (1, 5, 5, 1)), (dev([9]), dev([9] * 5), dev([9] * 5), n_free)):
+        start, pos, slot, left = qp.op_page_tables(none, none, P, none.view(0, 4), free, n_free, 3, 5, out=out)
+        assert (start.tolist(), pos.tolist(), slot.tolist(), left.tolist(), free.tolist()) == ([0], [-1] * 5, [-1] * 5, [3], [2, 1, 0])
+    q = qp.op_rope_paged_store(torch.zeros(0, (nh + 2 * nkv) * hd, device="cuda"), qp.RopeTable(hd), none, none, cache, nh)
+    assert q.shape == (0, nh * hd) and q.dtype == F32
+    assert qp.op_paged_attention(q, cache, none.view(0, 4), none, nh, lse=torch.zeros(0, nh, device="cuda")).shape == q.shape
+    logprob, entropy, top_ids, top_logprobs = qp.op_token_logprobs(torch.zeros(0, 50, device="cuda"), none, 3)
+    assert logprob.shape == entropy.shape == (0,) and top_ids.shape == top_logprobs.shape == (0, 3)
+    assert qp.op_token_logprobs(torch.zeros(0, 50, device="cuda"))[0] is None
