@@ -388,7 +388,8 @@ int minfer_op_gemm_noalloc(const int8_t* d_xq, const uint16_t* d_xd, int64_t M,
 /* A pool of n_pages pages of page_size K/V rows each; row s of page p, head h
  * starts at p*page_stride + s*row_stride + h*head_stride in both k and v, its
  * head_dim values are contiguous.  Slot p*page_size + s names row s of page p.
- * k and v are 16-byte aligned and so is every stride; head_dim is 64 or 128. */
+ * k and v are 16-byte aligned and so is every stride (here and below: of which
+ * there is more than one thing to step over); head_dim is 64 or 128. */
 typedef struct minfer_paged_cache {
   void* k;
   void* v;

@@ -55,11 +55,12 @@ def _type_of(t, what: str) -> int:
 class PagedCache:
     """A pool of K/V pages: k and v [n_pages, page_size, n_head_kv, head_dim], of
     one type and with the same strides (a permuted view whose last dimension is
-    contiguous will do, e.g. of [n_pages, n_head_kv, page_size, head_dim])."""
+    contiguous will do, e.g. of [n_pages, n_head_kv, page_size, head_dim]; the
+    stride of a dimension of one does not matter)."""
 
     def __init__(self, k, v):
         if not (k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.device == v.device
-                and k.stride() == v.stride() and k.stride(3) == 1):
+                and all(a == b for a, b, n in zip(k.stride(), v.stride(), k.shape) if n > 1) and k.stride(3) == 1):
             _refuse("PagedCache: k and v differ, or are not [pages][rows][heads][dims] with contiguous dims", k, v)
         self.k, self.v = k, v
         self.dtype, self.device, self.index = k.dtype, k.device, k.get_device()

@@ -17,8 +17,9 @@ constexpr int kMaxHeads = 65535;  // a row of heads is indexed with 32 bits
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool type_ok(int t) { return t == MINFER_F32 || t == MINFER_F16 || t == MINFER_BF16; }
 int type_size(int t) { return t == MINFER_F32 ? 4 : 2; }
-// a stride of `n` elements keeps 16-byte alignment
-bool stride_ok(int64_t n, int t) { return (n * type_size(t)) % 16 == 0; }
+// a stride of `n` elements between `count` things, which must keep 16-byte alignment if
+// there is more than one
+bool stride_ok(int64_t n, int64_t count, int t) { return count == 1 || (n >= 0 && (n * type_size(t)) % 16 == 0); }
 bool fits31(int64_t a, int64_t b) { return a * b <= INT_MAX; }  // a, b <= INT_MAX each
 
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? MINFER_OK : MINFER_ERR_CUDA; }
@@ -41,13 +42,14 @@ int check_cache(const minfer_paged_cache* c, PagedCache* out) {
   if (!c || !c->k || !c->v || c->n_pages <= 0 || c->page_size <= 0 || c->n_head_kv <= 0)
     return MINFER_ERR_ARG;
   if (!type_ok(c->type) || (c->head_dim != 64 && c->head_dim != 128)) return MINFER_ERR_SHAPE;
-  if (!aligned16(c->k) || !aligned16(c->v) || c->page_stride < 0 || c->row_stride < 0 ||
-      c->head_stride < 0 || !stride_ok(c->page_stride, c->type) || !stride_ok(c->row_stride, c->type) ||
-      !stride_ok(c->head_stride, c->type))
+  if (!aligned16(c->k) || !aligned16(c->v) || !stride_ok(c->page_stride, c->n_pages, c->type) ||
+      !stride_ok(c->row_stride, c->page_size, c->type) || !stride_ok(c->head_stride, c->n_head_kv, c->type))
     return MINFER_ERR_ARG;
   if (!fits31(c->n_pages, c->page_size)) return MINFER_ERR_TOO_LARGE;
+  // (strides between things of which there is one are never used; as 0 they do no harm)
   *out = PagedCache{c->k, c->v, c->n_pages, c->page_size, c->n_head_kv, c->head_dim,
-                    c->page_stride, c->row_stride, c->head_stride, PageDiv(c->page_size)};
+                    c->n_pages > 1 ? c->page_stride : 0, c->page_size > 1 ? c->row_stride : 0,
+                    c->n_head_kv > 1 ? c->head_stride : 0, PageDiv(c->page_size)};
   return MINFER_OK;
 }
 
@@ -137,7 +139,7 @@ int minfer_op_rope_paged_store(const void* d_qkv, int type, int64_t row_stride,
     return MINFER_ERR_SHAPE;
   const int64_t q = (int64_t)n_head * cache->head_dim, kv = (int64_t)cache->n_head_kv * cache->head_dim;
   if (!aligned16(d_qkv) || !aligned16(d_q_out) || !aligned16(d_bias) || !aligned16(d_qnorm) ||
-      !aligned16(d_knorm) || !stride_ok(row_stride, type) || !stride_ok(q_stride, cache->type) ||
+      !aligned16(d_knorm) || !stride_ok(row_stride, n_tokens, type) || !stride_ok(q_stride, n_tokens, cache->type) ||
       (n_tokens > 1 && (row_stride < q + 2 * kv || q_stride < q)))
     return MINFER_ERR_ARG;
   const int sms = current_sms();
@@ -184,8 +186,8 @@ int minfer_op_paged_attention(const void* d_q, int64_t q_stride, const minfer_pa
   if (!d_q || !d_table || !d_len || !d_o || !d_workspace || n_req <= 0 || n_head <= 0 ||
       n_head % cache->n_head_kv != 0 || max_pages <= 0 || !(scale >= 0) || !std::isfinite(scale))
     return MINFER_ERR_ARG;
-  if (!aligned16(d_q) || !aligned16(d_o) || !aligned16(d_workspace) || !stride_ok(q_stride, cache->type) ||
-      !stride_ok(o_stride, cache->type) || (n_req > 1 && (q_stride < q || o_stride < q || table_stride < max_pages)))
+  if (!aligned16(d_q) || !aligned16(d_o) || !aligned16(d_workspace) || !stride_ok(q_stride, n_req, cache->type) ||
+      !stride_ok(o_stride, n_req, cache->type) || (n_req > 1 && (q_stride < q || o_stride < q || table_stride < max_pages)))
     return MINFER_ERR_ARG;
   if (!fits31(max_pages, cache->page_size) || n_head > kMaxHeads) return MINFER_ERR_TOO_LARGE;
   const int sms = current_sms();

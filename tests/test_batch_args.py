@@ -208,3 +208,32 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(qp):
         qp.RopeTable(64, scaling="cubic")
     with pytest.raises(qp.MinferError, match="ERR_SHAPE"):
         qp.RopeTable(64, 65)
+
+
+# strides between things of which there is one: never used, whatever they are
+@pytest.mark.parametrize("change", [dict(n_pages=1, page_stride=2044), dict(n_pages=1, page_stride=-3), dict(page_size=1, row_stride=132),
+                                    dict(n_head_kv=1, head_stride=68), dict(n_head_kv=1, head_stride=-1),
+                                    dict(n_pages=1, page_size=1, n_head_kv=1, page_stride=1, row_stride=3, head_stride=5)])
+def test_unused_cache_strides(qp, change):
+    cache = _cache(qp, **change)
+    keep, args = _store_args(qp, cache=cache)
+    assert _call(qp.lib().minfer_op_rope_paged_store, args) == CUDA
+    assert _call(qp.lib().minfer_op_paged_attention, _attention_args(qp, cache)[1]) == CUDA
+
+
+@pytest.mark.parametrize("change", [dict(row_stride=515), dict(q_stride=3), dict(row_stride=1, q_stride=-7)])
+def test_unused_row_strides(qp, change):
+    keep, args = _store_args(qp)
+    assert _call(qp.lib().minfer_op_rope_paged_store, args, n_tokens=1, **change) == CUDA
+    assert _call(qp.lib().minfer_op_rope_paged_store, args, n_tokens=2, **change) == ARG
+    change = {{"row_stride": "o_stride"}.get(name, name): x for name, x in change.items()}
+    assert _call(qp.lib().minfer_op_paged_attention, _attention_args(qp)[1], n_req=1, **change) == CUDA
+    assert _call(qp.lib().minfer_op_paged_attention, _attention_args(qp)[1], n_req=2, **change) == ARG
+
+
+def test_the_binding_compares_used_strides_only(qp):
+    a = torch.zeros(1, 16, 1, 64)
+    b = torch.zeros(3, 16, 1, 64)[1:2].as_strided((1, 16, 1, 64), (7, 64, 9, 1))
+    assert qp.PagedCache(a, b).desc.n_pages == 1
+    with pytest.raises(qp.MinferError, match="differ"):
+        qp.PagedCache(torch.zeros(2, 16, 2, 64), torch.zeros(2, 2, 16, 64).transpose(1, 2))

@@ -304,3 +304,29 @@ def test_a_step_without_rows(qp):
     logprob, entropy, top_ids, top_logprobs = qp.op_token_logprobs(torch.zeros(0, 50, device="cuda"), none, 3)
     assert logprob.shape == entropy.shape == (0,) and top_ids.shape == top_logprobs.shape == (0, 3)
     assert qp.op_token_logprobs(torch.zeros(0, 50, device="cuda"))[0] is None
+
+
+@pytest.mark.parametrize("t", [F32, F16, BF16])
+def test_single_rows_of_any_stride(qp, t):
+    """One row out of a buffer of odd width, a cache of one KV head, of one page or of pages of one row out of odd views:
+    what contiguous copies give."""
+    for nh, nkv, hd, n_pages, P, m in ((4, 1, 64, 5, 16, 60), (4, 2, 64, 1, 48, 41), (6, 2, 128, 40, 1, 37)):
+        g = gen(m)
+        odd = lambda shape, n: torch.randn(n, generator=g, device="cuda").to(t).as_strided(  # noqa: E731
+            shape, [n if d == 1 else s for d, s in zip(shape, (P * nkv * hd, nkv * hd, hd, 1))])
+        n = n_pages * P * nkv * hd
+        k, v = (odd((n_pages, P, nkv, hd), n + (n + 1) % 2) for _ in range(2))
+        table = torch.randperm(n_pages, generator=g, device="cuda").to(I32)[None]
+        qkv = torch.randn(3, (nh + 2 * nkv) * hd + 1, generator=g, device="cuda").to(t)[:1, :-1]
+        out = torch.zeros(2, nh * hd + 1, dtype=t, device="cuda")[:1, :-1]
+        assert all(s % 8 for s, d in zip(k.stride(), k.shape) if d == 1) and qkv.stride(0) % 8
+        results = []
+        for fit in (lambda x: x, lambda x: x.clone(memory_format=torch.contiguous_format)):
+            kk, vv = torch.empty_strided(k.shape, k.stride(), dtype=t, device="cuda"), torch.empty_strided(v.shape, v.stride(), dtype=t, device="cuda")
+            kk, vv = (kk.copy_(k), vv.copy_(v)) if fit(k) is k else (fit(k), fit(v))
+            cache = qp.PagedCache(kk, vv)
+            q = qp.op_rope_paged_store(fit(qkv), qp.RopeTable(hd), dev([m - 1]), dev([int(table[0, (m - 1) // P]) * P + (m - 1) % P]), cache, nh,
+                                       out=fit(out))
+            results.append((q.clone(), qp.op_paged_attention(q, cache, table, dev([m]), nh, out=fit(out)).clone(), kk, vv))
+        assert all(torch.equal(a, b) for a, b in zip(*results))
+        assert (results[0][1] != 0).any()
