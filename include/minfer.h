@@ -487,7 +487,8 @@ int minfer_op_rope_paged_store(const void* d_qkv, int type, int64_t row_stride,
  * n_head query heads on the current device (no counterpart on the pages).  The
  * workspace is zero-filled once, before its first call; it holds counters that
  * every call leaves at zero, and carries nothing else from call to call: it may
- * serve any calls of this operator that it is large enough for.  Calls that
+ * serve any calls of this operator that it is large enough for, and none of the
+ * other's, which keeps its counters in other places.  Calls that
  * share one follow one another (on one stream, or ordered by events). */
 int minfer_op_paged_attention_workspace(int n_req, int n_head, const minfer_paged_cache* cache,
                                         int64_t* bytes);

@@ -92,11 +92,18 @@ class RopeTable:
 
 class Workspace:
     """Device memory of one operator's calls, zero-filled once; one call at a
-    time may use it (calls on one stream follow one another)."""
+    time may use it (calls on one stream follow one another).  It belongs to the
+    operator that uses it first (`op`): another one would find its counters
+    overwritten."""
 
-    def __init__(self, nbytes: int, device):
+    def __init__(self, nbytes: int, device, op: str | None = None):
         self.buffer = torch.zeros(nbytes, dtype=torch.uint8, device=device)
-        self.nbytes, self.index, self.ptr = nbytes, self.buffer.get_device(), self.buffer.data_ptr()
+        self.nbytes, self.index, self.ptr, self.op = nbytes, self.buffer.get_device(), self.buffer.data_ptr(), op
+
+    def claim(self, op: str):
+        if self.op is not None:
+            _refuse(f"workspace: one of {op} wanted, got one of {self.op}")
+        self.op = op
 
 
 def check_status(status):
@@ -220,7 +227,7 @@ def op_paged_attention_workspace(cache: PagedCache, n_req: int, n_head: int) -> 
     with torch.cuda.device(cache.device):
         check(_L.minfer_op_paged_attention_workspace(n_req, n_head, cache.ptr, ctypes.byref(n)),
               "op_paged_attention_workspace")
-        return Workspace(n.value, cache.device)
+        return Workspace(n.value, cache.device, "op_paged_attention")
 
 
 def op_paged_attention(q, cache: PagedCache, table, length, n_head: int, scale: float | None = None,
@@ -273,6 +280,8 @@ def op_paged_attention(q, cache: PagedCache, table, length, n_head: int, scale: 
         workspace = op_paged_attention_workspace(cache, n, n_head)
     elif workspace.index != dev:
         _refuse("workspace: on the tensors' device wanted", workspace.buffer)
+    elif workspace.op != "op_paged_attention":
+        workspace.claim("op_paged_attention")
     rc = _paged_attention(q.data_ptr(), q_stride, cache.ptr, table.data_ptr(), table_stride, max_pages,
                           length.data_ptr(), n, n_head, scale or 0.0, out.data_ptr(), o_stride,
                           None if lse is None else lse.data_ptr(), workspace.ptr, workspace.nbytes,
@@ -289,7 +298,7 @@ def op_token_logprobs_workspace(logits, k: int) -> Workspace:
     with torch.cuda.device(logits.device):
         check(_L.minfer_op_token_logprobs_workspace(logits.shape[0], logits.shape[1], k, ctypes.byref(n)),
               "op_token_logprobs_workspace")
-        return Workspace(n.value, logits.device)
+        return Workspace(n.value, logits.device, "op_token_logprobs")
 
 
 def op_token_logprobs(logits, ids=None, k: int = 0, out=None, workspace: Workspace | None = None, status=None):
@@ -351,6 +360,8 @@ def op_token_logprobs(logits, ids=None, k: int = 0, out=None, workspace: Workspa
         workspace = op_token_logprobs_workspace(logits, k)
     elif workspace.index != dev:
         _refuse("workspace: on the tensors' device wanted", workspace.buffer)
+    elif workspace.op != "op_token_logprobs":
+        workspace.claim("op_token_logprobs")
     rc = _token_logprobs(logits.data_ptr(), _type_of(logits, "logits"), rows, vocab, row_stride,
                          None if ids is None else ids.data_ptr(), k, None if logprob is None else logprob.data_ptr(),
                          None if entropy is None else entropy.data_ptr(), top_ids.data_ptr() if k else None,

@@ -227,8 +227,9 @@ def test_unused_row_strides(qp, change):
     assert _call(qp.lib().minfer_op_rope_paged_store, args, n_tokens=1, **change) == CUDA
     assert _call(qp.lib().minfer_op_rope_paged_store, args, n_tokens=2, **change) == ARG
     change = {{"row_stride": "o_stride"}.get(name, name): x for name, x in change.items()}
-    assert _call(qp.lib().minfer_op_paged_attention, _attention_args(qp)[1], n_req=1, **change) == CUDA
-    assert _call(qp.lib().minfer_op_paged_attention, _attention_args(qp)[1], n_req=2, **change) == ARG
+    keep, args = _attention_args(qp)
+    assert _call(qp.lib().minfer_op_paged_attention, args, n_req=1, **change) == CUDA
+    assert _call(qp.lib().minfer_op_paged_attention, args, n_req=2, **change) == ARG
 
 
 def test_the_binding_compares_used_strides_only(qp):
@@ -237,3 +238,11 @@ def test_the_binding_compares_used_strides_only(qp):
     assert qp.PagedCache(a, b).desc.n_pages == 1
     with pytest.raises(qp.MinferError, match="differ"):
         qp.PagedCache(torch.zeros(2, 16, 2, 64), torch.zeros(2, 2, 16, 64).transpose(1, 2))
+
+
+def test_a_workspace_is_claimed_once(qp):
+    w = qp.Workspace(64, "cpu")
+    assert w.op is None
+    w.claim("op_paged_attention")
+    with pytest.raises(qp.MinferError, match="got one of op_paged_attention"):
+        w.claim("op_token_logprobs")

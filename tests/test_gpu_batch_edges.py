@@ -330,3 +330,21 @@ def test_single_rows_of_any_stride(qp, t):
             results.append((q.clone(), qp.op_paged_attention(q, cache, table, dev([m]), nh, out=fit(out)).clone(), kk, vv))
         assert all(torch.equal(a, b) for a, b in zip(*results))
         assert (results[0][1] != 0).any()
+
+
+def test_a_workspace_belongs_to_one_operator(qp):
+    """What log probabilities leave in a workspace lies where attention has counters, so the other operator's is refused."""
+    nh, nkv, hd, length = 4, 2, 64, [700, 3]
+    q, k, v, table = attention_case(1, BF16, nh, nkv, hd, 16, length)
+    cache, x = qp.PagedCache(k, v), torch.randn(2, 5000, device="cuda")
+    size = 1 << 24
+    for mine in (qp.Workspace(size, "cuda"), qp.op_paged_attention_workspace(cache, 2, nh)):
+        o = qp.op_paged_attention(q, cache, table, dev(length), nh, workspace=mine)
+        with pytest.raises(qp.MinferError, match="one of op_token_logprobs wanted, got one of op_paged_attention"):
+            qp.op_token_logprobs(x, None, 3, workspace=mine)
+        assert torch.equal(o, qp.op_paged_attention(q, cache, table, dev(length), nh, workspace=mine))
+    for mine in (qp.Workspace(size, "cuda"), qp.op_token_logprobs_workspace(x, 3)):
+        a = qp.op_token_logprobs(x, None, 3, workspace=mine)
+        with pytest.raises(qp.MinferError, match="one of op_paged_attention wanted, got one of op_token_logprobs"):
+            qp.op_paged_attention(q, cache, table, dev(length), nh, workspace=mine)
+        assert torch.equal(a[2], qp.op_token_logprobs(x, None, 3, workspace=mine)[2])
