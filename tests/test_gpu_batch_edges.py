@@ -10,8 +10,9 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_batch import (BF16, F16, F32, I32, U, attention_by_definition, attention_case, close, dev, gen, half, qp,  # noqa: E402, F401
-                            status_word, tables_by_hand)
+from test_gpu_batch import (BF16, F16, F32, I32, ROPE_CASES, U, attention_by_definition, attention_case, check_logprobs,  # noqa: E402, F401
+                            close, dev, gen, half, qp, run_tables, status_word, tables_by_hand, tables_case)
+from test_gpu_batch import test_rope_paged_store as rope_against_the_formula  # noqa: E402
 
 
 # ------------------------------------------------------------------ paged attention: the weights' bits
@@ -348,3 +349,165 @@ def test_a_workspace_belongs_to_one_operator(qp):
         with pytest.raises(qp.MinferError, match="one of op_paged_attention wanted, got one of op_token_logprobs"):
             qp.op_paged_attention(q, cache, table, dev(length), nh, workspace=mine)
         assert torch.equal(a[2], qp.op_token_logprobs(x, None, 3, workspace=mine)[2])
+
+
+# ------------------------------------------------------------------ page tables: refusals in a cluster of sixteen
+@pytest.mark.parametrize("what,code", [("long length", -2), ("tokens", -10), ("pages", -7), ("depth", -1), ("free id", -1), ("shared page id", -1),
+                                       ("returned id", -1)])
+@pytest.mark.parametrize("n", [40, 1500])
+def test_page_tables_refusals_of_large_steps(qp, n, what, code):
+    """Steps of more than 8,192 rows, which sixteen CTAs do: nothing changes."""
+    P, W, max_tokens = 16, 24, 12000
+    length, target, table, free, n_free = tables_case(n, n, P, W, ["one", "same", "back", "over"])
+    for r, (a, b, row) in {3: (0, W * P, []), n - 2: (18, 19, [0, 1]), n - 1: (P * W, 3, list(range(W)))}.items():
+        length[r], target[r], table[r] = a, b, row + [-7] * (W - len(row))
+    free, n_free = list(range(n * W)), n * W
+    if what == "long length":
+        length[n - 1] = P * W + 1
+    elif what == "tokens":
+        length, target, table = [0] * n, [W * P] * n, [[-7] * W] * n
+    elif what == "pages":
+        n_free = W - 3
+        length, target, table = [0] * n, [0] * (n - 1) + [W * P], [[-7] * W] * n
+    elif what == "depth":
+        n_free = n * W + 1
+    elif what == "free id":
+        free[n_free - 5] = n * W
+    elif what == "shared page id":
+        table[n - 2][1] = -1
+    elif what == "returned id":
+        table[n - 1][W - 1] = n * W
+    if what == "tokens":
+        max_tokens = min(max_tokens, n * W * P - 1)
+    status = status_word()
+    t, f, left, start, pos, slot = run_tables(qp, (length, target, table, free, n_free), P, max_tokens, False, status)
+    assert int(status) == code
+    assert t == table and f == free and left == -9
+    assert start == [0] * (n + 1) and pos == [-1] * max_tokens and slot == [-1] * max_tokens
+
+
+# ------------------------------------------------------------------ RoPE: several tokens per CTA
+def rope_rows():
+    sms = torch.cuda.get_device_properties(0).multi_processor_count if torch.cuda.is_available() else 152
+    return 2 * 2 * sms, 4 * 2 * sms  # from here on two tokens a CTA, and four
+
+
+@pytest.mark.parametrize("case", range(len(ROPE_CASES)))
+@pytest.mark.parametrize("which,more", [(0, -1), (0, 1), (1, 0), (1, 3)])
+def test_rope_paged_store_of_many_rows(qp, case, which, more):
+    """CTAs of one, two and four tokens, the last of them in part behind the rows, padding beside live rows."""
+    n = rope_rows()[which] + more
+    rope_against_the_formula(qp, *ROPE_CASES[case], n, "heads" if (case + more) % 2 else "rows")
+
+
+@pytest.mark.parametrize("src,to", [(F32, F32), (F32, BF16), (F16, F16)])
+@pytest.mark.parametrize("which", [0, 1])
+def test_rope_rows_do_not_depend_on_their_neighbours(qp, src, to, which):
+    """Padding, refused slots and positions in every place of a CTA: the other rows are, bit for bit, what calls of a few rows give."""
+    nh, nkv, hd, P = 6, 2, 128, 16
+    g = gen(which)
+    n = rope_rows()[which] + 7
+    width = (nh + 2 * nkv) * hd
+    qkv = torch.randn(n, width, generator=g, device="cuda").to(src)
+    bias, norms = torch.randn(width, generator=g, device="cuda"), [1 + torch.rand(hd, generator=g, device="cuda") for _ in range(2)]
+    pages = -(-n // P)
+    pos = torch.randint(0, 100000, (n,), generator=g, device="cuda").to(I32)
+    slot = torch.randperm(pages * P, generator=g, device="cuda")[:n].to(I32)
+    kind = torch.randint(0, 6, (n,), generator=g, device="cuda")
+    kind[400:440] = 0  # whole CTAs of padding
+    slot[kind == 0], pos[kind == 1], slot[kind == 2] = -1, -1, pages * P
+    results, rope = [], qp.RopeTable(hd)
+    for step in (n, 150):
+        k, v = (torch.full((pages, P, nkv, hd), 3.0, dtype=to, device="cuda") for _ in range(2))
+        out, cache = torch.full((n, nh * hd), 3.0, dtype=to, device="cuda"), qp.PagedCache(k, v)
+        for i in range(0, n, step):
+            status = status_word()
+            qp.op_rope_paged_store(qkv[i:i + step], rope, pos[i:i + step], slot[i:i + step], cache, nh, bias=bias, q_norm=norms[0],
+                                   k_norm=norms[1], out=out[i:i + step], status=status)
+            assert int(status) == (-2 if ((kind[i:i + step] == 1) | (kind[i:i + step] == 2)).any() else 0)
+        results.append((out, k, v))
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    assert (results[0][0][kind < 3] == 3).all() and not (results[0][0][kind >= 3] == 3).all(1).any()
+
+
+# ------------------------------------------------------------------ log probabilities: 16-bit rows, large references
+HARD = ["equal", "two levels", "one left", "two left", "none left", "largest", "tiny", "peak", "zeros of both signs", "lowest", "all lowest",
+        "lowest first", "masked first", "climbing"]
+
+
+@pytest.mark.parametrize("t", [F32, F16, BF16])
+@pytest.mark.parametrize("kind", HARD)
+@pytest.mark.parametrize("rows,V,k", [(3, 5000, 20), (2, 151937, 32), (3, 40, 32), (650, 20001, 7)])
+def test_token_logprobs_hard_rows_of_every_type(qp, t, kind, rows, V, k):
+    g = gen(V)
+    lowest, top = torch.finfo(t).min, torch.finfo(t).max
+    x = torch.randn(rows, V, generator=g, device="cuda")
+    if kind == "equal":
+        x.fill_(1.25)
+    elif kind == "two levels":
+        x = (x > 1).float()
+    elif kind == "one left":
+        x.fill_(-math.inf)
+        x[:, V - 1] = -3.0
+    elif kind == "two left":
+        x.fill_(-math.inf)
+        x[:, 0], x[:, V // 2] = 2.0, 2.0
+    elif kind == "none left":
+        x[1].fill_(-math.inf)
+    elif kind == "largest":
+        x *= top / 16
+    elif kind == "tiny":
+        x *= torch.finfo(t).tiny * 4
+    elif kind == "peak":
+        x[:, 7] = 60.0
+    elif kind == "zeros of both signs":
+        x = torch.where(x > 0, 0.0, -0.0)
+    elif kind == "lowest":
+        x = torch.where(x > 1, x, lowest)
+    elif kind == "all lowest":
+        x.fill_(lowest)
+    elif kind == "lowest first":
+        x[:, :V // 3] = lowest
+        x[0, :V - 3] = lowest
+    elif kind == "masked first":
+        x[:, :V // 3] = -math.inf
+        x[0, :V - 3] = -math.inf
+    elif kind == "climbing":  # through references of every size, in each row of 650 by every warp
+        x += torch.linspace(-1, 1, V, device="cuda") * (50000 if t == F16 else 4e6)
+    ids = (torch.arange(rows, device="cuda") * 17 % V).to(I32)
+    ids[:3] = torch.tensor([0, V - 1, V // 2], device="cuda")[:rows]
+    check_logprobs(qp, x.to(t), ids, k)
+
+
+@pytest.mark.parametrize("t,at", [(F32, 1.0e6), (F32, 2.0 ** 20 - 8), (F32, 1.1e6), (F32, 300.0), (F32, 5e4), (F32, 1e8), (BF16, 300.0), (BF16, 1.0e6),
+                                  (BF16, 1.2e6), (BF16, 3e4), (F16, 300.0), (F16, 4000.0), (F16, 32700.0), (F16, 33000.0), (F16, 65000.0)])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("V", [3001, 151936])
+def test_token_logprobs_around_large_references(qp, t, at, sign, V):
+    """Logits a few steps around a large one: references below and above the size up to which terms are one multiply-add,
+    whose rounding the sums are corrected for."""
+    x = torch.randn(4, V, generator=gen(V), device="cuda")
+    x = (sign * at + torch.where(torch.rand(4, V, generator=gen(1), device="cuda") < 0.5, 2 * x, 0.0)).to(t)
+    x[3, 1::2] = -math.inf
+    x[2, ::3] = torch.finfo(t).min
+    assert torch.isfinite(x[:2]).all()
+    check_logprobs(qp, x, dev([0, V - 1, V // 2, 4]), 8)
+
+
+@pytest.mark.parametrize("t", [F32, F16, BF16])
+@pytest.mark.parametrize("V", [3000, 3007, 100000])
+def test_token_logprobs_nan_and_infinity_of_every_type(qp, t, V):
+    x = torch.randn(6, V, generator=gen(3), device="cuda").to(t)
+    x[0, 0], x[0, V - 1] = math.nan, math.inf
+    x[1, 5], x[1, 9] = math.inf, math.inf
+    x[2, 1:2000] = math.nan
+    x[4, ::2] = -math.inf
+    x[4, V - 1] = math.nan
+    x[5].fill_(-math.inf)
+    x[5, V // 2] = math.inf
+    logprob, entropy, ids, lps = qp.op_token_logprobs(x, dev([3] * 6), 5)
+    bad = [0, 1, 2, 4, 5]
+    assert torch.isnan(logprob[bad]).all() and torch.isnan(entropy[bad]).all() and torch.isnan(lps[bad]).all()
+    assert ids[0, :2].tolist() == [0, V - 1] and ids[1, :2].tolist() == [5, 9] and ids[2].tolist() == [1, 2, 3, 4, 5]
+    assert int(ids[4, 0]) == V - 1 and ids[5].tolist() == [V // 2, 0, 1, 2, 3]
+    check_logprobs(qp, x[3:4], dev([3]), 5)
