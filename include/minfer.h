@@ -430,8 +430,8 @@ typedef struct minfer_rope_table {
  * 2.5: RoPE by position with the hparams' frequency base; the scalings and the
  * interleaved pairs have no counterpart on the pages.  MINFER_ERR_SHAPE for a
  * head_dim other than 64 or 128 or an odd or too large rot_dim, MINFER_ERR_ARG
- * for an unknown style or scaling, theta <= 1, factor <= 0, or YaRN without
- * n_ctx_orig. */
+ * for an unknown style or scaling, theta <= 1, factor <= 0, YaRN without
+ * n_ctx_orig, or a factor that makes a frequency infinite. */
 int minfer_rope_prepare(const minfer_rope_spec* spec, minfer_rope_table* out);
 
 /* Block tables and slot maps of a step, from the requests' lengths.  The pages'

@@ -83,24 +83,25 @@ int minfer_rope_prepare(const minfer_rope_spec* spec, minfer_rope_table* out) {
     low = std::fmax(std::floor(pair_of(fast)), 0.0);
     high = std::fmin(std::ceil(pair_of(slow)), rot - 1.0);
   }
-  for (int i = 0; i < 64; ++i) {
-    out->turn[i] = 0;
-    if (i >= rot / 2) continue;
+  minfer_rope_table t = {};
+  for (int i = 0; i < rot / 2; ++i) {
     double f = std::pow(theta, -2.0 * i / rot);
     if (spec->scaling == MINFER_ROPE_LINEAR) f /= s;
     if (spec->scaling == MINFER_ROPE_YARN) {
       const double g = std::fmin(std::fmax((i - low) / std::fmax(high - low, 0.001), 0.0), 1.0);
       f = f / s * g + f * (1 - g);
     }
+    if (!std::isfinite(f)) return MINFER_ERR_ARG;
     const double turns = f / two_pi;  // per position; whole turns drop out
-    out->turn[i] = (uint64_t)std::ldexp(turns - std::floor(turns), 64);
+    t.turn[i] = (uint64_t)std::ldexp(turns - std::floor(turns), 64);
   }
-  out->mscale = (float)(spec->attn_factor != 0                    ? spec->attn_factor
+  t.mscale = (float)(spec->attn_factor != 0                    ? spec->attn_factor
                         : spec->scaling == MINFER_ROPE_YARN && s > 1 ? 0.1 * std::log(s) + 1
                                                                    : 1.0);
-  out->head_dim = spec->head_dim;
-  out->rot_dim = rot;
-  out->style = spec->style;
+  t.head_dim = spec->head_dim;
+  t.rot_dim = rot;
+  t.style = spec->style;
+  *out = t;
   return MINFER_OK;
 }
 

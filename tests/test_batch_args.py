@@ -246,3 +246,11 @@ def test_a_workspace_is_claimed_once(qp):
     w.claim("op_paged_attention")
     with pytest.raises(qp.MinferError, match="got one of op_paged_attention"):
         w.claim("op_token_logprobs")
+
+
+@pytest.mark.parametrize("change", [dict(scaling=1, factor=1e-320), dict(scaling=2, factor=1e-200, rot_dim=4),
+                                    dict(scaling=3, factor=1e-320, n_ctx_orig=4096), dict(scaling=1, factor=5e-324)])
+def test_rope_frequencies_past_the_range_of_a_double(qp, change):
+    """An infinite number of turns per position has no fraction: refused, and the table is left as it was."""
+    assert _rope(qp, **change)[0] == ARG
+    assert not any(bytes(_rope(qp, **change)[1]))
