@@ -25,7 +25,8 @@ from . import (MINFER_BF16, MINFER_F16, MINFER_F32, ROPE_SCALINGS, ROPE_STYLES, 
 
 _TYPES = {torch.float32: MINFER_F32, torch.float16: MINFER_F16, torch.bfloat16: MINFER_BF16}
 _I32, _F32 = torch.int32, torch.float32
-_ERR_ARG, _ERR_SHAPE = -1, -5
+_ERR_ARG, _ERR_SHAPE, _ERR_TOO_LARGE = -1, -5, -10
+_INT_MAX = 2 ** 31 - 1
 
 _L = lib()
 _page_tables = _L.minfer_op_page_tables
@@ -62,6 +63,8 @@ class PagedCache:
         if not (k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.device == v.device
                 and all(a == b for a, b, n in zip(k.stride(), v.stride(), k.shape) if n > 1) and k.stride(3) == 1):
             _refuse("PagedCache: k and v differ, or are not [pages][rows][heads][dims] with contiguous dims", k, v)
+        if max(k.shape) > _INT_MAX:
+            _refuse("PagedCache: sizes below 2^31 wanted", k, code=_ERR_TOO_LARGE)
         self.k, self.v = k, v
         self.dtype, self.device, self.index = k.dtype, k.device, k.get_device()
         self.n_pages, self.page_size, self.n_head_kv, self.head_dim = k.shape
@@ -135,6 +138,8 @@ def op_page_tables(length, target, page_size: int, table, free, n_free, n_pages:
         _refuse("free: int32 [n_pages] wanted", free)
     if not (n_free.dtype is _I32 and n_free.numel() == 1 and n_free.get_device() == dev):
         _refuse("n_free: int32 [1] wanted", n_free)
+    if page_size > _INT_MAX or max_tokens > _INT_MAX:
+        _refuse(f"page_size {page_size}, max_tokens {max_tokens}", code=_ERR_TOO_LARGE)
     if status is not None and not (status.dtype is _I32 and status.numel() == 1 and status.get_device() == dev):
         _refuse("status: int32 [1] wanted", status)
     if dev < 0:
@@ -322,10 +327,10 @@ def op_token_logprobs(logits, ids=None, k: int = 0, out=None, workspace: Workspa
         _refuse("ids: int32 [rows] wanted", ids)
     if status is not None and not (status.dtype is _I32 and status.numel() == 1 and status.get_device() == dev):
         _refuse("status: int32 [1] wanted", status)
+    if k < 0 or k > 32:
+        _refuse(f"k: {k}")
     if dev < 0:
         _refuse("a CUDA device wanted", logits)
-    if k < 0:
-        _refuse(f"k: {k}")
     if dev != _current():
         with torch.cuda.device(dev):
             return op_token_logprobs(logits, ids, k, out, workspace, status)

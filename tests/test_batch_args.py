@@ -254,3 +254,17 @@ def test_rope_frequencies_past_the_range_of_a_double(qp, change):
     """An infinite number of turns per position has no fraction: refused, and the table is left as it was."""
     assert _rope(qp, **change)[0] == ARG
     assert not any(bytes(_rope(qp, **change)[1]))
+
+
+def test_sizes_past_31_bits_are_refused(qp):
+    """The library's ints would drop their upper bits: 2^32 + 1 pages are not one page."""
+    one = torch.zeros(1, 1, 1, 64)
+    for shape in ((2 ** 32 + 1, 1, 1, 64), (1, 2 ** 32 + 16, 1, 64), (1, 1, 2 ** 31, 64)):
+        with pytest.raises(qp.MinferError, match="TOO_LARGE"):
+            qp.PagedCache(one.expand(shape), one.expand(shape))
+    n = torch.zeros(2, dtype=torch.int32)
+    for page_size, max_tokens in ((2 ** 32 + 16, 8), (16, 2 ** 32 + 8)):
+        with pytest.raises(qp.MinferError, match="TOO_LARGE"):
+            qp.op_page_tables(n, n, page_size, torch.zeros(2, 3, dtype=torch.int32), n.new_zeros(4), n[:1], 4, max_tokens)
+    with pytest.raises(qp.MinferError, match="k: 4294967301"):
+        qp.op_token_logprobs(torch.zeros(2, 50), n, 2 ** 32 + 5)
