@@ -194,16 +194,21 @@ __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t* hi, uint32_t* l
   *lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(*hi));
 }
 
-// Weights, at most 1, go into the sums of values times this, and results are divided by
-// it: 2^31 keys of the largest finite f32 or bf16 value do not overflow (a warp's sum,
-// under its own maximum, may be one of keys that weigh nothing in the end), and f16
-// weights stand well above 2^-24, where f16 ends.
+// Weights, at most 1, go into the sums of values times this power of two, and results
+// are divided by it.  f32 and bf16: 1 over the request's length, so that no sum of the
+// largest finite values overflows (a warp's, under its own maximum, may be one of keys
+// that weigh nothing in the end).  f16: 2^15, so that weights stand well above 2^-24,
+// where f16 ends.
 template <typename T>
-constexpr float kWeightScale = 0x1p-31f;
+__device__ __forceinline__ float weight_scale(int len) {
+  return __int_as_float((127 - (32 - __clz(len - 1))) << 23);
+}
 template <>
-constexpr float kWeightScale<__half> = 0x1p15f;
+__device__ __forceinline__ float weight_scale<__half>(int) {
+  return 0x1p15f;
+}
 
-// Two weights, each times kWeightScale the sum of an upper and a lower 16-bit number.
+// Two weights, each times weight_scale the sum of an upper and a lower 16-bit number.
 // The upper one is cut off below the weight, equal to it only for a weight of 0, so
 // that the lower one is positive as well: an infinite value times the weight is then
 // infinite and not 0 * inf.
@@ -212,20 +217,20 @@ constexpr float kWeightScale<__half> = 0x1p15f;
 //  f16: the upper number is the weight less 2^-12 of it, cut off; what is left, at
 //    most 1.25 * 2^-10, is rounded to 2^-11 of itself, or to a step of 2^-24 (2^-39 of
 //    the largest weight), which it keeps if the weight has one.
-__device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t* lo, __nv_bfloat16) {
-  a *= kWeightScale<__nv_bfloat16>;
-  b *= kWeightScale<__nv_bfloat16>;
+__device__ __forceinline__ void split2(float a, float b, float scale, uint32_t* hi, uint32_t* lo, __nv_bfloat16) {
+  a *= scale;
+  b *= scale;
   const uint32_t ua = (max(__float_as_uint(a), 1u) - 1) & 0xFFFF0000u, ub = (max(__float_as_uint(b), 1u) - 1) & 0xFFFF0000u;
   const __nv_bfloat162 l = __floats2bfloat162_rn(a - __uint_as_float(ua), b - __uint_as_float(ub));
   *hi = ua >> 16 | ub;
   *lo = *reinterpret_cast<const uint32_t*>(&l);
 }
-__device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t* lo, __half) {
-  constexpr float kS = kWeightScale<__half>, kBelow = kS * (1.f - 0x1p-12f);
-  asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(*hi) : "f"(b * kBelow), "f"(a * kBelow));
+__device__ __forceinline__ void split2(float a, float b, float scale, uint32_t* hi, uint32_t* lo, __half) {
+  const float below = scale * (1.f - 0x1p-12f);
+  asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(*hi) : "f"(b * below), "f"(a * below));
   const float2 h = __half22float2(*reinterpret_cast<const __half2*>(hi));
   constexpr float kStep = 0x1.01p-25f;  // rounds to a step
-  const __half2 l = __floats2half2_rn(fmaxf(fmaf(a, kS, -h.x), fminf(a * kS, kStep)), fmaxf(fmaf(b, kS, -h.y), fminf(b * kS, kStep)));
+  const __half2 l = __floats2half2_rn(fmaxf(fmaf(a, scale, -h.x), fminf(a * scale, kStep)), fmaxf(fmaf(b, scale, -h.y), fminf(b * scale, kStep)));
   *lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 __device__ __forceinline__ void store_as(float* p, float x) { *p = x; }
@@ -278,11 +283,11 @@ struct Shares {
 // Joins `count` partials.  Their outputs are copied to shared memory (ring, all
 // of them at once or as many as fit) while the weights are worked out, a warp
 // per row and a lane per partial; then every thread adds up four dims of a row
-// at a time.  final: the result goes to o and lse, else it replaces the first
+// at a time.  final: the result, over `scale` (weight_scale), goes to o and lse, else it replaces the first
 // partial.  A sum below 0 marks a piece that met a bad page; it spoils the
 // whole.  All threads; s.part is written before a barrier of the caller's.
 template <typename T, int HD, int R, int kWarps>
-__device__ void join_parts(JoinShared<R>& s, unsigned char* ring, int ring_bytes, int count, int rows, bool final, T* o, float* lse) {
+__device__ void join_parts(JoinShared<R>& s, unsigned char* ring, int ring_bytes, int count, int rows, bool final, float scale, T* o, float* lse) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kItems = (R * HD / 4 + kWarps * 32 - 1) / (kWarps * 32);  // of a thread
   const int items = rows * HD / 4, fit = min(count, ring_bytes / (items * 16));
@@ -368,7 +373,7 @@ __device__ void join_parts(JoinShared<R>& s, unsigned char* ring, int ring_bytes
     if (!final) {
       reinterpret_cast<float4*>(s.part[0] + 2 * R)[i] = acc[k];
     } else if (!bad) {
-      const float l = s.out[i / (HD / 4)].y, f = l == 0.f ? 0.f : 1.f / (l * kWeightScale<T>);
+      const float l = s.out[i / (HD / 4)].y, f = l == 0.f ? 0.f : 1.f / (l * scale);
       T* dst = o + i * 4;
       store_as(dst, acc[k].x * f);
       store_as(dst + 1, acc[k].y * f);
@@ -396,6 +401,7 @@ __device__ __forceinline__ unsigned arrive(unsigned* counter) {
 // A piece of a (request, head block) that other shares hold pieces of too.
 struct Piece {
   int r, head0, rows, c0, c1;  // c0..c1: the shares that hold one
+  float scale;                 // weight_scale of the request
 };
 
 template <typename T, int HD, int R>
@@ -588,6 +594,7 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
     const int seg_units = min(cw.units - cw.u, count - done);
     const bool whole = from_start && cw.u + seg_units == cw.units;
     const int seg_len = cw.len;
+    const float wscale = weight_scale<T>(seg_len);
     const int first_unit = cw.u, all_units = cw.units;
     // Q as the B operand: two dims of a head (16-bit types), or a dim's tf32 halves
     uint32_t qb[NH][kSteps][2], ql[kF32 ? NH : 1][kF32 ? kSteps : 1][2];
@@ -701,7 +708,7 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
         for (int h = 0; h < NH; ++h)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            split2(sc[h][2 * j], sc[h][2 * j + 1], &p[h][j], &pl[h][j], T());
+            split2(sc[h][2 * j], sc[h][2 * j + 1], wscale, &p[h][j], &pl[h][j], T());
             p[h][j] = transpose8(p[h][j]);
             pl[h][j] = transpose8(pl[h][j]);
           }
@@ -734,7 +741,7 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
 #pragma unroll
           for (int j = 0; j < 2; ++j)
             *reinterpret_cast<float2*>(pbuf + (g4 + 8 * j) * R + 8 * h + 2 * t4) =
-                make_float2(sc[h][2 * j] * kWeightScale<T>, sc[h][2 * j + 1] * kWeightScale<T>);
+                make_float2(sc[h][2 * j] * wscale, sc[h][2 * j + 1] * wscale);
         __syncwarp();
         uint32_t ph[NH][2][2], pl[NH][2][2];
 #pragma unroll
@@ -827,7 +834,7 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
       if (!whole) {
         reinterpret_cast<float2*>(part)[tid] = make_float2(mx, seg_bad ? -1.f : sum);
       } else {
-        const float f = sum == 0.f ? 0.f : 1.f / (sum * kWeightScale<T>);
+        const float f = sum == 0.f ? 0.f : 1.f / (sum * wscale);
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) c[k] *= f;
         if (!seg_bad && a.lse) a.lse[(int64_t)r * a.nh + head0 + tid] = fmaf(mx, kLn2, logf(sum));
@@ -867,7 +874,7 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
     if (!whole) {
       const int64_t first = begin + (done - seg_units) - first_unit;
       Piece& p = piece[from_start ? 1 : 0];
-      p = Piece{r, head0, rows, shares.of(first), shares.of(first + all_units - 1)};
+      p = Piece{r, head0, rows, shares.of(first), shares.of(first + all_units - 1), wscale};
     }
   }
 
@@ -900,7 +907,7 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
     if (hi > lo) {
       if (tid <= hi - lo) s_join.part[tid] = slot(lo + tid);
       __syncthreads();
-      join_parts<T, HD, R, kWarps>(s_join, smem, kWarps * C::kStages * C::kStageBytes, hi - lo + 1, p.rows, direct, o_row, lse_row);
+      join_parts<T, HD, R, kWarps>(s_join, smem, kWarps * C::kStages * C::kStageBytes, hi - lo + 1, p.rows, direct, p.scale, o_row, lse_row);
       __syncthreads();
     }
     if (!direct) {
@@ -912,7 +919,7 @@ __global__ void __launch_bounds__(Cfg<T, HD, R>::kWarps * 32, Cfg<T, HD, R>::kCt
       }
       if (tid <= g1 - g0) s_join.part[tid] = slot(max(p.c0, (g0 + tid) * kGroup));
       __syncthreads();
-      if (s_segbad[0]) join_parts<T, HD, R, kWarps>(s_join, smem, kWarps * C::kStages * C::kStageBytes, g1 - g0 + 1, p.rows, true, o_row, lse_row);
+      if (s_segbad[0]) join_parts<T, HD, R, kWarps>(s_join, smem, kWarps * C::kStages * C::kStageBytes, g1 - g0 + 1, p.rows, true, p.scale, o_row, lse_row);
       __syncthreads();
     }
   }

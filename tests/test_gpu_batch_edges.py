@@ -96,6 +96,19 @@ def test_paged_attention_weights_of_zero(qp, t):
     assert (o == 0.25).all()
 
 
+@pytest.mark.parametrize("t", [F32, BF16])
+@pytest.mark.parametrize("m", [1, 50, 5000])
+def test_paged_attention_tiny_values(qp, t, m):
+    """Values around 2^-100: the sums of a request's weights times them keep their bits."""
+    nh, nkv, hd, P = 4, 2, 64, 16
+    q, k, v, table = attention_case(4, t, nh, nkv, hd, P, [m], poison=False)
+    v *= 2.0 ** -100
+    q *= 0.5
+    o = qp.op_paged_attention(q, qp.PagedCache(k, v), table, dev([m]), nh)
+    want = attention_by_definition(q, k, v, table, [m], nh, 1 / 8)
+    close(o.view(1, nh, hd), want[0], weight_tolerance(t, want, m, 2))
+
+
 @pytest.mark.parametrize("t", [F32, F16, BF16])
 @pytest.mark.parametrize("sign", [1, -1])
 def test_paged_attention_largest_values(qp, t, sign):
