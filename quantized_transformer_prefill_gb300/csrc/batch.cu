@@ -136,7 +136,8 @@ int minfer_op_rope_paged_store(const void* d_qkv, int type, int64_t row_stride,
     return MINFER_ERR_ARG;
   if (n_head > kMaxHeads) return MINFER_ERR_TOO_LARGE;
   if ((type != MINFER_F32 && type != cache->type) || rope->head_dim != cache->head_dim ||
-      rope->rot_dim < 2 || rope->rot_dim > cache->head_dim || rope->rot_dim % 2)
+      rope->rot_dim < 2 || rope->rot_dim > cache->head_dim || rope->rot_dim % 2 ||
+      (rope->style != MINFER_ROPE_HALF && rope->style != MINFER_ROPE_INTERLEAVED))
     return MINFER_ERR_SHAPE;
   const int64_t q = (int64_t)n_head * cache->head_dim, kv = (int64_t)cache->n_head_kv * cache->head_dim;
   if (!aligned16(d_qkv) || !aligned16(d_q_out) || !aligned16(d_bias) || !aligned16(d_qnorm) ||

@@ -268,3 +268,13 @@ def test_sizes_past_31_bits_are_refused(qp):
             qp.op_page_tables(n, n, page_size, torch.zeros(2, 3, dtype=torch.int32), n.new_zeros(4), n[:1], 4, max_tokens)
     with pytest.raises(qp.MinferError, match="k: 4294967301"):
         qp.op_token_logprobs(torch.zeros(2, 50), n, 2 ** 32 + 5)
+
+
+@pytest.mark.parametrize("style", [2, 7, -1])
+@pytest.mark.parametrize("rot", [24, 64])
+def test_rope_store_refuses_a_table_of_an_unknown_style(qp, style, rot):
+    """A table that minfer_rope_prepare did not fill: its style decides what shared memory the launch asks for."""
+    table = _rope(qp, rot_dim=rot)[1]
+    table.style = style
+    keep, args = _store_args(qp, rope=table)
+    assert _call(qp.lib().minfer_op_rope_paged_store, args) == SHAPE
