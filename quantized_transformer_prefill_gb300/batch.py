@@ -240,7 +240,7 @@ def op_paged_attention(q, cache: PagedCache, table, length, n_head: int, scale: 
     """Attention of one new token per request over its pages
     (minfer_op_paged_attention): q [n_req][n_head*head_dim] in the cache's type,
     table int32 [n_req][max_pages], length int32 [n_req] rows to attend to, the
-    new one included.  Returns o like q; `lse` (float32 [n_req][n_head]), when
+    new one included, scale None or 0 for 1 / sqrt(head_dim).  Returns o like q; `lse` (float32 [n_req][n_head]), when
     given, gets ln sum exp(scale q.k).  Rows of refused requests are not written
     (without `out` they are zero)."""
     dev, width = q.get_device(), n_head * cache.head_dim
@@ -308,8 +308,8 @@ def op_token_logprobs_workspace(logits, k: int) -> Workspace:
 
 def op_token_logprobs(logits, ids=None, k: int = 0, out=None, workspace: Workspace | None = None, status=None):
     """Log probabilities of the tokens `ids` (int32 [rows], negative: skip the
-    row; or None) under logits [rows][vocab] (float32, float16 or bfloat16, any
-    row stride), the rows' entropy and k largest with their log probabilities
+    row; or None) under logits [rows][vocab] (float32, float16 or bfloat16, rows
+    of any distance that do not overlap), the rows' entropy and k largest with their log probabilities
     (minfer_op_token_logprobs).  Returns (logprob, entropy, top_ids,
     top_logprobs), or fills `out`, four such tensors (logprob without ids,
     entropy, and the last two with k = 0 may be None); logprob is None without

@@ -16,7 +16,7 @@ namespace {
 // One thread-block cluster does a step, or one CTA where there is little to write
 // (32 requests of one token 3.8 us against 4.5 with eight CTAs, 1,087 tokens 5.2
 // against 5.8, 2,164 tokens 6.0 against 5.8; sixteen where there is much: 6,364
-// tokens 6.3 with either, 21,500 tokens of 1,023 requests 7.1 against 8.6).  Every
+// tokens 6.3 with either, 21,500 tokens of 1,023 requests 7.0 against 8.4).  Every
 // CTA scans all requests (new tokens, grown pages, returned pages: three exclusive
 // prefix sums in its own shared memory), checks its share of the page ids the step
 // will use, works out its share of the outputs, and writes it after one cluster
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_tables_kernel(const PageTa
   // A thread's first grown page, returned page and shared page (the one that a
   // request's next row shares with its last one) are checked here, and all that a
   // thread will write first is worked out before the barrier, whose wait hides it
-  // (after the barrier, the mixed step took 8.6 us).  Nothing that is read here is
+  // (after the barrier, the mixed step took 9.5 us).  Nothing that is read here is
   // written by this step.
   int page0 = 0, back0 = 0, *entry0 = nullptr;
   int pos0[Q], slot0[Q];
@@ -348,8 +348,9 @@ constexpr int kRpMaxBias = 24576;
 constexpr int kRpRing = 8;       // units of a warp on their way or at work
 
 // Bound by HBM: 4096 f32 rows of 36 heads of 128 into a bf16 cache, 113 MB, take
-// 20 us (5.7 TB/s, 84% of the measured copy); 1,001 f16 rows with QK-norm 6.2 us;
-// 64 rows 2.5 us, a launch.
+// 20 us (5.7 TB/s, 84% of the measured copy); 1,001 f16 rows with QK-norm 6.0 us, in 501
+// CTAs of two tokens, 3.3 per SM: a warp has four units behind two barriers and the
+// cosines; 64 rows 2.3 us, a launch.
 //
 // A CTA takes 1, 2 or 4 tokens.  Its threads work out the tokens' cosines and
 // sines, one pair each, while the rows are on the way; then 8, 4 or 2 warps go

@@ -41,8 +41,8 @@
 //
 // Measured on a GB300 (us a call, device; bytes of K and V at the measured copy
 // rate of 6.77 TB/s in brackets): 64 requests of up to 4096 rows, 28/4 heads of
-// 128, bf16: 52 (44); one of 131,071, 12/2 heads of 128, f16: 30 (20); 33 of up to
-// 2048, 14/2 heads of 64, f32: 15 (5); one of 513: 6.3.  While units are worked on
+// 128, bf16: 53 (44); one of 131,071, 12/2 heads of 128, f16: 31 (20); 33 of up to
+// 2048, 14/2 heads of 64, f32: 15.5 (5); one of 513: 6.3.  While units are worked on
 // the rows come in at 7.1 TB/s; what is left is the start (lengths, page lookup,
 // first rows: 3 us), equal shares ending up to a tenth apart, and the join (report
 // 1 us, 2 to 3 us a level).  Small last shares for CTAs that start where one has
