@@ -25,10 +25,11 @@ def weight_tolerance(t, want, m, units):
     truncated to 24 bits or more.  f32: the halves' 20 U, in scores and weights."""
     o, lse, mean, size, top = want
     hd = o.shape[-1]
+    m = torch.tensor(m, dtype=torch.float64, device="cuda").view(-1, 1, 1)  # keys of each request
     split = 20 * U if t == F32 else 0
     score = size * ((hd // 8 + 2) * 2.0 ** -23 + split + 4 * U) + 8 * U
     weight = {BF16: 2.0 ** -15, F16: 1.25 * 2.0 ** -21, F32: 20 * U}[t]
-    rel = 2 * score + weight + (32 + 6 * math.log2(max(m, 2))) * U + 2 * units * 17 * 2.0 ** -23
+    rel = 2 * score + weight + (32 + 6 * torch.log2(m.clamp(min=2))) * U + 2 * units * 17 * 2.0 ** -23
     return half(t) * o.abs() + rel * mean + (m * 2.0 ** -39 * top + 2.0 ** -25 if t == F16 else 0)
 
 
@@ -186,6 +187,33 @@ def test_paged_attention_rising_and_falling_scores(qp, t, m):
         want = attention_by_definition(q, k, v, table, [m], nh, 1.0)
         close(o.view(1, nh, hd), want[0], weight_tolerance(t, want, m, 2))
         close(lse, want[1], 2 * want[3][..., 0] * (10 * 2.0 ** -23 + 24 * U) + 2.0 ** -18)
+
+
+@pytest.mark.parametrize("t", [F32, F16, BF16])
+@pytest.mark.parametrize("nh,nkv,hd", [(12, 2, 128), (32, 2, 64), (20, 1, 128)])
+@pytest.mark.parametrize("m", [200, 30001])
+def test_paged_attention_small_weights_of_every_layout(qp, t, nh, nkv, hd, m):
+    """The tail beside a dominant key in blocks of 8 and 16 heads, over one share, joins of one and of two levels."""
+    P, length, rows = 16, [m, 0, 40], (0, 2)
+    q, k, v, table = attention_case(m, t, nh, nkv, hd, P, length, "heads")
+    q.zero_()
+    q[:, ::hd] = 1.0
+    for r in rows:
+        pages = table[r, :-(-length[r] // P)].long()
+        kk, vv = (x[pages].reshape(-1, nkv, hd).float() for x in (k, v))
+        kk[:, :, 0] = torch.rand(kk.shape[0], nkv, generator=gen(m), device="cuda")
+        kk[length[r] // 3, :, 0] = 16
+        vv = 100 + 10 * vv  # (what lies behind the last row stays NaN)
+        vv[length[r] // 3] = 0
+        k[pages], v[pages] = (x.view(-1, P, nkv, hd).to(t) for x in (kk, vv))
+    lse = torch.empty(3, nh, device="cuda")
+    o = qp.op_paged_attention(q, qp.PagedCache(k, v), table, dev(length), nh, scale=1.0, lse=lse)
+    want = attention_by_definition(q, k, v, table, length, nh, 1.0)
+    tol = weight_tolerance(t, want, length, 30)
+    close(o.view(3, nh, hd), want[0], tol)
+    # half a step of the result is the largest part of the tolerance of 16-bit caches
+    if t != F32:
+        assert float((tol / want[0].abs())[list(rows)].max()) < (2.0 ** -7 if t == BF16 else 2.0 ** -9)
 
 
 @pytest.mark.parametrize("m", [131071])
