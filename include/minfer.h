@@ -518,6 +518,66 @@ int minfer_op_paged_attention(const void* d_q, int64_t q_stride, const minfer_pa
                               int64_t o_stride, float* d_lse, void* d_workspace,
                               int64_t workspace_bytes, int* d_status, void* stream);
 
+/* The same pool with its rows in Q8_0 blocks, the codec of the matmul inputs
+ * (walkthrough index, "CPU matmul kernels"; a quantized cache has no counterpart
+ * on the pages): k and v hold int8 codes, laid out as above; k_scale and v_scale
+ * hold the f16 bits of a scale per 32 values, head_dim / 32 of them contiguous at
+ * p*scale_page_stride + s*scale_row_stride + h*scale_head_stride.  A code c of a
+ * block with scale d stands for c * d; codes are any int8.  Strides count codes and
+ * scales.  k and v and their strides are 16-byte aligned; the scales and their
+ * strides are aligned to the head_dim / 32 scales of a row. */
+typedef struct minfer_paged_cache_q8 {
+  void* k;
+  void* v;
+  void* k_scale;
+  void* v_scale;
+  int n_pages, page_size, n_head_kv, head_dim;
+  int64_t page_stride, row_stride, head_stride;
+  int64_t scale_page_stride, scale_row_stride, scale_head_stride;
+} minfer_paged_cache_q8;
+
+/* minfer_op_rope_paged_store ("09 · Prefill", section 2.2) into such a pool: Q goes to d_q_out in q_type (F32,
+ * F16 or BF16; `type` is MINFER_F32 or q_type), K and V are quantized as they are
+ * stored, in f32, from their values before any other rounding: d = max|x| / 127 of
+ * 32 values, codes round(x * (1 / d)) ties away from zero, the scale is d rounded to
+ * f16.  A block with a NaN, an infinity or a scale past f16's range (a value above
+ * 8.3e6) is stored as codes of 0 with a scale of NaN: it reads back as NaN. */
+int minfer_op_rope_paged_store_q8(const void* d_qkv, int type, int64_t row_stride,
+                                  const float* d_bias, const float* d_qnorm,
+                                  const float* d_knorm, float eps, const minfer_rope_table* rope,
+                                  const int32_t* d_pos, const int32_t* d_slot, int n_tokens,
+                                  int n_head, const minfer_paged_cache_q8* cache, void* d_q_out,
+                                  int q_type, int64_t q_stride, int* d_status, void* stream);
+
+/* Reads rows of such a pool back ("05 · Graph build", section 2.5: kvcache_load;
+ * rows of f32 are what minfer_op_attention and minfer_kv_write take): row i of d_k
+ * and d_v (n_head_kv*head_dim values of `type`, out_stride elements apart, 16-byte
+ * aligned like the stride; either may be NULL) gets the values at slot d_slot[i],
+ * c * d in f32 rounded once.  Slots may repeat.  A row with a negative slot is not
+ * written.  Device errors: MINFER_ERR_POS_OOB for a slot past the pool (that row is
+ * not written). */
+int minfer_op_paged_read_q8(const minfer_paged_cache_q8* cache, const int32_t* d_slot, int n_rows,
+                            int type, void* d_k, void* d_v, int64_t out_stride, int* d_status,
+                            void* stream);
+
+/* minfer_op_paged_attention ("05 · Graph build", section 2.5) over such a pool: query rows and results of `type`
+ * (F32, F16 or BF16), everything else as there, the workspace's rules included; a
+ * workspace serves one of the two operators.  The codes are exact operands of the
+ * products; scales, scores, softmax statistics and sums are f32.  A query value is
+ * exact (f16), exact to 2^-40 of the largest of its head (bf16), or held in two
+ * 11-bit numbers (f32); a softmax weight times a row's scale is the sum of two bf16
+ * numbers (to 2^-17 of it), with f32 queries of three (2^-24).  What lies in scales
+ * and codes behind a request's last row is never used, whatever its bits.  Scales are
+ * finite: one of V that is not makes its 32 dims NaN. */
+int minfer_op_paged_attention_q8_workspace(int n_req, int n_head,
+                                           const minfer_paged_cache_q8* cache, int64_t* bytes);
+int minfer_op_paged_attention_q8(const void* d_q, int type, int64_t q_stride,
+                                 const minfer_paged_cache_q8* cache, const int32_t* d_table,
+                                 int64_t table_stride, int max_pages, const int32_t* d_len,
+                                 int n_req, int n_head, float scale, void* d_o, int64_t o_stride,
+                                 float* d_lse, void* d_workspace, int64_t workspace_bytes,
+                                 int* d_status, void* stream);
+
 /* Bytes of workspace of minfer_op_token_logprobs (no counterpart on the pages);
  * the same rules as above. */
 int minfer_op_token_logprobs_workspace(int64_t rows, int64_t vocab, int k, int64_t* bytes);

@@ -58,6 +58,15 @@ class PagedCacheDesc(ctypes.Structure):
                 ("head_stride", ctypes.c_int64)]
 
 
+class PagedCacheQ8Desc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("n_head_kv", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("scale_page_stride", ctypes.c_int64),
+                ("scale_row_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64)]
+
+
 class RopeSpec(ctypes.Structure):
     _fields_ = [("head_dim", ctypes.c_int), ("rot_dim", ctypes.c_int), ("style", ctypes.c_int),
                 ("scaling", ctypes.c_int), ("theta", ctypes.c_double), ("factor", ctypes.c_double),
@@ -108,6 +117,12 @@ SIGNATURES = {
     "minfer_op_paged_attention_workspace": ([_I, _I, _P, ctypes.POINTER(_I64)], _I),
     "minfer_op_paged_attention": ([_P, _I64, _P, _P, _I64, _I, _P, _I, _I, _F, _P, _I64, _P, _P,
                                    _I64, _P, _P], _I),
+    "minfer_op_rope_paged_store_q8": ([_P, _I, _I64, _P, _P, _P, _F, _P, _P, _P, _I, _I, _P, _P, _I,
+                                       _I64, _P, _P], _I),
+    "minfer_op_paged_read_q8": ([_P, _P, _I, _I, _P, _P, _I64, _P, _P], _I),
+    "minfer_op_paged_attention_q8_workspace": ([_I, _I, _P, ctypes.POINTER(_I64)], _I),
+    "minfer_op_paged_attention_q8": ([_P, _I, _I64, _P, _P, _I64, _I, _P, _I, _I, _F, _P, _I64, _P,
+                                      _P, _I64, _P, _P], _I),
     "minfer_op_token_logprobs_workspace": ([_I64, _I64, _I, ctypes.POINTER(_I64)], _I),
     "minfer_op_token_logprobs": ([_P, _I, _I64, _I64, _I64, _P, _I, _P, _P, _P, _P, _P, _I64, _P,
                                   _P], _I),
@@ -416,6 +431,8 @@ def op_rope_store(qkv, bias, pos, nh: int, nkv: int, hd: int, theta: float, K, V
 
 _BATCH = ("PagedCache", "RopeTable", "Workspace", "check_status", "op_page_tables",
           "op_rope_paged_store", "op_paged_attention_workspace", "op_paged_attention",
+          "PagedCacheQ8", "op_rope_paged_store_q8", "op_paged_read_q8",
+          "op_paged_attention_q8_workspace", "op_paged_attention_q8",
           "op_token_logprobs_workspace", "op_token_logprobs")
 
 

@@ -21,7 +21,7 @@ import ctypes
 import torch
 
 from . import (MINFER_BF16, MINFER_F16, MINFER_F32, ROPE_SCALINGS, ROPE_STYLES, MinferError,
-               PagedCacheDesc, RopeSpec, RopeTableDesc, check, lib)
+               PagedCacheDesc, PagedCacheQ8Desc, RopeSpec, RopeTableDesc, check, lib)
 
 _TYPES = {torch.float32: MINFER_F32, torch.float16: MINFER_F16, torch.bfloat16: MINFER_BF16}
 _I32, _F32 = torch.int32, torch.float32
@@ -32,6 +32,9 @@ _L = lib()
 _page_tables = _L.minfer_op_page_tables
 _rope_paged_store = _L.minfer_op_rope_paged_store
 _paged_attention = _L.minfer_op_paged_attention
+_rope_paged_store_q8 = _L.minfer_op_rope_paged_store_q8
+_paged_read_q8 = _L.minfer_op_paged_read_q8
+_paged_attention_q8 = _L.minfer_op_paged_attention_q8
 _token_logprobs = _L.minfer_op_token_logprobs
 
 # The raw handle of a device's current stream and the current device's index:
@@ -70,6 +73,30 @@ class PagedCache:
         self.n_pages, self.page_size, self.n_head_kv, self.head_dim = k.shape
         self.desc = PagedCacheDesc(k.data_ptr(), v.data_ptr(), _type_of(k, "PagedCache"), *k.shape,
                                    *k.stride()[:3])
+        self.ptr = ctypes.addressof(self.desc)
+
+
+class PagedCacheQ8:
+    """A pool of K/V pages in Q8_0 blocks: k and v int8 codes [n_pages, page_size,
+    n_head_kv, head_dim], k_scale and v_scale float16 [n_pages, page_size,
+    n_head_kv, head_dim / 32], the first two and the last two with the same strides
+    (permuted views as with PagedCache; with each head's rows of a page behind one
+    another, one head's scales share the sectors that attention reads)."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        for a, b, kind in ((k, v, torch.int8), (k_scale, v_scale, torch.float16)):
+            if not (a.dim() == 4 and a.shape == b.shape and a.dtype is kind and b.dtype is kind and a.device == b.device == k.device
+                    and all(x == y for x, y, n in zip(a.stride(), b.stride(), a.shape) if n > 1) and (a.stride(3) == 1 or a.shape[3] == 1)):
+                _refuse(f"PagedCacheQ8: two {kind} wanted, [pages][rows][heads][..] with contiguous dims and the same strides", a, b)
+        if k_scale.shape != (*k.shape[:3], k.shape[3] // 32) or k.shape[3] % 32:
+            _refuse("PagedCacheQ8: a scale per 32 codes wanted", k, k_scale)
+        if max(k.shape) > _INT_MAX:
+            _refuse("PagedCacheQ8: sizes below 2^31 wanted", k, code=_ERR_TOO_LARGE)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device, self.index = k.device, k.get_device()
+        self.n_pages, self.page_size, self.n_head_kv, self.head_dim = k.shape
+        self.desc = PagedCacheQ8Desc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *k.shape,
+                                     *k.stride()[:3], *k_scale.stride()[:3])
         self.ptr = ctypes.addressof(self.desc)
 
 
@@ -225,6 +252,100 @@ def op_rope_paged_store(qkv, rope: RopeTable, pos, slot, cache: PagedCache, n_he
     return out
 
 
+def op_rope_paged_store_q8(qkv, rope: RopeTable, pos, slot, cache: PagedCacheQ8, n_head: int, bias=None,
+                           q_norm=None, k_norm=None, eps: float = 1e-6, out=None, status=None):
+    """op_rope_paged_store with K and V quantized to Q8_0 as they are stored
+    (minfer_op_rope_paged_store_q8).  The rotated Q has the type of `out` (without
+    it that of qkv), and qkv that type or float32."""
+    dev, hd = qkv.get_device(), cache.head_dim
+    width = (n_head + 2 * cache.n_head_kv) * hd
+    shape = qkv.shape
+    if not (len(shape) == 2 and shape[1] == width and dev == cache.index):
+        _refuse(f"qkv: rows of {width} on the cache's device wanted", qkv)
+    n = shape[0]
+    row_stride, one = qkv.stride()
+    if one != 1:
+        _refuse("qkv: contiguous rows wanted", qkv)
+    if not (pos.dtype is _I32 and pos.numel() == n and pos.is_contiguous() and pos.get_device() == dev):
+        _refuse("pos: int32 [n] wanted", pos)
+    if not (slot.dtype is _I32 and slot.numel() == n and slot.is_contiguous() and slot.get_device() == dev):
+        _refuse("slot: int32 [n] wanted", slot)
+    if bias is not None and not (bias.dtype is _F32 and bias.numel() == width and bias.is_contiguous()
+                                 and bias.get_device() == dev):
+        _refuse(f"bias: float32 [{width}] wanted", bias)
+    for w in (q_norm, k_norm):
+        if w is not None and not (w.dtype is _F32 and w.numel() == hd and w.is_contiguous() and w.get_device() == dev):
+            _refuse(f"q_norm, k_norm: float32 [{hd}] wanted", w)
+    if status is not None and not (status.dtype is _I32 and status.numel() == 1 and status.get_device() == dev):
+        _refuse("status: int32 [1] wanted", status)
+    if dev < 0:
+        _refuse("a CUDA device wanted", qkv)
+    if dev != _current():
+        with torch.cuda.device(dev):
+            return op_rope_paged_store_q8(qkv, rope, pos, slot, cache, n_head, bias, q_norm, k_norm, eps, out, status)
+    q_type = src_type = _type_of(qkv, "qkv")
+    if out is None:
+        out = torch.zeros((n, n_head * hd), dtype=qkv.dtype, device=qkv.device)
+        q_stride = n_head * hd
+    else:
+        if not (out.shape == (n, n_head * hd) and out.get_device() == dev):
+            _refuse("out: [n][n_head*head_dim] wanted", out)
+        q_stride, one = out.stride()
+        if one != 1:
+            _refuse("out: contiguous rows wanted", out)
+        q_type = _type_of(out, "out")
+    if n == 0:
+        return out
+    rc = _rope_paged_store_q8(qkv.data_ptr(), src_type, row_stride, None if bias is None else bias.data_ptr(),
+                              None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
+                              eps, rope.ptr, pos.data_ptr(), slot.data_ptr(), n, n_head, cache.ptr, out.data_ptr(), q_type,
+                              q_stride, None if status is None else status.data_ptr(), _stream_of(dev))
+    if rc:
+        raise MinferError(rc, "op_rope_paged_store_q8")
+    return out
+
+
+def op_paged_read_q8(cache: PagedCacheQ8, slot, dtype=torch.float32, out=None, status=None):
+    """Rows of a quantized cache as floats (minfer_op_paged_read_q8): slot int32
+    [n].  Returns (k, v) [n][n_head_kv*head_dim] of `dtype`, or fills `out`, two such
+    tensors of one type and stride, either of which may be None.  Rows with a
+    negative slot are skipped (without `out` they are zero)."""
+    dev, n = slot.get_device(), slot.numel()
+    width = cache.n_head_kv * cache.head_dim
+    if not (slot.dtype is _I32 and slot.is_contiguous() and dev == cache.index):
+        _refuse("slot: int32 [n] on the cache's device wanted", slot)
+    if status is not None and not (status.dtype is _I32 and status.numel() == 1 and status.get_device() == dev):
+        _refuse("status: int32 [1] wanted", status)
+    if dev < 0:
+        _refuse("a CUDA device wanted", slot)
+    if dev != _current():
+        with torch.cuda.device(dev):
+            return op_paged_read_q8(cache, slot, dtype, out, status)
+    if out is None:
+        new = torch.zeros((2, n, width), dtype=dtype, device=slot.device)
+        out = k, v = new[0], new[1]
+        stride, some = width, new
+    else:
+        k, v = out
+        some = v if k is None else k
+        if some is None or not (some.shape == (n, width) and some.get_device() == dev):
+            _refuse("out: [n][n_head_kv*head_dim] wanted", k, v)
+        stride, one = some.stride()
+        if one != 1:
+            _refuse("out: contiguous rows wanted", some)
+        if k is not None and v is not None and not (v.dtype is k.dtype and v.shape == k.shape and (v.stride() == k.stride() or n == 1 and v.stride(1) == 1)
+                                                    and v.get_device() == dev):
+            _refuse("out: k and v differ", k, v)
+    kind = _type_of(some, "out")
+    if n == 0:
+        return out
+    rc = _paged_read_q8(cache.ptr, slot.data_ptr(), n, kind, None if k is None else k.data_ptr(), None if v is None else v.data_ptr(),
+                        stride, None if status is None else status.data_ptr(), _stream_of(dev))
+    if rc:
+        raise MinferError(rc, "op_paged_read_q8")
+    return out
+
+
 def op_paged_attention_workspace(cache: PagedCache, n_req: int, n_head: int) -> Workspace:
     """A workspace for op_paged_attention calls of up to n_req requests, one call
     at a time."""
@@ -293,6 +414,74 @@ def op_paged_attention(q, cache: PagedCache, table, length, n_head: int, scale: 
                           None if status is None else status.data_ptr(), _stream_of(dev))
     if rc:
         raise MinferError(rc, "op_paged_attention")
+    return out
+
+
+def op_paged_attention_q8_workspace(cache: PagedCacheQ8, n_req: int, n_head: int) -> Workspace:
+    """A workspace for op_paged_attention_q8 calls of up to n_req requests, one call
+    at a time."""
+    n = ctypes.c_int64()
+    with torch.cuda.device(cache.device):
+        check(_L.minfer_op_paged_attention_q8_workspace(n_req, n_head, cache.ptr, ctypes.byref(n)),
+              "op_paged_attention_q8_workspace")
+        return Workspace(n.value, cache.device, "op_paged_attention_q8")
+
+
+def op_paged_attention_q8(q, cache: PagedCacheQ8, table, length, n_head: int, scale: float | None = None,
+                          out=None, lse=None, workspace: Workspace | None = None, status=None):
+    """op_paged_attention over a quantized cache (minfer_op_paged_attention_q8): q
+    [n_req][n_head*head_dim] of any of the three types, o like q."""
+    dev, width = q.get_device(), n_head * cache.head_dim
+    shape = q.shape
+    if not (len(shape) == 2 and shape[1] == width and dev == cache.index):
+        _refuse(f"q: rows of {width} on {cache.device} wanted", q)
+    n = shape[0]
+    q_stride, one = q.stride()
+    if one != 1:
+        _refuse("q: contiguous rows wanted", q)
+    pages = table.shape
+    if not (table.dtype is _I32 and len(pages) == 2 and pages[0] == n and table.get_device() == dev):
+        _refuse("table: int32 [n_req][max_pages] wanted", table)
+    table_stride, one = table.stride()
+    max_pages = pages[1]
+    if one != 1 and max_pages > 1:
+        _refuse("table: contiguous rows wanted", table)
+    if not (length.dtype is _I32 and length.numel() == n and length.is_contiguous() and length.get_device() == dev):
+        _refuse("length: int32 [n_req] wanted", length)
+    if lse is not None and not (lse.dtype is _F32 and lse.shape == (n, n_head) and lse.is_contiguous()
+                                and lse.get_device() == dev):
+        _refuse("lse: float32 [n_req][n_head] wanted", lse)
+    if status is not None and not (status.dtype is _I32 and status.numel() == 1 and status.get_device() == dev):
+        _refuse("status: int32 [1] wanted", status)
+    if dev < 0:
+        _refuse("a CUDA device wanted", q)
+    if dev != _current():
+        with torch.cuda.device(dev):
+            return op_paged_attention_q8(q, cache, table, length, n_head, scale, out, lse, workspace, status)
+    if out is None:
+        out = torch.zeros((n, width), dtype=q.dtype, device=q.device)
+        o_stride = width
+    else:
+        if not (out.dtype is q.dtype and out.shape == shape and out.get_device() == dev):
+            _refuse("out: like q wanted", out)
+        o_stride, one = out.stride()
+        if one != 1:
+            _refuse("out: contiguous rows wanted", out)
+    kind = _type_of(q, "q")
+    if n == 0:
+        return out
+    if workspace is None:
+        workspace = op_paged_attention_q8_workspace(cache, n, n_head)
+    elif workspace.index != dev:
+        _refuse("workspace: on the tensors' device wanted", workspace.buffer)
+    elif workspace.op != "op_paged_attention_q8":
+        workspace.claim("op_paged_attention_q8")
+    rc = _paged_attention_q8(q.data_ptr(), kind, q_stride, cache.ptr, table.data_ptr(), table_stride, max_pages,
+                             length.data_ptr(), n, n_head, scale or 0.0, out.data_ptr(), o_stride,
+                             None if lse is None else lse.data_ptr(), workspace.ptr, workspace.nbytes,
+                             None if status is None else status.data_ptr(), _stream_of(dev))
+    if rc:
+        raise MinferError(rc, "op_paged_attention_q8")
     return out
 
 

@@ -53,6 +53,95 @@ int check_cache(const minfer_paged_cache* c, PagedCache* out) {
   return MINFER_OK;
 }
 
+int check_cache(const minfer_paged_cache_q8* c, PagedCache* out, PagedScales* scales) {
+  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || c->n_pages <= 0 || c->page_size <= 0 || c->n_head_kv <= 0)
+    return MINFER_ERR_ARG;
+  if (c->head_dim != 64 && c->head_dim != 128) return MINFER_ERR_SHAPE;
+  const int blocks = c->head_dim / 32;  // scales of a row
+  auto codes_ok = [](int64_t n, int64_t count) { return count == 1 || (n >= 0 && n % 16 == 0); };
+  auto scales_ok = [&](int64_t n, int64_t count) { return count == 1 || (n >= 0 && n % blocks == 0); };
+  auto scale_ok = [&](const void* p) { return reinterpret_cast<uintptr_t>(p) % (2 * blocks) == 0; };
+  if (!aligned16(c->k) || !aligned16(c->v) || !scale_ok(c->k_scale) || !scale_ok(c->v_scale) ||
+      !codes_ok(c->page_stride, c->n_pages) || !codes_ok(c->row_stride, c->page_size) ||
+      !codes_ok(c->head_stride, c->n_head_kv) || !scales_ok(c->scale_page_stride, c->n_pages) ||
+      !scales_ok(c->scale_row_stride, c->page_size) || !scales_ok(c->scale_head_stride, c->n_head_kv))
+    return MINFER_ERR_ARG;
+  if (!fits31(c->n_pages, c->page_size)) return MINFER_ERR_TOO_LARGE;
+  *out = PagedCache{c->k, c->v, c->n_pages, c->page_size, c->n_head_kv, c->head_dim,
+                    c->n_pages > 1 ? c->page_stride : 0, c->page_size > 1 ? c->row_stride : 0,
+                    c->n_head_kv > 1 ? c->head_stride : 0, PageDiv(c->page_size)};
+  *scales = PagedScales{c->k_scale, c->v_scale, c->n_pages > 1 ? c->scale_page_stride : 0,
+                        c->page_size > 1 ? c->scale_row_stride : 0, c->n_head_kv > 1 ? c->scale_head_stride : 0};
+  return MINFER_OK;
+}
+
+// The checks and arguments of the RoPE store behind those of the cache; to_type is
+// that of d_q_out.
+int rope_store_args(RopePagedArgs& a, const void* d_qkv, int type, int64_t row_stride, const float* d_bias,
+                    const float* d_qnorm, const float* d_knorm, float eps, const minfer_rope_table* rope,
+                    const int32_t* d_pos, const int32_t* d_slot, int n_tokens, int n_head, void* d_q_out, int to_type,
+                    int64_t q_stride, int* d_status) {
+  const int hd = a.c.hd, nkv = a.c.nkv;
+  if (!d_qkv || !rope || !d_pos || !d_slot || !d_q_out || n_tokens <= 0 || n_head <= 0 || n_head % nkv != 0 ||
+      (d_qnorm == nullptr) != (d_knorm == nullptr) || !(eps >= 0))
+    return MINFER_ERR_ARG;
+  if (n_head > kMaxHeads) return MINFER_ERR_TOO_LARGE;
+  if ((type != MINFER_F32 && type != to_type) || rope->head_dim != hd || rope->rot_dim < 2 || rope->rot_dim > hd ||
+      rope->rot_dim % 2 || (rope->style != MINFER_ROPE_HALF && rope->style != MINFER_ROPE_INTERLEAVED))
+    return MINFER_ERR_SHAPE;
+  const int64_t q = (int64_t)n_head * hd, kv = (int64_t)nkv * hd;
+  if (!aligned16(d_qkv) || !aligned16(d_q_out) || !aligned16(d_bias) || !aligned16(d_qnorm) ||
+      !aligned16(d_knorm) || !stride_ok(row_stride, n_tokens, type) || !stride_ok(q_stride, n_tokens, to_type) ||
+      (n_tokens > 1 && (row_stride < q + 2 * kv || q_stride < q)))
+    return MINFER_ERR_ARG;
+  a.qkv = d_qkv;
+  a.row_stride = row_stride;
+  a.bias = d_bias;
+  a.q_norm = d_qnorm;
+  a.k_norm = d_knorm;
+  a.eps = eps;
+  a.pos = d_pos;
+  a.slot = d_slot;
+  a.n_tokens = n_tokens;
+  a.nh = n_head;
+  a.q_out = d_q_out;
+  a.q_stride = q_stride;
+  a.status = d_status;
+  a.rope = *rope;
+  return MINFER_OK;
+}
+
+// The same of the attention; type is that of q and o.
+int attention_args(PagedAttnRows& a, const PagedCache& c, int type, const void* d_q, int64_t q_stride,
+                   const int32_t* d_table, int64_t table_stride, int max_pages, const int32_t* d_len, int n_req,
+                   int n_head, float scale, void* d_o, int64_t o_stride, float* d_lse, void* d_workspace,
+                   int* d_status) {
+  const int64_t q = (int64_t)n_head * c.hd;
+  if (!d_q || !d_table || !d_len || !d_o || !d_workspace || n_req <= 0 || n_head <= 0 || n_head % c.nkv != 0 ||
+      max_pages <= 0 || !(scale >= 0) || !std::isfinite(scale))
+    return MINFER_ERR_ARG;
+  if (!aligned16(d_q) || !aligned16(d_o) || !aligned16(d_workspace) || !stride_ok(q_stride, n_req, type) ||
+      !stride_ok(o_stride, n_req, type) ||
+      (n_req > 1 && (q_stride < q || o_stride < q || table_stride < max_pages)))
+    return MINFER_ERR_ARG;
+  if (!fits31(max_pages, c.page_size) || n_head > kMaxHeads) return MINFER_ERR_TOO_LARGE;
+  a.q = d_q;
+  a.q_stride = q_stride;
+  a.table = d_table;
+  a.table_stride = table_stride;
+  a.max_pages = max_pages;
+  a.len = d_len;
+  a.n_req = n_req;
+  a.nh = n_head;
+  a.scale = scale == 0.f ? 1.0f / std::sqrt((float)c.hd) : scale;
+  a.o = d_o;
+  a.o_stride = o_stride;
+  a.lse = d_lse;
+  a.ws = d_workspace;
+  a.status = d_status;
+  return MINFER_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -129,37 +218,13 @@ int minfer_op_rope_paged_store(const void* d_qkv, int type, int64_t row_stride,
                                const minfer_paged_cache* cache, void* d_q_out, int64_t q_stride,
                                int* d_status, void* stream) {
   RopePagedArgs a;
-  const int rc = check_cache(cache, &a.c);
+  int rc = check_cache(cache, &a.c);
   if (rc != MINFER_OK) return rc;
-  if (!d_qkv || !rope || !d_pos || !d_slot || !d_q_out || n_tokens <= 0 || n_head <= 0 ||
-      n_head % cache->n_head_kv != 0 || (d_qnorm == nullptr) != (d_knorm == nullptr) || !(eps >= 0))
-    return MINFER_ERR_ARG;
-  if (n_head > kMaxHeads) return MINFER_ERR_TOO_LARGE;
-  if ((type != MINFER_F32 && type != cache->type) || rope->head_dim != cache->head_dim ||
-      rope->rot_dim < 2 || rope->rot_dim > cache->head_dim || rope->rot_dim % 2 ||
-      (rope->style != MINFER_ROPE_HALF && rope->style != MINFER_ROPE_INTERLEAVED))
-    return MINFER_ERR_SHAPE;
-  const int64_t q = (int64_t)n_head * cache->head_dim, kv = (int64_t)cache->n_head_kv * cache->head_dim;
-  if (!aligned16(d_qkv) || !aligned16(d_q_out) || !aligned16(d_bias) || !aligned16(d_qnorm) ||
-      !aligned16(d_knorm) || !stride_ok(row_stride, n_tokens, type) || !stride_ok(q_stride, n_tokens, cache->type) ||
-      (n_tokens > 1 && (row_stride < q + 2 * kv || q_stride < q)))
-    return MINFER_ERR_ARG;
+  rc = rope_store_args(a, d_qkv, type, row_stride, d_bias, d_qnorm, d_knorm, eps, rope, d_pos, d_slot, n_tokens, n_head,
+                       d_q_out, cache->type, q_stride, d_status);
+  if (rc != MINFER_OK) return rc;
   const int sms = current_sms();
   if (sms == 0) return MINFER_ERR_CUDA;
-  a.qkv = d_qkv;
-  a.row_stride = row_stride;
-  a.bias = d_bias;
-  a.q_norm = d_qnorm;
-  a.k_norm = d_knorm;
-  a.eps = eps;
-  a.pos = d_pos;
-  a.slot = d_slot;
-  a.n_tokens = n_tokens;
-  a.nh = n_head;
-  a.q_out = d_q_out;
-  a.q_stride = q_stride;
-  a.status = d_status;
-  a.rope = *rope;
   return from_cuda(rope_paged_launch(a, type, cache->type, sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -182,35 +247,83 @@ int minfer_op_paged_attention(const void* d_q, int64_t q_stride, const minfer_pa
                               int64_t o_stride, float* d_lse, void* d_workspace,
                               int64_t workspace_bytes, int* d_status, void* stream) {
   PagedAttnArgs a;
-  const int rc = check_cache(cache, &a.c);
+  int rc = check_cache(cache, &a.c);
   if (rc != MINFER_OK) return rc;
-  const int64_t q = (int64_t)n_head * cache->head_dim;
-  if (!d_q || !d_table || !d_len || !d_o || !d_workspace || n_req <= 0 || n_head <= 0 ||
-      n_head % cache->n_head_kv != 0 || max_pages <= 0 || !(scale >= 0) || !std::isfinite(scale))
-    return MINFER_ERR_ARG;
-  if (!aligned16(d_q) || !aligned16(d_o) || !aligned16(d_workspace) || !stride_ok(q_stride, n_req, cache->type) ||
-      !stride_ok(o_stride, n_req, cache->type) || (n_req > 1 && (q_stride < q || o_stride < q || table_stride < max_pages)))
-    return MINFER_ERR_ARG;
-  if (!fits31(max_pages, cache->page_size) || n_head > kMaxHeads) return MINFER_ERR_TOO_LARGE;
+  rc = attention_args(a, a.c, cache->type, d_q, q_stride, d_table, table_stride, max_pages, d_len, n_req, n_head, scale, d_o,
+                      o_stride, d_lse, d_workspace, d_status);
+  if (rc != MINFER_OK) return rc;
   const int sms = current_sms();
   if (sms == 0) return MINFER_ERR_CUDA;
-  if (workspace_bytes < paged_attn_workspace(n_head / a.c.nkv, a.c.hd, cache->type, sms))
-    return MINFER_ERR_TOO_LARGE;
-  a.q = d_q;
-  a.q_stride = q_stride;
-  a.table = d_table;
-  a.table_stride = table_stride;
-  a.max_pages = max_pages;
-  a.len = d_len;
-  a.n_req = n_req;
-  a.nh = n_head;
-  a.scale = scale == 0.f ? 1.0f / std::sqrt((float)cache->head_dim) : scale;
-  a.o = d_o;
-  a.o_stride = o_stride;
-  a.lse = d_lse;
-  a.ws = d_workspace;
-  a.status = d_status;
+  if (workspace_bytes < paged_attn_workspace(n_head / a.c.nkv, a.c.hd, cache->type, sms)) return MINFER_ERR_TOO_LARGE;
   return from_cuda(paged_attn_launch(a, cache->type, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int minfer_op_rope_paged_store_q8(const void* d_qkv, int type, int64_t row_stride, const float* d_bias,
+                                  const float* d_qnorm, const float* d_knorm, float eps,
+                                  const minfer_rope_table* rope, const int32_t* d_pos, const int32_t* d_slot,
+                                  int n_tokens, int n_head, const minfer_paged_cache_q8* cache, void* d_q_out,
+                                  int q_type, int64_t q_stride, int* d_status, void* stream) {
+  RopePagedQ8Args a;
+  int rc = check_cache(cache, &a.c, &a.s);
+  if (rc != MINFER_OK) return rc;
+  if (!type_ok(q_type)) return MINFER_ERR_SHAPE;
+  rc = rope_store_args(a, d_qkv, type, row_stride, d_bias, d_qnorm, d_knorm, eps, rope, d_pos, d_slot, n_tokens, n_head,
+                       d_q_out, q_type, q_stride, d_status);
+  if (rc != MINFER_OK) return rc;
+  const int sms = current_sms();
+  if (sms == 0) return MINFER_ERR_CUDA;
+  return from_cuda(rope_paged_q8_launch(a, type, q_type, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int minfer_op_paged_read_q8(const minfer_paged_cache_q8* cache, const int32_t* d_slot, int n_rows, int type,
+                            void* d_k, void* d_v, int64_t out_stride, int* d_status, void* stream) {
+  PagedReadArgs a;
+  const int rc = check_cache(cache, &a.c, &a.s);
+  if (rc != MINFER_OK) return rc;
+  if (!type_ok(type)) return MINFER_ERR_SHAPE;
+  if (!d_slot || (!d_k && !d_v) || n_rows <= 0 || !aligned16(d_k) || !aligned16(d_v) ||
+      !stride_ok(out_stride, n_rows, type) || (n_rows > 1 && out_stride < (int64_t)a.c.nkv * a.c.hd))
+    return MINFER_ERR_ARG;
+  if (a.c.nkv > kMaxHeads) return MINFER_ERR_TOO_LARGE;
+  if (current_sms() == 0) return MINFER_ERR_CUDA;
+  a.slot = d_slot;
+  a.n_rows = n_rows;
+  a.k = d_k;
+  a.v = d_v;
+  a.out_stride = out_stride;
+  a.status = d_status;
+  return from_cuda(paged_read_launch(a, type, static_cast<cudaStream_t>(stream)));
+}
+
+int minfer_op_paged_attention_q8_workspace(int n_req, int n_head, const minfer_paged_cache_q8* cache,
+                                           int64_t* bytes) {
+  PagedCache c;
+  PagedScales s;
+  const int rc = check_cache(cache, &c, &s);
+  if (rc != MINFER_OK) return rc;
+  if (!bytes || n_req <= 0 || n_head <= 0 || n_head % c.nkv != 0) return MINFER_ERR_ARG;
+  if (n_head > kMaxHeads) return MINFER_ERR_TOO_LARGE;
+  const int sms = current_sms();
+  if (sms == 0) return MINFER_ERR_CUDA;
+  *bytes = paged_attn_q8_workspace(c.hd, sms);
+  return MINFER_OK;
+}
+
+int minfer_op_paged_attention_q8(const void* d_q, int type, int64_t q_stride, const minfer_paged_cache_q8* cache,
+                                 const int32_t* d_table, int64_t table_stride, int max_pages, const int32_t* d_len,
+                                 int n_req, int n_head, float scale, void* d_o, int64_t o_stride, float* d_lse,
+                                 void* d_workspace, int64_t workspace_bytes, int* d_status, void* stream) {
+  PagedAttnQ8Args a;
+  int rc = check_cache(cache, &a.c, &a.s);
+  if (rc != MINFER_OK) return rc;
+  if (!type_ok(type)) return MINFER_ERR_SHAPE;
+  rc = attention_args(a, a.c, type, d_q, q_stride, d_table, table_stride, max_pages, d_len, n_req, n_head, scale, d_o, o_stride,
+                      d_lse, d_workspace, d_status);
+  if (rc != MINFER_OK) return rc;
+  const int sms = current_sms();
+  if (sms == 0) return MINFER_ERR_CUDA;
+  if (workspace_bytes < paged_attn_q8_workspace(a.c.hd, sms)) return MINFER_ERR_TOO_LARGE;
+  return from_cuda(paged_attn_q8_launch(a, type, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int minfer_op_token_logprobs_workspace(int64_t rows, int64_t vocab, int k, int64_t* bytes) {

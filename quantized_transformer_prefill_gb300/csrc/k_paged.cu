@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -313,6 +314,13 @@ struct alignas(E * sizeof(T)) Vec {
   T v[E];
 };
 
+// the larger of two, or NaN if one is
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 // cos and sin of 2 pi * f / 2^64.  The quadrant comes off in integers; the rest,
 // at most an eighth of a turn, is taken to 2^-34 of a turn (an angle of 4e-10,
 // below f32's step for a sine or cosine), and its sine and cosine are the Taylor
@@ -360,8 +368,14 @@ constexpr int kRpRing = 8;       // units of a warp on their way or at work
 // partner of an element lies in the lane itself (interleaved pairs), in another
 // lane at the same place (half a rotation is a multiple of E), or, with rotated
 // sizes that are no multiples of E, anywhere, and comes through shared memory.
-template <typename TS, typename TD, int HD>
-__global__ void __launch_bounds__(kRpWarps * 32) rope_paged_kernel(const __grid_constant__ RopePagedArgs a, int tokens, int swap_floats, int bias_floats) {
+//
+// Into a pool of Q8_0 rows (Args = RopePagedQ8Args; TD is then Q's type alone) a
+// block is 32 / E neighbouring lanes of a unit: its maximum takes two or three
+// shuffles, and a lane stores its E codes as one vector.
+template <typename TS, typename TD, int HD, typename Args>
+__global__ void __launch_bounds__(kRpWarps * 32) rope_paged_kernel(const __grid_constant__ Args a, int tokens, int swap_floats, int bias_floats) {
+  constexpr bool kQ8 = std::is_same<Args, RopePagedQ8Args>::value;
+  using TC = typename std::conditional<kQ8, int8_t, TD>::type;  // of the cache
   constexpr int E = 16 / sizeof(TS), kLanes = HD / E, kPer = 32 / kLanes;  // lanes of a head, heads of a unit
   using VS = Vec<TS, E>;
   using VD = Vec<TD, E>;
@@ -447,8 +461,8 @@ __global__ void __launch_bounds__(kRpWarps * 32) rope_paged_kernel(const __grid_
   const int page = a.c.div.of(slot);
   const int64_t at = (int64_t)page * a.c.page_stride + (int64_t)(slot - page * a.c.page_size) * a.c.row_stride;
   TD* const qdst = static_cast<TD*>(a.q_out) + (int64_t)t * a.q_stride + d0;
-  TD* const kdst = static_cast<TD*>(a.c.k) + (at + d0 - a.nh * a.c.head_stride);
-  TD* const vdst = static_cast<TD*>(a.c.v) + (at + d0 - nqk * a.c.head_stride);
+  TC* const kdst = static_cast<TC*>(a.c.k) + (at + d0 - a.nh * a.c.head_stride);
+  TC* const vdst = static_cast<TC*>(a.c.v) + (at + d0 - nqk * a.c.head_stride);
   const float* const bias = !a.bias ? nullptr : (bias_floats ? rp_smem + swap_floats : a.bias) + lane * E;
 
   int stage = 0;
@@ -524,7 +538,36 @@ __global__ void __launch_bounds__(kRpWarps * 32) rope_paged_kernel(const __grid_
           for (int e = 0; e < E; ++e) y[e] = fmaf(z[e], sn[e], y[e] * cs[e]);
         }
       }
-      if (h < heads) {
+      if constexpr (kQ8) {
+        if ((u + 1) * kPer > a.nh) {  // some head of the unit is one of K or V
+          float amax = fabsf(y[0]);
+#pragma unroll
+          for (int e = 1; e < E; ++e) amax = max_nan(amax, fabsf(y[e]));
+#pragma unroll
+          for (int o = 16 / E; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          float d = __fdiv_rn(amax, 127.f);
+          __half d16 = __float2half_rn(d);
+          const bool fine = __half2float(d16) <= 65504.f;
+          if (!fine) d16 = __ushort_as_half(0x7FFF);
+          const float id = fine && d >= 0x1p-126f ? q8_inv(d) : 0.f;
+          if (h >= a.nh && h < heads) {
+            Vec<int8_t, E> out;
+#pragma unroll
+            // (a code is the low byte of the sum's bits)
+            for (int e = 0; e < E; ++e) out.v[e] = (int8_t)__float_as_uint((fine ? q8_code(y[e], id) : 0.f) + 0x1.8p23f);
+            const int64_t sat = (int64_t)page * a.s.page_stride + (int64_t)(slot - page * a.c.page_size) * a.s.row_stride + d0 / 32;
+            *reinterpret_cast<Vec<int8_t, E>*>((h < nqk ? kdst : vdst) + h * a.c.head_stride) = out;
+            if (d0 % 32 == 0)
+              (h < nqk ? static_cast<__half*>(a.s.k) - a.nh * a.s.head_stride : static_cast<__half*>(a.s.v) - nqk * a.s.head_stride)[sat + h * a.s.head_stride] = d16;
+          }
+        }
+        if (h < a.nh) {
+          VD out;
+#pragma unroll
+          for (int e = 0; e < E; ++e) out.v[e] = from_f32<TD>(y[e]);
+          *reinterpret_cast<VD*>(qdst + h * HD) = out;
+        }
+      } else if (h < heads) {
         VD out;
 #pragma unroll
         for (int e = 0; e < E; ++e) out.v[e] = from_f32<TD>(y[e]);
@@ -535,8 +578,8 @@ __global__ void __launch_bounds__(kRpWarps * 32) rope_paged_kernel(const __grid_
   }
 }
 
-template <typename TS, typename TD, int HD>
-cudaError_t rope_paged_sized(const RopePagedArgs& a, int num_sms, cudaStream_t st) {
+template <typename TS, typename TD, int HD, typename Args>
+cudaError_t rope_paged_sized(const Args& a, int num_sms, cudaStream_t st) {
   constexpr int E = 16 / sizeof(TS);
   // One token per CTA while that keeps the GPU from being full, for its eight
   // warps finish sooner; else up to four, which share the work before the heads.
@@ -545,14 +588,85 @@ cudaError_t rope_paged_sized(const RopePagedArgs& a, int num_sms, cudaStream_t s
   const bool swap = a.rope.style == MINFER_ROPE_HALF ? (a.rope.rot_dim / 2) % E != 0 : a.rope.rot_dim % E != 0;
   const int swap_floats = swap ? kRpWarps * 32 * E : 0, width = (a.nh + 2 * a.c.nkv) * HD;
   const int bias_floats = a.bias && width <= kRpMaxBias ? width : 0, smem = (swap_floats + bias_floats) * (int)sizeof(float);
-  const cudaError_t e = allow_smem<rope_paged_kernel<TS, TD, HD>>((kRpWarps * 32 * E + kRpMaxBias) * (int)sizeof(float));
+  const cudaError_t e = allow_smem<rope_paged_kernel<TS, TD, HD, Args>>((kRpWarps * 32 * E + kRpMaxBias) * (int)sizeof(float));
   if (e != cudaSuccess) return e;
-  return launch_pdl(rope_paged_kernel<TS, TD, HD>, dim3((unsigned)((a.n_tokens - 1) / tokens + 1)), dim3(32 * kRpWarps), smem, st, a, tokens,
+  return launch_pdl(rope_paged_kernel<TS, TD, HD, Args>, dim3((unsigned)((a.n_tokens - 1) / tokens + 1)), dim3(32 * kRpWarps), smem, st, a, tokens,
                     swap_floats, bias_floats);
 }
-template <typename TS, typename TD>
-cudaError_t rope_paged_typed(const RopePagedArgs& a, int num_sms, cudaStream_t st) {
+template <typename TS, typename TD, typename Args>
+cudaError_t rope_paged_typed(const Args& a, int num_sms, cudaStream_t st) {
   return a.c.hd == 64 ? rope_paged_sized<TS, TD, 64>(a, num_sms, st) : rope_paged_sized<TS, TD, 128>(a, num_sms, st);
+}
+// `type` is the cache's, or with a pool of Q8_0 rows Q's
+template <typename Args>
+cudaError_t rope_paged_any(const Args& a, int src_type, int type, int num_sms, cudaStream_t st) {
+  if (type == MINFER_F32) return rope_paged_typed<float, float>(a, num_sms, st);
+  if (type == MINFER_F16)
+    return src_type == MINFER_F32 ? rope_paged_typed<float, __half>(a, num_sms, st)
+                                  : rope_paged_typed<__half, __half>(a, num_sms, st);
+  return src_type == MINFER_F32 ? rope_paged_typed<float, __nv_bfloat16>(a, num_sms, st)
+                                : rope_paged_typed<__nv_bfloat16, __nv_bfloat16>(a, num_sms, st);
+}
+
+// ------------------------------------------------------------------ read back
+// Rows of a pool of Q8_0 rows as floats.  Bound by HBM.  A CTA takes neighbouring
+// rows, a thread 16 bytes of output at a time, kRdFlight of them on their way at once,
+// so that loads and stores of a warp are contiguous.
+constexpr int kRdThreads = 256, kRdFlight = 4;
+
+template <typename TO, int HD>
+__global__ void __launch_bounds__(kRdThreads) paged_read_kernel(const __grid_constant__ PagedReadArgs a, int rows, PageDiv vectors) {
+  constexpr int E = 16 / sizeof(TO), kLanes = HD / E;  // values of a vector, vectors of a head
+  pdl_trigger();
+  pdl_wait();
+  const int64_t r0 = (int64_t)blockIdx.x * rows;
+  const int items = (int)min((int64_t)rows, a.n_rows - r0) * vectors.d, slots = a.c.n_pages * a.c.page_size;
+  const int of_k = a.k ? a.c.nkv * kLanes : 0;  // vectors of K in a row; those of V follow
+  for (int i0 = threadIdx.x; i0 < items; i0 += kRdThreads * kRdFlight) {
+    Vec<int8_t, E> code[kRdFlight];
+    __half d[kRdFlight];
+    TO* dst[kRdFlight];
+#pragma unroll
+    for (int j = 0; j < kRdFlight; ++j) {
+      const int i = i0 + j * kRdThreads;
+      dst[j] = nullptr;
+      if (i >= items) continue;
+      const int row = vectors.of(i);
+      int at = i - row * vectors.d;
+      const int slot = a.slot[r0 + row];
+      if (slot < 0 || slot >= slots) {
+        if (slot >= 0 && at == 0) set_error(a.status, MINFER_ERR_POS_OOB);
+        continue;
+      }
+      const bool is_v = at >= of_k;
+      if (is_v) at -= of_k;
+      const int head = at / kLanes, d0 = (at % kLanes) * E, page = a.c.div.of(slot), in_page = slot - page * a.c.page_size;
+      code[j] = *reinterpret_cast<const Vec<int8_t, E>*>(static_cast<const int8_t*>(is_v ? a.c.v : a.c.k) + page * a.c.page_stride +
+                                                         in_page * a.c.row_stride + head * a.c.head_stride + d0);
+      d[j] = (static_cast<const __half*>(is_v ? a.s.v : a.s.k) + page * a.s.page_stride + in_page * a.s.row_stride + head * a.s.head_stride)[d0 / 32];
+      dst[j] = static_cast<TO*>(is_v ? a.v : a.k) + (r0 + row) * a.out_stride + at * E;
+    }
+#pragma unroll
+    for (int j = 0; j < kRdFlight; ++j) {
+      if (!dst[j]) continue;
+      const float f = __half2float(d[j]);
+      Vec<TO, E> out;
+#pragma unroll
+      for (int e = 0; e < E; ++e) out.v[e] = from_f32<TO>((float)code[j].v[e] * f);
+      *reinterpret_cast<Vec<TO, E>*>(dst[j]) = out;
+    }
+  }
+}
+
+template <typename TO, int HD>
+cudaError_t paged_read_sized(const PagedReadArgs& a, cudaStream_t st) {
+  const int vectors = a.c.nkv * HD * (int)sizeof(TO) / 16 * ((a.k ? 1 : 0) + (a.v ? 1 : 0));
+  const int rows = std::max(1, kRdThreads * kRdFlight / vectors);
+  return launch_pdl(paged_read_kernel<TO, HD>, dim3((unsigned)((a.n_rows - 1) / rows + 1)), dim3(kRdThreads), 0, st, a, rows, PageDiv(vectors));
+}
+template <typename TO>
+cudaError_t paged_read_typed(const PagedReadArgs& a, cudaStream_t st) {
+  return a.c.hd == 64 ? paged_read_sized<TO, 64>(a, st) : paged_read_sized<TO, 128>(a, st);
 }
 
 // Whether the current device runs a cluster of sixteen CTAs, more than the portable
@@ -613,12 +727,16 @@ cudaError_t page_tables_launch(const PageTablesArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t rope_paged_launch(const RopePagedArgs& a, int src_type, int cache_type, int num_sms, cudaStream_t st) {
-  if (cache_type == MINFER_F32) return rope_paged_typed<float, float>(a, num_sms, st);
-  if (cache_type == MINFER_F16)
-    return src_type == MINFER_F32 ? rope_paged_typed<float, __half>(a, num_sms, st)
-                                  : rope_paged_typed<__half, __half>(a, num_sms, st);
-  return src_type == MINFER_F32 ? rope_paged_typed<float, __nv_bfloat16>(a, num_sms, st)
-                                : rope_paged_typed<__nv_bfloat16, __nv_bfloat16>(a, num_sms, st);
+  return rope_paged_any(a, src_type, cache_type, num_sms, st);
+}
+cudaError_t rope_paged_q8_launch(const RopePagedQ8Args& a, int src_type, int q_type, int num_sms, cudaStream_t st) {
+  return rope_paged_any(a, src_type, q_type, num_sms, st);
+}
+
+cudaError_t paged_read_launch(const PagedReadArgs& a, int type, cudaStream_t st) {
+  return type == MINFER_F32   ? paged_read_typed<float>(a, st)
+         : type == MINFER_F16 ? paged_read_typed<__half>(a, st)
+                              : paged_read_typed<__nv_bfloat16>(a, st);
 }
 
 }  // namespace minfer

@@ -395,11 +395,37 @@ struct RopePagedArgs {
 cudaError_t rope_paged_launch(const RopePagedArgs& a, int src_type, int cache_type, int num_sms,
                               cudaStream_t stream);
 
+// The scales of a pool of Q8_0 rows (strides in scales); the codes are a PagedCache
+// of one byte per element.
+struct PagedScales {
+  void* k;
+  void* v;
+  int64_t page_stride, row_stride, head_stride;
+};
+// The same with K and V quantized into such a pool; q_out has q_type.
+struct RopePagedQ8Args : RopePagedArgs {
+  PagedScales s;
+};
+cudaError_t rope_paged_q8_launch(const RopePagedQ8Args& a, int src_type, int q_type, int num_sms,
+                                 cudaStream_t stream);
+
+// k_paged.cu: rows of a pool of Q8_0 rows as floats.
+struct PagedReadArgs {
+  PagedCache c;
+  PagedScales s;
+  const int32_t* slot;
+  int n_rows;
+  void* k;  // either may be null
+  void* v;
+  int64_t out_stride;
+  int* status;
+};
+cudaError_t paged_read_launch(const PagedReadArgs& a, int type, cudaStream_t stream);
+
 // k_paged_attn.cu: one query row per request over its pages.
-struct PagedAttnArgs {
+struct PagedAttnRows {  // all but the cache
   const void* q;
   int64_t q_stride;
-  PagedCache c;
   const int32_t* table;
   int64_t table_stride;
   int max_pages;
@@ -412,8 +438,19 @@ struct PagedAttnArgs {
   void* ws;
   int* status;
 };
+struct PagedAttnArgs : PagedAttnRows {
+  PagedCache c;
+};
 int64_t paged_attn_workspace(int G, int hd, int type, int num_sms);
 cudaError_t paged_attn_launch(const PagedAttnArgs& a, int type, int num_sms, cudaStream_t stream);
+
+// k_paged_attn_q8.cu: the same over a pool of Q8_0 rows; `type` is that of q and o.
+struct PagedAttnQ8Args : PagedAttnRows {
+  PagedCache c;
+  PagedScales s;
+};
+int64_t paged_attn_q8_workspace(int hd, int num_sms);
+cudaError_t paged_attn_q8_launch(const PagedAttnQ8Args& a, int type, int num_sms, cudaStream_t stream);
 
 // k_logprobs.cu: log probabilities, entropy and top k of logits rows.
 struct LogprobsArgs {
