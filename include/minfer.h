@@ -604,6 +604,36 @@ int minfer_op_token_logprobs(const void* d_logits, int type, int64_t rows, int64
                              void* d_workspace, int64_t workspace_bytes, int* d_status,
                              void* stream);
 
+/* The next token of logits rows (walkthrough index, master table, row "Sampler":
+ * top-k, top-p, temperature, in that order; min-p and the other order have no
+ * counterpart on the pages).  Row r of d_logits (`type`, row_stride apart, vocab
+ * values, any alignment of the type) with settings of its own:
+ *   d_u[r]: a random number in [0, 1); a negative one marks a padding row, of which
+ *     no output is written;
+ *   d_temperature[r]: 1e-6 to 1e6, or 0 for the largest logit, whatever the rest says;
+ *   d_top_k[r]: how many tokens may be left; 0, less or vocab and more: all;
+ *   d_top_p[r] >= 0; 1 and more: off;
+ *   d_min_p[r] in [0, 1].
+ * The four may be NULL: 1, 0, 1 and 0.  Tokens in descending order of their logits,
+ * equal ones by ascending id: the first top_k; of those the shortest beginning whose
+ * weights reach top_p of their sum; of those the ones that weigh at least min_p times
+ * the first.  (At least the first is left.)  The weights of these filters are
+ * exp(x - max), or, with temperature_first, exp((x - max) / temperature).  What is left
+ * is drawn from with weights exp((x - max) / temperature): d_token[r] is the first id
+ * at which the sum of the weights of ids up to it exceeds u times the whole;
+ * d_logprob[r] (may be NULL) is the logarithm of its share.  A token that weighs less
+ * than 2^-60 of the first is not drawn.  Weights are held to 2^-31 of themselves, as
+ * whole numbers in units of 2^-(62 - log2 vocab) of the first, and summed without
+ * rounding (a u of 0 draws the first id that is left, however little it weighs): the
+ * result depends on the row and its settings alone, bit for bit.
+ * -inf logits are masked tokens; a row with nothing else gets token -1 and log
+ * probability -inf.  Device errors: MINFER_ERR_ARG for a setting out of its range, a
+ * NaN or +inf among the logits (no output of that row is written). */
+int minfer_op_sample(const void* d_logits, int type, int64_t rows, int64_t vocab, int64_t row_stride,
+                     const float* d_u, const float* d_temperature, const int32_t* d_top_k,
+                     const float* d_top_p, const float* d_min_p, int temperature_first,
+                     int32_t* d_token, float* d_logprob, int* d_status, void* stream);
+
 /* ---------------------------------------------------------------- misc */
 /* A static, NUL-terminated name of an error code (never NULL; "unknown error"
  * for codes outside the list).  The codes restate the pages' failures as

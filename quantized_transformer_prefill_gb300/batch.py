@@ -36,6 +36,7 @@ _rope_paged_store_q8 = _L.minfer_op_rope_paged_store_q8
 _paged_read_q8 = _L.minfer_op_paged_read_q8
 _paged_attention_q8 = _L.minfer_op_paged_attention_q8
 _token_logprobs = _L.minfer_op_token_logprobs
+_sample = _L.minfer_op_sample
 
 # The raw handle of a device's current stream and the current device's index:
 # torch's own accessors take 2 us for the first and 0.3 us for the second.
@@ -563,4 +564,63 @@ def op_token_logprobs(logits, ids=None, k: int = 0, out=None, workspace: Workspa
                          None if status is None else status.data_ptr(), _stream_of(dev))
     if rc:
         raise MinferError(rc, "op_token_logprobs")
+    return out
+
+
+def op_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, temperature_first: bool = False,
+              out=None, status=None):
+    """The next token of logits [rows][vocab] (float32, float16 or bfloat16, rows of
+    any distance that do not overlap) from the random numbers u (float32 [rows] in [0,
+    1), negative: skip the row), with settings per row (minfer_op_sample):
+    temperature float32 (None: 1; 0: the largest logit), top_k int32 (None, 0: off),
+    top_p float32 (None, 1: off), min_p float32 (None, 0: off).  The filters see the
+    logits as they are, or divided by the temperature with temperature_first.
+    Returns (token int32 [rows], logprob float32 [rows]: under what was drawn from),
+    or fills `out`, two such tensors, the second of which may be None.  Skipped and
+    refused rows are not written (without `out` token -1 and logprob 0)."""
+    dev, shape = logits.get_device(), logits.shape
+    if len(shape) != 2:
+        _refuse("logits: [rows][vocab] wanted", logits)
+    rows, vocab = shape
+    row_stride, one = logits.stride()
+    if one != 1 and vocab > 1:
+        _refuse("logits: contiguous rows wanted", logits)
+    if not (u.dtype is _F32 and u.numel() == rows and u.is_contiguous() and u.get_device() == dev):
+        _refuse("u: float32 [rows] wanted", u)
+    if temperature is not None and not (temperature.dtype is _F32 and temperature.numel() == rows and temperature.is_contiguous()
+                                        and temperature.get_device() == dev):
+        _refuse("temperature: float32 [rows] wanted", temperature)
+    if top_k is not None and not (top_k.dtype is _I32 and top_k.numel() == rows and top_k.is_contiguous() and top_k.get_device() == dev):
+        _refuse("top_k: int32 [rows] wanted", top_k)
+    if top_p is not None and not (top_p.dtype is _F32 and top_p.numel() == rows and top_p.is_contiguous() and top_p.get_device() == dev):
+        _refuse("top_p: float32 [rows] wanted", top_p)
+    if min_p is not None and not (min_p.dtype is _F32 and min_p.numel() == rows and min_p.is_contiguous() and min_p.get_device() == dev):
+        _refuse("min_p: float32 [rows] wanted", min_p)
+    if status is not None and not (status.dtype is _I32 and status.numel() == 1 and status.get_device() == dev):
+        _refuse("status: int32 [1] wanted", status)
+    if dev < 0:
+        _refuse("a CUDA device wanted", logits)
+    if dev != _current():
+        with torch.cuda.device(dev):
+            return op_sample(logits, u, temperature, top_k, top_p, min_p, temperature_first, out, status)
+    if out is None:
+        token = torch.full((rows,), -1, dtype=_I32, device=logits.device)
+        logprob = torch.zeros(rows, dtype=_F32, device=logits.device)
+        out = token, logprob
+    else:
+        token, logprob = out
+        if not (token.dtype is _I32 and token.numel() == rows and token.is_contiguous() and token.get_device() == dev):
+            _refuse("token: int32 [rows] wanted", token)
+        if logprob is not None and not (logprob.dtype is _F32 and logprob.numel() == rows and logprob.is_contiguous()
+                                        and logprob.get_device() == dev):
+            _refuse("logprob: float32 [rows] wanted", logprob)
+    if rows == 0:
+        return out
+    rc = _sample(logits.data_ptr(), _type_of(logits, "logits"), rows, vocab, row_stride, u.data_ptr(),
+                 None if temperature is None else temperature.data_ptr(), None if top_k is None else top_k.data_ptr(),
+                 None if top_p is None else top_p.data_ptr(), None if min_p is None else min_p.data_ptr(), bool(temperature_first),
+                 token.data_ptr(), None if logprob is None else logprob.data_ptr(), None if status is None else status.data_ptr(),
+                 _stream_of(dev))
+    if rc:
+        raise MinferError(rc, "op_sample")
     return out

@@ -469,4 +469,20 @@ constexpr int kLogprobsMaxTop = 32;
 int64_t logprobs_workspace(int64_t rows, int64_t vocab, int k, int num_sms);
 cudaError_t logprobs_launch(const LogprobsArgs& a, int type, int num_sms, cudaStream_t stream);
 
+// k_sample.cu: the next token of logits rows.
+struct SampleArgs {
+  const void* x;
+  int64_t rows, vocab, row_stride;
+  const float* u;
+  const float* temperature;  // these four may be null
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  int temperature_first;
+  int32_t* token;
+  float* logprob;  // may be null
+  int* status;
+};
+cudaError_t sample_launch(const SampleArgs& a, int type, int num_sms, cudaStream_t stream);
+
 }  // namespace minfer

@@ -1,4 +1,4 @@
-"""The operators of a quantized paged cache without a GPU: every refusal that needs no device, and the binding's own checks.
+"""The operators of a quantized paged cache and sampling without a GPU: every refusal that needs no device, and the binding's own checks.
 
 The pointers given here are never dereferenced: the library checks its host arguments before it enqueues anything, and
 without a device a call that passes the checks returns MINFER_ERR_CUDA."""
@@ -169,3 +169,30 @@ def test_the_binding_refuses(qp):
     two = torch.zeros(1, 1, 1, 2, dtype=torch.float16)
     with refused("TOO_LARGE"):
         qp.PagedCacheQ8(one.expand(2 ** 32 + 1, 1, 1, 64), one.expand(2 ** 32 + 1, 1, 1, 64), two.expand(2 ** 32 + 1, 1, 1, 2), two.expand(2 ** 32 + 1, 1, 1, 2))
+
+
+SAMPLE = dict(logits=PTR, type=F32, rows=3, vocab=100, row_stride=101, u=PTR, temperature=PTR, top_k=PTR, top_p=PTR, min_p=PTR, first=0,
+              token=PTR, logprob=PTR, status=None, stream=None)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(), CUDA), (dict(logits=PTR + 4), CUDA), (dict(type=BF16, logits=PTR + 2), CUDA), (dict(temperature=None, top_k=None, top_p=None, min_p=None), CUDA),
+    (dict(logprob=None), CUDA), (dict(rows=1, row_stride=0), CUDA), (dict(first=1), CUDA),
+    (dict(logits=None), ARG), (dict(u=None), ARG), (dict(token=None), ARG), (dict(rows=0), ARG), (dict(rows=-1), ARG), (dict(vocab=0), ARG),
+    (dict(row_stride=99), ARG), (dict(rows=1, row_stride=-1), ARG), (dict(logits=PTR + 2), ARG), (dict(type=F16, logits=PTR + 1), ARG),
+    (dict(type=8), SHAPE), (dict(vocab=2 ** 31, row_stride=2 ** 31), TOO_LARGE), (dict(rows=2 ** 31), TOO_LARGE)])
+def test_sample_arguments(qp, change, code):
+    assert _call(qp.lib().minfer_op_sample, SAMPLE, **change) == code
+
+
+def test_the_binding_refuses_samples(qp):
+    x, u, i32 = torch.zeros(2, 50), torch.zeros(2), torch.zeros(2, dtype=I32)
+    refused = lambda match: pytest.raises(qp.MinferError, match=match)  # noqa: E731
+    with refused("CUDA device wanted"):
+        qp.op_sample(x, u, u, i32, u, u)
+    for args, match in (((x[0], u), "rows"), ((x.t(), u), "contiguous rows"), ((x, u[:1]), "u:"), ((x, u.double()), "u:"), ((x, u, i32), "temperature"),
+                        ((x, u, u, u), "top_k"), ((x, u, u, i32.long()), "top_k"), ((x, u, u, i32, i32), "top_p"), ((x, u, u, i32, u, u[:1]), "min_p")):
+        with refused(match):
+            qp.op_sample(*args)
+    with refused("status"):
+        qp.op_sample(x, u, status=u)
