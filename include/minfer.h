@@ -604,6 +604,11 @@ int minfer_op_token_logprobs(const void* d_logits, int type, int64_t rows, int64
                              void* d_workspace, int64_t workspace_bytes, int* d_status,
                              void* stream);
 
+/* Bytes of workspace of minfer_op_sample, 0 for calls that need none, on the current
+ * device (no counterpart on the pages).  It needs no preparation and holds nothing
+ * between calls, so any call that follows may use it for something else. */
+int minfer_op_sample_workspace(int64_t rows, int64_t vocab, int type, int64_t* bytes);
+
 /* The next token of logits rows (walkthrough index, master table, row "Sampler":
  * top-k, top-p, temperature, in that order; min-p and the other order have no
  * counterpart on the pages).  Row r of d_logits (`type`, row_stride apart, vocab
@@ -632,7 +637,8 @@ int minfer_op_token_logprobs(const void* d_logits, int type, int64_t rows, int64
 int minfer_op_sample(const void* d_logits, int type, int64_t rows, int64_t vocab, int64_t row_stride,
                      const float* d_u, const float* d_temperature, const int32_t* d_top_k,
                      const float* d_top_p, const float* d_min_p, int temperature_first,
-                     int32_t* d_token, float* d_logprob, int* d_status, void* stream);
+                     int32_t* d_token, float* d_logprob, void* d_workspace, int64_t workspace_bytes,
+                     int* d_status, void* stream);
 
 /* ---------------------------------------------------------------- misc */
 /* A static, NUL-terminated name of an error code (never NULL; "unknown error"

@@ -126,7 +126,9 @@ SIGNATURES = {
     "minfer_op_token_logprobs_workspace": ([_I64, _I64, _I, ctypes.POINTER(_I64)], _I),
     "minfer_op_token_logprobs": ([_P, _I, _I64, _I64, _I64, _P, _I, _P, _P, _P, _P, _P, _I64, _P,
                                   _P], _I),
-    "minfer_op_sample": ([_P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P], _I),
+    "minfer_op_sample_workspace": ([_I64, _I64, _I, ctypes.POINTER(_I64)], _I),
+    "minfer_op_sample": ([_P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _P, _I, _P, _P, _P, _I64, _P, _P],
+                         _I),
     "minfer_strerror": ([_I], ctypes.c_char_p),
     "minfer_device_status": ([_P], _I),
     "minfer_debug_fault": ([_P, _I, _I64], _I),
@@ -434,7 +436,8 @@ _BATCH = ("PagedCache", "RopeTable", "Workspace", "check_status", "op_page_table
           "op_rope_paged_store", "op_paged_attention_workspace", "op_paged_attention",
           "PagedCacheQ8", "op_rope_paged_store_q8", "op_paged_read_q8",
           "op_paged_attention_q8_workspace", "op_paged_attention_q8",
-          "op_token_logprobs_workspace", "op_token_logprobs", "op_sample")
+          "op_token_logprobs_workspace", "op_token_logprobs",
+          "op_sample_workspace", "op_sample")
 
 
 def __getattr__(name: str):

@@ -37,6 +37,7 @@ _paged_read_q8 = _L.minfer_op_paged_read_q8
 _paged_attention_q8 = _L.minfer_op_paged_attention_q8
 _token_logprobs = _L.minfer_op_token_logprobs
 _sample = _L.minfer_op_sample
+_sample_workspace = _L.minfer_op_sample_workspace
 
 # The raw handle of a device's current stream and the current device's index:
 # torch's own accessors take 2 us for the first and 0.3 us for the second.
@@ -567,8 +568,17 @@ def op_token_logprobs(logits, ids=None, k: int = 0, out=None, workspace: Workspa
     return out
 
 
+def op_sample_workspace(logits):
+    """A workspace (uint8, uninitialized) for op_sample calls on logits of this shape
+    and type, one call at a time; None where none is needed."""
+    n = ctypes.c_int64()
+    with torch.cuda.device(logits.device):
+        check(_sample_workspace(logits.shape[0], logits.shape[1], _type_of(logits, "logits"), ctypes.byref(n)), "op_sample_workspace")
+    return torch.empty(n.value, dtype=torch.uint8, device=logits.device) if n.value else None
+
+
 def op_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, temperature_first: bool = False,
-              out=None, status=None):
+              out=None, workspace=None, status=None):
     """The next token of logits [rows][vocab] (float32, float16 or bfloat16, rows of
     any distance that do not overlap) from the random numbers u (float32 [rows] in [0,
     1), negative: skip the row), with settings per row (minfer_op_sample):
@@ -577,7 +587,8 @@ def op_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
     logits as they are, or divided by the temperature with temperature_first.
     Returns (token int32 [rows], logprob float32 [rows]: under what was drawn from),
     or fills `out`, two such tensors, the second of which may be None.  Skipped and
-    refused rows are not written (without `out` token -1 and logprob 0)."""
+    refused rows are not written (without `out` token -1 and logprob 0).  workspace:
+    what op_sample_workspace gives, taken anew by every call that is not given one."""
     dev, shape = logits.get_device(), logits.shape
     if len(shape) != 2:
         _refuse("logits: [rows][vocab] wanted", logits)
@@ -602,7 +613,7 @@ def op_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
         _refuse("a CUDA device wanted", logits)
     if dev != _current():
         with torch.cuda.device(dev):
-            return op_sample(logits, u, temperature, top_k, top_p, min_p, temperature_first, out, status)
+            return op_sample(logits, u, temperature, top_k, top_p, min_p, temperature_first, out, workspace, status)
     if out is None:
         token = torch.full((rows,), -1, dtype=_I32, device=logits.device)
         logprob = torch.zeros(rows, dtype=_F32, device=logits.device)
@@ -616,11 +627,22 @@ def op_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
             _refuse("logprob: float32 [rows] wanted", logprob)
     if rows == 0:
         return out
-    rc = _sample(logits.data_ptr(), _type_of(logits, "logits"), rows, vocab, row_stride, u.data_ptr(),
+    kind = _type_of(logits, "logits")
+    if workspace is None:
+        n = ctypes.c_int64()
+        rc = _sample_workspace(rows, vocab, kind, ctypes.byref(n))
+        if rc:
+            raise MinferError(rc, "op_sample")
+        if n.value:
+            workspace = torch.empty(n.value, dtype=torch.uint8, device=logits.device)
+    elif not (workspace.get_device() == dev and workspace.dtype is torch.uint8 and workspace.is_contiguous()):
+        _refuse("workspace: uint8 on the logits' device wanted", workspace)
+    work, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    rc = _sample(logits.data_ptr(), kind, rows, vocab, row_stride, u.data_ptr(),
                  None if temperature is None else temperature.data_ptr(), None if top_k is None else top_k.data_ptr(),
                  None if top_p is None else top_p.data_ptr(), None if min_p is None else min_p.data_ptr(), bool(temperature_first),
-                 token.data_ptr(), None if logprob is None else logprob.data_ptr(), None if status is None else status.data_ptr(),
-                 _stream_of(dev))
+                 token.data_ptr(), None if logprob is None else logprob.data_ptr(), work, nbytes,
+                 None if status is None else status.data_ptr(), _stream_of(dev))
     if rc:
         raise MinferError(rc, "op_sample")
     return out

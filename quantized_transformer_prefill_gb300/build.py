@@ -12,7 +12,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB_PATH = os.path.join(HERE, "libminfer.so")
 SOURCES = ["minfer.cu", "k_gemm.cu", "k_rows.cu", "k_attn.cu", "k_attn_tc.cu", "noalloc.cu", "batch.cu",
            "k_paged.cu", "k_paged_attn.cu", "k_paged_attn_q8.cu", "k_logprobs.cu",
-           "k_sample.cu"]
+           "k_sample.cu", "k_sample_stream.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]
 

@@ -355,20 +355,33 @@ int minfer_op_token_logprobs(const void* d_logits, int type, int64_t rows, int64
   return from_cuda(logprobs_launch(a, type, sms, static_cast<cudaStream_t>(stream)));
 }
 
-int minfer_op_sample(const void* d_logits, int type, int64_t rows, int64_t vocab, int64_t row_stride,
-                     const float* d_u, const float* d_temperature, const int32_t* d_top_k, const float* d_top_p,
-                     const float* d_min_p, int temperature_first, int32_t* d_token, float* d_logprob, int* d_status,
-                     void* stream) {
-  if (!d_logits || !d_u || !d_token || rows <= 0 || vocab <= 0 || row_stride < 0 || (rows > 1 && row_stride < vocab))
-    return MINFER_ERR_ARG;
+int minfer_op_sample_workspace(int64_t rows, int64_t vocab, int type, int64_t* bytes) {
+  if (!bytes || rows <= 0 || vocab <= 0) return MINFER_ERR_ARG;
   if (!type_ok(type)) return MINFER_ERR_SHAPE;
-  if (reinterpret_cast<uintptr_t>(d_logits) % type_size(type)) return MINFER_ERR_ARG;
   if (rows > INT_MAX || vocab > INT_MAX) return MINFER_ERR_TOO_LARGE;
   const int sms = current_sms();
   if (sms == 0) return MINFER_ERR_CUDA;
+  *bytes = sample_stream_bytes(rows, vocab, type, sms);
+  return MINFER_OK;
+}
+
+int minfer_op_sample(const void* d_logits, int type, int64_t rows, int64_t vocab, int64_t row_stride,
+                     const float* d_u, const float* d_temperature, const int32_t* d_top_k, const float* d_top_p,
+                     const float* d_min_p, int temperature_first, int32_t* d_token, float* d_logprob,
+                     void* d_workspace, int64_t workspace_bytes, int* d_status, void* stream) {
+  if (!d_logits || !d_u || !d_token || rows <= 0 || vocab <= 0 || row_stride < 0 || (rows > 1 && row_stride < vocab))
+    return MINFER_ERR_ARG;
+  if (!type_ok(type)) return MINFER_ERR_SHAPE;
+  if (reinterpret_cast<uintptr_t>(d_logits) % type_size(type) || !aligned16(d_workspace)) return MINFER_ERR_ARG;
+  if (rows > INT_MAX || vocab > INT_MAX) return MINFER_ERR_TOO_LARGE;
+  const int sms = current_sms();
+  if (sms == 0) return MINFER_ERR_CUDA;
+  const int64_t bytes = sample_stream_bytes(rows, vocab, type, sms);
+  if (bytes > 0 && (!d_workspace || workspace_bytes < bytes)) return MINFER_ERR_TOO_LARGE;
   const SampleArgs a{d_logits, rows,  vocab, row_stride,        d_u,     d_temperature, d_top_k,
                      d_top_p,  d_min_p, temperature_first != 0, d_token, d_logprob,     d_status};
-  return from_cuda(sample_launch(a, type, sms, static_cast<cudaStream_t>(stream)));
+  return from_cuda(bytes > 0 ? sample_stream_launch(a, type, sms, d_workspace, static_cast<cudaStream_t>(stream))
+                             : sample_launch(a, type, sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

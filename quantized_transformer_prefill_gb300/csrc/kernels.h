@@ -483,6 +483,17 @@ struct SampleArgs {
   float* logprob;  // may be null
   int* status;
 };
-cudaError_t sample_launch(const SampleArgs& a, int type, int num_sms, cudaStream_t stream);
+// With `list`, only the rows list[0, *count) of device memory.
+struct SampleLeft {
+  int row;
+  unsigned long long whole;  // the sum of its weights, if top-p wants it
+};
+cudaError_t sample_launch(const SampleArgs& a, int type, int num_sms, cudaStream_t stream,
+                          const SampleLeft* list = nullptr, const int* count = nullptr);
+// k_sample_stream.cu: the same for many rows, streamed once; what it leaves goes to
+// sample_launch.  Scratch needs no preparation; 0 bytes: sample_launch serves alone.
+int64_t sample_stream_bytes(int64_t rows, int64_t vocab, int type, int num_sms);
+cudaError_t sample_stream_launch(const SampleArgs& a, int type, int num_sms, void* scratch,
+                                 cudaStream_t stream);
 
 }  // namespace minfer

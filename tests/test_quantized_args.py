@@ -172,7 +172,7 @@ def test_the_binding_refuses(qp):
 
 
 SAMPLE = dict(logits=PTR, type=F32, rows=3, vocab=100, row_stride=101, u=PTR, temperature=PTR, top_k=PTR, top_p=PTR, min_p=PTR, first=0,
-              token=PTR, logprob=PTR, status=None, stream=None)
+              token=PTR, logprob=PTR, ws=PTR, ws_bytes=2 ** 40, status=None, stream=None)
 
 
 @pytest.mark.parametrize("change,code", [
@@ -180,6 +180,7 @@ SAMPLE = dict(logits=PTR, type=F32, rows=3, vocab=100, row_stride=101, u=PTR, te
     (dict(logprob=None), CUDA), (dict(rows=1, row_stride=0), CUDA), (dict(first=1), CUDA),
     (dict(logits=None), ARG), (dict(u=None), ARG), (dict(token=None), ARG), (dict(rows=0), ARG), (dict(rows=-1), ARG), (dict(vocab=0), ARG),
     (dict(row_stride=99), ARG), (dict(rows=1, row_stride=-1), ARG), (dict(logits=PTR + 2), ARG), (dict(type=F16, logits=PTR + 1), ARG),
+    (dict(ws=PTR + 8), ARG), (dict(ws=None), CUDA),
     (dict(type=8), SHAPE), (dict(vocab=2 ** 31, row_stride=2 ** 31), TOO_LARGE), (dict(rows=2 ** 31), TOO_LARGE)])
 def test_sample_arguments(qp, change, code):
     assert _call(qp.lib().minfer_op_sample, SAMPLE, **change) == code
