@@ -38,7 +38,8 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kList = 512;    // tokens that the first CTA sorts
+constexpr int kList = 512;    // tokens between which a border is looked for, sorted by the first CTA
+constexpr int kShort = 2048;  // tokens that a row's only CTA sorts; of a cluster kList, for they come one by one
 constexpr int kPicked = 1024; // tokens of a warp's segment that are picked out of it, at most
 constexpr int kGuess = 128;   // of top-p alone: tokens that the first bound aims at
 constexpr int kCopies = 4;    // of the table, against bank conflicts
@@ -82,7 +83,10 @@ struct SampleShared {
   uint2 table[256 * kCopies];
   u64 list[kList];
   uint32_t bins[2][kBins];         // tokens, and their weights as shares of 2^31
-  uint16_t picked[kWarps][kPicked];  // where they lie in the segment
+  union {
+    uint16_t picked[kWarps][kPicked];  // where they lie in the segment
+    u64 longer[kShort];                // a list of the short way
+  };
   u64 ex[2][kSlots][kMaxCluster];  // what the CTAs of the cluster tell, by turns
   u64 red[kWarps][kSlots];
   u64 part[kWarps];                // of one warp's segment
@@ -324,13 +328,13 @@ struct Wide {
   }
 
   // Logits of `from` and more, to the first CTA's list, in any order; returns how many.
-  __device__ __forceinline__ int gather(float from) {
+  __device__ __forceinline__ int gather(float from, u64* list, int entries) {
     r.each_from(from, [&](const float (&y)[E], int i0) {
 #pragma unroll
       for (int e = 0; e < E; ++e)
         if (y[e] >= from) {
           const int at = peer_add(peer(&s.count, 0), 1);
-          if (at < kList) put(peer(&s.list[at], 0), by_logit(y[e], i0 + e));
+          if (at < entries) put(peer(&list[at], 0), by_logit(y[e], i0 + e));
         }
     });
     cluster_sync();
@@ -701,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       // ---- the short way
       bool wide = list != nullptr;
       float from = kLowest;
-      if (!wide && a.vocab > kList) {
+      if (!wide && a.vocab > (cluster == 1 ? kShort : kList)) {
         if (set.k > 0) {
           wide = aim == 0;
           from = set.top_p < 1.f ? b : fmaxf(b, floor_x);
@@ -714,9 +718,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
       }
       if (!wide) {
-        const int n = row_in.gather(from);
-        wide = n > kList;
-        if (!wide && rank == 0) finish_list<kThreads, kList, kCopies>(s.list, &s.red[0][0], n, set, wf, wd, table, floor_x, whole, false, write);
+        const int entries = cluster == 1 ? kShort : kList, n = row_in.gather(from, s.longer, entries);
+        wide = n > entries;
+        if (!wide && rank == 0) finish_list<kThreads, kShort, kCopies>(s.longer, &s.red[0][0], n, set, wf, wd, table, floor_x, whole, false, write);
       }
 
       // ---- the wide way
@@ -763,13 +767,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 }
 
 template <typename T>
+int cluster_of(int64_t vocab) {  // the fewest CTAs that keep a row
+  constexpr int E = Logits<T>::E;
+  const int64_t all = (vocab + 2 * E - 2) / E;
+  int cluster = 1;
+  while (cluster < kMaxCluster && (all + cluster - 1) / cluster * 16 > kRoom) cluster *= 2;
+  return cluster;
+}
+
+template <typename T>
 cudaError_t sample_typed(const SampleArgs& a, int num_sms, cudaStream_t st, const SampleLeft* list, const int* count) {
   constexpr int E = Logits<T>::E;
   const int64_t all = (a.vocab + 2 * E - 2) / E;  // vectors of a row, wherever it begins
   // As many CTAs as keep the row; more while they leave SMs idle and have something to do.
-  int cluster = 1;
+  int cluster = cluster_of<T>(a.vocab);
   auto slice = [&] { return (all + cluster - 1) / cluster; };
-  while (cluster < kMaxCluster && (slice() * 16 > kRoom || (a.rows * cluster * 2 <= num_sms && slice() * 16 > 8192))) cluster *= 2;
+  while (cluster < kMaxCluster && a.rows * cluster * 2 <= num_sms && slice() * 16 > 8192) cluster *= 2;
   const int room = (int)std::min<int64_t>(slice(), kRoom / 16);
   const int smem = (int)((sizeof(SampleShared) + 15) / 16 * 16) + room * 16;
   const cudaError_t e = allow_smem<sample_kernel<T>>((int)((sizeof(SampleShared) + 15) / 16 * 16) + kRoom);
@@ -795,6 +808,10 @@ cudaError_t sample_typed(const SampleArgs& a, int num_sms, cudaStream_t st, cons
 }
 
 }  // namespace
+
+int sample_cluster(int64_t vocab, int type) {
+  return type == MINFER_F32 ? cluster_of<float>(vocab) : cluster_of<__half>(vocab);
+}
 
 cudaError_t sample_launch(const SampleArgs& a, int type, int num_sms, cudaStream_t st, const SampleLeft* list, const int* count) {
   return type == MINFER_F32   ? sample_typed<float>(a, num_sms, st, list, count)

@@ -10,11 +10,10 @@
 // parts that reach it are read again and what lies above goes to a list, which is cut,
 // sorted and drawn from (finish_list).  Top-p alone takes the first 128 parts, and
 // compares the list's weights with the row's.  Without a filter the
-// blocks' sums name the block that is drawn from.  Rows that need more (a k past 384, a
+// blocks' sums name the block that is drawn from.  Rows that need more (a k past 640, a
 // nucleus past the list, weights whose exponents are taken from x - max) are
 // left to sample_kernel.
 #include <algorithm>
-#include <cstdlib>
 
 #include "sample.cuh"
 
@@ -27,8 +26,10 @@ constexpr int kBlockDown = 10;         // of its weights: up to 1,024 of them
 constexpr int kMaxParts = 8192;        // of a row: their maxima are kept in shared memory
 constexpr int kScanThreads = 256, kScanCopies = 8;
 constexpr int kRowThreads = 512, kRowWarps = kRowThreads / 32;
-constexpr int kList = 512;             // tokens that a CTA sorts
-constexpr int kLargeK = 384;           // past it lists overflow, or take as long as sample_kernel
+constexpr int kList = 2048;            // tokens that a CTA sorts
+// Past it lists overflow (64 rows of 151,936: k = 500 38 us, left to sample_kernel 60; k =
+// 1,000 109 and 61).
+constexpr int kLargeK = 640;
 constexpr int kGuess = 128;            // of top-p alone: parts whose tokens are looked at
 constexpr float kFar = 8300.f;         // exponents of blocks reach a little past those of rows
 
@@ -437,12 +438,13 @@ auto typed(int type, F f) {
 int64_t sample_stream_bytes(int64_t rows, int64_t vocab, int type, int num_sms) {
   return typed(type, [&](auto t) -> int64_t {
     using T = decltype(t);
-    static const char* e = getenv("STREAM_ROWS");
-    if (rows < (e ? atoi(e) : 1)) return 0;
-    if (vocab < 4096 || vocab / 32 > (int64_t)kMaxParts * Logits<T>::E) return 0;
+    // While the clusters that keep the rows fit the GPU at once, there is nothing to stream
+    // (nor for rows that are short): f32, settings of all kinds, device time: 16 rows of
+    // 151,936 38 us against 51, 256 161 against 120; 256 of 10,007 66 against 83.
+    if (vocab * (int64_t)sizeof(T) < (64 << 10) || rows * sample_cluster(vocab, type) <= 2 * num_sms) return 0;
+    if (vocab / 32 > (int64_t)kMaxParts * Logits<T>::E) return 0;
     const int blocks = blocks_of<T>(vocab);
     if (blocks * kParts > kMaxParts || rows * blocks > (1ll << 30)) return 0;
-    (void)num_sms;
     return bytes_of<T>(rows, vocab, nullptr, nullptr);
   });
 }

@@ -490,6 +490,7 @@ struct SampleLeft {
 };
 cudaError_t sample_launch(const SampleArgs& a, int type, int num_sms, cudaStream_t stream,
                           const SampleLeft* list = nullptr, const int* count = nullptr);
+int sample_cluster(int64_t vocab, int type);  // CTAs that keep a row
 // k_sample_stream.cu: the same for many rows, streamed once; what it leaves goes to
 // sample_launch.  Scratch needs no preparation; 0 bytes: sample_launch serves alone.
 int64_t sample_stream_bytes(int64_t rows, int64_t vocab, int type, int num_sms);

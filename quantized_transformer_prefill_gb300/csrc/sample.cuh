@@ -301,6 +301,8 @@ __device__ __forceinline__ void sort_list(u64* list, int n) {
       sort_wide<kThreads, 1>(list, n);
     else if (kEntries >= 2 * kThreads && n <= 2 * kThreads)
       sort_wide<kThreads, 2>(list, n);
+    else if (kEntries > 4 * kThreads && n <= 4 * kThreads)
+      sort_wide<kThreads, 4>(list, n);
     else
       sort_wide<kThreads, kEntries / kThreads>(list, n);
     return;
