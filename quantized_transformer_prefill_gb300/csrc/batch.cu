@@ -285,14 +285,15 @@ int minfer_op_paged_read_q8(const minfer_paged_cache_q8* cache, const int32_t* d
       !stride_ok(out_stride, n_rows, type) || (n_rows > 1 && out_stride < (int64_t)a.c.nkv * a.c.hd))
     return MINFER_ERR_ARG;
   if (a.c.nkv > kMaxHeads) return MINFER_ERR_TOO_LARGE;
-  if (current_sms() == 0) return MINFER_ERR_CUDA;
+  const int sms = current_sms();
+  if (sms == 0) return MINFER_ERR_CUDA;
   a.slot = d_slot;
   a.n_rows = n_rows;
   a.k = d_k;
   a.v = d_v;
   a.out_stride = out_stride;
   a.status = d_status;
-  return from_cuda(paged_read_launch(a, type, static_cast<cudaStream_t>(stream)));
+  return from_cuda(paged_read_launch(a, type, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int minfer_op_paged_attention_q8_workspace(int n_req, int n_head, const minfer_paged_cache_q8* cache,

@@ -30,11 +30,12 @@
 namespace minfer {
 namespace {
 
-constexpr int kKeys = 16;  // keys of a unit that one warp takes
 constexpr int R = 8;       // query heads of a head block
 
-template <typename T, int HD>
+// KT: tiles of 16 keys that a warp takes at a time.
+template <typename T, int HD, int KT>
 struct Cfg {
+  static constexpr int kKeys = 16 * KT;  // keys of a unit that one warp takes
   static constexpr bool kF32 = sizeof(T) == 4;
   static constexpr int kBlocks = HD / 32;
   static constexpr int kChunks = HD / 16;         // 16-byte chunks of a row's codes
@@ -44,7 +45,7 @@ struct Cfg {
   static constexpr int kWarps = 4;
   static constexpr int kCtas = HD == 64 ? 4 : 3;
   static constexpr int kUnit = kWarps * kKeys;  // keys of a unit
-  static constexpr int kStatic = (int)sizeof(JoinShared<R>) + 512 + kWarps * R * 8 + R * 16;
+  static constexpr int kStatic = (int)sizeof(JoinShared<R>) + 512 + kWarps * (R * 8 + 4) + R * 16;
   static constexpr int kFit = (233472 / kCtas - 1024 - kStatic) / (kWarps * kStageBytes);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
   static constexpr int kSmem = kWarps * kStages * kStageBytes;
@@ -65,30 +66,15 @@ __device__ __forceinline__ int v_at(int row, int c) {
   return (row >> 1) * 128 + ((((row & 1) << 2 | c) ^ ((row >> 1) & 3)) << 4);
 }
 
-// Codes of bytes 0 and 2 of x as two f16, or bf16, numbers.
+// Codes of bytes 0 and 2 of x as two f16 numbers.
 __device__ __forceinline__ uint32_t codes_f16(uint32_t x) {
   const uint32_t y = (x & 0x00FF00FFu) ^ 0x64806480u;  // 1024 + (c + 128)
   const __half2 z = __hsub2(*reinterpret_cast<const __half2*>(&y), __half2half2(__ushort_as_half(0x6480)));
   return *reinterpret_cast<const uint32_t*>(&z);
 }
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t x) {
-  const uint32_t y = (x & 0x007F007Fu) | 0x43004300u;  // 128 + the lower seven bits
-  const uint32_t s = (x & 0x00800080u) | 0x43004300u;  // 128, or 256 of a negative code
-  const __nv_bfloat162 z = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&y), *reinterpret_cast<const __nv_bfloat162*>(&s));
-  return *reinterpret_cast<const uint32_t*>(&z);
-}
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 z = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&z);
-}
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const __nv_bfloat162 z = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&z);
-}
-// what is left of (a, b) when the bf16 numbers in x are taken off
-__device__ __forceinline__ void less_bf16(float& a, float& b, uint32_t x) {
-  a -= __uint_as_float(x << 16);
-  b -= __uint_as_float(x & 0xFFFF0000u);
 }
 __device__ __forceinline__ float2 halves(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
 
@@ -110,12 +96,12 @@ __device__ __forceinline__ void cp_scales(uint32_t dst, const void* src, bool li
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(HD / 16), "r"(live ? HD / 16 : 0) : "memory");
 }
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(Cfg<T, HD>::kWarps * 32, Cfg<T, HD>::kCtas)
+template <typename T, int HD, int KT>
+__global__ void __launch_bounds__(Cfg<T, HD, KT>::kWarps * 32, Cfg<T, HD, KT>::kCtas)
     paged_attn_q8_kernel(const __grid_constant__ PagedAttnQ8Args a, int n_groups, float scale_log2) {
-  using C = Cfg<T, HD>;
+  using C = Cfg<T, HD, KT>;
   constexpr bool kF32 = C::kF32;
-  constexpr int kWarps = C::kWarps, kUnit = C::kUnit, kBlocks = C::kBlocks;
+  constexpr int kWarps = C::kWarps, kUnit = C::kUnit, kBlocks = C::kBlocks, kKeys = C::kKeys;
   constexpr int kTiles = HD / 16;  // m16 tiles of the output
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int64_t s_scan[kWarps];
@@ -125,6 +111,7 @@ __global__ void __launch_bounds__(Cfg<T, HD>::kWarps * 32, Cfg<T, HD>::kCtas)
   __shared__ JoinShared<R> s_join;
   __shared__ float2 m_ml[kWarps * R];  // the warps' (max, sum) at the end of a piece
   __shared__ float4 m_w[R];            // their weights
+  __shared__ float m_unit[kWarps];     // what their outputs are in units of
   static_assert(kWarps == 4, "a float4 of weights");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int P = a.c.page_size, cap = a.max_pages * P;
@@ -145,12 +132,12 @@ __global__ void __launch_bounds__(Cfg<T, HD>::kWarps * 32, Cfg<T, HD>::kCtas)
   Walk cw = s_walk;  // the unit being computed
   Walk lw = cw;      // the unit being loaded
 
-  // ---- loads: lane l looks up the page of key l % 16 and copies the scales of its K
-  // (l < 16) or V row; then all lanes copy the codes
+  // ---- loads: lane l looks up the page of key l % kKeys and copies the scales of its rows;
+  // then all lanes copy the codes
   const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStageBytes;
   int page_next = 0;  // page id that this lane looked up for unit lw
   auto lookup = [&](const Walk& w) {
-    const int key = w.u * kUnit + warp * kKeys + (lane & 15);
+    const int key = w.u * kUnit + warp * kKeys + (lane & (kKeys - 1));
     if (key >= w.len) return 0;
     return a.table[(int64_t)w.r * a.table_stride + a.c.div.of(key)];
   };
@@ -158,11 +145,12 @@ __global__ void __launch_bounds__(Cfg<T, HD>::kWarps * 32, Cfg<T, HD>::kCtas)
   constexpr int kRowsPer = 32 / C::kChunks;  // rows of one copy instruction
   const uint64_t policy = stream_policy();
   const int c = lane % C::kChunks, row0 = lane / C::kChunks;
-  const bool one_page = (P & (kKeys - 1)) == 0;
+  const bool whole_tiles = (P & 15) == 0;  // a tile lies in one page
+  const int64_t step = kRowsPer * a.c.row_stride, off0 = (int64_t)row0 * a.c.row_stride + c * 16;
   auto load_unit = [&](int stage) {
     const uint32_t kdst = ring + stage * C::kStageBytes, vdst = kdst + C::kCodeBytes, sdst = vdst + C::kCodeBytes;
-    const int key0 = lw.u * kUnit + warp * kKeys, key = key0 + (lane & 15);
-    const int in_page = key - a.c.div.of(key) * P, head = lw.v / n_groups;
+    const int key0 = lw.u * kUnit + warp * kKeys, key = key0 + (lane & (kKeys - 1));
+    const int in_page = key - a.c.div.of(key) * P, head = n_groups == 1 ? lw.v : lw.v / n_groups;
     const bool wanted = key < lw.len, ok = wanted && (unsigned)page_next < (unsigned)a.c.n_pages;
     const bool any_bad = __any_sync(0xffffffffu, wanted && !ok);
     if (lane == 0) s_bad[warp][stage] = any_bad;
@@ -171,24 +159,32 @@ __global__ void __launch_bounds__(Cfg<T, HD>::kWarps * 32, Cfg<T, HD>::kCtas)
       off = (int64_t)page_next * a.c.page_stride + (int64_t)in_page * a.c.row_stride + (int64_t)head * a.c.head_stride;
       soff = (int64_t)page_next * a.s.page_stride + (int64_t)in_page * a.s.row_stride + (int64_t)head * a.s.head_stride;
     }
-    cp_scales<HD>(sdst + lane * C::kScaleBytes, static_cast<const __half*>(lane < 16 ? a.s.k : a.s.v) + soff, ok);
-    if (one_page) {
-      // the first key's row, and from there in steps
-      const int live = __shfl_sync(0xffffffffu, ok, 0) ? lw.len - key0 : 0;
-      const int64_t o = live > 0 ? __shfl_sync(0xffffffffu, off, 0) + (int64_t)row0 * a.c.row_stride : 0;
-      const unsigned char* kp = static_cast<const unsigned char*>(a.c.k) + o + c * 16;
-      const unsigned char* vp = static_cast<const unsigned char*>(a.c.v) + o + c * 16;
-      const int64_t step = kRowsPer * a.c.row_stride;
+    if constexpr (KT == 1) {
+      cp_scales<HD>(sdst + lane * C::kScaleBytes, static_cast<const __half*>(lane < 16 ? a.s.k : a.s.v) + soff, ok);
+    } else {
+      cp_scales<HD>(sdst + lane * C::kScaleBytes, static_cast<const __half*>(a.s.k) + soff, ok);
+      cp_scales<HD>(sdst + (kKeys + lane) * C::kScaleBytes, static_cast<const __half*>(a.s.v) + soff, ok);
+    }
+    const unsigned live = __ballot_sync(0xffffffffu, ok);
+    if (whole_tiles) {
 #pragma unroll
-      for (int j = 0; j < kKeys / kRowsPer; ++j) {
-        const int row = j * kRowsPer + row0, bytes = row < live ? 16 : 0;
-        cp16_stream(kdst + k_at<HD>(row, c), kp, bytes, policy);
-        cp16_stream(vdst + v_at<HD>(row, c), vp, bytes, policy);
-        kp += step;
-        vp += step;
+      for (int t = 0; t < KT; ++t) {
+        // the tile's first row, and from there in steps
+        const int rows = (live >> (16 * t)) & 1 ? lw.len - key0 - 16 * t : 0;
+        int64_t o = __shfl_sync(0xffffffffu, off, 16 * t);
+        o = rows > 0 ? o + off0 : 0;
+        const unsigned char* kp = static_cast<const unsigned char*>(a.c.k) + o;
+        const unsigned char* vp = static_cast<const unsigned char*>(a.c.v) + o;
+#pragma unroll
+        for (int j = 0; j < 16 / kRowsPer; ++j) {
+          const int row = 16 * t + j * kRowsPer + row0, bytes = j * kRowsPer + row0 < rows ? 16 : 0;
+          cp16_stream(kdst + k_at<HD>(row, c), kp, bytes, policy);
+          cp16_stream(vdst + v_at<HD>(row, c), vp, bytes, policy);
+          kp += step;
+          vp += step;
+        }
       }
     } else {
-      const unsigned live = __ballot_sync(0xffffffffu, ok);
 #pragma unroll
       for (int j = 0; j < kKeys / kRowsPer; ++j) {
         const int row = j * kRowsPer + row0;
@@ -289,14 +285,16 @@ __global__ void __launch_bounds__(Cfg<T, HD>::kWarps * 32, Cfg<T, HD>::kCtas)
       fac[1] = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
     }
 
-    // the thread's query heads are 2 t4 and the next, its keys g4 and g4 + 8; its dims
-    // of tile n are 16 n + 2 g4 and the next
+    // the thread's query heads are 2 t4 and the next, its keys of a tile g4 and g4 + 8; its
+    // dims of output tile n are 16 n + 2 g4 and the next
     float o[kTiles][4], m[2], l[2];
     m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.f;
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     bool bad = false;
+    // V's scales so far are at most top_d, a power of two; outputs are in units of top_d 2^-15
+    float top_d = 0x1p-24f;
 
 #pragma unroll 1
     for (int i = 0; i < seg_units; ++i, ++done) {
@@ -316,17 +314,18 @@ __global__ void __launch_bounds__(Cfg<T, HD>::kWarps * 32, Cfg<T, HD>::kCtas)
       const uint32_t ks = ring + stage * C::kStageBytes, vs = ks + C::kCodeBytes, ss = vs + C::kCodeBytes;
 
       // S^T = K Q^T, block by block
-      float sc[4];
-      {
+      float sc[KT][4];
+#pragma unroll
+      for (int t = 0; t < KT; ++t) {
         float d0[kBlocks], d1[kBlocks];
-        load_scales<HD>(d0, ss + g4 * C::kScaleBytes);
-        load_scales<HD>(d1, ss + (g4 + 8) * C::kScaleBytes);
+        load_scales<HD>(d0, ss + (16 * t + g4) * C::kScaleBytes);
+        load_scales<HD>(d1, ss + (16 * t + g4 + 8) * C::kScaleBytes);
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
           uint32_t x[2], y[2];  // 8 codes of key g4, and of key g4 + 8
           const int half = (t4 & 1) * 8;
-          asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(ks + k_at<HD>(g4, 2 * b + (t4 >> 1)) + half));
-          asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(y[0]), "=r"(y[1]) : "r"(ks + k_at<HD>(g4 + 8, 2 * b + (t4 >> 1)) + half));
+          asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(ks + k_at<HD>(16 * t + g4, 2 * b + (t4 >> 1)) + half));
+          asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(y[0]), "=r"(y[1]) : "r"(ks + k_at<HD>(16 * t + g4 + 8, 2 * b + (t4 >> 1)) + half));
           float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int i2 = 0; i2 < 2; ++i2) {
@@ -335,19 +334,23 @@ __global__ void __launch_bounds__(Cfg<T, HD>::kWarps * 32, Cfg<T, HD>::kCtas)
             if constexpr (kF32) mma(acc, k4, ql[b][i2][0], ql[b][i2][1], __half());
           }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sc[j] = b == 0 ? acc[j] * (j < 2 ? d0[b] : d1[b]) : fmaf(acc[j], j < 2 ? d0[b] : d1[b], sc[j]);
+          for (int j = 0; j < 4; ++j) sc[t][j] = b == 0 ? acc[j] * (j < 2 ? d0[b] : d1[b]) : fmaf(acc[j], j < 2 ? d0[b] : d1[b], sc[t][j]);
         }
       }
 
       // online softmax in log2 units
-      const int live = seg_len - ((first_unit + i) * kUnit + warp * kKeys);  // keys of this warp's 16
+      const int live = seg_len - ((first_unit + i) * kUnit + warp * kKeys);  // keys of this warp's
       float cf[2];
       bool moved = false;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sc[j] = g4 + (j >> 1) * 8 < live ? sc[j] * fac[j & 1] : -INFINITY;
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc[t][j] = 16 * t + g4 + (j >> 1) * 8 < live ? sc[t][j] * fac[j & 1] : -INFINITY;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float n = fmaxf(sc[j], sc[j + 2]);
+        float n = fmaxf(sc[0][j], sc[0][j + 2]);
+#pragma unroll
+        for (int t = 1; t < KT; ++t) n = fmaxf(n, fmaxf(sc[t][j], sc[t][j + 2]));
         n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 4));
         n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 8));
         n = fmaxf(m[j], fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 16)));
@@ -356,10 +359,43 @@ __global__ void __launch_bounds__(Cfg<T, HD>::kWarps * 32, Cfg<T, HD>::kCtas)
         cf[j] = ex2(m[j] - z);
         moved |= n != m[j];
         m[j] = n;
-        sc[j] = ex2(sc[j] - z);
-        sc[j + 2] = ex2(sc[j + 2] - z);
+        float sum = 0.f;
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+          sc[t][j] = ex2(sc[t][j] - z);
+          sc[t][j + 2] = ex2(sc[t][j + 2] - z);
+          sum += sc[t][j] + sc[t][j + 2];
+        }
         // the sums stay per thread until the end of the piece
-        l[j] = fmaf(l[j], cf[j], sc[j] + sc[j + 2]);
+        l[j] = fmaf(l[j], cf[j], sum);
+      }
+
+      // V's scales of keys 2 t4, 2 t4 + 1, and 8 further, and the largest of all
+      uint32_t vd[KT][4][kBlocks / 2];
+      {
+        __half2 top = __float2half2_rn(0.f);
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t at = ss + (kKeys + 16 * t + 2 * t4 + (j & 1) + (j >> 1) * 8) * C::kScaleBytes;
+            if constexpr (HD == 128)
+              asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(vd[t][j][0]), "=r"(vd[t][j][1]) : "r"(at));
+            else
+              vd[t][j][0] = lds32(at);
+#pragma unroll
+            for (int b = 0; b < kBlocks / 2; ++b) top = __hmax2(top, __habs2(*reinterpret_cast<const __half2*>(&vd[t][j][b])));
+          }
+        float d = fmaxf(__low2float(top), __high2float(top));
+        d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, 1));
+        d = fminf(fmaxf(d, __shfl_xor_sync(0xffffffffu, d, 2)), 65504.f);
+        if (d > top_d) {  // (the same for all lanes)
+          const float up = __uint_as_float((__float_as_uint(d) + 0x7FFFFFu) & 0xFF800000u);
+          cf[0] *= top_d / up;
+          cf[1] *= top_d / up;
+          top_d = up;
+          moved = true;
+        }
       }
       if (!kF32 && __any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -367,51 +403,52 @@ __global__ void __launch_bounds__(Cfg<T, HD>::kWarps * 32, Cfg<T, HD>::kCtas)
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[n][j] *= cf[j & 1];
       }
+      const float unit = 0x1p15f / top_d;
 
-      // weights of keys 2 t4, 2 t4 + 1, and 8 further, under head g4
-      float p[4];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t u = __float_as_uint(sc[2 * j]), v = __float_as_uint(sc[2 * j + 1]);
-        const uint32_t hi = transpose8(__byte_perm(u, v, 0x7632)), lo = transpose8(__byte_perm(u, v, 0x5410));
-        p[2 * j] = __uint_as_float(__byte_perm(lo, hi, 0x5410));
-        p[2 * j + 1] = __uint_as_float(__byte_perm(lo, hi, 0x7632));
-      }
       // O^T += V^T (P d)^T
-      float d[4][kBlocks];
+      float add[kF32 ? kTiles : 1][4];
+      if constexpr (kF32)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) load_scales<HD>(d[j], ss + (kKeys + 2 * t4 + (j & 1) + (j >> 1) * 8) * C::kScaleBytes);
+        for (int n = 0; n < kTiles; ++n) add[n][0] = add[n][1] = add[n][2] = add[n][3] = 0.f;
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b) {
-        constexpr int kTerms = kF32 ? 3 : 2;
-        uint32_t w[kTerms][2];
+      for (int t = 0; t < KT; ++t) {
+        // weights of the scales' keys under head g4
+        float p[4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float x = p[2 * j] * d[2 * j][b], y = p[2 * j + 1] * d[2 * j + 1][b];
+          const uint32_t u = __float_as_uint(sc[t][2 * j] * unit), v = __float_as_uint(sc[t][2 * j + 1] * unit);
+          const uint32_t hi = transpose8(__byte_perm(u, v, 0x7632)), lo = transpose8(__byte_perm(u, v, 0x5410));
+          p[2 * j] = __uint_as_float(__byte_perm(lo, hi, 0x5410));
+          p[2 * j + 1] = __uint_as_float(__byte_perm(lo, hi, 0x7632));
+        }
 #pragma unroll
-          for (int t = 0; t < kTerms; ++t) {
-            w[t][j] = pack_bf16(x, y);
-            if (t + 1 < kTerms) less_bf16(x, y, w[t][j]);
+        for (int b = 0; b < kBlocks; ++b) {
+          uint32_t w[2][2];  // the upper and the lower numbers
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float2 d0 = halves(vd[t][2 * j][b >> 1]), d1 = halves(vd[t][2 * j + 1][b >> 1]);
+            const float x = p[2 * j] * (b & 1 ? d0.y : d0.x), y = p[2 * j + 1] * (b & 1 ? d1.y : d1.x);
+            w[0][j] = pack_f16(x, y);
+            const float2 h = halves(w[0][j]);
+            w[1][j] = pack_f16(x - h.x, y - h.y);
+          }
+          // matrices: keys 0-7 and 8-15 of the block's first 16 dims, the same of its others
+          uint32_t x[4];
+          ldsm4t(x, vs + v_at<HD>(16 * t + (lane & 15), 2 * b + (lane >> 4)));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t v4[4] = {codes_f16(x[2 * h]), codes_f16(x[2 * h] >> 8), codes_f16(x[2 * h + 1]), codes_f16(x[2 * h + 1] >> 8)};
+            float(&to)[4] = kF32 ? add[kF32 ? 2 * b + h : 0] : o[2 * b + h];
+            mma(to, v4, w[1][0], w[1][1], __half());
+            mma(to, v4, w[0][0], w[0][1], __half());
           }
         }
-        // matrices: keys 0-7 and 8-15 of the block's first 16 dims, the same of its others
-        uint32_t x[4];
-        ldsm4t(x, vs + v_at<HD>(lane & 15, 2 * b + (lane >> 4)));
+      }
+      if constexpr (kF32) {  // the tensor core's adds cut off, so f32 sums are added up here
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t v4[4] = {codes_bf16(x[2 * h]), codes_bf16(x[2 * h] >> 8), codes_bf16(x[2 * h + 1]), codes_bf16(x[2 * h + 1] >> 8)};
-          if constexpr (!kF32) {
+        for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-            for (int t = 0; t < kTerms; ++t) mma(o[2 * b + h], v4, w[t][0], w[t][1], __nv_bfloat16());
-          } else {
-            // the tensor core's adds cut off, so f32 sums are added up here
-            float f[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int t = kTerms - 1; t >= 0; --t) mma(f, v4, w[t][0], w[t][1], __nv_bfloat16());
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[2 * b + h][j] = fmaf(o[2 * b + h][j], cf[j & 1], f[j]);
-          }
-        }
+          for (int j = 0; j < 4; ++j) o[n][j] = fmaf(o[n][j], cf[j & 1], add[n][j]);
       }
       if (++stage == C::kStages) stage = 0;
     }
@@ -444,6 +481,7 @@ __global__ void __launch_bounds__(Cfg<T, HD>::kWarps * 32, Cfg<T, HD>::kCtas)
           *reinterpret_cast<float2*>(mo + head * HD + ((n * 16 + 2 * g4) ^ ((t4 & 1) * 16))) = make_float2(o[n][j], o[n][j + 2]);
       }
     }
+    if (lane == 0) m_unit[warp] = top_d * 0x1p-15f;
     if (bad && lane == 0) s_segbad[seg & 1] = 1;
     __syncthreads();
     const bool seg_bad = s_segbad[seg & 1] != 0;
@@ -468,7 +506,7 @@ __global__ void __launch_bounds__(Cfg<T, HD>::kWarps * 32, Cfg<T, HD>::kCtas)
         for (int k = 0; k < kWarps; ++k) w[k] *= f;
         if (!seg_bad && a.lse) a.lse[(int64_t)r * a.nh + head0 + tid] = fmaf(mx, kLn2, logf(sum));
       }
-      m_w[tid] = make_float4(w[0], w[1], w[2], w[3]);
+      m_w[tid] = make_float4(w[0] * m_unit[0], w[1] * m_unit[1], w[2] * m_unit[2], w[3] * m_unit[3]);
     }
     __syncthreads();
     if (seg_bad && tid == 0) set_error(a.status, MINFER_ERR_POS_OOB);
@@ -511,44 +549,40 @@ __global__ void __launch_bounds__(Cfg<T, HD>::kWarps * 32, Cfg<T, HD>::kCtas)
   idle_requests<T, HD, kWarps * 32>(a, cap);
 }
 
-template <typename T, int HD>
+template <int HD>
 int ctas(int num_sms) {
-  return std::min(num_sms * Cfg<T, HD>::kCtas, kMaxShares);
+  static_assert(Cfg<float, HD, 1>::kCtas == Cfg<__half, HD, 2>::kCtas, "the shares of a call are the same for every type");
+  return std::min(num_sms * Cfg<float, HD, 1>::kCtas, kMaxShares);
 }
 
-// Runs f with the type and head size of a call.
-template <typename F>
-auto with_config(int type, int hd, F f) {
-  auto sized = [&](auto t) {
-    using T = decltype(t);
-    return hd == 64 ? f.template operator()<T, 64>() : f.template operator()<T, 128>();
-  };
-  return type == MINFER_F32 ? sized(float()) : type == MINFER_F16 ? sized(__half()) : sized(__nv_bfloat16());
+template <typename T, int HD, int KT>
+cudaError_t launch(const PagedAttnQ8Args& a, int num_sms, cudaStream_t st) {
+  using C = Cfg<T, HD, KT>;
+  const int G = a.nh / a.c.nkv, n_groups = (G + R - 1) / R;
+  const cudaError_t e = allow_smem<paged_attn_q8_kernel<T, HD, KT>>(C::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(paged_attn_q8_kernel<T, HD, KT>, dim3((unsigned)ctas<HD>(num_sms)), dim3(C::kWarps * 32), C::kSmem, st, a, n_groups,
+                    a.scale * kLog2e);
+}
+template <typename T, int HD>
+cudaError_t launch(const PagedAttnQ8Args& a, int num_sms, cudaStream_t st) {
+  // Two tiles at a time, where the registers allow it (64 of up to 4096, 28/4 heads of 128,
+  // bf16: 42 us against 48; heads of 64 and f32 the same either way).
+  return launch<T, HD, HD == 128 && sizeof(T) == 2 ? 2 : 1>(a, num_sms, st);
+}
+template <typename T>
+cudaError_t launch(const PagedAttnQ8Args& a, int num_sms, cudaStream_t st) {
+  return a.c.hd == 64 ? launch<T, 64>(a, num_sms, st) : launch<T, 128>(a, num_sms, st);
 }
 
-struct Launch {
-  const PagedAttnQ8Args& a;
-  int num_sms;
-  cudaStream_t st;
-  template <typename T, int HD>
-  cudaError_t operator()() {
-    using C = Cfg<T, HD>;
-    const int G = a.nh / a.c.nkv, n_groups = (G + R - 1) / R;
-    const cudaError_t e = allow_smem<paged_attn_q8_kernel<T, HD>>(C::kSmem);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(paged_attn_q8_kernel<T, HD>, dim3((unsigned)ctas<T, HD>(num_sms)), dim3(C::kWarps * 32), C::kSmem, st, a, n_groups,
-                      a.scale * kLog2e);
-  }
-};
 }  // namespace
 
-// (the shares of a call, and so its workspace, are the same for every type)
 int64_t paged_attn_q8_workspace(int hd, int num_sms) {
-  return kPartOffset + (int64_t)(hd == 64 ? ctas<float, 64>(num_sms) : ctas<float, 128>(num_sms)) * 2 * part_floats(R, hd) * 4;
+  return kPartOffset + (int64_t)(hd == 64 ? ctas<64>(num_sms) : ctas<128>(num_sms)) * 2 * part_floats(R, hd) * 4;
 }
 
 cudaError_t paged_attn_q8_launch(const PagedAttnQ8Args& a, int type, int num_sms, cudaStream_t st) {
-  return with_config(type, a.c.hd, Launch{a, num_sms, st});
+  return type == MINFER_F32 ? launch<float>(a, num_sms, st) : type == MINFER_F16 ? launch<__half>(a, num_sms, st) : launch<__nv_bfloat16>(a, num_sms, st);
 }
 
 }  // namespace minfer

@@ -420,7 +420,7 @@ struct PagedReadArgs {
   int64_t out_stride;
   int* status;
 };
-cudaError_t paged_read_launch(const PagedReadArgs& a, int type, cudaStream_t stream);
+cudaError_t paged_read_launch(const PagedReadArgs& a, int type, int num_sms, cudaStream_t stream);
 
 // k_paged_attn.cu: one query row per request over its pages.
 struct PagedAttnRows {  // all but the cache
