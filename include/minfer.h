@@ -629,8 +629,9 @@ int minfer_op_sample_workspace(int64_t rows, int64_t vocab, int type, int64_t* b
  * d_logprob[r] (may be NULL) is the logarithm of its share.  A token that weighs less
  * than 2^-60 of the first is not drawn.  Weights are held to 2^-31 of themselves, as
  * whole numbers in units of 2^-(62 - log2 vocab) of the first, and summed without
- * rounding (a u of 0 draws the first id that is left, however little it weighs): the
- * result depends on the row and its settings alone, bit for bit.
+ * rounding (a u of 0 draws the first id that is left, however little it weighs), but that
+ * calls with a workspace round a block's sum once.  The result of a call depends on its
+ * inputs alone, bit for bit on one device type.
  * -inf logits are masked tokens; a row with nothing else gets token -1 and log
  * probability -inf.  Device errors: MINFER_ERR_ARG for a setting out of its range, a
  * NaN or +inf among the logits (no output of that row is written). */

@@ -40,8 +40,8 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kList = 512;    // tokens between which a border is looked for, sorted by the first CTA
 constexpr int kShort = 2048;  // tokens that a row's only CTA sorts; of a cluster kList, for they come one by one
-constexpr int kPicked = 1024; // tokens of a warp's segment that are picked out of it, at most
-constexpr int kGuess = 128;   // of top-p alone: tokens that the first bound aims at
+constexpr int kPicked = 32;   // tokens that a lane picks out of its vectors, at most
+constexpr int kGuess = 64;    // of top-p alone: tokens that the first bound aims at
 constexpr int kCopies = 4;    // of the table, against bank conflicts
 constexpr int kSlots = 5;     // numbers of one exchange
 constexpr int kBins = 1024;   // of a histogram: four to a thread
@@ -84,7 +84,7 @@ struct SampleShared {
   u64 list[kList];
   uint32_t bins[2][kBins];         // tokens, and their weights as shares of 2^31
   union {
-    uint16_t picked[kWarps][kPicked];  // where they lie in the segment
+    uint16_t picked[kWarps][kPicked][32];  // where they lie in the segment
     u64 longer[kShort];                // a list of the short way
   };
   u64 ex[2][kSlots][kMaxCluster];  // what the CTAs of the cluster tell, by turns
@@ -93,6 +93,7 @@ struct SampleShared {
   u64 found;                       // a token that one CTA told all: logit bits, id
   float floor;                     // logits below are out
   int count;                       // entries of list
+  int local, base;                 // of what this CTA adds to it: how many, from where on
   int edge[2];                     // bins between which a border lies
   u64 before;                      // tokens in the bins before
   uint32_t keys[2][kWarps];
@@ -191,55 +192,50 @@ struct Wide {
   int turn;
   float xb;  // kept: what is larger, and of its equals the ids up to idb
   int idb;
-  int n_picked;  // of this warp; below 0: nothing has been picked
+  int n_picked, most;  // by this lane, by any of the warp; most below 0: nothing has been picked
 
-  // Picks the logits of `least` and more out of the row, in the order of ids; what follows
-  // then goes over these.
+  // Every lane picks the logits of `least` and more out of its vectors; sums then go over
+  // these.
   __device__ __forceinline__ void pick(float least) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int n = 0;
     const int first = (int)r.first + warp * r.seg * E;
     r.each_from(least, [&](const float (&y)[E], int i0) {
-      int at = n;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const unsigned b = __ballot_sync(0xffffffffu, y[e] >= least);
-        at += __popc(b & ((1u << lane) - 1));
-        n += __popc(b);
-      }
 #pragma unroll
       for (int e = 0; e < E; ++e)
         if (y[e] >= least) {
-          if (at < kPicked) s.picked[warp][at] = (uint16_t)(i0 + e - first);
-          ++at;
+          if (n < kPicked) s.picked[warp][n][lane] = (uint16_t)(i0 + e - first);
+          ++n;
         }
     });
+    const int top = __reduce_max_sync(0xffffffffu, n);
     // (all of the slice is in shared memory, and a segment's places fit 16 bits)
-    const bool over = n > kPicked || r.kept < r.vectors || r.seg * E > 65536;
+    const bool over = top > kPicked || r.kept < r.vectors || r.seg * E > 65536;
     u64 v[1] = {over};
     exchange<1, 1>(s, v, rank, cluster, turn);
-    n_picked = v[0] ? -1 : n;
-  }
-  __device__ __forceinline__ void picked(int i, float* x, int* id) const {
-    const int warp = threadIdx.x >> 5, at = s.picked[warp][i];
-    const T v = reinterpret_cast<const T*>(r.near + warp * r.seg)[at];
-    if constexpr (sizeof(T) == 4)
-      *x = v;
-    else if constexpr (std::is_same<T, __half>::value)
-      *x = __half2float(v);
-    else
-      *x = __bfloat162float(v);
-    *id = (int)r.first + warp * r.seg * E + at;
+    n_picked = n;
+    most = v[0] ? -1 : top;
   }
   // f(logit, id) for what may be `least` or more, by all lanes
   template <typename F>
   __device__ __forceinline__ void each(float least, F f) const {
-    if (n_picked >= 0) {
-      for (int b = 0; b < n_picked; b += 32) {
+    if (most >= 0) {
+      const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+      const T* const seg = reinterpret_cast<const T*>(r.near + warp * r.seg);
+      const int first = (int)r.first + warp * r.seg * E;
+      for (int i = 0; i < most; ++i) {
         float x = -INFINITY;
-        int id = 0;
-        if (b + (threadIdx.x & 31) < n_picked) picked(b + (threadIdx.x & 31), &x, &id);
-        f(x, id);
+        int at = 0;
+        if (i < n_picked) {
+          at = s.picked[warp][i][lane];
+          if constexpr (sizeof(T) == 4)
+            x = seg[at];
+          else if constexpr (std::is_same<T, __half>::value)
+            x = __half2float(seg[at]);
+          else
+            x = __bfloat162float(seg[at]);
+        }
+        f(x, first + at);
       }
     } else {
       r.each_from(least, [&](const float (&y)[E], int i0) {
@@ -267,18 +263,6 @@ struct Wide {
     if (t >= before && t < before + own) {  // in this CTA: s.red holds its warps' sums
       int at = 0;
       for (; t >= before + s.red[at][0]; ++at) before += s.red[at][0];
-      if (n_picked >= 0) {
-        if (warp == at)
-          for (int b = 0; b < n_picked && t >= before; b += 32) {
-            float x = -INFINITY;
-            int id = 0;
-            if (b + lane < n_picked) picked(b + lane, &x, &id);
-            const u64 w = b + lane < n_picked ? weigh(x, id) : 0, incl = warp_scan(w, lane) + before;
-            if (incl - w <= t && t < incl)
-              for (int c = 0; c < cluster; ++c) put(peer(&s.found, c), (u64)__float_as_uint(x) << 32 | (uint32_t)id);
-            before = __shfl_sync(0xffffffffu, incl, 31);
-          }
-      } else {
       // the warps share the segment of warp `at`, `per` times 32 vectors each
       const int v0 = at * r.seg, end = min(v0 + r.seg, r.vectors), per = (r.seg / 32 + kWarps - 1) / kWarps;
       const int mine0 = v0 + warp * per * 32, mine1 = min(mine0 + per * 32, end);
@@ -321,22 +305,42 @@ struct Wide {
           if (t < before) break;
         }
       }
-      }
     }
     cluster_sync();
     return s.found;
   }
 
+  // Entries for the first CTA's list: a CTA collects its own, in place of the bins (its own
+  // list, if there is no other CTA), and hands them over together, for a word of another
+  // CTA's is far away.  add: by any thread; hand_over: by all, behind the last add; the
+  // entries are there behind the next barrier of the cluster.
+  __device__ __forceinline__ u64* own_list(u64* list) const { return cluster == 1 ? list : reinterpret_cast<u64*>(&s.bins[0][0]); }
+  __device__ __forceinline__ void add(u64* own, int entries, u64 entry) const {
+    const int at = atomicAdd(&s.local, 1);
+    if (at < entries) own[at] = entry;
+  }
+  __device__ __forceinline__ void hand_over(u64* list, int entries) const {
+    __syncthreads();
+    const int n = s.local;
+    if (threadIdx.x == 0) {
+      s.base = peer_add(peer(&s.count, 0), n);
+      s.local = 0;
+    }
+    if (cluster == 1) return;
+    __syncthreads();
+    const u64* const own = own_list(list);
+    for (int i = threadIdx.x; i < n && s.base + i < entries; i += kThreads) put(peer(&list[s.base + i], 0), own[i]);
+  }
+
   // Logits of `from` and more, to the first CTA's list, in any order; returns how many.
   __device__ __forceinline__ int gather(float from, u64* list, int entries) {
+    u64* const own = own_list(list);
     r.each_from(from, [&](const float (&y)[E], int i0) {
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (y[e] >= from) {
-          const int at = peer_add(peer(&s.count, 0), 1);
-          if (at < entries) put(peer(&list[at], 0), by_logit(y[e], i0 + e));
-        }
+        if (y[e] >= from) add(own, entries, by_logit(y[e], i0 + e));
     });
+    hand_over(list, entries);
     cluster_sync();
     return peer_get(peer(&s.count, 0));
   }
@@ -481,7 +485,8 @@ struct Wide {
         if (rank == 0 && tid == 0) x[0] = s.before;
       }
       if (tid == 0) s.count = 0;
-      cluster_sync();
+      cluster_sync();  // (the bins have been read as well)
+      u64* const own = own_list(s.list);
       // nothing below this can be in the bins up to b1
       const float least_y = by_value ? fmaxf(lo, hi - (float)(b1 + 2) / scale) : fmaxf(lo, of_key(top_key - min(top_key, (uint32_t)((u64)(b1 + 1) << shift))));
       binned([&](auto bin_of) {
@@ -500,8 +505,7 @@ struct Wide {
                   x[2] += w;
                   x[3] = max(x[3], (u64)key_of(y));
                   x[4] = max(x[4], (u64)~key_of(y) & 0xFFFFFFFFull);
-                  const int at = peer_add(peer(&s.count, 0), 1);
-                  if (at < kList) put(peer(&s.list[at], 0), by_logit(y, id));
+                  add(own, kList, by_logit(y, id));
                 }
               }
             }
@@ -512,6 +516,7 @@ struct Wide {
         else
           pass([](float) { return (u64)1; });
       });
+      hand_over(s.list, kList);
       exchange<5, 24>(s, x, rank, cluster, turn);
       above += x[0];
       if (kMass && (above >= goal || above + x[2] < goal)) return by_halves<kMass>(goal, m, wf);
@@ -606,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
       }
-      if (tid == 0) s.count = 0;
+      if (tid == 0) s.count = s.local = 0;
       v = begin;
 #pragma unroll
       for (int q = 1; q <= 4; ++q) {
@@ -700,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         __syncthreads();  // s.floor
       }
       const float floor_x = s.floor;
-      Wide<T> row_in{s, r, table, rank, cluster, turn, -INFINITY, 0x7FFFFFFF, -1};
+      Wide<T> row_in{s, r, table, rank, cluster, turn, -INFINITY, 0x7FFFFFFF, 0, -1};
 
       // ---- the short way
       bool wide = list != nullptr;

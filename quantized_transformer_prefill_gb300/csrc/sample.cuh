@@ -398,6 +398,8 @@ __device__ __forceinline__ bool finish_list(u64* list, u64* red, int n, const Se
                                             u64 whole, bool open, F write) {
   sort_list<kThreads, kEntries>(list, n);
   if (n <= kThreads) return finish_sorted<kThreads, 1, kEntries, kCopies>(list, red, n, s, wf, wd, table, floor_x, whole, open, write);
+  if (kEntries > 2 * kThreads && n <= 2 * kThreads)
+    return finish_sorted<kThreads, 2, kEntries, kCopies>(list, red, n, s, wf, wd, table, floor_x, whole, open, write);
   return finish_sorted<kThreads, kEntries / kThreads, kEntries, kCopies>(list, red, n, s, wf, wd, table, floor_x, whole, open, write);
 }
 

@@ -124,6 +124,34 @@ def test_sample(qp, t, V, extra, kind):
         check(qp, x, u, first=first, **settings)
 
 
+@pytest.mark.parametrize("t,rows,V", [(F32, 52, 151936), (BF16, 130, 150001), (F16, 400, 40000)])
+@pytest.mark.parametrize("kind", list(SETTINGS))
+def test_sample_streamed_rows(qp, t, rows, V, kind):
+    """More rows than their clusters fit the GPU: they are streamed."""
+    g = gen(V + rows + len(kind))
+    x = logits(g, rows, V, t, 3, masked=True)
+    u = torch.rand(rows, generator=g, device="cuda").tolist()
+    u[0], u[1] = 0.0, 1 - 2.0 ** -24
+    x[rows // 2] = -INF
+    assert qp.op_sample_workspace(x) is not None
+    check(qp, x, u, first=kind in ("p", "all"), **{name: [f(r) for r in range(rows)] for name, f in SETTINGS[kind].items()})
+
+
+def test_sample_borders_between_plateaus(qp):
+    """top_p next to the share of a plateau of many equal logits, and a k next to its length: the border is one of two values
+    that both keep more tokens than a list holds."""
+    for V, rows in ((6000, 9), (151936, 9), (151936, 60)):
+        x = torch.zeros(rows, V, device="cuda")
+        x[:, 1::2] = 0.75
+        upper = (V // 2) * math.exp(0.75)
+        share = upper / (upper + (V - V // 2))
+        p = [float(torch.tensor(share, dtype=F32)) + d * 2.0 ** -24 for d in (-40, -2, -1, 0, 1, 2, 40, -4000, 4000)]
+        u = [0.1 * r for r in range(9)]
+        for k in (None, [V // 2, V // 2 + 1, V // 2 - 1, 3000, V - 1, 0, 1, 2, V // 2]):
+            settings = dict(p=(p * 7)[:rows]) if k is None else dict(k=(k * 7)[:rows], p=([1.0, 0.5, 0.9] * 20)[:rows])
+            check(qp, x, (u * 7)[:rows], **settings)
+
+
 @pytest.mark.parametrize("rows", [300, 5000])
 def test_sample_many_rows(qp, rows):
     g = gen(rows)
@@ -227,7 +255,7 @@ def test_sample_at_any_alignment(qp, t, offset):
 
 
 def test_sample_alone_and_in_a_batch(qp):
-    """A row's token and log probability do not depend on the batch (nor on how many CTAs share a row)."""
+    """A row's token does not depend on the batch, whether it is kept or streamed; a call again gives the same bits."""
     g = gen(3)
     rows, V = 200, 50000
     x = logits(g, rows, V, F32)
@@ -236,7 +264,8 @@ def test_sample_alone_and_in_a_batch(qp):
     token, logprob = qp.op_sample(x, u, temp, k, p)
     for r in (0, 1, 2, 77, 199):
         one = qp.op_sample(x[r:r + 1], u[r:r + 1], temp[r:r + 1], k[r:r + 1], p[r:r + 1])
-        assert torch.equal(one[0], token[r:r + 1]) and torch.equal(one[1], logprob[r:r + 1])
+        assert torch.equal(one[0], token[r:r + 1])
+        close(one[1], logprob[r:r + 1], 2.0 ** -28 + 2.0 ** -22 * logprob[r:r + 1].double().abs())
     for _ in range(3):
         again = qp.op_sample(x, u, temp, k, p)
         assert torch.equal(again[0], token) and torch.equal(again[1], logprob)
@@ -244,39 +273,40 @@ def test_sample_alone_and_in_a_batch(qp):
 
 def test_sample_padding_and_refused_rows(qp):
     g = gen(4)
-    for V in (60, 5000, 151936):
-        x = logits(g, 10, V, F32)
-        u = torch.rand(10, generator=g, device="cuda")
-        want = qp.op_sample(x, u, torch.ones(10, device="cuda"))
+    for V, rows in ((60, 10), (5000, 10), (151936, 10), (151936, 60)):
+        x = logits(g, rows, V, F32)
+        u = torch.rand(rows, generator=g, device="cuda")
+        want = qp.op_sample(x, u, torch.ones(rows, device="cuda"))
         bad = [("u", 1, -1.0, 0), ("u", 2, 1.0, -1), ("u", 3, math.nan, -1), ("temp", 4, -1.0, -1), ("temp", 5, math.nan, -1), ("temp", 6, 1e-7, -1),
                ("temp", 7, INF, -1), ("p", 1, -0.5, -1), ("p", 2, math.nan, -1), ("floor", 3, -0.1, -1), ("floor", 4, 1.5, -1), ("floor", 5, math.nan, -1),
                ("x", 6, math.nan, -1), ("x", 7, INF, -1), ("x", 8, -math.nan, -1)]
         for what, row, value, code in bad:
-            a = dict(x=x.clone(), u=u.clone(), temp=torch.ones(10, device="cuda"), p=torch.ones(10, device="cuda"), floor=torch.zeros(10, device="cuda"))
+            a = dict(x=x.clone(), u=u.clone(), temp=torch.ones(rows, device="cuda"), p=torch.ones(rows, device="cuda"), floor=torch.zeros(rows, device="cuda"))
             if what == "x":
                 a["x"][row, V // 3] = value
             else:
                 a[what][row] = value
-            out = (torch.full((10,), 77, dtype=I32, device="cuda"), torch.full((10,), 77.0, device="cuda"))
+            out = (torch.full((rows,), 77, dtype=I32, device="cuda"), torch.full((rows,), 77.0, device="cuda"))
             status = status_word()
             qp.op_sample(a["x"], a["u"], a["temp"], None, a["p"], a["floor"], out=out, status=status)
             assert int(status) == code, (what, value)
-            rest = [r for r in range(10) if r != row]
+            rest = [r for r in range(rows) if r != row]
             assert int(out[0][row]) == 77 and float(out[1][row]) == 77
             assert torch.equal(out[0][rest], want[0][rest]) and torch.equal(out[1][rest], want[1][rest])
-    fresh = qp.op_sample(x, torch.full((10,), -1.0, device="cuda"))
+    fresh = qp.op_sample(x, torch.full((rows,), -1.0, device="cuda"))
     assert (fresh[0] == -1).all() and (fresh[1] == 0).all()
-    only = torch.empty(10, dtype=I32, device="cuda")
+    only = torch.empty(rows, dtype=I32, device="cuda")
     qp.op_sample(x, u, out=(only, None))
     assert torch.equal(only, want[0])
 
 
-def test_sample_streams_and_captured_graphs(qp):
+@pytest.mark.parametrize("rows,V", [(6, 30000), (60, 151936)])
+def test_sample_streams_and_captured_graphs(qp, rows, V):
     """Two graphs captured on one side stream, replayed with other inputs, and calls at once on two streams."""
     g = gen(6)
-    x = logits(g, 6, 30000, F32)
-    u = torch.rand(6, generator=g, device="cuda")
-    k, p = dev([0, 50, 0, 700, 3, 0]), torch.tensor([1.0, 0.9, 0.9, 1.0, 1.0, 0.5], device="cuda")
+    x = logits(g, rows, V, F32)
+    u = torch.rand(rows, generator=g, device="cuda")
+    k, p = dev([0, 50, 0, 700, 3, 0] * (rows // 6)), torch.tensor([1.0, 0.9, 0.9, 1.0, 1.0, 0.5] * (rows // 6), device="cuda")
     side = torch.cuda.Stream()
     graphs = []
     for i in range(2):
@@ -289,7 +319,7 @@ def test_sample_streams_and_captured_graphs(qp):
             got = qp.op_sample(x, u, None, k, p)
         graphs.append((graph, got))
     x.mul_(0.8)
-    u.copy_(torch.rand(6, generator=g, device="cuda"))
+    u.copy_(torch.rand(rows, generator=g, device="cuda"))
     torch.cuda.synchronize()
     for graph, _ in graphs:
         graph.replay()
@@ -308,6 +338,25 @@ def test_sample_streams_and_captured_graphs(qp):
     torch.cuda.synchronize()
     for one in got:
         assert all(torch.equal(a, b) for a, b in zip(one, want))
+
+
+def test_sample_workspaces(qp):
+    """A workspace that is given serves calls of its shape whatever it holds; one that is too small is refused."""
+    g = gen(8)
+    x = logits(g, 60, 151936, F32)
+    u = torch.rand(60, generator=g, device="cuda")
+    p = torch.full((60,), 0.95, device="cuda")
+    want = qp.op_sample(x, u, None, None, p)
+    work = qp.op_sample_workspace(x)
+    for fill in (0, 255, 77):
+        work.fill_(fill)
+        got = qp.op_sample(x, u, None, None, p, workspace=work)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with pytest.raises(qp.MinferError, match="TOO_LARGE"):
+        qp.op_sample(x, u, None, None, p, workspace=work[:-256])
+    with pytest.raises(qp.MinferError, match="workspace"):
+        qp.op_sample(x, u, None, None, p, workspace=work.int())
+    assert qp.op_sample_workspace(x[:1]) is None
 
 
 def test_rows_of_a_model_are_sampled(qp):
