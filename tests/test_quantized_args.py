@@ -171,6 +171,21 @@ def test_the_binding_refuses(qp):
         qp.PagedCacheQ8(one.expand(2 ** 32 + 1, 1, 1, 64), one.expand(2 ** 32 + 1, 1, 1, 64), two.expand(2 ** 32 + 1, 1, 1, 2), two.expand(2 ** 32 + 1, 1, 1, 2))
 
 
+def test_caches_of_the_other_kind_are_refused(qp):
+    """Their descriptions have other layouts: a call that read one as the other would take scales' addresses for sizes."""
+    codes, scales = torch.zeros(4, 16, 2, 64, dtype=torch.int8), torch.zeros(4, 16, 2, 2, dtype=torch.float16)
+    q8, plain = qp.PagedCacheQ8(codes, codes, scales, scales), qp.PagedCache(codes.half(), codes.half())
+    n, table = torch.zeros(2, dtype=I32), torch.zeros(2, 3, dtype=I32)
+    for call in (lambda: qp.op_rope_paged_store_q8(torch.zeros(2, 512), qp.RopeTable(64), n, n, plain, 4), lambda: qp.op_paged_read_q8(plain, n),
+                 lambda: qp.op_paged_attention_q8(torch.zeros(2, 256), plain, table, n, 4), lambda: qp.op_paged_attention_q8_workspace(plain, 2, 4)):
+        with pytest.raises(qp.MinferError, match="PagedCacheQ8 wanted"):
+            call()
+    for call in (lambda: qp.op_rope_paged_store(torch.zeros(2, 512), qp.RopeTable(64), n, n, q8, 4), lambda: qp.op_paged_attention(torch.zeros(2, 256), q8, table, n, 4),
+                 lambda: qp.op_paged_attention_workspace(q8, 2, 4)):
+        with pytest.raises((qp.MinferError, AttributeError)):
+            call()
+
+
 SAMPLE = dict(logits=PTR, type=F32, rows=3, vocab=100, row_stride=101, u=PTR, temperature=PTR, top_k=PTR, top_p=PTR, min_p=PTR, first=0,
               token=PTR, logprob=PTR, ws=PTR, ws_bytes=2 ** 40, status=None, stream=None)
 
