@@ -2,7 +2,9 @@
 implementations: RoPE with the quantizing store, rows read back, attention of one
 token per request, and a run of them together."""
 import math
+import os
 import random
+import re
 
 import pytest
 
@@ -212,8 +214,9 @@ def q8_tolerance(t, hd, length, want):
     """attention_by_definition's terms.  Score error: the MMA sums of a block cut off (2^-23 of the partial sum, hd / 8 + 2 of
     them over the row with the blocks' multiply-adds); f32 queries in two f16 numbers lose 2^-22, bf16 ones 2^-39 of the
     largest; the scaled score's rounding and the exponential's 2 ulp come on top.  Each weight's relative error is the score
-    error twice (its own and the sum's); times its scale it is rounded (U) and split: two bf16 numbers leave 2^-18, three
-    2^-27; sums of up to 64 + units adds, the tensor core's (2 U) two or three a unit of 64 keys for 16-bit results."""
+    error twice (its own and the sum's); times its scale it is rounded (U) and split: two f16 numbers leave 2^-22, 4 U as
+    counted for f32, less than the 2^-18 counted for 16-bit results; sums of up to 64 + units adds, the tensor core's (2 U) two
+    or three a unit of 64 keys for 16-bit results."""
     o, lse, mean, size, top = want
     score = size * ((hd // 8 + 2) * 2.0 ** -23 + 2.0 ** -22 + 4 * U) + 8 * U
     m = torch.tensor([max(x, 1) for x in length], dtype=torch.float64, device="cuda")[:, None, None]
@@ -569,3 +572,36 @@ def test_a_quantized_context_is_extended_by_the_prompt_attention(qp):
     s.masked_fill_(torch.arange(n + more, device="cuda") > pos[:, None, None, None], -math.inf)
     want = torch.einsum("thgj,jhd->thgd", torch.softmax(s, -1), vv).reshape(more, nh * hd)
     close(got, want, 2e-5 * float(want.abs().max()))
+
+
+def test_the_readmes_quantized_step(qp):
+    """The README's step over a quantized cache: requests of a prompt, of one token and of none, down to their tokens."""
+    nh, nkv, hd, P, V, n_pages = 4, 2, 64, 16, 300, 12
+    text = open(os.path.join(os.path.dirname(__file__), "..", "README.md")).read()
+    block = next(b for b in re.findall(r"```python\n(.*?)```", text, re.S) if "op_paged_attention_q8" in b)
+    g = gen(21)
+    codes, scales = torch.zeros(2, n_pages, P, nkv, hd, dtype=torch.int8, device="cuda"), torch.zeros(2, n_pages, P, nkv, 2, dtype=F16, device="cuda")
+    table, free, n_free = torch.full((3, 4), -1, dtype=I32, device="cuda"), torch.arange(n_pages, dtype=I32, device="cuda"), dev([n_pages])
+    logits = torch.randn(3, V, generator=g, device="cuda")
+    s = dict(qp=qp, rope=qp.RopeTable(hd), n_head=nh, bias=None, table=table, logits=logits, k_codes=codes[0], v_codes=codes[1], k_scales=scales[0],
+             v_scales=scales[1], temperature=torch.tensor([0.0, 1.0, 0.5], device="cuda"), top_k=dev([0, 1, 0]), top_p=torch.tensor([1.0, 1.0, 0.9], device="cuda"),
+             min_p=torch.zeros(3, device="cuda"), u=torch.tensor([0.5, 0.9, -1.0], device="cuda"))
+    have = [0, 0, 0]
+    for want in ([30, 7, 0], [31, 8, 0], [32, 8, 0]):
+        status = status_word()
+        start, pos, slot, n_free = qp.op_page_tables(dev(have), dev(want), P, table, free, n_free, n_pages, 40, status=status)
+        slots = [[int(table[r, p // P]) * P + p % P for p in range(want[r])] for r in range(3)]
+        s.update(start=start, pos=pos, slot=slot, rows=dev(want), status=status, slots=dev(slots[0] + slots[1]),
+                 qkv=torch.randn(40, (nh + 2 * nkv) * hd, generator=g, device="cuda"))
+        exec(block, s)
+        k, v = (x.double().view(-1, nkv, hd).split(want[:2]) for x in (s["k"], s["v"]))
+        last = s["q"][(start[1:].long() - 1).clamp(min=0)].double().view(3, nkv, nh // nkv, hd)
+        for r in range(2):
+            assert (k[r] != 0).any() and (v[r] != 0).any()
+            p = torch.softmax(torch.einsum("hgd,jhd->hgj", last[r], k[r]) / math.sqrt(hd), -1)
+            # (as in the test above: |q|, |k|, |v| < 6, a score's error 2^-20 of its sum of sizes)
+            size = float(last[r].abs().sum() / math.sqrt(hd)) * 6
+            close(s["o"][r], torch.einsum("hgj,jhd->hgd", p, v[r]).flatten(), 6 * (2 * size * 2.0 ** -20 + 2.0 ** -18))
+        assert (s["o"][2] == 0).all()
+        assert s["token"].tolist() == [int(logits[0].argmax()), int(logits[1].argmax()), -1] and (s["logprob"] == 0).all()
+        have = want
