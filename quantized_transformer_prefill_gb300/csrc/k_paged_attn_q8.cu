@@ -9,19 +9,33 @@
 // with keys and dims as the rows and 8 query heads as the columns.  What differs:
 //
 //  - Half the bytes a key, so twice the keys a second: a row is turned into MMA
-//    operands in registers, which must cost little.  A code is exact in f16 and bf16:
-//    one logic operation puts two codes under the exponent of 1024 (f16) or 128 (bf16),
-//    one packed subtraction takes that off again.
+//    operands in registers, which must cost little.  A code is exact in f16: one logic
+//    operation puts two of them under the exponent of 1024, one packed subtraction
+//    takes that off again.
 //  - Q K^T: the sum over a block is an accumulator of its own, two k16 MMAs of f16;
 //    the block's scale comes in as an f32 multiply-add.  Which 16 dims an MMA takes is
 //    free as long as Q follows, so a lane reads 8 neighbouring codes of a key.  Q is
 //    f16: exact, or times a power of two that brings the head's largest value near
 //    2^15 (bf16, which loses what lies 2^-40 below it; f32, as the sum of two).
-//  - P V: a weight times the row's scale is what the MMAs take, per block of 32 dims,
-//    in bf16, whose range is that of f32: as the sum of two numbers, three with f32
-//    queries.  The weights change from the layout of S^T to that of P^T as f32, in two
-//    halves of 16 bits (transpose8); V's codes come transposed out of ldmatrix, two
-//    neighbouring dims in a 16-bit element.
+//  - P V: a weight times the row's scale is what the MMAs take, per block of 32 dims, as
+//    the sum of two f16 numbers (one would leave 2^-11 of the weight, more than a
+//    result's own rounding).  They count in units of 2^-15 of a power of two that no scale
+//    of the piece so far exceeds; when a larger one comes, the outputs are scaled down as
+//    they are for a new maximum.  So none overflows, and what is lost lies 2^-22 below the
+//    weight or 2^-40 below the largest.  The weights change from the layout of S^T to that
+//    of P^T as f32, in two halves of 16 bits (transpose8); V's codes come transposed out
+//    of ldmatrix, two neighbouring dims in a 16-bit element.
+//  - With 16-bit queries and heads of 128 a warp takes two tiles of 16 keys at a time: two
+//    chains of dependent steps instead of one.
+//
+// Measured: 64 requests of up to 4096 tokens, 28/4 heads of 128, bf16, 144 MB: 42 us (3.4
+// TB/s); one of 131,071, 12/2 heads of 128, f16, 71 MB: 26 us; 33 of up to 2048, 14/2 heads
+// of 64, f32: 13.4 us; one of 513: 7.2 us.  Of the first 13 us are start, uneven ends and
+// join; of the rest the loads alone take 15 and the arithmetic alone 22, so issue slots bound
+// it: a key and head block of 8 costs the same MMAs and conversions whether 7 or 8 of its
+// columns are heads.  Four CTAs an SM with one tile took 51 us (registers spill), branches
+// that leave out the masks of whole tiles 44, packed f16 products of weights and scales the
+// same 42 and more with heads of 64.
 #include <algorithm>
 #include <type_traits>
 

@@ -17,18 +17,25 @@
 // itself) and shifted to a fixed point that is the same for the whole row; their sums
 // are exact in 64 bits and do not depend on who adds what first.
 //
-// Many rows are streamed once (k_sample_stream.cu); this file: rows that a thread-block cluster keeps.  A CTA copies its slice of the row
-// into shared memory (cp.async, all of it on its way at once; a thread reads what it has
-// copied itself), so further passes cost no memory traffic.  What lies behind the room in
-// shared memory is read again from L2.
+// Many rows are streamed once (k_sample_stream.cu); this file: rows that a thread-block
+// cluster keeps.  A CTA copies its slice of the row into shared memory (cp.async, all of it
+// on its way at once; a thread reads what it has copied itself), so further passes cost no
+// memory traffic.  What lies behind the room in shared memory is read again from L2.
 //
 // Most rows need two or three exchanges in the cluster: (1) the maximum, and a bound
-// under which nothing can be among the first k, from the maxima of half threads; (2) with top-p and no top-k, the sum of all weights; (3) what lies
-// above the bound goes to the first CTA, which sorts it (a few hundred tokens), cuts it
-// by the three filters, sorts what is left by id and draws.  Rows for which that list
-// overflows or does not reach (no filter, high temperatures, large k) go the wide way:
-// a histogram brackets the border of a filter until a list holds what lies between, and
-// the draw goes segment by segment.
+// under which nothing can be among the first k, from the maxima of half threads; (2) with
+// top-p and no top-k, the sum of all weights; (3) what lies above the bound goes to the
+// first CTA, which sorts it (a few hundred tokens), cuts it by the three filters, sorts
+// what is left by id and draws.  Rows for which that list overflows or does not reach (no
+// filter, high temperatures, large k) go the wide way: a histogram brackets the border of a
+// filter until a list holds what lies between, and the draw goes segment by segment.
+//
+// Measured, f32 rows of 151,936: one with top-k and top-p 12.9 us, four top-p alone 22 us:
+// a chain of memory round trip, barriers of the cluster (1 us each) and a sort.  65 bf16
+// rows of 150,001 with top-p alone and temperatures up to 1.3, whose nuclei hold thousands of
+// tokens, 100 us (0.2 TB/s): issue slots, with two CTAs an SM; the longest row sets the time.
+// It weighs all of its tokens (15 us), counts them into the histogram (10 to 20), weighs
+// those above the border exactly (15 to 28), and again to draw (5 to 15).
 #include <algorithm>
 
 #include "sample.cuh"
@@ -345,12 +352,24 @@ struct Wide {
     return peer_get(peer(&s.count, 0));
   }
 
+  // The nth token (from 1 on), in the order of ids, that is kept and lies in [lo, hi].  (The
+  // rare cases are functions of their own.)
+  __device__ __noinline__ u64 nth_of(float lo, float hi, u64 nth) {
+    u64 sum;
+    return locate(lo, [&](float y, int id) { return (u64)(y >= lo && y <= hi && kept(y, id)); }, [&](u64) { return nth - 1; }, &sum);
+  }
+  __device__ __forceinline__ u64 nth(float lo, float hi, u64 n) {
+    Wide w = *this;  // (its address is taken: this one stays in registers)
+    const u64 found = w.nth_of(lo, hi, n);
+    turn = w.turn;
+    return found;
+  }
+
   // What is left of `cut` when the border is one value: of its equals the first ones.
   template <bool kMass>
   __device__ __forceinline__ void cut_equals(float at, u64 rest, const Weigh& wf) {
-    const u64 w = kMass ? wf.one<kCopies>(at, table) : 1, nth = (rest + w - 1) / w;
-    u64 sum;
-    const u64 found = locate(at, [&](float y, int id) { return (u64)(y == at && kept(y, id)); }, [&](u64) { return nth - 1; }, &sum);
+    const u64 w = kMass ? wf.one<kCopies>(at, table) : 1;
+    const u64 found = nth(at, at, (rest + w - 1) / w);
     xb = at;
     idb = (int)(uint32_t)found;
   }
@@ -381,7 +400,7 @@ struct Wide {
 
   template <bool kMass>
   __device__ __forceinline__ void by_halves(u64 goal, float m, const Weigh& wf) {
-    Wide w = *this;  // (its address is taken: this one stays in registers)
+    Wide w = *this;
     const Weigh copy = wf;
     w.template bisect<kMass>(goal, m, copy);
     xb = w.xb;
@@ -415,24 +434,17 @@ struct Wide {
       const uint32_t top_key = key_of(hi);
       const int shift = max(0, 22 - (int)__clz(top_key - key_of(lo)));  // 1,024 steps of 2^shift hold all
       const float unit = kMass ? exp2f((float)(62 - wf.down)) / (float)whole * 0x1p31f : 0.f;
-      // calls f(bin of y) with y in [lo, hi] (hi is the maximum while steps are by value)
-      auto binned = [&](auto f) {
-        if (by_value)
-          f([&](float y) { return min((int)((hi - y) * scale), kBins - 1); });
-        else
-          f([&](float y) { return (int)((top_key - key_of(y)) >> shift); });
-      };
+      // of y in [lo, hi] (hi is the maximum while steps are by value)
+      auto bin_of = [&](float y) { return by_value ? min((int)((hi - y) * scale), kBins - 1) : (int)((top_key - key_of(y)) >> shift); };
       auto inside = [&](float y, int id) { return y >= lo && y <= hi && kept(y, id); };
       for (int i = tid; i < 2 * kBins; i += kThreads) (&s.bins[0][0])[i] = 0;
       __syncthreads();
-      binned([&](auto bin_of) {
-        each(lo, [&](float y, int id) {
-          if (inside(y, id)) {
-            const int b = bin_of(y);
-            atomicAdd(&s.bins[0][b], 1u);
-            if constexpr (kMass) atomicAdd(&s.bins[1][b], __float2uint_rn(ex2(fmaf(y - m, wf.c, first)) * unit));
-          }
-        });
+      each(lo, [&](float y, int id) {
+        if (inside(y, id)) {
+          const int b = bin_of(y);
+          atomicAdd(&s.bins[0][b], 1u);
+          if constexpr (kMass) atomicAdd(&s.bins[1][b], __float2uint_rn(ex2(fmaf(y - m, wf.c, first)) * unit));
+        }
       });
       cluster_sync();
       // the whole cluster's: four bins of this thread
@@ -489,32 +501,24 @@ struct Wide {
       u64* const own = own_list(s.list);
       // nothing below this can be in the bins up to b1
       const float least_y = by_value ? fmaxf(lo, hi - (float)(b1 + 2) / scale) : fmaxf(lo, of_key(top_key - min(top_key, (uint32_t)((u64)(b1 + 1) << shift))));
-      binned([&](auto bin_of) {
-        auto pass = [&](auto weigh) {
-          each(least_y, [&](float y, int id) {
-            if (y >= least_y && inside(y, id)) {
-              const int b = bin_of(y);
-              if (b <= b1) {
-                u64 w = 1;
-                if constexpr (kMass) {
-                  w = weigh(y);
-                  if (b < b0) x[0] += w;
-                }
-                if (b >= b0) {
-                  x[1] += 1;
-                  x[2] += w;
-                  x[3] = max(x[3], (u64)key_of(y));
-                  x[4] = max(x[4], (u64)~key_of(y) & 0xFFFFFFFFull);
-                  add(own, kList, by_logit(y, id));
-                }
-              }
+      each(least_y, [&](float y, int id) {
+        if (y >= least_y && inside(y, id)) {
+          const int b = bin_of(y);
+          if (b <= b1) {
+            u64 w = 1;
+            if constexpr (kMass) {
+              w = wf.one<kCopies>(y, table);
+              if (b < b0) x[0] += w;
             }
-          });
-        };
-        if constexpr (kMass)
-          wf.each<kCopies>(table, pass);
-        else
-          pass([](float) { return (u64)1; });
+            if (b >= b0) {
+              x[1] += 1;
+              x[2] += w;
+              x[3] = max(x[3], (u64)key_of(y));
+              x[4] = max(x[4], (u64)~key_of(y) & 0xFFFFFFFFull);
+              add(own, kList, by_logit(y, id));
+            }
+          }
+        }
       });
       hand_over(s.list, kList);
       exchange<5, 24>(s, x, rank, cluster, turn);
@@ -688,15 +692,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       bool covered = false;
       if (set.k == 0 && set.top_p < 1.f && whole == 0) {
         u64 v3[2] = {0, 0};
-        wf.each<kCopies>(table, [&](auto weigh) {
-          r.each([&](const float (&y)[E], int) {
+        r.each([&](const float (&y)[E], int) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-              const u64 w = weigh(y[e]);
-              v3[0] += w;
-              v3[1] += y[e] >= b ? w : 0;
-            }
-          });
+          for (int e = 0; e < E; ++e) {
+            const u64 w = wf.one<kCopies>(y[e], table);
+            v3[0] += w;
+            v3[1] += y[e] >= b ? w : 0;
+          }
         });
         exchange<2>(s, v3, rank, cluster, turn);
         whole = v3[0];
@@ -735,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           row_in.template cut<false>((u64)set.k, 0, m, b, wf);
           if (set.top_p < 1.f) {
             u64 v1[1] = {0};
-            wf.each<kCopies>(table, [&](auto weigh) { row_in.each(row_in.xb, [&](float y, int id) { v1[0] += row_in.kept(y, id) ? weigh(y) : 0; }); });
+            row_in.each(row_in.xb, [&](float y, int id) { v1[0] += row_in.kept(y, id) ? wf.one<kCopies>(y, table) : 0; });
             exchange<1>(s, v1, rank, cluster, row_in.turn);
             whole = v1[0];
           }
@@ -749,17 +751,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           if (set.k == 0) row_in.pick(low);
           row_in.template cut<true>(need, whole, m, low, wf);
         }
-        u64 count, found = 0;
         from = fmaxf(floor_x, row_in.xb);
-        wd.each<kCopies>(table, [&](auto weigh) {
-          found = row_in.locate(from, [&](float y, int id) { return y >= from && row_in.kept(y, id) ? weigh(y) : 0; },
-                                [&](u64 n) {
-                                  bool rest;
-                                  return times(n, set.u, &rest);
-                                },
-                                &whole);
-        });
-        if (set.u == 0.f) found = row_in.locate(from, [&](float y, int id) { return (u64)(y >= from && row_in.kept(y, id)); }, [](u64) { return (u64)0; }, &count);
+        u64 found = row_in.locate(from, [&](float y, int id) { return y >= from && row_in.kept(y, id) ? wd.one<kCopies>(y, table) : 0; },
+                                  [&](u64 n) {
+                                    bool rest;
+                                    return times(n, set.u, &rest);
+                                  },
+                                  &whole);
+        if (set.u == 0.f) found = row_in.nth(from, m, 1);
         turn = row_in.turn;
         if (rank == 0 && tid == 0) {
           const float y = __uint_as_float((uint32_t)(found >> 32));

@@ -177,33 +177,33 @@ struct Weigh {
     top = 0;
     top = whole_of(max);
   }
-  // t = (x or x - m) log2(e) / T as th + tl
-  template <bool kApart>
+  // t = (x or x - m) log2(e) / T as th + tl; kApart false: the caller knows that the row is
+  // not apart
+  template <bool kApart = true>
   __device__ __forceinline__ void exponent(float x, float* th, float* tl) const {
-    if constexpr (!kApart) {
-      x = fmaxf(x, lim);
-      *th = __fmul_rn(x, c);
-      *tl = fmaf(x, c_low, fmaf(x, c, -*th));
-    } else {
+    float low = 0.f;
+    if (kApart && apart) {
       float d = __fsub_rn(x, m);
       const float b = __fsub_rn(d, x);
-      float low = __fadd_rn(__fsub_rn(x, __fsub_rn(d, b)), __fsub_rn(-m, b));
+      low = __fadd_rn(__fsub_rn(x, __fsub_rn(d, b)), __fsub_rn(-m, b));
       if (!(d > lim)) d = lim, low = 0.f;
-      *th = __fmul_rn(d, c);
-      *tl = fmaf(low, c, fmaf(d, c_low, fmaf(d, c, -*th)));
+      x = d;
+    } else {
+      x = fmaxf(x, lim);
     }
+    *th = __fmul_rn(x, c);
+    *tl = fmaf(x, c_low, fmaf(x, c, -*th));
+    if (kApart) *tl = fmaf(low, c, *tl);
   }
   __device__ __forceinline__ int whole_of(float x) const {
     float th, tl;
-    if (apart)
-      exponent<true>(x, &th, &tl);
-    else
-      exponent<false>(x, &th, &tl);
+    exponent(x, &th, &tl);
     return (int)(__float_as_uint(th + kStep) - __float_as_uint(kStep)) >> 8;
   }
-  // table: the caller's copy, entry j at j * kCopies
-  template <bool kApart, int kCopies>
-  __device__ __forceinline__ u64 weight(float x, const uint2* table) const {
+  // table: the caller's copy, entry j at j * kCopies.  (One piece of code for rows that are
+  // apart and rows that are not: the kernels wait for their instructions.)
+  template <int kCopies, bool kApart = true>
+  __device__ __forceinline__ u64 one(float x, const uint2* table) const {
     float th, tl;
     exponent<kApart>(x, &th, &tl);
     const float k = __fadd_rn(th, kStep);
@@ -217,18 +217,6 @@ struct Weigh {
     u64 w;  // rounded: cut off, 150,000 small weights would lose 2^-28 of the largest
     asm("shr.b64 %0, %1, %2;" : "=l"(w) : "l"((u64)mant << 32), "r"(top - whole + down - 1));
     return (w + 1) >> 1;
-  }
-  template <int kCopies>
-  __device__ __forceinline__ u64 one(float x, const uint2* table) const {
-    return apart ? weight<true, kCopies>(x, table) : weight<false, kCopies>(x, table);
-  }
-  // f(weight of x) without a branch per weight: calls f(function of x)
-  template <int kCopies, typename F>
-  __device__ __forceinline__ void each(const uint2* table, F f) const {
-    if (apart)
-      f([&](float x) { return weight<true, kCopies>(x, table); });
-    else
-      f([&](float x) { return weight<false, kCopies>(x, table); });
   }
 };
 
