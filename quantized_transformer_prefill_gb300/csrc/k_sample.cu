@@ -89,7 +89,7 @@ __device__ __forceinline__ int peer_get(uint32_t a) {
 struct SampleShared {
   uint2 table[256 * kCopies];
   u64 list[kList];
-  uint32_t bins[2][kBins];         // tokens, and their weights as shares of 2^31
+  uint32_t bins[kBins];            // tokens, or their weights as shares of 2^31
   union {
     uint16_t picked[kWarps][kPicked][32];  // where they lie in the segment
     u64 longer[kShort];                // a list of the short way
@@ -321,7 +321,7 @@ struct Wide {
   // list, if there is no other CTA), and hands them over together, for a word of another
   // CTA's is far away.  add: by any thread; hand_over: by all, behind the last add; the
   // entries are there behind the next barrier of the cluster.
-  __device__ __forceinline__ u64* own_list(u64* list) const { return cluster == 1 ? list : reinterpret_cast<u64*>(&s.bins[0][0]); }
+  __device__ __forceinline__ u64* own_list(u64* list) const { return cluster == 1 ? list : reinterpret_cast<u64*>(s.bins); }
   __device__ __forceinline__ void add(u64* own, int entries, u64 entry) const {
     const int at = atomicAdd(&s.local, 1);
     if (at < entries) own[at] = entry;
@@ -410,7 +410,7 @@ struct Wide {
 
   // Moves the border (xb, idb) to the last token, in descending order, before which less
   // than `goal` is kept: tokens (kMass false) or weights, of which there are `whole`.  It is
-  // not expected below `low`.
+  // not expected below `low`; no more than n_in tokens lie above that.
   //
   // A histogram over [lo, hi], first in equal steps of the value, then of its bits, says
   // between which two of its bins the border lies (weights in it are rounded to 2^-31 of all
@@ -418,7 +418,7 @@ struct Wide {
   // exactly what lies above them and collects what lies in them: sorted, if the list holds
   // it, else [lo, hi] closes in on it.
   template <bool kMass>
-  __device__ __forceinline__ void cut(u64 goal, u64 whole, float m, float low, const Weigh& wf) {
+  __device__ __forceinline__ void cut(u64 goal, u64 whole, float m, float low, u64 n_in, const Weigh& wf) {
     const int tid = threadIdx.x;
     float hi = m, lo = fmaxf(low, kLowest), first = 0.f;
     if constexpr (kMass) {  // the maximum's exponent less wf.top
@@ -434,58 +434,58 @@ struct Wide {
       const uint32_t top_key = key_of(hi);
       const int shift = max(0, 22 - (int)__clz(top_key - key_of(lo)));  // 1,024 steps of 2^shift hold all
       const float unit = kMass ? exp2f((float)(62 - wf.down)) / (float)whole * 0x1p31f : 0.f;
-      // of y in [lo, hi] (hi is the maximum while steps are by value)
-      auto bin_of = [&](float y) { return by_value ? min((int)((hi - y) * scale), kBins - 1) : (int)((top_key - key_of(y)) >> shift); };
+      // of y in [lo, hi] (hi is the maximum while steps are by value); the sum's last bits are
+      // the nearest whole number (a conversion has a quarter of an addition's rate)
+      auto bin_of = [&](float y) {
+        return by_value ? min((int)(__float_as_uint(fmaf(hi - y, scale, 0x1p23f)) & 0x7FFFFFu), kBins - 1) : (int)((top_key - key_of(y)) >> shift);
+      };
       auto inside = [&](float y, int id) { return y >= lo && y <= hi && kept(y, id); };
-      for (int i = tid; i < 2 * kBins; i += kThreads) (&s.bins[0][0])[i] = 0;
+      for (int i = tid; i < kBins; i += kThreads) s.bins[i] = 0;
       __syncthreads();
       each(lo, [&](float y, int id) {
         if (inside(y, id)) {
-          const int b = bin_of(y);
-          atomicAdd(&s.bins[0][b], 1u);
-          if constexpr (kMass) atomicAdd(&s.bins[1][b], __float2uint_rn(ex2(fmaf(y - m, wf.c, first)) * unit));
+          uint32_t n = 1;
+          if constexpr (kMass) n = __float2uint_rn(ex2(fmaf(y - m, wf.c, first)) * unit);
+          atomicAdd(&s.bins[bin_of(y)], n);
         }
       });
       cluster_sync();
       // the whole cluster's: four bins of this thread
       u64 v[4] = {0, 0, 0, 0};
       for (int c = 0; c < cluster; ++c) {
-        uint32_t n[4], w[4] = {0, 0, 0, 0};
-        get4(peer(&s.bins[0][4 * tid], c), n);
-        if constexpr (kMass) get4(peer(&s.bins[1][4 * tid], c), w);
+        uint32_t n[4];
+        get4(peer(&s.bins[4 * tid], c), n);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += (u64)n[i] << 32 | w[i];
+        for (int i = 0; i < 4; ++i) v[i] += n[i];
       }
       if (tid == 0) s.edge[0] = s.edge[1] = kBins - 1;
-      const u64 own0 = v[0] >> 32;
-      const u64 all = scan_all<kThreads, 4>(&s.red[0][0], v);
-      const uint32_t n_all = (uint32_t)(all >> 32);
+      const u64 own0 = v[0], all = scan_all<kThreads, 4>(&s.red[0][0], v);
       bool below = false;  // the border lies below lo
       if constexpr (kMass) {
         const float share = (float)(goal - above) / (float)whole * 0x1p31f;
-        const float slack = (float)n_all + 16384.f;  // a unit a token, and 2^-17: 62 2^-23 of an exponent and the rest
+        const float slack = (float)n_in + 16384.f;  // a unit a token, and 2^-17: 62 2^-23 of an exponent and the rest
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float w = (float)(uint32_t)v[i];
+          const float w = (float)v[i];
           if (w + slack >= share) atomicMin(&s.edge[0], 4 * tid + i);
           if (w - slack >= share) atomicMin(&s.edge[1], 4 * tid + i);
         }
       } else {
-        below = above + n_all < goal;
+        below = above + all < goal;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (above + (v[i] >> 32) >= goal) atomicMin(&s.edge[0], 4 * tid + i), atomicMin(&s.edge[1], 4 * tid + i);
+          if (above + v[i] >= goal) atomicMin(&s.edge[0], 4 * tid + i), atomicMin(&s.edge[1], 4 * tid + i);
         __syncthreads();
         // the tokens in the bins above the border's are counted already
         const int at = s.edge[0] - 4 * tid;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (at == i) s.before = i > 0 ? v[i > 0 ? i - 1 : 0] >> 32 : (v[0] >> 32) - own0;
+          if (at == i) s.before = i > 0 ? v[i > 0 ? i - 1 : 0] : v[0] - own0;
       }
       __syncthreads();
       if (below) {
         if (lo == kLowest) return;  // all of it is kept
-        above += n_all;
+        above += all;
         hi = of_key(key_of(lo) - 1);
         lo = kLowest;
         cluster_sync();  // the bins have been read
@@ -552,6 +552,7 @@ struct Wide {
       hi = of_key(top);
       lo = of_key(least);
       whole = x[2];
+      n_in = n;
     }
   }
 };
@@ -734,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (wide) {
         if (set.k > 0) {
           row_in.pick(b);
-          row_in.template cut<false>((u64)set.k, 0, m, b, wf);
+          row_in.template cut<false>((u64)set.k, 0, m, b, 0, wf);
           if (set.top_p < 1.f) {
             u64 v1[1] = {0};
             row_in.each(row_in.xb, [&](float y, int id) { v1[0] += row_in.kept(y, id) ? wf.one<kCopies>(y, table) : 0; });
@@ -749,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           const float share = (float)(whole > need ? whole - need : 0) / (float)a.vocab * exp2f((float)(down - 63));
           const float low = fmaxf(m + set.sharp * (logf(fmaxf(share, 0x1p-62f)) - 0.01f) - fabsf(m) * 0x1p-20f, kLowest);
           if (set.k == 0) row_in.pick(low);
-          row_in.template cut<true>(need, whole, m, low, wf);
+          row_in.template cut<true>(need, whole, m, low, (u64)a.vocab, wf);
         }
         from = fmaxf(floor_x, row_in.xb);
         u64 found = row_in.locate(from, [&](float y, int id) { return y >= from && row_in.kept(y, id) ? wd.one<kCopies>(y, table) : 0; },
