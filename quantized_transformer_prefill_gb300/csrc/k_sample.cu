@@ -47,6 +47,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kList = 512;    // tokens between which a border is looked for, sorted by the first CTA
 constexpr int kShort = 2048;  // tokens that a row's only CTA sorts; of a cluster kList, for they come one by one
+constexpr int kPair = 2;      // tokens that are picked, side by side
 constexpr int kPicked = 32;   // tokens that a lane picks out of its vectors, at most
 constexpr int kGuess = 64;    // of top-p alone: tokens that the first bound aims at
 constexpr int kCopies = 4;    // of the table, against bank conflicts
@@ -105,6 +106,9 @@ struct SampleShared {
   u64 before;                      // tokens in the bins before
   uint32_t keys[2][kWarps];
 };
+
+template <typename A>
+constexpr int kLength = std::extent<typename std::remove_reference<A>::type>::value;
 
 // What a CTA has of a row.
 template <typename T>
@@ -223,31 +227,40 @@ struct Wide {
     n_picked = n;
     most = v[0] ? -1 : top;
   }
-  // f(logit, id) for what may be `least` or more, by all lanes
+  // f(logits, ids) for what may be `least` or more, by all lanes; kPair or E of them at a time,
+  // so that their chains of steps overlap
   template <typename F>
   __device__ __forceinline__ void each(float least, F f) const {
     if (most >= 0) {
       const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
       const T* const seg = reinterpret_cast<const T*>(r.near + warp * r.seg);
       const int first = (int)r.first + warp * r.seg * E;
-      for (int i = 0; i < most; ++i) {
-        float x = -INFINITY;
-        int at = 0;
-        if (i < n_picked) {
-          at = s.picked[warp][i][lane];
-          if constexpr (sizeof(T) == 4)
-            x = seg[at];
-          else if constexpr (std::is_same<T, __half>::value)
-            x = __half2float(seg[at]);
-          else
-            x = __bfloat162float(seg[at]);
+      for (int i = 0; i < most; i += kPair) {
+        float x[kPair];
+        int id[kPair];
+#pragma unroll
+        for (int e = 0; e < kPair; ++e) {
+          x[e] = -INFINITY;
+          id[e] = 0;
+          if (i + e < n_picked) {
+            const int at = s.picked[warp][i + e][lane];
+            if constexpr (sizeof(T) == 4)
+              x[e] = seg[at];
+            else if constexpr (std::is_same<T, __half>::value)
+              x[e] = __half2float(seg[at]);
+            else
+              x[e] = __bfloat162float(seg[at]);
+            id[e] = first + at;
+          }
         }
-        f(x, first + at);
+        f(x, id);
       }
     } else {
       r.each_from(least, [&](const float (&y)[E], int i0) {
+        int id[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) f(y[e], i0 + e);
+        for (int e = 0; e < E; ++e) id[e] = i0 + e;
+        f(y, id);
       });
     }
   }
@@ -255,14 +268,20 @@ struct Wide {
   // (nothing is compared with xb before there is a border: xb is -inf)
   __device__ __forceinline__ bool kept(float x, int id) const { return x >= xb && (x != xb || id <= idb); }
 
-  // The first token, in the order of ids, at which the sum of weigh(x, id) exceeds
-  // target(whole): to all threads of the cluster, with the whole.  Logits below `least`
+  // The first token, in the order of ids, at which the sum of what weigh(logits, ids, weights)
+  // gives exceeds target(whole): to all threads of the cluster, with the whole.  Logits below `least`
   // weigh nothing.
   template <typename W, typename F>
   __device__ __forceinline__ u64 locate(float least, W weigh, F target, u64* whole) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     u64 mine = 0;
-    each(least, [&](float y, int id) { mine += weigh(y, id); });
+    each(least, [&](const auto& y, const auto& id) {
+      constexpr int N = kLength<decltype(y)>;
+      u64 w[N];
+      weigh(y, id, w);
+#pragma unroll
+      for (int e = 0; e < N; ++e) mine += w[e];
+    });
     u64 v[1] = {mine}, before, own;
     exchange<1>(s, v, rank, cluster, turn, &before, &own);
     *whole = v[0];
@@ -274,15 +293,17 @@ struct Wide {
       const int v0 = at * r.seg, end = min(v0 + r.seg, r.vectors), per = (r.seg / 32 + kWarps - 1) / kWarps;
       const int mine0 = v0 + warp * per * 32, mine1 = min(mine0 + per * 32, end);
       auto vector = [&](int b, float (&y)[E], u64 (&w)[E]) {  // of this lane, in the 32 from b on; returns its sum
-        const bool there = b + lane < end;
-        if (there) r.load(b + lane, y);
-        const int i0 = (int)r.first + (b + lane) * E;
-        u64 sum = 0;
+        int id[E];
+        if (b + lane < end) r.load(b + lane, y);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          w[e] = there ? weigh(y[e], i0 + e) : 0;
-          sum += w[e];
+          if (b + lane >= end) y[e] = -INFINITY;
+          id[e] = (int)r.first + (b + lane) * E + e;
         }
+        weigh(y, id, w);
+        u64 sum = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum += w[e];
         return sum;
       };
       float y[E];
@@ -356,7 +377,13 @@ struct Wide {
   // rare cases are functions of their own.)
   __device__ __noinline__ u64 nth_of(float lo, float hi, u64 nth) {
     u64 sum;
-    return locate(lo, [&](float y, int id) { return (u64)(y >= lo && y <= hi && kept(y, id)); }, [&](u64) { return nth - 1; }, &sum);
+    return locate(lo,
+                  [&](const auto& y, const auto& id, auto& w) {
+                    constexpr int N = kLength<decltype(y)>;
+#pragma unroll
+                    for (int e = 0; e < N; ++e) w[e] = y[e] >= lo && y[e] <= hi && kept(y[e], id[e]);
+                  },
+                  [&](u64) { return nth - 1; }, &sum);
   }
   __device__ __forceinline__ u64 nth(float lo, float hi, u64 n) {
     Wide w = *this;  // (its address is taken: this one stays in registers)
@@ -384,8 +411,12 @@ struct Wide {
       const uint32_t mid = first ? lo : lo + (hi - lo) / 2;
       const float t = of_key(mid);
       u64 v[1] = {0};
-      each(t, [&](float y, int id) {
-        if (y >= t && kept(y, id)) v[0] += kMass ? wf.one<kCopies>(y, table) : 1;
+      each(t, [&](const auto& y, const auto& id) {
+        constexpr int N = kLength<decltype(y)>;
+        u64 w[N];
+        if constexpr (kMass) wf.all<kCopies>(y, w, table);
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[0] += y[e] >= t && kept(y[e], id[e]) ? (kMass ? w[e] : 1) : 0;
       });
       exchange<1>(s, v, rank, cluster, turn);
       if (v[0] >= goal)
@@ -423,7 +454,7 @@ struct Wide {
     float hi = m, lo = fmaxf(low, kLowest), first = 0.f;
     if constexpr (kMass) {  // the maximum's exponent less wf.top
       float th = 0.f, tl = 0.f;
-      if (!wf.apart) wf.exponent<false>(m, &th, &tl);
+      if (!wf.apart) wf.exponent<false>(m, 0.f, &th, &tl);
       first = (th - (float)wf.top) + tl;
     }
     u64 above = 0;  // the measure of what is larger than hi
@@ -442,12 +473,18 @@ struct Wide {
       auto inside = [&](float y, int id) { return y >= lo && y <= hi && kept(y, id); };
       for (int i = tid; i < kBins; i += kThreads) s.bins[i] = 0;
       __syncthreads();
-      each(lo, [&](float y, int id) {
-        if (inside(y, id)) {
-          uint32_t n = 1;
-          if constexpr (kMass) n = __float2uint_rn(ex2(fmaf(y - m, wf.c, first)) * unit);
-          atomicAdd(&s.bins[bin_of(y)], n);
+      each(lo, [&](const auto& y, const auto& id) {
+        constexpr int N = kLength<decltype(y)>;
+        uint32_t n[N];
+        int b[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          n[e] = kMass ? __float2uint_rn(ex2(fmaf(y[e] - m, wf.c, first)) * unit) : 1;
+          b[e] = bin_of(y[e]);
         }
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (inside(y[e], id[e])) atomicAdd(&s.bins[b[e]], n[e]);
       });
       cluster_sync();
       // the whole cluster's: four bins of this thread
@@ -501,24 +538,25 @@ struct Wide {
       u64* const own = own_list(s.list);
       // nothing below this can be in the bins up to b1
       const float least_y = by_value ? fmaxf(lo, hi - (float)(b1 + 2) / scale) : fmaxf(lo, of_key(top_key - min(top_key, (uint32_t)((u64)(b1 + 1) << shift))));
-      each(least_y, [&](float y, int id) {
-        if (y >= least_y && inside(y, id)) {
-          const int b = bin_of(y);
-          if (b <= b1) {
-            u64 w = 1;
-            if constexpr (kMass) {
-              w = wf.one<kCopies>(y, table);
-              if (b < b0) x[0] += w;
-            }
-            if (b >= b0) {
-              x[1] += 1;
-              x[2] += w;
-              x[3] = max(x[3], (u64)key_of(y));
-              x[4] = max(x[4], (u64)~key_of(y) & 0xFFFFFFFFull);
-              add(own, kList, by_logit(y, id));
-            }
-          }
+      each(least_y, [&](const auto& y, const auto& id) {
+        constexpr int N = kLength<decltype(y)>;
+        u64 w[N];
+        int b[N];
+        if constexpr (kMass) wf.all<kCopies>(y, w, table);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          b[e] = y[e] >= least_y && inside(y[e], id[e]) ? bin_of(y[e]) : kBins;
+          if constexpr (kMass) x[0] += b[e] < b0 ? w[e] : 0;
         }
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (b[e] >= b0 && b[e] <= b1) {
+            x[1] += 1;
+            x[2] += kMass ? w[e] : 1;
+            x[3] = max(x[3], (u64)key_of(y[e]));
+            x[4] = max(x[4], (u64)~key_of(y[e]) & 0xFFFFFFFFull);
+            add(own, kList, by_logit(y[e], id[e]));
+          }
       });
       hand_over(s.list, kList);
       exchange<5, 24>(s, x, rank, cluster, turn);
@@ -694,11 +732,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (set.k == 0 && set.top_p < 1.f && whole == 0) {
         u64 v3[2] = {0, 0};
         r.each([&](const float (&y)[E], int) {
+          u64 w[E];
+          wf.all<kCopies>(y, w, table);
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            const u64 w = wf.one<kCopies>(y[e], table);
-            v3[0] += w;
-            v3[1] += y[e] >= b ? w : 0;
+            v3[0] += w[e];
+            v3[1] += y[e] >= b ? w[e] : 0;
           }
         });
         exchange<2>(s, v3, rank, cluster, turn);
@@ -738,7 +777,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           row_in.template cut<false>((u64)set.k, 0, m, b, 0, wf);
           if (set.top_p < 1.f) {
             u64 v1[1] = {0};
-            row_in.each(row_in.xb, [&](float y, int id) { v1[0] += row_in.kept(y, id) ? wf.one<kCopies>(y, table) : 0; });
+            row_in.each(row_in.xb, [&](const auto& y, const auto& id) {
+              constexpr int N = kLength<decltype(y)>;
+              u64 w[N];
+              wf.all<kCopies>(y, w, table);
+#pragma unroll
+              for (int e = 0; e < N; ++e) v1[0] += row_in.kept(y[e], id[e]) ? w[e] : 0;
+            });
             exchange<1>(s, v1, rank, cluster, row_in.turn);
             whole = v1[0];
           }
@@ -753,7 +798,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           row_in.template cut<true>(need, whole, m, low, (u64)a.vocab, wf);
         }
         from = fmaxf(floor_x, row_in.xb);
-        u64 found = row_in.locate(from, [&](float y, int id) { return y >= from && row_in.kept(y, id) ? wd.one<kCopies>(y, table) : 0; },
+        u64 found = row_in.locate(from,
+                                  [&](const auto& y, const auto& id, auto& w) {
+                                    constexpr int N = kLength<decltype(y)>;
+                                    wd.all<kCopies>(y, w, table);
+#pragma unroll
+                                    for (int e = 0; e < N; ++e)
+                                      if (!(y[e] >= from && row_in.kept(y[e], id[e]))) w[e] = 0;
+                                  },
                                   [&](u64 n) {
                                     bool rest;
                                     return times(n, set.u, &rest);

@@ -177,46 +177,66 @@ struct Weigh {
     top = 0;
     top = whole_of(max);
   }
-  // t = (x or x - m) log2(e) / T as th + tl; kApart false: the caller knows that the row is
-  // not apart
-  template <bool kApart = true>
-  __device__ __forceinline__ void exponent(float x, float* th, float* tl) const {
-    float low = 0.f;
+  // What exponents are taken from, x (or x - m) as a sum of two; kApart false: the caller
+  // knows that the row is not apart.
+  template <int N, bool kApart>
+  __device__ __forceinline__ void bases(const float (&x)[N], float (&v)[N], float (&low)[N]) const {
     if (kApart && apart) {
-      float d = __fsub_rn(x, m);
-      const float b = __fsub_rn(d, x);
-      low = __fadd_rn(__fsub_rn(x, __fsub_rn(d, b)), __fsub_rn(-m, b));
-      if (!(d > lim)) d = lim, low = 0.f;
-      x = d;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        v[e] = __fsub_rn(x[e], m);
+        const float b = __fsub_rn(v[e], x[e]);
+        low[e] = __fadd_rn(__fsub_rn(x[e], __fsub_rn(v[e], b)), __fsub_rn(-m, b));
+        if (!(v[e] > lim)) v[e] = lim, low[e] = 0.f;
+      }
     } else {
-      x = fmaxf(x, lim);
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] = fmaxf(x[e], lim), low[e] = 0.f;
     }
-    *th = __fmul_rn(x, c);
-    *tl = fmaf(x, c_low, fmaf(x, c, -*th));
+  }
+  // t = (v + low) log2(e) / T as th + tl
+  template <bool kApart>
+  __device__ __forceinline__ void exponent(float v, float low, float* th, float* tl) const {
+    *th = __fmul_rn(v, c);
+    *tl = fmaf(v, c_low, fmaf(v, c, -*th));
     if (kApart) *tl = fmaf(low, c, *tl);
   }
   __device__ __forceinline__ int whole_of(float x) const {
-    float th, tl;
-    exponent(x, &th, &tl);
+    float at[1] = {x}, v[1], low[1], th, tl;
+    bases<1, true>(at, v, low);
+    exponent<true>(v[0], low[0], &th, &tl);
     return (int)(__float_as_uint(th + kStep) - __float_as_uint(kStep)) >> 8;
   }
-  // table: the caller's copy, entry j at j * kCopies.  (One piece of code for rows that are
-  // apart and rows that are not: the kernels wait for their instructions.)
+  // N weights side by side.  table: the caller's copy, entry j at j * kCopies.  (One piece of
+  // code for rows that are apart and rows that are not, with a branch for all N: the kernels
+  // wait for their instructions.)
+  template <int kCopies, bool kApart = true, int N>
+  __device__ __forceinline__ void all(const float (&x)[N], u64 (&w)[N], const uint2* table) const {
+    float v[N], low[N];
+    bases<N, kApart>(x, v, low);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float th, tl;
+      exponent<kApart>(v[i], low[i], &th, &tl);
+      const float k = __fadd_rn(th, kStep);
+      const uint32_t bits = __float_as_uint(k);
+      // t = whole + j / 256 + r, |r| <= 2^-9 and what tl brings
+      const float r = __fadd_rn(__fsub_rn(th, __fsub_rn(k, kStep)), tl);
+      const int whole = (int)(bits - __float_as_uint(kStep)) >> 8;
+      const uint2 e = table[(bits & 255u) * kCopies];
+      const float p = r * fmaf(r, 0.24022651f, 0.69314718f);  // 2^r - 1
+      const uint32_t mant = e.y + __float_as_uint(fmaf(__uint_as_float(e.x), p, kUnit));  // 2^30 2^(j/256 + r)
+      u64 y;  // rounded: cut off, 150,000 small weights would lose 2^-28 of the largest
+      asm("shr.b64 %0, %1, %2;" : "=l"(y) : "l"((u64)mant << 32), "r"(top - whole + down - 1));
+      w[i] = (y + 1) >> 1;
+    }
+  }
   template <int kCopies, bool kApart = true>
   __device__ __forceinline__ u64 one(float x, const uint2* table) const {
-    float th, tl;
-    exponent<kApart>(x, &th, &tl);
-    const float k = __fadd_rn(th, kStep);
-    const uint32_t bits = __float_as_uint(k);
-    // t = whole + j / 256 + r, |r| <= 2^-9 and what tl brings
-    const float r = __fadd_rn(__fsub_rn(th, __fsub_rn(k, kStep)), tl);
-    const int whole = (int)(bits - __float_as_uint(kStep)) >> 8;
-    const uint2 e = table[(bits & 255u) * kCopies];
-    const float p = r * fmaf(r, 0.24022651f, 0.69314718f);  // 2^r - 1
-    const uint32_t mant = e.y + __float_as_uint(fmaf(__uint_as_float(e.x), p, kUnit));  // 2^30 2^(j/256 + r)
-    u64 w;  // rounded: cut off, 150,000 small weights would lose 2^-28 of the largest
-    asm("shr.b64 %0, %1, %2;" : "=l"(w) : "l"((u64)mant << 32), "r"(top - whole + down - 1));
-    return (w + 1) >> 1;
+    const float at[1] = {x};
+    u64 w[1];
+    all<kCopies, kApart>(at, w, table);
+    return w[0];
   }
 };
 
