@@ -350,12 +350,10 @@ struct Wide {
   __device__ __forceinline__ void hand_over(u64* list, int entries) const {
     __syncthreads();
     const int n = s.local;
-    if (threadIdx.x == 0) {
-      s.base = peer_add(peer(&s.count, 0), n);
-      s.local = 0;
-    }
+    if (threadIdx.x == 0) s.base = peer_add(peer(&s.count, 0), n);
+    __syncthreads();  // s.base; and all have read s.local
+    if (threadIdx.x == 0) s.local = 0;
     if (cluster == 1) return;
-    __syncthreads();
     const u64* const own = own_list(list);
     for (int i = threadIdx.x; i < n && s.base + i < entries; i += kThreads) put(peer(&list[s.base + i], 0), own[i]);
   }

@@ -389,3 +389,21 @@ def test_outputs_of_another_layout_are_refused(qp):
         qp.op_sample(x, u, torch.ones(2, device="cuda"))
     with pytest.raises(qp.MinferError, match="top_k"):
         qp.op_sample(x, u, None, torch.ones(3, device="cuda"))
+
+
+@pytest.mark.parametrize("t,rows,V", [(F16, 400, 40000), (BF16, 130, 150001), (F32, 52, 151936), (BF16, 13, 151936)])
+def test_sample_again_and_again(qp, t, rows, V):
+    """The same call gives the same bits, however its warps happen to run: top-p borders in long tails, whose lists every CTA of
+    a row's cluster adds to."""
+    g = gen(V)
+    x = logits(g, rows, V, t, 3, masked=True)
+    u = torch.rand(rows, generator=g, device="cuda")
+    p = torch.tensor([[0.5, 0.9, 0.97, 0.999, 0.9999999][r % 5] for r in range(rows)], device="cuda")
+    temp = torch.full((rows,), 1.1, device="cuda")
+    status = status_word()
+    want = qp.op_sample(x, u, temp, top_p=p, temperature_first=True, status=status)
+    off = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(400):
+        got = qp.op_sample(x, u, temp, top_p=p, temperature_first=True, status=status)
+        off += (got[0] != want[0]).sum() + (got[1] != want[1]).sum()
+    assert int(status) == 0 and int(off) == 0
