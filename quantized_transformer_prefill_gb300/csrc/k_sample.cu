@@ -33,9 +33,9 @@
 // Measured, f32 rows of 151,936: one with top-k and top-p 12.9 us, four top-p alone 22 us:
 // a chain of memory round trip, barriers of the cluster (1 us each) and a sort.  65 bf16
 // rows of 150,001 with top-p alone and temperatures up to 1.3, whose nuclei hold thousands of
-// tokens, 100 us (0.2 TB/s): issue slots, with two CTAs an SM; the longest row sets the time.
-// It weighs all of its tokens (15 us), counts them into the histogram (10 to 20), weighs
-// those above the border exactly (15 to 28), and again to draw (5 to 15).
+// tokens, 94 us (0.2 TB/s): the longest row sets the time.  It weighs all of its tokens, adds
+// them to a histogram, weighs those above the border exactly, and again to draw, each 10 to
+// 25 us of issue slots with two CTAs an SM, and barriers.
 #include <algorithm>
 
 #include "sample.cuh"
@@ -47,7 +47,6 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kList = 512;    // tokens between which a border is looked for, sorted by the first CTA
 constexpr int kShort = 2048;  // tokens that a row's only CTA sorts; of a cluster kList, for they come one by one
-constexpr int kPair = 2;      // tokens that are picked, side by side
 constexpr int kPicked = 32;   // tokens that a lane picks out of its vectors, at most
 constexpr int kGuess = 64;    // of top-p alone: tokens that the first bound aims at
 constexpr int kCopies = 4;    // of the table, against bank conflicts
@@ -227,31 +226,26 @@ struct Wide {
     n_picked = n;
     most = v[0] ? -1 : top;
   }
-  // f(logits, ids) for what may be `least` or more, by all lanes; kPair or E of them at a time,
-  // so that their chains of steps overlap
+  // f(logits, ids) for what may be `least` or more, by all lanes; one of them at a time, or, where
+  // whole vectors are gone through, E, whose chains of steps overlap
   template <typename F>
   __device__ __forceinline__ void each(float least, F f) const {
     if (most >= 0) {
       const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
       const T* const seg = reinterpret_cast<const T*>(r.near + warp * r.seg);
       const int first = (int)r.first + warp * r.seg * E;
-      for (int i = 0; i < most; i += kPair) {
-        float x[kPair];
-        int id[kPair];
-#pragma unroll
-        for (int e = 0; e < kPair; ++e) {
-          x[e] = -INFINITY;
-          id[e] = 0;
-          if (i + e < n_picked) {
-            const int at = s.picked[warp][i + e][lane];
-            if constexpr (sizeof(T) == 4)
-              x[e] = seg[at];
-            else if constexpr (std::is_same<T, __half>::value)
-              x[e] = __half2float(seg[at]);
-            else
-              x[e] = __bfloat162float(seg[at]);
-            id[e] = first + at;
-          }
+      for (int i = 0; i < most; ++i) {
+        float x[1] = {-INFINITY};
+        int id[1] = {0};
+        if (i < n_picked) {
+          const int at = s.picked[warp][i][lane];
+          if constexpr (sizeof(T) == 4)
+            x[0] = seg[at];
+          else if constexpr (std::is_same<T, __half>::value)
+            x[0] = __half2float(seg[at]);
+          else
+            x[0] = __bfloat162float(seg[at]);
+          id[0] = first + at;
         }
         f(x, id);
       }
@@ -588,7 +582,7 @@ struct Wide {
       hi = of_key(top);
       lo = of_key(least);
       whole = x[2];
-      n_in = n;
+      if constexpr (kMass) n_in = n;
     }
   }
 };
