@@ -208,6 +208,8 @@ def op_rope_paged_store(qkv, rope: RopeTable, pos, slot, cache: PagedCache, n_he
     (minfer_op_rope_paged_store).  Returns the rotated Q [n][n_head*head_dim]
     in the cache's type; rows with a negative slot are skipped (without `out`
     they are zero)."""
+    if isinstance(cache, PagedCacheQ8):  # (its description has another layout)
+        _refuse("cache: a PagedCache wanted, got a PagedCacheQ8")
     dev, hd = qkv.get_device(), cache.head_dim
     width = (n_head + 2 * cache.n_head_kv) * hd
     shape = qkv.shape
@@ -259,7 +261,7 @@ def op_rope_paged_store_q8(qkv, rope: RopeTable, pos, slot, cache: PagedCacheQ8,
     """op_rope_paged_store with K and V quantized to Q8_0 as they are stored
     (minfer_op_rope_paged_store_q8).  The rotated Q has the type of `out` (without
     it that of qkv), and qkv that type or float32."""
-    if type(cache) is not PagedCacheQ8:
+    if not isinstance(cache, PagedCacheQ8):
         _refuse(f"cache: a PagedCacheQ8 wanted, got {type(cache).__name__}")
     dev, hd = qkv.get_device(), cache.head_dim
     width = (n_head + 2 * cache.n_head_kv) * hd
@@ -314,7 +316,7 @@ def op_paged_read_q8(cache: PagedCacheQ8, slot, dtype=torch.float32, out=None, s
     [n].  Returns (k, v) [n][n_head_kv*head_dim] of `dtype`, or fills `out`, two such
     tensors of one type and stride, either of which may be None.  Rows with a
     negative slot are skipped (without `out` they are zero)."""
-    if type(cache) is not PagedCacheQ8:
+    if not isinstance(cache, PagedCacheQ8):
         _refuse(f"cache: a PagedCacheQ8 wanted, got {type(cache).__name__}")
     dev, n = slot.get_device(), slot.numel()
     width = cache.n_head_kv * cache.head_dim
@@ -355,7 +357,7 @@ def op_paged_read_q8(cache: PagedCacheQ8, slot, dtype=torch.float32, out=None, s
 def op_paged_attention_workspace(cache: PagedCache, n_req: int, n_head: int) -> Workspace:
     """A workspace for op_paged_attention calls of up to n_req requests, one call
     at a time."""
-    if type(cache) is PagedCacheQ8:
+    if isinstance(cache, PagedCacheQ8):
         _refuse("cache: a PagedCache wanted, got a PagedCacheQ8")
     n = ctypes.c_int64()
     with torch.cuda.device(cache.device):
@@ -372,6 +374,8 @@ def op_paged_attention(q, cache: PagedCache, table, length, n_head: int, scale: 
     new one included, scale None or 0 for 1 / sqrt(head_dim).  Returns o like q; `lse` (float32 [n_req][n_head]), when
     given, gets ln sum exp(scale q.k).  Rows of refused requests are not written
     (without `out` they are zero)."""
+    if isinstance(cache, PagedCacheQ8):  # (its description has another layout)
+        _refuse("cache: a PagedCache wanted, got a PagedCacheQ8")
     dev, width = q.get_device(), n_head * cache.head_dim
     shape = q.shape
     if not (q.dtype is cache.dtype and len(shape) == 2 and shape[1] == width and dev == cache.index):
@@ -428,7 +432,7 @@ def op_paged_attention(q, cache: PagedCache, table, length, n_head: int, scale: 
 def op_paged_attention_q8_workspace(cache: PagedCacheQ8, n_req: int, n_head: int) -> Workspace:
     """A workspace for op_paged_attention_q8 calls of up to n_req requests, one call
     at a time."""
-    if type(cache) is not PagedCacheQ8:
+    if not isinstance(cache, PagedCacheQ8):
         _refuse(f"cache: a PagedCacheQ8 wanted, got {type(cache).__name__}")
     n = ctypes.c_int64()
     with torch.cuda.device(cache.device):
@@ -441,7 +445,7 @@ def op_paged_attention_q8(q, cache: PagedCacheQ8, table, length, n_head: int, sc
                           out=None, lse=None, workspace: Workspace | None = None, status=None):
     """op_paged_attention over a quantized cache (minfer_op_paged_attention_q8): q
     [n_req][n_head*head_dim] of any of the three types, o like q."""
-    if type(cache) is not PagedCacheQ8:
+    if not isinstance(cache, PagedCacheQ8):
         _refuse(f"cache: a PagedCacheQ8 wanted, got {type(cache).__name__}")
     dev, width = q.get_device(), n_head * cache.head_dim
     shape = q.shape

@@ -186,6 +186,27 @@ def test_caches_of_the_other_kind_are_refused(qp):
             call()
 
 
+def test_operators_over_float_pages_refuse_a_quantized_cache_by_its_class(qp):
+    """Not by what it happens to lack: one with a `dtype`, which the other checks would let through, is refused as well."""
+    codes, scales = torch.zeros(4, 16, 2, 64, dtype=torch.int8), torch.zeros(4, 16, 2, 2, dtype=torch.float16)
+    n, table = torch.zeros(2, dtype=I32), torch.zeros(2, 3, dtype=I32)
+
+    class Named(qp.PagedCacheQ8):
+        dtype = torch.float16
+
+    for q8 in (qp.PagedCacheQ8(codes, codes, scales, scales), Named(codes, codes, scales, scales)):
+        for call in (lambda: qp.op_rope_paged_store(torch.zeros(2, 512, dtype=torch.float16), qp.RopeTable(64), n, n, q8, 4),  # noqa: B023
+                     lambda: qp.op_paged_attention(torch.zeros(2, 256, dtype=torch.float16), q8, table, n, 4),  # noqa: B023
+                     lambda: qp.op_paged_attention_workspace(q8, 2, 4)):  # noqa: B023
+            with pytest.raises(qp.MinferError, match="cache: a PagedCache wanted"):
+                call()
+        # (what is made for it takes a class derived from it)
+        with pytest.raises(qp.MinferError, match="CUDA device wanted"):
+            qp.op_paged_attention_q8(torch.zeros(2, 256), q8, table, n, 4)
+        with pytest.raises(qp.MinferError, match="CUDA device wanted"):
+            qp.op_paged_read_q8(q8, n)
+
+
 SAMPLE = dict(logits=PTR, type=F32, rows=3, vocab=100, row_stride=101, u=PTR, temperature=PTR, top_k=PTR, top_p=PTR, min_p=PTR, first=0,
               token=PTR, logprob=PTR, ws=PTR, ws_bytes=2 ** 40, status=None, stream=None)
 
