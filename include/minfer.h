@@ -627,7 +627,8 @@ int minfer_op_sample_workspace(int64_t rows, int64_t vocab, int type, int64_t* b
  * is drawn from with weights exp((x - max) / temperature): d_token[r] is the first id
  * at which the sum of the weights of ids up to it exceeds u times the whole;
  * d_logprob[r] (may be NULL) is the logarithm of its share.  A token that weighs less
- * than 2^-60 of the first is not drawn.  Weights are held to 2^-31 of themselves, as
+ * than 2^-60 of the first is not drawn.  Weights are held to 2^-29 of themselves (2^-28
+ * where the largest logit lies more than 690 temperatures from 0), as
  * whole numbers in units of 2^-(62 - log2 vocab) of the first, and summed without
  * rounding (a u of 0 draws the first id that is left, however little it weighs), but that
  * calls with a workspace round a block's sum once.  The result of a call depends on its

@@ -13,9 +13,9 @@
 // A token depends on sums over a whole row to a precision that f32 does not have: a
 // border between two tokens of 150,000 lies within 1e-6 of any random number, so sums
 // that are off by 1e-7 give another token in one row of ten.  Weights are therefore whole
-// numbers: 2^t is put together from a table of 2^(j/256) and a quadratic (to 2^-31 of
-// itself) and shifted to a fixed point that is the same for the whole row; their sums
-// are exact in 64 bits and do not depend on who adds what first.
+// numbers: 2^t is put together from a table of 2^(j/256) and a quadratic (to 2^-29 of
+// itself, see Weigh) and shifted to a fixed point that is the same for the whole row; their
+// sums are exact in 64 bits and do not depend on who adds what first.
 //
 // Many rows are streamed once (k_sample_stream.cu); this file: rows that a thread-block
 // cluster keeps.  A CTA copies its slice of the row into shared memory (cp.async, all of it
