@@ -58,3 +58,59 @@ def test_weights_are_as_exact_as_promised(qp, far, bound):
     want = (gap >= 0).int()
     assert torch.equal(token[sure], want[sure])
     assert int((sure & (gap.abs() < 4 * slack)).sum()) > 1000  # (some of them are near)
+
+
+def first_left(x, temp=1.0, k=0, p=1.0, floor=0.0, first=False):
+    """The first id of what is left of a row, and the logarithm of its share: [(id, log share)] for every length that top-p may leave when its
+    border is off by 2^-30 of the whole.  A draw from a random number of 0 is one of these, and no sum of weights decides it."""
+    x = x.double()
+    at = torch.nonzero(x > -INF)[:, 0]
+    if not len(at):
+        return [(-1, -INF)]
+    if temp == 0:
+        return [(int(torch.nonzero(x == x.max())[0, 0]), 0.0)]
+    sharp = temp if first else 1.0
+    order = at[torch.sort(x[at], descending=True, stable=True).indices]
+    if k > 0:
+        order = order[:k]
+    lengths = [len(order)]
+    if p < 1:
+        w = torch.exp((x[order] - x[order[0]]) / sharp)
+        before, whole = w.cumsum(0) - w, w.sum()
+        lengths = [max(1, int((before < (p + d) * whole).sum())) for d in (-2.0 ** -30, 2.0 ** -30)]
+    got = []
+    for n in range(lengths[0], lengths[-1] + 1):
+        left = order[:n]
+        z = x[left] - x[order[0]]
+        keep = z / temp >= -60 * math.log(2)
+        if floor > 0:
+            keep &= torch.exp(z / sharp) >= floor
+        left = left[keep].sort().values
+        z = (x[left] - x[order[0]]) / temp
+        got.append((int(left[0]), float(z[0] - torch.logsumexp(z, 0))))
+    return got
+
+
+@pytest.mark.parametrize("t,rows,V,extra", [(F32, 11, 40, 0), (BF16, 11, 5000, 3), (F16, 11, 32001, 5), (F32, 7, 151936, 0),
+                                            (F32, 52, 151936, 0), (BF16, 130, 150001, 3), (F16, 400, 40000, 1)])  # the last three are streamed
+@pytest.mark.parametrize("kind", ["plain", "k", "k and p", "p", "min", "large k", "hot", "all", "each its own"])
+def test_a_random_number_of_0_draws_the_first_token_left(qp, t, rows, V, extra, kind):
+    """However little it weighs: without a filter the first token of a row is one of 2^-20 and less of the whole, which no comparison of
+    sums within their accuracy would tell from the next one."""
+    from test_gpu_sample import SETTINGS, logits
+    x = logits(gen(V + rows + len(kind)), rows, V, t, extra, masked=V % 2 == 1)
+    x[rows // 2] = -INF
+    settings = {name: [f(r) for r in range(rows)] for name, f in SETTINGS[kind].items()}
+    tensor = lambda name, dt=F32: torch.tensor(settings[name], dtype=dt, device="cuda") if name in settings else None  # noqa: E731
+    args = tensor("temp"), tensor("k", I32), tensor("p"), tensor("floor")
+    for first in (False, True):
+        status = status_word()
+        token, logprob = qp.op_sample(x, torch.zeros(rows, device="cuda"), *args, temperature_first=first, status=status)
+        assert int(status) == 0
+        for r in range(rows):
+            row = {name: a[r].item() for name, a in zip(("temp", "k", "p", "floor"), args) if a is not None}
+            row["k"] = max(row.get("k", 0), 0)
+            want = first_left(x[r], first=first, **row)
+            assert int(token[r]) in [i for i, _ in want], (r, int(token[r]), want[:3])
+            if len(want) == 1:
+                close(logprob[r:r + 1], torch.tensor([want[0][1]], dtype=torch.float64, device="cuda"), 2.0 ** -28 + 2.0 ** -23 * min(abs(want[0][1]), 1e30))
