@@ -631,8 +631,12 @@ int minfer_op_sample_workspace(int64_t rows, int64_t vocab, int type, int64_t* b
  * where the largest logit lies more than 690 temperatures from 0), as
  * whole numbers in units of 2^-(62 - log2 vocab) of the first, and summed without
  * rounding (a u of 0 draws the first id that is left, however little it weighs), but that
- * calls with a workspace round a block's sum once.  The result of a call depends on its
- * inputs alone, bit for bit on one device type.
+ * calls with a workspace round a block's sum once, to the nearest unit.  The result of a
+ * call depends on its inputs alone, bit for bit on one device type; where it wants a
+ * workspace (which rows, vocab and type decide) a row's address modulo 16 is one of them, for
+ * it says where blocks begin: where a border lies within these roundings of d_u[r] or
+ * d_top_p[r], the same logits at another address, or in a call that wants none, may give
+ * another token.
  * -inf logits are masked tokens; a row with nothing else gets token -1 and log
  * probability -inf.  Device errors: MINFER_ERR_ARG for a setting out of its range, a
  * NaN or +inf among the logits (no output of that row is written). */

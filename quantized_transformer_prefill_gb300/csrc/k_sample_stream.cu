@@ -3,7 +3,8 @@
 //
 // The pass is bound by HBM.  A warp takes a block of 128 vectors of 16 bytes and leaves
 // the maxima of its four parts and, where a row wants it (top-p without top-k, or no
-// filter at all), the sum of its weights, relative to the block's own maximum.
+// filter at all), the sum of its weights, relative to the block's own maximum.  Blocks begin
+// at addresses that are multiples of 16: which tokens share one depends on the row's.
 //
 // A row's CTA finds its maximum and, for top-k, the k-th largest of the parts' maxima:
 // at least k tokens reach it and hardly more, for the first k rarely share a part.  The

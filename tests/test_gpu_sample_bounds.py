@@ -114,3 +114,37 @@ def test_a_random_number_of_0_draws_the_first_token_left(qp, t, rows, V, extra, 
             assert int(token[r]) in [i for i, _ in want], (r, int(token[r]), want[:3])
             if len(want) == 1:
                 close(logprob[r:r + 1], torch.tensor([want[0][1]], dtype=torch.float64, device="cuda"), 2.0 ** -28 + 2.0 ** -23 * min(abs(want[0][1]), 1e30))
+
+
+@pytest.mark.parametrize("t,rows,V", [(F32, 60, 151936), (BF16, 130, 150001), (F16, 400, 40000)])
+def test_streamed_rows_at_other_addresses(qp, t, rows, V):
+    """Blocks of a streamed row begin where its address modulo 16 says, and a block's sum is rounded once: the same logits elsewhere may be
+    drawn from differently, but only where the border lies within these roundings; at the same address modulo 16 they never are."""
+    from test_gpu_sample import check, logits
+    E, width = 16 // t.itemsize, V + 16
+    one = logits(gen(V), rows, V, t, masked=True)
+    u = torch.rand(rows, generator=gen(2), device="cuda").tolist()
+    for offset in {1, E // 2, E - 1}:
+        x = torch.empty(rows, width, dtype=t, device="cuda")[:, offset:offset + V]
+        x.copy_(one)
+        assert qp.op_sample_workspace(x) is not None
+        for settings in (dict(temp=[0.9] * rows), dict(temp=[1.1] * rows, p=[0.97] * rows), dict(k=[50] * rows, p=[0.9] * rows)):
+            check(qp, x, u, **settings)
+    # Two tokens of 0.3 units next to a block's end, and behind them two that weigh half of the row each: with u = 0.5 the first of these is
+    # drawn if the small ones count for a unit, the second if they do not.  Both are within 2^-(62 - log2 V) of the border.
+    unit = 62 - math.ceil(math.log2(V))
+    x = torch.empty(rows, width | 1, dtype=t, device="cuda").fill_(-INF)[:, 1:1 + V]  # every row at another address
+    end, a, b = 128 * E, 640 * E + 7, V - 1
+    x[:, end - 1] = x[:, end - E] = (math.log(0.3) - unit * math.log(2))
+    x[:, a] = x[:, b] = 0
+    half = torch.full((rows,), 0.5, device="cuda")
+    assert qp.op_sample_workspace(x) is not None
+    token, logprob = qp.op_sample(x, half)
+    assert all(i in (a, b) for i in token.tolist())
+    close(logprob, torch.full((rows,), -math.log(2), dtype=torch.float64, device="cuda"), 2.0 ** -23)
+    by_address = {}
+    for r in range(rows):
+        by_address.setdefault(x[r].data_ptr() % 16, set()).add(int(token[r]))
+    assert len(by_address) == E and all(len(tokens) == 1 for tokens in by_address.values())
+    again = qp.op_sample(x, half)
+    assert torch.equal(again[0], token) and torch.equal(again[1], logprob)
