@@ -45,7 +45,7 @@ __device__ __forceinline__ u64 warp_scan(u64 v, int lane) {  // inclusive
   return v;
 }
 
-// floor(n * f) for 0 <= f < 1, exactly; *rest: whether something was cut off
+// floor(n * f) for 0 <= f < 1 (and not -0), exactly; *rest: whether something was cut off
 __device__ __forceinline__ u64 times(u64 n, float f, bool* rest) {
   const uint32_t b = __float_as_uint(f), e = b >> 23;
   const u64 mant = (u64)(e ? (b & 0x7FFFFFu) | 0x800000u : b & 0x7FFFFFu);  // f = mant 2^(max(e, 1) - 150)
@@ -71,9 +71,9 @@ struct Settings {
 };
 __device__ __forceinline__ Settings settings_of(const SampleArgs& a, int64_t row) {
   Settings s;
-  s.u = a.u[row];
+  s.u = a.u[row] + 0.f;  // (-0 as 0: `times` reads the bits)
   s.temp = a.temperature ? a.temperature[row] : 1.f;
-  s.top_p = a.top_p ? a.top_p[row] : 1.f;
+  s.top_p = a.top_p ? a.top_p[row] + 0.f : 1.f;
   s.min_p = a.min_p ? a.min_p[row] : 0.f;
   const int k = a.top_k ? a.top_k[row] : 0;
   s.k = k > 0 && k < a.vocab ? k : 0;

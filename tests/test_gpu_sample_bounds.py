@@ -148,3 +148,21 @@ def test_streamed_rows_at_other_addresses(qp, t, rows, V):
     assert len(by_address) == E and all(len(tokens) == 1 for tokens in by_address.values())
     again = qp.op_sample(x, half)
     assert torch.equal(again[0], token) and torch.equal(again[1], logprob)
+
+
+@pytest.mark.parametrize("rows,V", [(12, 40), (12, 5000), (6, 151936), (60, 151936)])
+def test_negative_zeros_are_zeros(qp, rows, V):
+    """As random numbers (they mark no padding), temperatures, top_p and min_p."""
+    from test_gpu_sample import logits
+    x = logits(gen(V + rows), rows, V, F32, 1)
+    u = torch.rand(rows, generator=gen(1), device="cuda")
+    zero, one = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+    k = torch.tensor([[0, 50, 1000][r % 3] for r in range(rows)], dtype=I32, device="cuda")
+    for first in (False, True):
+        for args in ((zero, one, None, None, None), (zero, one, k, 0.9 * one, None), (u, one, k, zero, None), (u, one, None, zero, zero), (zero, one, None, zero, zero),
+                     (u, zero, k, None, None), (u, one, k, None, zero)):
+            status = status_word()
+            want = qp.op_sample(x, *args, temperature_first=first, status=status)
+            got = qp.op_sample(x, *(-a if a is zero else a for a in args), temperature_first=first, status=status)
+            assert int(status) == 0 and (want[0] >= 0).all()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
