@@ -564,9 +564,10 @@ int minfer_op_paged_read_q8(const minfer_paged_cache_q8* cache, const int32_t* d
  * (F32, F16 or BF16), everything else as there, the workspace's rules included; a
  * workspace serves one of the two operators.  The codes are exact operands of the
  * products; scales, scores, softmax statistics and sums are f32.  A query value is
- * exact (f16), exact to 2^-40 of the largest of its head (bf16), or held in two
- * 11-bit numbers (f32); a softmax weight times a row's scale is held in two as well (to
- * 2^-22 of it, or 2^-40 of the request's largest scale so far).  What lies in scales
+ * exact (f16), exact to 2^-39 of the largest of its head (bf16), or held in two
+ * 11-bit numbers (f32: to 2^-22 of it, or 2^-39 of the largest of its head); a softmax
+ * weight times a row's scale is held in two as well (to 2^-22 of it, or 2^-39 of the
+ * request's largest scale so far).  What lies in scales
  * and codes behind a request's last row is never used, whatever its bits.  Scales are
  * finite: one of V that is not makes its 32 dims NaN. */
 int minfer_op_paged_attention_q8_workspace(int n_req, int n_head,

@@ -15,14 +15,16 @@
 //  - Q K^T: the sum over a block is an accumulator of its own, two k16 MMAs of f16;
 //    the block's scale comes in as an f32 multiply-add.  Which 16 dims an MMA takes is
 //    free as long as Q follows, so a lane reads 8 neighbouring codes of a key.  Q is
-//    f16: exact, or times a power of two that brings the head's largest value near
-//    2^15 (bf16, which loses what lies 2^-40 below it; f32, as the sum of two).
+//    f16: exact, or times a power of two that brings the head's largest value to between
+//    2^14 and 2^15 (bf16, and f32 as the sum of two), so that f16's steps of 2^-24 lose 2^-39 of
+//    it at most.
 //  - P V: a weight times the row's scale is what the MMAs take, per block of 32 dims, as
 //    the sum of two f16 numbers (one would leave 2^-11 of the weight, more than a
 //    result's own rounding).  They count in units of 2^-15 of a power of two that no scale
 //    of the piece so far exceeds; when a larger one comes, the outputs are scaled down as
 //    they are for a new maximum.  So none overflows, and what is lost lies 2^-22 below the
-//    weight or 2^-40 below the largest.  The weights change from the layout of S^T to that
+//    weight or 2^-39 below the largest scale (half a step of 2^-24 of these units, which are at
+//    most twice that large).  The weights change from the layout of S^T to that
 //    of P^T as f32, in two halves of 16 bits (transpose8); V's codes come transposed out
 //    of ldmatrix, two neighbouring dims in a 16-bit element.
 //  - With 16-bit queries and heads of 128 a warp takes two tiles of 16 keys at a time: two

@@ -605,3 +605,46 @@ def test_the_readmes_quantized_step(qp):
         assert (s["o"][2] == 0).all()
         assert s["token"].tolist() == [int(logits[0].argmax()), int(logits[1].argmax()), -1] and (s["logprob"] == 0).all()
         have = want
+
+
+@pytest.mark.parametrize("t", [F32, BF16])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attention_small_values_beside_large_queries(qp, t, hd):
+    """A query is held to steps of 2^-38 of its head's largest value (a power of two here, the worst case), so to 2^-39 of it: values
+    half way between two steps under keys that do not look at the largest one.  All steps are rounded the same way."""
+    nh, P = 4, 16
+    codes, scales = torch.zeros(1, P, nh, hd, dtype=torch.int8, device="cuda"), torch.ones(1, P, nh, hd // 32, dtype=F16, device="cuda")
+    codes[0, 0, :, 1:] = 127
+    q = torch.empty(1, nh, hd, device="cuda")
+    q[:] = (2 * (torch.arange(hd, device="cuda") % 31) + 0.5) * 2.0 ** -38
+    q[..., 0] = 1
+    scale = 2.0 ** 20
+    lse = torch.empty(1, nh, device="cuda")
+    qp.op_paged_attention_q8(q.view(1, -1).to(t), qp.PagedCacheQ8(codes, codes.clone(), scales, scales.clone()), dev([[0]]), dev([1]), nh, scale=scale, lse=lse)
+    want = (q[..., 1:].to(t).double() * 127).sum(-1) * scale
+    lost = (hd - 1) * 127 * scale * 2.0 ** -39
+    assert float(lost) > 2.0 ** -8  # (far more than the sums' own roundings)
+    close(lse, want, lost + want.abs() * ((hd // 8 + 2) * 2.0 ** -23 + 4 * U) + 8 * U)
+
+
+@pytest.mark.parametrize("t", [F32, F16, BF16])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attention_small_scales_beside_large_ones(qp, t, hd):
+    """A weight times its row's scale is held to steps of 2^-38 of the request's largest scale so far, at worst: rows of subnormal scales half way
+    between two steps, all rounded the same way, beside one of a large scale that weighs next to nothing."""
+    nh, P, n = 4, 16, 9
+    k, v = (torch.zeros(1, P, nh, hd, dtype=torch.int8, device="cuda") for _ in range(2))
+    ks, vs = (torch.ones(1, P, nh, hd // 32, dtype=F16, device="cuda") for _ in range(2))
+    k[0, 0] = -100  # the first row scores -100, the others 0
+    v[0, :n] = 127
+    large = 2.0 ** 15 + 2.0 ** 5  # just past a power of two
+    small = (4 * torch.arange(1, n, device="cuda") + 1) * 2.0 ** -24
+    vs[0, 0], vs[0, 1:n] = large, small[:, None, None].to(F16)
+    q = torch.zeros(1, nh, hd, device="cuda")
+    q[..., 0] = 1
+    o = qp.op_paged_attention_q8(q.view(1, -1).to(t), qp.PagedCacheQ8(k, v, ks, vs), dev([[0]]), dev([n]), nh, scale=1.0)
+    p = torch.exp(torch.tensor([-100.0] + [0.0] * (n - 1), dtype=torch.float64, device="cuda"))
+    want = (127 * (p * torch.cat([torch.tensor([large], device="cuda"), small]).double()).sum() / p.sum()).expand(1, nh * hd)
+    lost = 127 * 2.0 ** -39 * large
+    assert lost > 2.0 ** -8 * float(want.abs().max())  # (far more than the sums' own roundings)
+    close(o, want, lost + want.abs() * (2.0 ** -20 + (0 if t == F32 else half(t))) + (2.0 ** -25 if t == F16 else 0))
