@@ -782,11 +782,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
         if (set.top_p < 1.f) {
           // All that weighs less than a token's share of what may be left out is left out
-          // (2^(63 - down) is more than any weight; the margin is for the logarithm).
+          // (2^(63 - down) is more than any weight; the margin is for the logarithm).  A unit
+          // less than this share: a weight counts for up to half a unit more than it is, and the
+          // whole, if it comes from blocks, for half a unit a token more than their weights'
+          // sum.  So what is picked reaches `need`, and nothing else is ever kept.
           const u64 need = need_of(whole, set.top_p);
-          const float share = (float)(whole > need ? whole - need : 0) / (float)a.vocab * exp2f((float)(down - 63));
+          const float share = ((float)(whole > need ? whole - need : 0) / (float)a.vocab - 1.f) * exp2f((float)(down - 63));
           const float low = fmaxf(m + set.sharp * (logf(fmaxf(share, 0x1p-62f)) - 0.01f) - fabsf(m) * 0x1p-20f, kLowest);
           if (set.k == 0) row_in.pick(low);
+          if (low > row_in.xb) row_in.xb = low, row_in.idb = 0x7FFFFFFF;
           row_in.template cut<true>(need, whole, m, low, (u64)a.vocab, wf);
         }
         from = fmaxf(floor_x, row_in.xb);

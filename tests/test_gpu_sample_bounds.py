@@ -166,3 +166,29 @@ def test_negative_zeros_are_zeros(qp, rows, V):
             got = qp.op_sample(x, *(-a if a is zero else a for a in args), temperature_first=first, status=status)
             assert int(status) == 0 and (want[0] >= 0).all()
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("rows", [1, 5, 60])  # the last are streamed, and left to the clusters
+@pytest.mark.parametrize("V,m,tail", [(152064, 0.69, 13.51), (152631, 0.69, 13.502)])
+def test_a_nucleus_among_weights_of_a_few_units(qp, rows, V, m, tail):
+    """One token, and all others at `tail` units of the row's fixed point, which count for 14: a little more than their share of what top_p = 1 - 2^-24
+    leaves out, while `tail` is a little less.  A beginning of the others is left beside the first, by ids; of a streamed row, whose blocks sum up
+    `tail` itself, the first alone may be left as well."""
+    big = V // 2
+    W = math.exp(m - math.floor(m / math.log(2)) * math.log(2)) * 2.0 ** (62 - 18)
+    x = torch.full((rows, V), m + math.log(tail / W), device="cuda")
+    x[:, big] = m
+    units = math.exp(float(x[0, 0]) - float(x[0, big])) * W
+    assert 13.5 < units - 2.0 ** -20 and units + 2.0 ** -20 < 14
+    whole = W + 14 * (V - 1)
+    n = math.ceil((14 * (V - 1) - whole * 2.0 ** -24) / 14)  # tokens left beside the first
+    assert 0 < n < big
+    p = torch.full((rows,), 1 - 2.0 ** -24, device="cuda")
+    for u in (0.0, 2.0 ** -33, 2.0 ** -32, 2.0 ** -31, 2.0 ** -20, 0.5, 1 - 2.0 ** -24):
+        token, logprob = qp.op_sample(x, torch.full((rows,), u, device="cuda"), None, None, p)
+        want = u * (W + 14 * n) / 14  # of the others, 14 units each
+        want = int(want) if want < n else big
+        for r in range(rows):
+            assert abs(int(token[r]) - want) <= 1 or rows == 60 and int(token[r]) == big, (u, int(token[r]), want)
+            share = 1.0 if int(token[r]) == big else units / W
+            close(logprob[r:r + 1], torch.tensor([math.log(share)], dtype=torch.float64, device="cuda"), 2.0 ** -22 + 2.0 ** -23 * abs(math.log(share)))
