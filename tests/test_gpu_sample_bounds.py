@@ -192,3 +192,30 @@ def test_a_nucleus_among_weights_of_a_few_units(qp, rows, V, m, tail):
             assert abs(int(token[r]) - want) <= 1 or rows == 60 and int(token[r]) == big, (u, int(token[r]), want)
             share = 1.0 if int(token[r]) == big else units / W
             close(logprob[r:r + 1], torch.tensor([math.log(share)], dtype=torch.float64, device="cuda"), 2.0 ** -22 + 2.0 ** -23 * abs(math.log(share)))
+
+
+@pytest.mark.parametrize("rows,V", [(15000, 151936), (290001, 7501)])  # streamed, and kept by clusters
+def test_logits_past_32_bits(qp, rows, V):
+    """More than 2^31 logits: the rows of one call are those of calls on parts of them."""
+    from test_gpu_sample import by_definition
+    assert rows * V > 2 ** 31
+    g = gen(9)
+    x = torch.empty(rows, V, device="cuda").normal_(0, 3, generator=g)
+    u = torch.rand(rows, generator=g, device="cuda")
+    kinds = torch.arange(rows, device="cuda") % 4
+    temp, k = torch.where(kinds == 0, 0.0, 0.8), torch.where(kinds == 1, 50, 0).to(I32)
+    p = torch.where(kinds == 2, 0.9, 1.0)
+    status = status_word()
+    token, logprob = qp.op_sample(x, u, temp, k, p, status=status)
+    assert int(status) == 0
+    part = (rows + 5) // 6 // 4 * 4  # (the same addresses modulo 16)
+    for at in range(0, rows, part):
+        s = slice(at, min(at + part, rows))
+        if V > 100000 and s.stop - at < 1000:
+            continue  # (so few are kept)
+        got = qp.op_sample(x[s], u[s], temp[s], k[s], p[s])
+        assert torch.equal(got[0], token[s]) and torch.equal(got[1], logprob[s])
+    edge = 2 ** 31 // V
+    for r in (0, edge - 1, edge, edge + 1, rows - 3, rows - 2, rows - 1):
+        want, _, near = by_definition(x[r], float(u[r]), float(temp[r]), int(k[r]), float(p[r]))
+        assert near or int(token[r]) == want
