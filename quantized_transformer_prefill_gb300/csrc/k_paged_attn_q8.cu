@@ -30,8 +30,9 @@
 //  - With 16-bit queries and heads of 128 a warp takes two tiles of 16 keys at a time: two
 //    chains of dependent steps instead of one.
 //
-// Measured: 64 requests of up to 4096 tokens, 28/4 heads of 128, bf16, 144 MB: 42 us (3.4
-// TB/s); one of 131,071, 12/2 heads of 128, f16, 71 MB: 26 us; 33 of up to 2048, 14/2 heads
+// Measured: 64 requests of up to 4096 tokens, 28/4 heads of 128, bf16, 144 MB: 39 to 42 us, by
+// the lengths (3.4 TB/s; f32 50 where bf16 takes 39: twice the MMAs in Q K^T, one tile at a time,
+// sums added up outside the tensor core, 52 bytes of registers spilled); one of 131,071, 12/2 heads of 128, f16, 71 MB: 26 us; 33 of up to 2048, 14/2 heads
 // of 64, f32: 13.4 us; one of 513: 7.2 us.  Of the first 13 us are start, uneven ends and
 // join; of the rest the loads alone take 15 and the arithmetic alone 22, so issue slots bound
 // it: a key and head block of 8 costs the same MMAs and conversions whether 7 or 8 of its

@@ -30,10 +30,12 @@
 // filter, high temperatures, large k) go the wide way: a histogram brackets the border of a
 // filter until a list holds what lies between, and the draw goes segment by segment.
 //
-// Measured, f32 rows of 151,936: one with top-k and top-p 12.9 us, four top-p alone 22 us:
+// Measured, f32 rows of 151,936: one with top-k and top-p 13 to 17 us, by its settings, four
+// with top-p alone 25; of 200,001, which shared memory does not hold, one 28 to 39 us, eight 31
+// without a filter, 60 with top-p and 102 with top-k and top-p:
 // a chain of memory round trip, barriers of the cluster (1 us each) and a sort.  65 bf16
 // rows of 150,001 with top-p alone and temperatures up to 1.3, whose nuclei hold thousands of
-// tokens, 94 us (0.2 TB/s): the longest row sets the time.  It weighs all of its tokens, adds
+// tokens, 93 us (0.2 TB/s): the longest row sets the time.  It weighs all of its tokens, adds
 // them to a histogram, weighs those above the border exactly, and again to draw, each 10 to
 // 25 us of issue slots with two CTAs an SM, and barriers.
 #include <algorithm>

@@ -15,9 +15,10 @@
 // nucleus past the list, weights whose exponents are taken from x - max) are
 // left to sample_kernel.
 //
-// 512 f32 rows of 151,936 (311 MB): greedy 64 us, plain 126, top-k 154, top-k and top-p 200,
-// top-p 206, min-p 77, all of them mixed 159, of which the pass takes 70 (4.4 TB/s), the rows
-// 30 and those left 52.
+// 512 f32 rows of 151,936 (311 MB): greedy 64 us, plain 125, top-k 164, top-k and top-p 221,
+// top-p 212, min-p 77, all of them mixed 158, of which the pass takes 70 (4.4 TB/s), the rows
+// 30 and those left 52.  (Of the rows with a k an eighth have 1,000, which is left, and an eighth
+// all tokens.)
 #include <algorithm>
 
 #include "sample.cuh"
